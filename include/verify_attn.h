@@ -435,6 +435,120 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
                               va_stream_t stream);
 
 /*
+ * Attention of a chunk of new tokens over the cache: the pass that fills it
+ * (pieces of prompts), that decodes without a draft tree (one token per
+ * request), or both in one ragged batch.  Same rows, widths and precision as
+ * the verify calls; the new tokens are a causal run instead of a tree, and a
+ * request may bring any number of them.
+ *
+ * Request b's new tokens are query tokens q_indptr[b] .. q_indptr[b+1] - 1, n_b
+ * of them (0 is allowed); its keys are its P_b = prefix_len[b] cached keys
+ * followed by the new tokens' own rows, which the caller has already written
+ * into the pool.  Token i sits at position P_b + i and sees key j when
+ *   j <= P_b + i   and   (window == 0 or j > P_b + i - window or j < sinks):
+ * with a window, the last `window` keys up to its own and the first `sinks`
+ * keys of the list.
+ *   q              bf16 [total_q, H, 576], contiguous, 16-byte aligned.
+ *   slot_idx       int32; request b's P_b prefix slots in order, then the
+ *                  slots of its new tokens, start at slot_idx[kv_indptr[b]].
+ *   kv_indptr      int32 [B+1] device; a list may hold more entries than
+ *                  P_b + n_b (they are not read).
+ *   kv_start       (contiguous form) int64 [B] device: key j is pool row
+ *                  kv_start[b] + j.
+ *   prefix_len     int32 [B] device.
+ *   q_indptr       int32 [B+1] device, non-decreasing, within [0, total_q].
+ *   total_q        query tokens in q, out and lse.  Rows that no request owns
+ *                  (before q_indptr[0], behind q_indptr[B]) are left as they
+ *                  were, so a captured call can serve smaller batches.
+ *   1 <= B <= 65535, 1 <= H, 0 <= total_q, total_q * H <= VA_CHUNK_ROWS_MAX.
+ *   window, sinks  >= 0; host values, the same for every request.
+ *   flags          VA_PATH_*.
+ *   workspace      device, >= va_chunk_workspace_bytes(B, total_q, H, flags)
+ *                  bytes, 256-byte aligned; first 4 bytes: the status word,
+ *                  rewritten by every call.
+ *   out            bf16 [total_q, H, 512], 16-byte aligned; lse float
+ *                  [total_q, H] (natural log).  A token none of whose keys has
+ *                  a valid pool row gets out 0 and lse -inf.
+ * Device-data errors: bounds outside the arrays, or a list shorter than
+ * P_b + n_b, are clamped (the prefix gives way) and set
+ * VA_STATUS_BAD_INDPTR; a slot outside the pool is skipped and sets
+ * VA_STATUS_BAD_SLOT when a token would have seen it.  What keys hold that a
+ * token does not see (later tokens, keys outside the window), NaN and
+ * infinities included, does not change that token's result.
+ */
+#define VA_CHUNK_ROWS_MAX (1 << 24)
+size_t va_chunk_workspace_bytes(int B, int total_q, int H, int flags);
+int va_chunk_attn_paged(const void *q, const void *kv_pool, int64_t num_slots,
+                        int64_t kv_row_stride, const int32_t *slot_idx, const int32_t *kv_indptr,
+                        const int32_t *prefix_len, const int32_t *q_indptr, int B, int total_q,
+                        int H, float sm_scale, int window, int sinks, int flags, void *workspace,
+                        size_t workspace_bytes, void *out, float *lse, va_stream_t stream);
+int va_chunk_attn_contiguous(const void *q, const void *kv_pool, int64_t num_slots,
+                             int64_t kv_row_stride, const int64_t *kv_start,
+                             const int32_t *prefix_len, const int32_t *q_indptr, int B,
+                             int total_q, int H, float sm_scale, int window, int sinks, int flags,
+                             void *workspace, size_t workspace_bytes, void *out, float *lse,
+                             va_stream_t stream);
+
+/*
+ * Attention weight that each listed key received from a chunk's rows, added
+ * to a running total -- the measure by which va_kv_evict chooses:
+ *   weights_out[e] = weights_in[e] + sum_r exp(sm_scale <q_r, kv_j> - lse_r),
+ * e = kv_indptr[b] + j, over the rows r = (token, head) of request b that see
+ * key j (as in va_chunk_attn_paged with the same window and sinks).  lse is
+ * that call's result; the rows may also be a part of its tokens (the last
+ * ones of a chunk, with prefix_len counting the tokens before them).  A row
+ * at lse -inf gives nothing.
+ *   weights_in     float [num_entries] device or NULL (totals start at 0);
+ *                  may be weights_out itself, but must not overlap it
+ *                  otherwise.
+ *   weights_out    float [num_entries] device.  Written for the entries of
+ *                  every request's P_b + n_b keys; other entries are left.
+ *   num_entries    entries of slot_idx, weights_in and weights_out.
+ *   workspace      >= va_kv_weights_workspace_bytes(...) bytes, 256-byte
+ *                  aligned; first 4 bytes: the status word.
+ * The requests' lists must not overlap.  Sums are taken in a fixed order: the
+ * result is deterministic.  Other arguments as for va_chunk_attn_paged.
+ */
+size_t va_kv_weights_workspace_bytes(int B, int total_q, int H, int64_t num_entries, int flags);
+int va_kv_weights_paged(const void *q, const void *kv_pool, int64_t num_slots,
+                        int64_t kv_row_stride, const int32_t *slot_idx, const int32_t *kv_indptr,
+                        const int32_t *prefix_len, const int32_t *q_indptr, const float *lse,
+                        const float *weights_in, int64_t num_entries, int B, int total_q, int H,
+                        float sm_scale, int window, int sinks, int flags, void *workspace,
+                        size_t workspace_bytes, float *weights_out, va_stream_t stream);
+
+/*
+ * Eviction by accumulated weight.  A request with L = prefix_len[b] > budget
+ * listed keys keeps `budget` of them: the first `sinks`, the last `recent`, and
+ * of the others those with the largest weights (equal weights: the lower
+ * index stays; NaN counts as -inf).  The kept entries move, in list order, to
+ * the front of the request's list in slot_idx_out and weights_out; entries of
+ * the outputs past them are left.  prefix_len_out[b] = min(L, budget).
+ *   budget, sinks, recent  host values >= 0, sinks + recent <= budget.
+ *   free_slots     int32 [free_capacity] device, or NULL: the free list of
+ *                  va_tree_build.  The evicted slots, request by request and in
+ *                  list order, are written in front of its head:
+ *                  free_slots[*free_head - total ..), and *free_head_out =
+ *                  *free_head - total (0 at least).  Slots that do not fit the
+ *                  list are dropped and set VA_STATUS_BAD_DST.  Pass NULL when
+ *                  requests share slots.
+ *   slot_idx_out, prefix_len_out, weights_out, free_head_out  may each be the
+ *                  matching input itself (in place), but must not overlap it
+ *                  otherwise.  The requests' lists must not overlap.
+ *   num_entries    entries of slot_idx, weights and their outputs; a list that
+ *                  leaves them, or is shorter than prefix_len, is clamped and
+ *                  sets VA_STATUS_BAD_INDPTR.
+ *   status         uint32 device word or NULL; bits are OR-ed in (the caller
+ *                  clears it).
+ */
+int va_kv_evict(const int32_t *slot_idx, const int32_t *kv_indptr, const int32_t *prefix_len,
+                const float *weights, int64_t num_entries, int B, int budget, int sinks,
+                int recent, int32_t *free_slots, int64_t free_capacity, const int32_t *free_head,
+                int32_t *slot_idx_out, int32_t *prefix_len_out, float *weights_out,
+                int32_t *free_head_out, uint32_t *status, va_stream_t stream);
+
+/*
  * Benchmark helper: while both handles are non-NULL, every verify call on this
  * process records cudaEvent_t `before` on its stream immediately before it
  * launches the split-K partial kernel and `after` immediately after, so the

@@ -7,7 +7,8 @@ library has not been built, :func:`load` raises.
 
 Names follow the C ABI: ``verify_attn_paged``, ``verify_attn_contiguous``,
 ``verify_attn_defrag``, ``workspace_bytes``, ``auto_nsplit``, ``init``,
-``read_status``.
+``read_status``; ``chunk_attn_paged``, ``chunk_attn_contiguous``, ``kv_weights``
+and ``kv_evict`` (with ``prepare_`` forms) for the calls around them.
 """
 from __future__ import annotations
 
@@ -91,6 +92,21 @@ def load() -> ctypes.CDLL:
     lib.va_kv_append_contiguous.restype = i32
     lib.va_kv_compact_accepted.argtypes = [P, i64, i64, P, P, P, P, P, i32, i32, P, P]
     lib.va_kv_compact_accepted.restype = i32
+    lib.va_chunk_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.va_chunk_workspace_bytes.restype = sz
+    lib.va_chunk_attn_paged.argtypes = [P, P, i64, i64, P, P, P, P, i32, i32, i32, f32, i32, i32,
+                                        i32, P, sz, P, P, P]
+    lib.va_chunk_attn_paged.restype = i32
+    lib.va_chunk_attn_contiguous.argtypes = [P, P, i64, i64, P, P, P, i32, i32, i32, f32, i32, i32,
+                                             i32, P, sz, P, P, P]
+    lib.va_chunk_attn_contiguous.restype = i32
+    lib.va_kv_weights_workspace_bytes.argtypes = [i32, i32, i32, i64, i32]
+    lib.va_kv_weights_workspace_bytes.restype = sz
+    lib.va_kv_weights_paged.argtypes = [P, P, i64, i64, P, P, P, P, P, P, i64, i32, i32, i32, f32,
+                                        i32, i32, i32, P, sz, P, P]
+    lib.va_kv_weights_paged.restype = i32
+    lib.va_kv_evict.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, P, i64, P, P, P, P, P, P, P]
+    lib.va_kv_evict.restype = i32
     lib.verify_attn_paged_noalloc.argtypes = [P, P, i64, i64, P, P, P, P, P, i32, i32, i32, f32,
                                               i32, i32, P, P, P]
     lib.verify_attn_paged_noalloc.restype = i32
@@ -541,6 +557,296 @@ def tree_build(cand_tokens: torch.Tensor, cand_logp: torch.Tensor, T: int,
                               _stream(stream))
     _check("va_tree_build", rc)
     return par, tok, depth, (loc if free_slots is not None else None)
+
+
+class BoundCall:
+    """A chunk, weight or eviction call whose arguments were checked and
+    marshalled once.
+
+    Calling it launches again on the same buffers, whose contents may change
+    between calls, on the stream it was prepared for, or, when none was given,
+    on the current stream of the buffers' device at the time of the call.  The
+    host work per call is one C call.  It keeps the tensors it refers to alive;
+    `result` is what it returns.
+    """
+
+    def __init__(self, name: str, args: tuple, result, keep: tuple, device: int, stream):
+        self._fn = getattr(load(), name)
+        self._name = name
+        self._args = args
+        self.result = result
+        self._keep = keep
+        self._device = device
+        self._stream = None if stream is None else _stream(stream)
+
+    @property
+    def workspace(self) -> Optional[torch.Tensor]:
+        """The workspace (its first word is the call's status, see read_status)."""
+        return self._keep[0]
+
+    def __call__(self):
+        st = self._stream
+        if st is None:
+            st = torch.cuda.current_stream(self._device).cuda_stream
+        if torch.cuda.current_device() == self._device:
+            rc = self._fn(*self._args, st)
+        else:   # kernels launch on the buffers' device, whichever is current
+            with torch.cuda.device(self._device):
+                rc = self._fn(*self._args, st)
+        if rc < 0:
+            raise VaError(self._name, rc)
+        return self.result
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pool_arg(kv_pool: torch.Tensor) -> None:
+    """A pool's rows may be wider than 576 or a view of wider ones."""
+    if not kv_pool.is_cuda:
+        raise ValueError("kv_pool must be a CUDA tensor")
+    if kv_pool.dtype != torch.bfloat16:
+        raise TypeError(f"kv_pool must be {torch.bfloat16}, got {kv_pool.dtype}")
+    if kv_pool.dim() != 2 or kv_pool.shape[1] < D_QK or kv_pool.stride(1) != 1:
+        raise ValueError(f"kv_pool must be a row-major [num_slots, >= {D_QK}] tensor")
+
+
+def _chunk_args(q, kv_pool, prefix_len, q_indptr, **lists):
+    """Checks shared by the chunk calls: (B, total_q, H)."""
+    _dev(q, "q", torch.bfloat16)
+    _pool_arg(kv_pool)
+    _dev(prefix_len, "prefix_len", torch.int32)
+    _dev(q_indptr, "q_indptr", torch.int32)
+    if q.dim() != 3 or q.shape[2] != D_QK:
+        raise ValueError(f"q must be [total_q, H, {D_QK}], got {tuple(q.shape)}")
+    B = prefix_len.numel()
+    if q_indptr.numel() != B + 1:
+        raise ValueError(f"q_indptr must hold B + 1 = {B + 1} offsets")
+    for name, (t, dt, n) in lists.items():
+        _dev(t, name, dt)
+        if n is not None and t.numel() != n(B):
+            raise ValueError(f"{name} must hold {n(B)} entries")
+    _same_device(q.device, kv_pool=kv_pool, prefix_len=prefix_len, q_indptr=q_indptr,
+                 **{k: v[0] for k, v in lists.items()})
+    return B, q.shape[0], q.shape[1]
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, device, func: str) -> torch.Tensor:
+    if need == 0:
+        raise VaError(func, -2)
+    if given is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _dev(given, "workspace", torch.uint8)
+    _same_device(device, workspace=given)
+    return given
+
+
+def _prepare_chunk(name, q, kv_pool, keys, dims, prefix_len, q_indptr, sm_scale, window, sinks,
+                   flags, workspace, out, lse, stream) -> BoundCall:
+    B, total_q, H = dims
+    init(q.device.index)
+    workspace = _workspace(workspace, load().va_chunk_workspace_bytes(B, total_q, H, flags),
+                           q.device, "va_chunk_workspace_bytes")
+    out, lse = _outputs(total_q, H, q.device, out, lse)
+    _same_device(q.device, out=out, lse=lse)
+    args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), *(_ptr(k) for k in keys),
+            _ptr(prefix_len), _ptr(q_indptr), B, total_q, H, float(sm_scale), int(window),
+            int(sinks), int(flags), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse))
+    return BoundCall(name, args, (out, lse),
+                     (workspace, q, kv_pool, keys, prefix_len, q_indptr, out, lse),
+                     q.device.index, stream)
+
+
+def prepare_chunk_paged(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
+                        kv_indptr: torch.Tensor, prefix_len: torch.Tensor,
+                        q_indptr: torch.Tensor, *, sm_scale: float, window: int = 0,
+                        sinks: int = 0, flags: int = PATH_AUTO,
+                        workspace: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        stream=None) -> BoundCall:
+    """chunk_attn_paged's checks and marshalling, done once."""
+    dims = _chunk_args(q, kv_pool, prefix_len, q_indptr, slot_idx=(slot_idx, torch.int32, None),
+                       kv_indptr=(kv_indptr, torch.int32, lambda B: B + 1))
+    return _prepare_chunk("va_chunk_attn_paged", q, kv_pool, (slot_idx, kv_indptr), dims,
+                          prefix_len, q_indptr, sm_scale, window, sinks, flags, workspace, out,
+                          lse, stream)
+
+
+def chunk_attn_paged(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
+                     kv_indptr: torch.Tensor, prefix_len: torch.Tensor, q_indptr: torch.Tensor,
+                     *, sm_scale: float, window: int = 0, sinks: int = 0, flags: int = PATH_AUTO,
+                     workspace: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention of each request's new tokens over its paged cache; returns
+    (out bf16 [total_q, H, 512], lse fp32 [total_q, H]).
+
+    q [total_q, H, 576] bf16: request b's new tokens are q[q_indptr[b]:q_indptr[b+1]]
+    (int32 [B+1]).  Its keys are the pool rows named by slot_idx from kv_indptr[b] on:
+    prefix_len[b] cached ones, then the new tokens' own.  With window > 0 a token sees
+    the last `window` keys up to its own and the first `sinks` keys.  Rows of out and lse
+    that no request owns are left as they were.  See va_chunk_attn_paged in verify_attn.h.
+    """
+    return prepare_chunk_paged(q, kv_pool, slot_idx, kv_indptr, prefix_len, q_indptr,
+                               sm_scale=sm_scale, window=window, sinks=sinks, flags=flags,
+                               workspace=workspace, out=out, lse=lse, stream=stream)()
+
+
+def prepare_chunk_contiguous(q: torch.Tensor, kv_pool: torch.Tensor, kv_start: torch.Tensor,
+                             prefix_len: torch.Tensor, q_indptr: torch.Tensor, *,
+                             sm_scale: float, window: int = 0, sinks: int = 0,
+                             flags: int = PATH_AUTO, workspace: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None, stream=None) -> BoundCall:
+    """chunk_attn_contiguous's checks and marshalling, done once."""
+    dims = _chunk_args(q, kv_pool, prefix_len, q_indptr,
+                       kv_start=(kv_start, torch.int64, lambda B: B))
+    return _prepare_chunk("va_chunk_attn_contiguous", q, kv_pool, (kv_start,), dims, prefix_len,
+                          q_indptr, sm_scale, window, sinks, flags, workspace, out, lse, stream)
+
+
+def chunk_attn_contiguous(q: torch.Tensor, kv_pool: torch.Tensor, kv_start: torch.Tensor,
+                          prefix_len: torch.Tensor, q_indptr: torch.Tensor, *, sm_scale: float,
+                          window: int = 0, sinks: int = 0, flags: int = PATH_AUTO,
+                          workspace: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None,
+                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """chunk_attn_paged over contiguous rows: key j of request b is pool row
+    kv_start[b] + j (int64 [B])."""
+    return prepare_chunk_contiguous(q, kv_pool, kv_start, prefix_len, q_indptr,
+                                    sm_scale=sm_scale, window=window, sinks=sinks, flags=flags,
+                                    workspace=workspace, out=out, lse=lse, stream=stream)()
+
+
+def prepare_kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
+                       kv_indptr: torch.Tensor, prefix_len: torch.Tensor, q_indptr: torch.Tensor,
+                       lse: torch.Tensor, weights_in: Optional[torch.Tensor] = None, *,
+                       sm_scale: float, window: int = 0, sinks: int = 0, flags: int = PATH_AUTO,
+                       workspace: Optional[torch.Tensor] = None,
+                       weights_out: Optional[torch.Tensor] = None, stream=None) -> BoundCall:
+    """kv_weights' checks and marshalling, done once."""
+    B, total_q, H = _chunk_args(q, kv_pool, prefix_len, q_indptr,
+                                slot_idx=(slot_idx, torch.int32, None),
+                                kv_indptr=(kv_indptr, torch.int32, lambda B: B + 1),
+                                lse=(lse, torch.float32, None))
+    if tuple(lse.shape) != (total_q, H):
+        raise ValueError(f"lse must be [{total_q}, {H}], got {tuple(lse.shape)}")
+    n = slot_idx.numel()
+    if weights_out is None:
+        # entries that no request's keys cover keep their totals (or zero)
+        weights_out = torch.zeros(n, dtype=torch.float32, device=q.device) \
+            if weights_in is None else weights_in.clone()
+    for t, name in ((weights_in, "weights_in"), (weights_out, "weights_out")):
+        if t is not None:
+            _dev(t, name, torch.float32)
+            if t.numel() != n:
+                raise ValueError(f"{name} must hold one entry per entry of slot_idx ({n})")
+    _same_device(q.device, weights_in=weights_in, weights_out=weights_out)
+    init(q.device.index)
+    workspace = _workspace(workspace,
+                           load().va_kv_weights_workspace_bytes(B, total_q, H, n, flags),
+                           q.device, "va_kv_weights_workspace_bytes")
+    args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), _ptr(slot_idx),
+            _ptr(kv_indptr), _ptr(prefix_len), _ptr(q_indptr), _ptr(lse), _ptr(weights_in), n, B,
+            total_q, H, float(sm_scale), int(window), int(sinks), int(flags), _ptr(workspace),
+            workspace.numel(), _ptr(weights_out))
+    return BoundCall("va_kv_weights_paged", args, weights_out,
+                     (workspace, q, kv_pool, slot_idx, kv_indptr, prefix_len, q_indptr, lse,
+                      weights_in, weights_out), q.device.index, stream)
+
+
+def kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
+               kv_indptr: torch.Tensor, prefix_len: torch.Tensor, q_indptr: torch.Tensor,
+               lse: torch.Tensor, weights_in: Optional[torch.Tensor] = None, *, sm_scale: float,
+               window: int = 0, sinks: int = 0, flags: int = PATH_AUTO,
+               workspace: Optional[torch.Tensor] = None,
+               weights_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention weight that each listed key received from the rows of a
+    chunk_attn_paged call (same arguments, and the lse it returned), added to
+    weights_in (fp32, one entry per entry of slot_idx; None: zeros).  Returns
+    weights_out, which may be given, weights_in itself included (in place).  See
+    va_kv_weights_paged in verify_attn.h."""
+    return prepare_kv_weights(q, kv_pool, slot_idx, kv_indptr, prefix_len, q_indptr, lse,
+                              weights_in, sm_scale=sm_scale, window=window, sinks=sinks,
+                              flags=flags, workspace=workspace, weights_out=weights_out,
+                              stream=stream)()
+
+
+def prepare_kv_evict(slot_idx: torch.Tensor, kv_indptr: torch.Tensor, prefix_len: torch.Tensor,
+                     weights: torch.Tensor, *, budget: int, sinks: int = 0, recent: int = 0,
+                     free_slots: Optional[torch.Tensor] = None,
+                     free_head: Optional[torch.Tensor] = None, outputs=None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> BoundCall:
+    """kv_evict's checks and marshalling, done once."""
+    _dev(slot_idx, "slot_idx", torch.int32)
+    _dev(kv_indptr, "kv_indptr", torch.int32)
+    _dev(prefix_len, "prefix_len", torch.int32)
+    _dev(weights, "weights", torch.float32)
+    B, n = prefix_len.numel(), slot_idx.numel()
+    if kv_indptr.numel() != B + 1:
+        raise ValueError(f"kv_indptr must hold B + 1 = {B + 1} offsets")
+    if weights.numel() != n:
+        raise ValueError(f"weights must hold one entry per entry of slot_idx ({n})")
+    if (free_slots is None) != (free_head is None):
+        raise ValueError("free_slots and free_head go together")
+    if outputs is None:
+        outputs = (slot_idx, prefix_len, weights, free_head)
+    slot_out, len_out, w_out, head_out = outputs
+    for t, name, dt, size in ((slot_out, "slot_idx_out", torch.int32, n),
+                              (len_out, "prefix_len_out", torch.int32, B),
+                              (w_out, "weights_out", torch.float32, n)):
+        _dev(t, name, dt)
+        if t.numel() != size:
+            raise ValueError(f"{name} must hold {size} entries")
+    if free_slots is not None:
+        _dev(free_slots, "free_slots", torch.int32)
+        for t, name in ((free_head, "free_head"), (head_out, "free_head_out")):
+            if t is None:
+                raise ValueError("free_head_out is needed with free_slots")
+            _dev(t, name, torch.int32)
+            if t.numel() != 1:
+                raise ValueError(f"{name} must hold one int32")
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    dev = slot_idx.device
+    _same_device(dev, kv_indptr=kv_indptr, prefix_len=prefix_len, weights=weights,
+                 free_slots=free_slots, free_head=free_head, slot_idx_out=slot_out,
+                 prefix_len_out=len_out, weights_out=w_out, status=status,
+                 free_head_out=head_out if free_slots is not None else None)
+    init(dev.index)
+    args = (_ptr(slot_idx), _ptr(kv_indptr), _ptr(prefix_len), _ptr(weights), n, B, int(budget),
+            int(sinks), int(recent), _ptr(free_slots),
+            0 if free_slots is None else free_slots.numel(),
+            None if free_slots is None else _ptr(free_head), _ptr(slot_out), _ptr(len_out),
+            _ptr(w_out), None if free_slots is None else _ptr(head_out), _ptr(status))
+    return BoundCall("va_kv_evict", args, (slot_out, len_out, w_out,
+                                           head_out if free_slots is not None else None),
+                     (None, slot_idx, kv_indptr, prefix_len, weights, free_slots, free_head,
+                      outputs, status), dev.index, stream)
+
+
+def kv_evict(slot_idx: torch.Tensor, kv_indptr: torch.Tensor, prefix_len: torch.Tensor,
+             weights: torch.Tensor, *, budget: int, sinks: int = 0, recent: int = 0,
+             free_slots: Optional[torch.Tensor] = None,
+             free_head: Optional[torch.Tensor] = None, outputs=None,
+             status: Optional[torch.Tensor] = None, stream=None):
+    """Cuts every request's list (slot_idx from kv_indptr[b] on, prefix_len[b]
+    entries) to `budget` keys: the first `sinks`, the last `recent` and, of the
+    others, those with the largest weights (fp32, one per entry of slot_idx).
+
+    Kept entries move to the front of the list in order, in place unless
+    `outputs` = (slot_idx_out, prefix_len_out, weights_out, free_head_out) names
+    other buffers; with free_slots / free_head (tree_build's free list) the
+    evicted slots are put back in front of the head.  Returns the four outputs
+    (free_head_out None without a free list).  See va_kv_evict in
+    verify_attn.h."""
+    return prepare_kv_evict(slot_idx, kv_indptr, prefix_len, weights, budget=budget, sinks=sinks,
+                            recent=recent, free_slots=free_slots, free_head=free_head,
+                            outputs=outputs, status=status, stream=stream)()
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -261,6 +261,14 @@ __device__ __forceinline__ bool va_trace_first_of_role() {
 #define VA_PH_STORE(role) ((void)0)
 #endif
 
+// What va_init recorded of the current device, for the entry points outside
+// va_host.cu: VA_OK, VA_ERR_UNSUPPORTED before va_init, or VA_ERR_CUDA.
+struct DeviceInfo {
+  int num_sms;
+  int pairs, quads;   // resident clusters of the tensor-core kernel (2, 4 CTAs)
+};
+int device_info(DeviceInfo* out);
+
 // Launchers (defined in the kernel translation units).
 cudaError_t launch_tree_bits(const Params& p, uint64_t* bits_out, cudaStream_t st);
 cudaError_t launch_partial_fma(const Params& p, int num_sms, cudaStream_t st);

@@ -202,6 +202,16 @@ cudaError_t resolve_noalloc(int dev) {
 
 }  // namespace
 
+int va::device_info(DeviceInfo* out) {
+  DeviceState ds;
+  const int rc = current_state(&ds);
+  if (rc != VA_OK) return rc;
+  out->num_sms = ds.num_sms;
+  out->pairs = ds.tc_pairs;
+  out->quads = ds.tc_quads;
+  return VA_OK;
+}
+
 VA_API int va_version(void) { return 100; }
 
 VA_API int va_init(int device) {

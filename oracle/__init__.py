@@ -53,6 +53,11 @@ Functions and the passages they follow (page titles and sections):
                    its prefix, and after acceptance the accepted path's rows
                    are moved to directly after the prefix, which grows by the
                    accepted count.
+  chunk_attn, chunk_weights, evict
+                -- the definitions in include/verify_attn.h (causal attention
+                   of ragged chunks with a window and sinks, the attention
+                   weight each key receives, eviction by that weight), in plain
+                   numpy; no page gives them.
 """
 from __future__ import annotations
 
@@ -476,3 +481,88 @@ def compact_accepted(pool_bits, kv_start, prefix_len, capacity, accept_len, acce
             pool[ks[b] + P + k, :cols] = r
         new_pl[b] = P + n
     return pool, new_pl, bad
+
+
+def _widen(bits_u16) -> np.ndarray:
+    """bf16 bit patterns -> float64, exactly."""
+    b = np.asarray(bits_u16, dtype=np.uint16)
+    return (b.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def chunk_sees(pos: int, window: int, sinks: int) -> np.ndarray:
+    """bool [pos + 1]: which keys 0 .. pos the token at position `pos` sees."""
+    j = np.arange(pos + 1)
+    if window <= 0:
+        return np.ones(pos + 1, dtype=bool)
+    return (j > pos - window) | (j < sinks)
+
+
+def chunk_attn(q_bits, kv_bits, key_rows, prefix_len, q_indptr, sm_scale: float, window: int = 0,
+               sinks: int = 0):
+    """Attention of ragged chunks.  key_rows[b]: the pool row of each of request
+    b's prefix_len[b] + n_b keys, -1 for a key without one.  Returns (out
+    [total_q, H, 512], lse [total_q, H], mass [total_q, H, 512], spread), where
+    mass = sum_j p_j |v_j| and spread = max |sm_scale| sum |q_d k_d| over the
+    rows and keys -- what error bounds need.  Rows that no request owns: NaN."""
+    q = _widen(q_bits)
+    total, H, _ = q.shape
+    out = np.full((total, H, D_V), np.nan)
+    lse = np.full((total, H), np.nan)
+    mass = np.full((total, H, D_V), np.nan)
+    spread = 0.0
+    for b in range(len(prefix_len)):
+        rows = np.asarray(key_rows[b], dtype=np.int64)
+        for i, t in enumerate(range(int(q_indptr[b]), int(q_indptr[b + 1]))):
+            pos = int(prefix_len[b]) + i
+            r = rows[:pos + 1]
+            r = r[chunk_sees(pos, window, sinks) & (r >= 0)]
+            if r.size == 0:
+                out[t], lse[t], mass[t] = 0.0, -np.inf, 0.0
+                continue
+            k = _widen(kv_bits[r][:, :D_QK])
+            with np.errstate(invalid="ignore", over="ignore"):
+                s = sm_scale * (q[t] @ k.T)
+                m = s.max(axis=1, keepdims=True)
+                e = np.exp(s - m)
+                l = e.sum(axis=1, keepdims=True)
+                out[t] = (e / l) @ k[:, :D_V]
+                lse[t] = (m + np.log(l))[:, 0]
+                mass[t] = (e / l) @ np.abs(k[:, :D_V])
+                spread = max(spread, float(np.abs(sm_scale) * (np.abs(q[t]) @ np.abs(k).T).max()))
+    return out, lse, mass, spread
+
+
+def chunk_weights(q_bits, kv_bits, key_rows, prefix_len, q_indptr, lse, sm_scale: float,
+                  window: int = 0, sinks: int = 0):
+    """Per request, the weight each of its keys receives from its rows: list of
+    arrays [prefix_len[b] + n_b]; keys without a row receive 0."""
+    q = _widen(q_bits)
+    res = []
+    for b in range(len(prefix_len)):
+        rows = np.asarray(key_rows[b], dtype=np.int64)
+        n = int(q_indptr[b + 1]) - int(q_indptr[b])
+        w = np.zeros(int(prefix_len[b]) + n)
+        for i, t in enumerate(range(int(q_indptr[b]), int(q_indptr[b + 1]))):
+            pos = int(prefix_len[b]) + i
+            j = np.flatnonzero(chunk_sees(pos, window, sinks) & (rows[:pos + 1] >= 0))
+            k = _widen(kv_bits[rows[j]][:, :D_QK])
+            for h in range(q.shape[1]):
+                if lse[t, h] != -np.inf:
+                    w[j] += np.exp(sm_scale * (k @ q[t, h]) - float(lse[t, h]))
+        res.append(w)
+    return res
+
+
+def evict(slots, weights, budget: int, sinks: int, recent: int):
+    """One request's list cut to `budget` entries: (kept indices in order,
+    evicted indices in order)."""
+    L = len(slots)
+    if L <= budget:
+        return np.arange(L), np.arange(0)
+    w = np.array([-np.inf if np.isnan(x) else float(x) for x in weights])
+    middle = sorted(range(sinks, L - recent), key=lambda j: (-w[j], j))
+    stay = set(range(sinks)) | set(range(L - recent, L)) | \
+        set(middle[:budget - sinks - recent])
+    kept = [j for j in range(L) if j in stay]
+    return np.array(kept, dtype=np.int64), \
+        np.array([j for j in range(L) if j not in stay], dtype=np.int64)
