@@ -8,6 +8,12 @@
 // The output is the latent attention of the verify calls (softmax over 576
 // columns, value = the first 512) in one pass over the visible keys with a
 // running maximum and sum.
+//
+// Two paths: the tensor-core kernel of the verify calls in its chunk mode
+// (va_tc.cu), followed by chunk_finish_kernel, which merges the splits; and one
+// warp per row on CUDA cores (VA_PATH_FMA), an independent implementation that
+// the finish kernel also uses for the rare rows that the products may have
+// spoilt (see kFlagHiddenNonfinite).
 #include <string.h>
 
 #include "va_chunk.cuh"
@@ -44,6 +50,179 @@ __global__ void __launch_bounds__(kRowThreads) chunk_fma_kernel(const ChunkParam
   if (lane == 0 && bits) atomicOr(p.status, bits);
 }
 
+// Merge of the splits (and the call's status word).  Split s of a row left its
+// normalised partial o_s and lse_s; with L = ln sum_s exp(lse_s) the row is
+// sum_s exp(lse_s - L) o_s, in a fixed order.  The batch's rows are dealt to the
+// CTAs in turn; a CTA looks at 256 units at a time, a thread each, for units in
+// more than one split (or flagged), and then takes its rows of those.  A thread
+// holds four columns of every other split.  Bound by the partials' bytes (2 KB
+// per row and split, from L2) and, with few rows, by three dependent loads.
+constexpr int kFinishThreads = 256;
+constexpr int kMaxNs = 512;   // splits of a unit: at most the launch's target + 1
+
+__global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const ChunkTcParams p) {
+  __shared__ float w[kMaxNs];
+  __shared__ float4 half[kDv / 4];
+  __shared__ int list[kFinishThreads];
+  __shared__ int s_count;
+  __shared__ uint32_t s_bits;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int G = gridDim.x;
+  griddep_wait();                // the split kernel's results are complete
+  griddep_launch_dependents();   // the next kernel may start its set-up
+  const int total_units = p.totals[0];
+  const int U = p.sched.unit_rows;
+  for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    const int u = u0 + tid;
+    if (u < total_units) {
+      const ChunkUnit x = p.units[u];
+      uint32_t f = 0u;
+      for (int s = 0; s < x.ns; ++s)
+        for (int c = 0; c < p.ctas; ++c)
+          f |= p.cta_flags[size_t(x.item + s * x.pstride) * p.ctas + c];
+      const bool redo = f & kFlagHiddenNonfinite;
+      // (the order of the list does not matter: a row is one CTA's alone)
+      if (x.ns > 1 || redo) list[atomicAdd(&s_count, 1)] = redo ? ~u : u;
+    }
+    __syncthreads();
+    const int count = s_count;
+    for (int k = 0; k < count; ++k) {
+      const bool redo = list[k] < 0;
+      const int v = redo ? ~list[k] : list[k];
+      const ChunkUnit x = p.units[v];
+      const int turn = int((int64_t(v) * U) % G);
+      for (int r = (blockIdx.x - turn + G) % G; r < x.rows; r += G) {
+        if (redo) {
+          if (tid < 32) {
+            const ChunkReq rq = chunk_req(p, x.b);
+            bool bad = false;
+            chunk_row(p, rq, (x.i0 + r) / p.H, (x.i0 + r) % p.H, lane, &bad);
+          }
+          continue;
+        }
+        const size_t slot = size_t(x.pslot), step = size_t(x.pstride);
+        const int ns = x.ns < kMaxNs ? x.ns : kMaxNs;
+        __syncthreads();   // w and half of the row before are read
+        if (tid < 32) {
+          float m = -INFINITY;
+          for (int s = lane; s < ns; s += 32) {
+            const float ls = p.part_lse[(slot + s * step) * U + r];
+            w[s] = ls;
+            m = fmaxf(m, ls);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          float z = 0.f;
+          for (int s = lane; s < ns; s += 32)
+            if (w[s] != -INFINITY) z += expf(w[s] - m);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+          const float L = z == 0.f ? -INFINITY : m + logf(z);
+          for (int s = lane; s < ns; s += 32) w[s] = w[s] == -INFINITY ? 0.f : expf(w[s] - L);
+          if (lane == 0) p.lse[x.row0 + r] = L;
+        }
+        __syncthreads();
+        const int col = tid & 127, group = tid >> 7;
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot * U + r) * kDv) + col;
+        const size_t sstep = step * U * (kDv / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = group; s < ns; s += 2) {
+          const float4 v4 = src[s * sstep];
+          const float ws = w[s];
+          acc.x = fmaf(ws, v4.x, acc.x);
+          acc.y = fmaf(ws, v4.y, acc.y);
+          acc.z = fmaf(ws, v4.z, acc.z);
+          acc.w = fmaf(ws, v4.w, acc.w);
+        }
+        if (group) half[col] = acc;
+        __syncthreads();
+        if (!group) {
+          const float4 h = half[col];
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x + h.x, acc.y + h.y);
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z + h.z, acc.w + h.w);
+          uint2 o;
+          o.x = *reinterpret_cast<const uint32_t*>(&lo);
+          o.y = *reinterpret_cast<const uint32_t*>(&hi);
+          reinterpret_cast<uint2*>(p.out + size_t(x.row0 + r) * kDv)[col] = o;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // the status word: every CTA's bits, and requests whose bounds were clamped
+  if (blockIdx.x == 0) {
+    if (tid == 0) s_bits = 0u;
+    __syncthreads();
+    uint32_t bits = 0u;
+    const int n = p.totals[1] * p.ctas;
+    for (int i = tid; i < n; i += kFinishThreads) bits |= p.cta_flags[i] & ~kFlagHiddenNonfinite;
+    for (int b = tid; b < p.B; b += kFinishThreads)
+      if (chunk_req(p, b).bad) bits |= VA_STATUS_BAD_INDPTR;
+    if (bits) atomicOr(&s_bits, bits);
+    __syncthreads();
+    if (tid == 0) *p.status = s_bits;
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+// Clusters of the tensor-core kernel that a GB300's 152 SMs hold at most; the
+// workspace is sized for them, so that sizing it takes no device call.
+constexpr int kMaxPairs = 76, kMaxQuads = 38;
+// With many units, splits are cut so that about this many waves of clusters run.
+constexpr int kWaves = 3;
+
+struct ChunkPlan {
+  bool pair;
+  int unit_rows, ctas, max_clusters;
+  int units_bound;   // units the batch can have
+  bool one_wave;
+  size_t off_units, off_flags, off_lse, off_o, total;
+};
+
+// Two-SM products when the average request has more than 128 rows.
+ChunkPlan chunk_plan(int B, int total_q, int H, int flags) {
+  ChunkPlan c;
+  const int64_t rows = int64_t(total_q) * H;
+  const int busy = B < total_q ? B : total_q;   // requests with tokens, at most
+  c.pair = flags != VA_PATH_TC_1SM && rows > 128 * int64_t(busy);
+  c.unit_rows = c.pair ? 256 : 128;
+  c.ctas = c.pair ? 4 : 2;
+  c.max_clusters = c.pair ? kMaxQuads : kMaxPairs;
+  c.units_bound = int((rows + c.unit_rows - 1) / c.unit_rows) + busy;
+  c.one_wave = 2 * c.units_bound <= c.max_clusters;
+  // items: one wave's clusters, or target + one per unit; partial slots: items
+  // of requests in two or more splits, fewer than twice the target
+  const size_t target = size_t(kWaves) * c.max_clusters;
+  const size_t items = c.one_wave ? size_t(c.max_clusters) : target + c.units_bound;
+  const size_t slots = c.one_wave ? size_t(c.max_clusters) : 2 * target;
+  c.off_units = kHeaderBytes;
+  c.off_flags = c.off_units + align256(size_t(c.units_bound) * sizeof(ChunkUnit));
+  c.off_lse = c.off_flags + align256(items * c.ctas * sizeof(uint32_t));
+  c.off_o = c.off_lse + align256(slots * c.unit_rows * sizeof(float));
+  c.total = c.off_o + slots * c.unit_rows * kDv * sizeof(float);
+  return c;
+}
+
+cudaError_t launch_finish(const ChunkTcParams& p, int num_sms, cudaStream_t st) {
+  const int64_t rows = int64_t(p.total_q) * p.H;
+  const int64_t wave = int64_t(num_sms) * 8;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(unsigned(rows < wave ? rows : wave), 1, 1);
+  cfg.blockDim = dim3(kFinishThreads, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_finish_kernel, p);
+}
+
 }  // namespace
 
 int chunk_check(const ChunkParams& p, bool paged, float sm_scale, int flags, const void* ws) {
@@ -76,13 +255,34 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   p.num_entries = 0x7fffffff;
   p.scale_log2 = sm_scale * kLog2e;
   p.status = static_cast<uint32_t*>(ws);
-  if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return VA_ERR_LAUNCH;
-  if (p.total_q == 0) return VA_OK;
   const int64_t rows = int64_t(p.total_q) * p.H;
-  const int64_t want = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  const int64_t wave = int64_t(di.num_sms) * 8;
-  chunk_fma_kernel<<<unsigned(want < wave ? want : wave), kRowThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
+  if (flags == VA_PATH_FMA || rows == 0) {
+    if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return VA_ERR_LAUNCH;
+    if (rows == 0) return VA_OK;
+    const int64_t want = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    const int64_t wave = int64_t(di.num_sms) * 8;
+    chunk_fma_kernel<<<unsigned(want < wave ? want : wave), kRowThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
+  }
+  const ChunkPlan c = chunk_plan(p.B, p.total_q, p.H, flags);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  ChunkTcParams t;
+  memset(&t, 0, sizeof t);
+  static_cast<ChunkParams&>(t) = p;
+  const int resident = c.pair ? di.quads : di.pairs;
+  t.sched.unit_rows = c.unit_rows;
+  t.sched.clusters = resident < c.max_clusters ? resident : c.max_clusters;
+  t.sched.one_wave = c.one_wave ? 1 : 0;
+  t.sched.target = kWaves * t.sched.clusters;
+  t.ctas = c.ctas;
+  t.totals = reinterpret_cast<int32_t*>(w) + 4;
+  t.units = reinterpret_cast<ChunkUnit*>(w + c.off_units);
+  t.cta_flags = reinterpret_cast<uint32_t*>(w + c.off_flags);
+  t.part_lse = reinterpret_cast<float*>(w + c.off_lse);
+  t.part_o = reinterpret_cast<float*>(w + c.off_o);
+  const int items = c.one_wave ? t.sched.clusters : t.sched.target + c.units_bound;
+  if (launch_chunk_tc(t, items, c.pair, st) != cudaSuccess) return VA_ERR_LAUNCH;
+  return launch_finish(t, di.num_sms, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -92,7 +292,8 @@ VA_API size_t va_chunk_workspace_bytes(int B, int total_q, int H, int flags) {
   if (B < 1 || B > 65535 || total_q < 0 || H < 1 || flags < VA_PATH_AUTO ||
       flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX)
     return 0;
-  return va::kHeaderBytes;
+  if (total_q == 0 || flags == VA_PATH_FMA) return va::kHeaderBytes;
+  return va::chunk_plan(B, total_q, H, flags).total;
 }
 
 VA_API int va_chunk_attn_paged(const void* q, const void* kv_pool, int64_t num_slots,

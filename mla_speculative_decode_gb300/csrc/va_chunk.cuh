@@ -9,6 +9,10 @@
 
 namespace va {
 
+// With many units a split takes at least this many tiles: a cluster's set-up,
+// fill and write-out cost about as much as ten tiles.
+constexpr int kMinSplitTiles = 8;
+
 // Arguments of a chunk call (va_chunk_attn_*, va_kv_weights_paged), by value.
 // Request b's new tokens are query tokens q_indptr[b] .. q_indptr[b+1] - 1; its
 // keys are P = prefix_len[b] prefix rows followed by the new tokens' own rows.
@@ -163,6 +167,199 @@ __device__ inline void chunk_row(const ChunkParams& p, const ChunkReq& r, int i,
   }
   if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
+
+// ---------------------------------------------------------------- schedule
+//
+// Work is cut where the tokens are: a unit is `unit_rows` consecutive rows
+// (token, head) of one request, and a unit's keys are tiles of 64 list
+// positions: the tiles that hold sinks, then those from the first key that the
+// unit's first token sees to the last token's own key.  Lengths live on the
+// device, so a launch has a fixed grid of clusters ("items") and each cluster
+// finds its own piece: (request, unit, split of the unit's tiles).
+
+// The tiles of one unit, or of one split of them.
+struct ChunkTiles {
+  int t0;       // first tile, counted through the unit's tiles
+  int ntiles;
+  int nst;      // tiles that hold sinks, before the window's
+  int wt;       // the window's first tile, as a list position / 64
+  int k1;       // keys past the unit's last token start here
+  int first;    // first key past the sinks that the unit's first token sees
+  int sinks;
+  __device__ int tile_key(int t) const {
+    const int g = t0 + t;
+    return (g < nst ? g : g - nst + wt) * 64;
+  }
+  // whether some row of the unit sees key j
+  __device__ bool sees(int j) const { return j < k1 && (j >= first || j < sinks); }
+  // whether some row sees every key of the tile that starts at key tk0
+  __device__ bool whole(int tk0) const {
+    return tk0 + 64 <= k1 && (tk0 >= first || tk0 + 64 <= sinks);
+  }
+};
+
+// All tiles of rows [row0, row0 + rows) of a request (rows >= 1).
+__device__ inline ChunkTiles chunk_tiles(const ChunkParams& p, const ChunkReq& r, int row0,
+                                         int rows) {
+  ChunkTiles t;
+  const int i0 = row0 / p.H, i1 = (row0 + rows - 1) / p.H;
+  t.k1 = r.P + i1 + 1;
+  t.first = window_first(p.window, r.P + i0);
+  t.sinks = p.sinks;
+  const int s = p.sinks < t.first ? p.sinks : t.first;   // sinks before the window
+  t.nst = (s + 63) / 64;
+  t.wt = t.first / 64 > t.nst ? t.first / 64 : t.nst;
+  t.t0 = 0;
+  t.ntiles = t.nst + (t.k1 + 63) / 64 - t.wt;
+  return t;
+}
+
+struct ChunkSched {
+  int unit_rows;   // 128, or 256 with two-SM products
+  int clusters;    // clusters resident at once
+  int one_wave;    // few units: at most `clusters` items, else about `target`
+  int target;
+};
+
+struct ChunkItem {
+  int b, unit, split;
+  int units;        // of the request
+  int ns;           // splits of each of the request's units
+  int unit0;        // units of the requests before it
+  int item0;        // its first item
+  int pslot0;       // its first partial slot (requests with ns > 1 have units * ns)
+  int total_units, total_items;   // of the batch (valid for item 0)
+  bool live;
+};
+
+// A request's units and the tiles of its longest (last) unit.
+__device__ inline void chunk_work(const ChunkParams& p, const ChunkSched& s, int b, int* units,
+                                  int* tiles) {
+  const ChunkReq r = chunk_req(p, b);
+  const int rows = r.n * p.H;
+  *units = (rows + s.unit_rows - 1) / s.unit_rows;
+  *tiles = 0;
+  if (rows > 0) {
+    const int row0 = (*units - 1) * s.unit_rows;
+    *tiles = chunk_tiles(p, r, row0, rows - row0).ntiles;
+  }
+}
+
+// Item `item` of the batch; a whole warp takes part, lane l looking at requests
+// l, l + 32, ...  With W = the sum of units x tiles, a split takes `chunk`
+// tiles: about W / target of them, or, when one wave of clusters is to hold
+// everything, the smallest such count (grown by eighths from W / clusters) whose
+// items fit.  A request with t tiles gets ns = ceil(t / chunk) splits; items run
+// split by split, and within a split from the last unit (the most keys) to the
+// first, so that units that read the same keys run together.
+__device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s, int item,
+                                       int lane) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  int u0 = 0, t0 = 0;   // requests 0 .. 31 stay in registers
+  int64_t work = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    int u, t;
+    chunk_work(p, s, b, &u, &t);
+    if (b < 32) { u0 = u; t0 = t; }
+    work += int64_t(u) * t;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(kAll, work, o);
+  int chunk;
+  if (s.one_wave) {
+    chunk = int((work + s.clusters - 1) / s.clusters);
+    if (chunk < 1) chunk = 1;
+    // (one split per unit always fits: a launch in one wave has at most half
+    // as many units as clusters)
+    for (;;) {
+      int n = 0;
+      for (int b = lane; b < p.B; b += 32) {
+        int u = u0, t = t0;
+        if (b >= 32) chunk_work(p, s, b, &u, &t);
+        n += u * ((t + chunk - 1) / chunk);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+      if (n <= s.clusters || chunk > (1 << 26)) break;
+      chunk += chunk / 8 + 1;
+    }
+  } else {
+    const int64_t c = (work + s.target - 1) / s.target;
+    chunk = c < kMinSplitTiles ? kMinSplitTiles : int(c);
+  }
+  ChunkItem it;
+  it.live = false;
+  it.b = it.unit = it.split = it.units = it.ns = it.unit0 = it.item0 = it.pslot0 = 0;
+  int items = 0, slots = 0, units = 0;   // of the requests before this round
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int u = u0, t = t0;
+    if (b0 > 0) {
+      u = t = 0;
+      if (b < p.B) chunk_work(p, s, b, &u, &t);
+    }
+    const int ns = (t + chunk - 1) / chunk;
+    const int n_items = u * ns, n_slots = ns > 1 ? n_items : 0;
+    int ci = n_items, cs = n_slots, cu = u;   // inclusive sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(kAll, ci, o), c = __shfl_up_sync(kAll, cs, o),
+                d = __shfl_up_sync(kAll, cu, o);
+      if (lane >= o) { ci += a; cs += c; cu += d; }
+    }
+    const uint32_t mine =
+        __ballot_sync(kAll, item >= items + ci - n_items && item < items + ci);
+    if (mine) {
+      const int src = __ffs(int(mine)) - 1;
+      it.live = true;
+      it.b = b0 + src;
+      it.units = __shfl_sync(kAll, u, src);
+      it.ns = __shfl_sync(kAll, ns, src);
+      it.unit0 = units + __shfl_sync(kAll, cu, src) - it.units;
+      it.item0 = items + __shfl_sync(kAll, ci, src) - it.units * it.ns;
+      it.pslot0 = slots + __shfl_sync(kAll, cs, src) - (it.ns > 1 ? it.units * it.ns : 0);
+      const int k = item - it.item0;
+      it.split = k / it.units;
+      it.unit = it.units - 1 - k % it.units;
+      if (item != 0) break;
+    }
+    items += __shfl_sync(kAll, ci, 31);
+    slots += __shfl_sync(kAll, cs, 31);
+    units += __shfl_sync(kAll, cu, 31);
+  }
+  it.total_units = units;
+  it.total_items = items;
+  return it;
+}
+
+// One unit's entry in the workspace, written by its first split's cluster for
+// the kernel that merges the splits.
+struct alignas(16) ChunkUnit {
+  int row0, rows;        // rows of out / lse
+  int ns;                // splits that hold keys (1: already in out and lse)
+  int pslot, pstride;    // partial slot of split 0, and from split to split
+  int item;              // item of split 0 (then pstride apart)
+  int b, i0;             // request, row within it
+};
+
+// Arguments of the tensor-core launch and of the merge.
+struct ChunkTcParams : ChunkParams {
+  ChunkSched sched;
+  int ctas;              // CTAs per item
+  int32_t* totals;       // [2]: units, items (written by item 0)
+  ChunkUnit* units;
+  uint32_t* cta_flags;   // [items][ctas] status bits of each CTA
+  float* part_lse;       // [slots][unit_rows]
+  float* part_o;         // [slots][unit_rows][512], normalised by the split's row sum
+};
+
+// Bit of a CTA's status word: a hidden key's score was not finite, so products
+// with its value may have spoilt rows that do not see it; the merge kernel
+// computes the unit's rows again on CUDA cores.
+constexpr uint32_t kFlagHiddenNonfinite = 0x80000000u;
+
+// Tensor-core kernel (va_tc.cu).
+cudaError_t launch_chunk_tc(const ChunkTcParams& p, int grid_items, bool pair, cudaStream_t st);
 
 // Checks shared by the chunk calls (va_chunk.cu).
 int chunk_check(const ChunkParams& p, bool paged, float sm_scale, int flags, const void* ws);

@@ -46,6 +46,12 @@
 //     rare tiles whose reference max moved, then normalise and write the
 //     split's partial, each warpgroup for 256 of the 512 columns.
 //
+// The same kernel serves the chunk calls (the template's `Mode`): there a unit
+// is 128 or 256 consecutive rows of a request's causal run of new tokens, its
+// keys are the tiles that some row of the unit sees (two runs of them under a
+// window with sinks), and a unit whose tiles are not split writes its rows
+// straight to out and lse.
+//
 // The design follows the pages' split-K / online-softmax / partial-reduce
 // structure (The Milestone Commit, "The Thinking Process Revealed"; The Commit
 // That Locked In 6x Decode, "Input Knowledge Required"), moved onto tcgen05,
@@ -57,6 +63,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "va_chunk.cuh"
 #include "va_common.cuh"
 #include "va_sm100.cuh"
 
@@ -264,23 +271,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b, float& sum) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What a call's mode decides: how a cluster finds its rows and keys.
+// A verify call's split is one run of keys [k0, k1).
+struct VerifyRange : SplitRange {
+  __device__ int tile_key(int t) const { return k0 + t * kTile; }
+  __device__ bool sees(int j) const { return j < k1; }
+  __device__ bool whole(int tk0) const { return tk0 + kTile <= k1; }
+};
+struct VerifyMode {
+  static constexpr bool kChunk = false;
+  using P = Params;
+  using Req = ReqInfo;
+  using Range = VerifyRange;
+};
+struct ChunkMode {
+  static constexpr bool kChunk = true;
+  using P = ChunkTcParams;
+  using Req = ChunkReq;
+  using Range = ChunkTiles;
+};
+
+// The n lowest bits of a 64-bit mask (any n).
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 // Raw pool row of key j of the split as stored in the slot list (contiguous
 // pools: the row itself; segmented lists: the draft list past the prefix), or
-// -1 when j is past the split or the list.  The value is only range-checked
+// -1 when no row of the unit sees key j or the list ends before it.  The value is only range-checked
 // when it is used, a tile later, so the load's latency overlaps the current
 // tile's copies instead of stalling the warp.
-__device__ __forceinline__ int fetch_row(const Params& p, const ReqInfo& ri, int j, int k1) {
-  if (j >= k1 || j >= ri.nlist) return -1;
+template <class Mode>
+__device__ __forceinline__ int fetch_row(const typename Mode::P& p, const typename Mode::Req& ri,
+                                         const typename Mode::Range& sr, int j) {
+  if (!sr.sees(j) || j >= ri.nlist) return -1;
   if (p.kv_start) {
     const int64_t r = ri.base + j;
     return (r >= 0 && r < p.num_slots && r <= 0x7fffffff) ? int(r) : -1;
   }
-  if (p.draft_slots && j >= ri.P) return __ldg(p.draft_slots + ri.dbase + j);
+  if constexpr (!Mode::kChunk)
+    if (p.draft_slots && j >= ri.P) return __ldg(p.draft_slots + ri.dbase + j);
   return __ldg(p.slot_idx + ri.base + j);
 }
 // A fetched row, or -1 (no row: the copy zero-fills) when out of the pool.
-__device__ __forceinline__ int checked_row(const Params& p, int raw) {
-  return (raw >= 0 && int64_t(raw) < p.num_slots) ? raw : -1;
+__device__ __forceinline__ int checked_row(int64_t num_slots, int raw) {
+  return (raw >= 0 && int64_t(raw) < num_slots) ? raw : -1;
 }
 
 // Producer warps (224 threads): bring the CTA's share of each 64-key tile
@@ -320,8 +355,9 @@ __device__ __noinline__ bool gate_wait(const int32_t* flag, long long limit_cycl
 }
 #endif
 
-template <bool kPair, int kBlocks, int kRing, bool kMask>
-__device__ __forceinline__ bool produce(const Params& p, const ReqInfo& ri, const SplitRange& sr,
+template <bool kPair, class Mode, int kBlocks, int kRing, bool kMask>
+__device__ __forceinline__ bool produce(const typename Mode::P& p, const typename Mode::Req& ri,
+                                        const typename Mode::Range& sr,
                                         int ntiles, int ptid, uint32_t ring, uint32_t full0,
                                         uint32_t empty0, int* srow, uint32_t* valid32,
                                         uint32_t vready0, volatile int* abort_flag,
@@ -384,11 +420,10 @@ __device__ __forceinline__ bool produce(const Params& p, const ReqInfo& ri, cons
     if (ptid == 0) VA_TRACE_EVENT(kMask ? 0 : 3, 0, t);
     VA_PH(0);
     if (ptid < 64) {
-      const int rw = checked_row(p, raw);
+      const int rw = checked_row(p.num_slots, raw);
       srow[(t & 1) * 64 + ptid] = rw;
       if (kMask) {
-        const int j = sr.k0 + t * kTile + ptid;
-        bad_slot |= j < sr.k1 && rw < 0;
+        bad_slot |= sr.sees(sr.tile_key(t) + ptid) && rw < 0;
         const uint32_t bal = __ballot_sync(0xffffffffu, rw >= 0);
         if (lane == 0) valid32[(t % C::kValidRing) * 2 + (ptid >> 5)] = bal;
       }
@@ -401,12 +436,13 @@ __device__ __forceinline__ bool produce(const Params& p, const ReqInfo& ri, cons
     const int fi = t % C::kFullRing;
     const uint32_t fb = full0 + 8u * uint32_t(fi);
     // contiguous rows, whole tile inside the split and the pool: box loads
-    const int tk0 = sr.k0 + t * kTile;
+    const int tk0 = sr.tile_key(t);
     // a tile with draft keys, when the call appends their rows first: after
     // the append (in the kernel before this one) has completed
-    if (p.draft_kv && tk0 + kTile > ri.P) griddep_wait();
+    if constexpr (!Mode::kChunk)
+      if (p.draft_kv && tk0 + kTile > ri.P) griddep_wait();
     const int64_t row0 = p.kv_start ? ri.base + tk0 : -1;
-    bool boxes = p.kv_start != nullptr && tk0 + kTile <= sr.k1 && tk0 + kTile <= ri.nlist &&
+    bool boxes = p.kv_start != nullptr && sr.whole(tk0) && tk0 + kTile <= ri.nlist &&
                  row0 >= 0 && row0 + kTile <= p.num_slots && row0 + kTile <= 0x7fffffff;
     if (kPair && !kMask && !box3d) boxes = false;   // the PV pair share needs the 3-D map
     if (kMask && ptid == 0) mbar_arrive(vready0 + 8u * uint32_t(t % C::kValidRing));
@@ -432,7 +468,7 @@ __device__ __forceinline__ bool produce(const Params& p, const ReqInfo& ri, cons
         mbar_arrive(fb);
       }
     }
-    if (ptid < 64 && t + 1 < ntiles) raw = fetch_row(p, ri, sr.k0 + (t + 1) * kTile + ptid, sr.k1);
+    if (ptid < 64 && t + 1 < ntiles) raw = fetch_row<Mode>(p, ri, sr, sr.tile_key(t + 1) + ptid);
     if (!boxes) {
       // this lane's chunks lane + 32j lie in the share's blocks lane/8 + 4j,
       // at chunk position lane%8 inside their 128-byte row
@@ -518,9 +554,10 @@ __device__ __forceinline__ bool load_q(int half, int q4, int lane, uint32_t tmem
   return ok;
 }
 
-template <bool kPair>
+template <bool kPair, class Mode>
 __global__ void __launch_bounds__(kThreads, 1)
-    partial_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tmap_k,
+    partial_tc_kernel(const __grid_constant__ typename Mode::P p,
+                      const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ CUtensorMap tmap_2d,
                       const __grid_constant__ CUtensorMap tmap_q, int box3d) {
@@ -541,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool issuer_cta = hh == 0;
   const uint32_t other = kPair ? (rank ^ 2u) : (rank ^ 1u);
   const uint32_t mate = rank ^ 1u;
-  const int split = blockIdx.x / C::kCtas, rb = blockIdx.y, b = blockIdx.z;
+  constexpr bool kChunk = Mode::kChunk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 #ifdef VA_TRACE
   const int trace_role = rank < 2u ? 6 + int(rank) : 14 + int(rank);   // per-CTA marks
@@ -565,31 +602,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   // call appends draft rows first, the append kernel (launched after the
   // stream's earlier work) precedes it instead, and the producers wait
   // (griddepcontrol.wait) only before a tile holding draft keys.
-  if (!p.draft_kv) griddep_wait();
+  if constexpr (kChunk) {
+    griddep_wait();
+  } else {
+    if (!p.draft_kv) griddep_wait();
+  }
   // the merge kernel may be scheduled as clusters retire (only after the
   // wait above: it reads the call's bounds before its own wait)
   griddep_launch_dependents();
-  const ReqInfo ri = req_info(p, b, false);
-  const SplitRange sr = split_range(ri.N, p.nsplit, split);
+  // The cluster's piece of the call: request b, row block, split, the tiles of
+  // keys, and where its rows go (part_lse / part_o rows, or out and lse).
+  int b, rb, split, R, row0, ntiles;
+  typename Mode::Req ri;
+  typename Mode::Range sr;
+  uint32_t* flag_word;
+  [[maybe_unused]] size_t rows_total = 0;
+  [[maybe_unused]] ChunkItem it;
+  [[maybe_unused]] bool direct = false;          // chunk: the unit's rows are final
+  [[maybe_unused]] int pos_first = 0, pos_last = 0;   // chunk: positions of the unit's tokens
+  if constexpr (kChunk) {
+    const int item = blockIdx.x / C::kCtas;
+    it = chunk_item(p, p.sched, item, lane);
+    if (item == 0 && rank == 0 && tid == 0) {
+      p.totals[0] = it.total_units;
+      p.totals[1] = it.total_items;
+    }
+    if (!it.live) return;   // every CTA of the cluster leaves together
+    b = it.b;
+    rb = it.unit;
+    split = it.split;
+    ri = chunk_req(p, b);
+    R = ri.n * p.H;
+    const int urow = rb * C::kUnitRows;
+    const int urows = R - urow < C::kUnitRows ? R - urow : C::kUnitRows;
+    sr = chunk_tiles(p, ri, urow, urows);
+    pos_first = ri.P + urow / p.H;
+    pos_last = sr.k1 - 1;
+    const int per = ceil_div(sr.ntiles, it.ns), ns = ceil_div(sr.ntiles, per);
+    direct = ns == 1;
+    if (split == 0 && rank == 0 && tid == 0) {
+      ChunkUnit u;
+      u.row0 = ri.q0 * p.H + urow;
+      u.rows = urows;
+      u.ns = ns;
+      u.pslot = it.pslot0 + rb;
+      u.pstride = it.units;
+      u.item = item;
+      u.b = b;
+      u.i0 = urow;
+      p.units[it.unit0 + rb] = u;
+    }
+    flag_word = p.cta_flags + size_t(item) * C::kCtas + rank;
+    if (split >= ns) {
+      if (tid == 0) *flag_word = 0u;
+      return;
+    }
+    sr.t0 = split * per;
+    if (sr.ntiles - sr.t0 < per) sr.ntiles -= sr.t0;
+    else sr.ntiles = per;
+    ntiles = sr.ntiles;
+    row0 = urow + hh * kRows;
+  } else {
+    split = blockIdx.x / C::kCtas;
+    rb = blockIdx.y;
+    b = blockIdx.z;
+    ri = req_info(p, b, false);
+    static_cast<SplitRange&>(sr) = split_range(ri.N, p.nsplit, split);
   // this CTA's status word, for the merge kernel to OR into the status word
   // (words [request][128-row block][split][QK, PV]; every CTA of the grid
   // owns one and stores it, so the merge ORs them all without bounds)
-  uint32_t* const flag_word =
-      p.cta_flags +
-      ((size_t(b) * p.flag_blocks + (kPair ? 2 * rb + hh : rb)) * p.nsplit + split) * 2 + (qk ? 0 : 1);
-  if (split >= sr.nsplit_eff) {   // every CTA of the cluster leaves together
-    if (threadIdx.x == 0) *flag_word = 0u;
-    return;
+    flag_word =
+        p.cta_flags +
+        ((size_t(b) * p.flag_blocks + (kPair ? 2 * rb + hh : rb)) * p.nsplit + split) * 2 + (qk ? 0 : 1);
+    if (split >= sr.nsplit_eff) {   // every CTA of the cluster leaves together
+      if (threadIdx.x == 0) *flag_word = 0u;
+      return;
+    }
+    R = p.rows_per_req;
+    row0 = rb * C::kUnitRows + hh * kRows;
+    ntiles = ceil_div(sr.k1 - sr.k0, kTile);
+    rows_total = size_t(p.B) * R;
   }
-  const int R = p.rows_per_req;
-  const int row0 = rb * C::kUnitRows + hh * kRows;
-  const int ntiles = ceil_div(sr.k1 - sr.k0, kTile);
-  const size_t rows_total = size_t(p.B) * R;
 
   const bool producer = warp == 0 || warp == 2 || warp == 3 || warp >= 12;
   const int ptid = warp == 0 ? lane : (warp < 4 ? warp - 1 : warp - 9) * 32 + lane;
   // raw pool rows of the first tile (producers), loaded during the set-up
-  const int raw0 = producer && ptid < 64 ? fetch_row(p, ri, sr.k0 + ptid, sr.k1) : -1;
+  const int raw0 = producer && ptid < 64 ? fetch_row<Mode>(p, ri, sr, sr.tile_key(0) + ptid) : -1;
 
   uint32_t* cta_flags = reinterpret_cast<uint32_t*>(gb + C::kOffFlags);
   auto fail = [&]() {
@@ -630,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint64_t* valid_ring = reinterpret_cast<volatile uint64_t*>(gb + C::kOffValid);
     if (producer) {
       // ---- producers: the CTA's keys of each tile (all 576 columns)
-      if (!produce<kPair, kKBlocks, C::kRingK, true>(
+      if (!produce<kPair, Mode, kKBlocks, C::kRingK, true>(
               p, ri, sr, ntiles, ptid, sb + C::kOffK, bar(C::B_FULL), bar(C::B_EMPTY), srow,
               reinterpret_cast<uint32_t*>(gb + C::kOffValid), bar(C::B_VREADY), abort_flag,
               &tmap_k, &tmap_2d, box3d != 0, bar(C::B_QREADY), raw0, cta_flags, hh) &&
@@ -642,7 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Issued here, after the cluster barrier: issued before it, the copy
       // in flight held the barrier back by about half a microsecond.
       if (lane == 0) {
-        const int qrow = b * R + row0;
+        int qrow;
+        if constexpr (kChunk) qrow = ri.q0 * p.H + row0;
+        else qrow = b * R + row0;
         mbar_arrive_expect_tx(bar(C::B_QTMA), 2u * C::kQBoxBytes);
         tma_load_3d(sb + C::kOffQ, &tmap_q, 0, qrow, 0, bar(C::B_QTMA));
         tma_load_3d(sb + C::kOffQ + C::kQBoxBytes, &tmap_q, 0, qrow + 64, 0, bar(C::B_QTMA));
@@ -734,8 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every tile for row r
       // the request's tree parents, staged for the ancestor walk below while
       // Q is on its way
-      int* par = reinterpret_cast<int*>(gb + C::kOffPar);
-      if (p.tree_parent && tid - 128 < p.T) par[tid - 128] = p.tree_parent[size_t(b) * p.T + (tid - 128)];
+      [[maybe_unused]] int* par = reinterpret_cast<int*>(gb + C::kOffPar);
+      if constexpr (!kChunk)
+        if (p.tree_parent && tid - 128 < p.T)
+          par[tid - 128] = p.tree_parent[size_t(b) * p.T + (tid - 128)];
       if (!load_q(half, q4, lane, tmem, sb + C::kOffQ, bar(C::B_QTMA), abort_flag) && tid == 128)
         fail();
       tc_fence_before();
@@ -745,10 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa(bar(C::B_QREADYP), mate));
       }
-      if (split == 0 && rb == 0 && hh == 0 && tid == 128) {
-        bool bad = false;
-        (void)req_info(p, b, false, &bad);
-        if (bad) atomicOr(cta_flags, VA_STATUS_BAD_INDPTR);
+      if constexpr (!kChunk) {
+        if (split == 0 && rb == 0 && hh == 0 && tid == 128) {
+          bool bad = false;
+          (void)req_info(p, b, false, &bad);
+          if (bad) atomicOr(cta_flags, VA_STATUS_BAD_INDPTR);
+        }
       }
       if (tid == 128) VA_TRACE_CTA(6, 5);
       const int r = q4 * 32 + lane;
@@ -762,9 +866,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // stops below such a node), from the dense mask rows (the last T
       // entries of the node's row; entries past the mask read as 0 and are
       // flagged), or as the caller gave them.
-      named_sync(kSoftmaxBar, kSoftmax);   // parents staged
-      uint64_t nbits = 0ull;
-      if (row_ok) {
+      [[maybe_unused]] uint64_t nbits = 0ull;
+      // chunk: the row's position, and the first key that it sees past the sinks
+      [[maybe_unused]] int pos = 0, first = 0;
+      [[maybe_unused]] int first_last = 0;   // ... and that the unit's last row sees
+      [[maybe_unused]] bool hidden_nonfinite = false;
+      if constexpr (kChunk) {
+        pos = ri.P + (row_ok ? lr : R - 1) / p.H;
+        first = window_first(p.window, pos);
+        first_last = window_first(p.window, pos_last);
+      } else {
+       named_sync(kSoftmaxBar, kSoftmax);   // parents staged
+       if (row_ok) {
         const int node = lr / p.H;
         if (p.tree_parent) {
           nbits = 1ull << node;
@@ -796,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           nbits = p.bits[size_t(b) * p.T + node];
         }
+       }
       }
       float* mx = reinterpret_cast<float*>(gb + C::kOffMx);
       const uint32_t pv_p = mapa(sb + C::kOffP, other);
@@ -810,16 +924,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < ntiles; ++t) {
         const int bs = t & 1;             // S buffer and staging buffer
         const int pb = t % kPBufs;        // P buffer of the PV CTA
-        const int tk0 = sr.k0 + t * kTile;
-        // visibility: prefix keys always, draft key k when bit k of the node's mask
-        const int off = ri.P - tk0;
+        const int tk0 = sr.tile_key(t);
         uint64_t vis;
-        if (off >= 64) {
+        if constexpr (kChunk) {
+          // keys up to the row's own, from its window's first or among the
+          // sinks; most tiles lie inside for every row of the unit
           vis = ~0ull;
-        } else if (off > 0) {
-          vis = ((1ull << off) - 1ull) | (nbits << off);
+          if (tk0 + kTile > pos_first + 1 || (tk0 < first_last && tk0 + kTile > p.sinks))
+            vis = low_bits(pos + 1 - tk0) & (~low_bits(first - tk0) | low_bits(p.sinks - tk0));
         } else {
-          vis = (-off) >= 64 ? 0ull : (nbits >> (-off));
+          // visibility: prefix keys always, draft key k when bit k of the node's mask
+          const int off = ri.P - tk0;
+          if (off >= 64) {
+            vis = ~0ull;
+          } else if (off > 0) {
+            vis = ((1ull << off) - 1ull) | (nbits << off);
+          } else {
+            vis = (-off) >= 64 ? 0ull : (nbits >> (-off));
+          }
         }
         if (!row_ok) vis = 0ull;
 
@@ -841,6 +963,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tl + kTmemS + 64u * uint32_t(bs) + 32u * uint32_t(half), sv);
           tmem_wait_ld();
           tc_fence_before();
+          if constexpr (kChunk) {
+            // a hidden key's score that is not finite: its row holds NaN or an
+            // infinity, which times the zero probability of the rows that do
+            // not see it spoils them (the merge computes the unit again)
+            if (row_ok && v32 != 0xffffffffu) {
+              const uint32_t held =
+                  uint32_t(valid_ring[t % C::kValidRing] >> (32 * half)) & ~v32;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                hidden_nonfinite |= ((held >> c) & 1u) && (sv[c] & 0x7f800000u) == 0x7f800000u;
+            }
+          }
           if (!kPair || issuer_cta) {
             mbar_arrive(bar(C::B_SEMPTY + bs));
           } else {
@@ -897,10 +1031,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mr = m_ref == -INFINITY ? 0.f : m_ref;
         const float sc = p.scale_log2 > 0.f ? p.scale_log2 : 1.f;
         uint32_t pk[16];
+        if constexpr (kChunk) {
+          // the tile's sum first, so that the row sum's rounding grows with
+          // the tiles of a long context and not with its keys
+          float lt = 0.f;
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          pk[c] = pack_bf16(ex2_approx(fmaf(x[2 * c], sc, -mr)),
-                            ex2_approx(fmaf(x[2 * c + 1], sc, -mr)), l);
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16(ex2_approx(fmaf(x[2 * c], sc, -mr)),
+                              ex2_approx(fmaf(x[2 * c + 1], sc, -mr)), lt);
+          l += lt;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16(ex2_approx(fmaf(x[2 * c], sc, -mr)),
+                              ex2_approx(fmaf(x[2 * c + 1], sc, -mr)), l);
+        }
         if (tid == 128) VA_TRACE_EVENT(2, 1, t);
         VA_PH(3);
         // this row's 32 keys into the staging buffer (K-major, 128B swizzle)
@@ -937,15 +1082,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         VA_PH(6);
       }
       if (tid == 128) VA_PH_STORE(8 + 5 * hh);
+      if constexpr (kChunk)
+        if (hidden_nonfinite) atomicOr(cta_flags, kFlagHiddenNonfinite);
       // row sums: the two warpgroups' partial sums share the reference max
       if (ok) {
         mx[half * kRows + r] = l;
         named_sync(kSoftmaxBar, kSoftmax);
         if (half == 0) {
           const float lt = mx[r] + mx[kRows + r];
-          const float lse = lt > 0.f ? (m_ref + log2f(lt)) * kLn2 : -INFINITY;
-          if (row_ok) p.part_lse[size_t(split) * rows_total + size_t(b) * R + lr] = lse;
-          st_cluster_f32(pv_fin + uint32_t(r) * 4u, lt > 0.f ? 1.f / lt : 0.f);
+          if constexpr (kChunk) {
+            // (a NaN or infinite score that the row sees makes lt NaN, and the
+            // row's results with it)
+            const float lse = lt == 0.f ? -INFINITY : (m_ref + log2f(lt)) * kLn2;
+            if (row_ok) {
+              if (direct) p.lse[size_t(ri.q0) * p.H + lr] = lse;
+              else
+                p.part_lse[(size_t(it.pslot0) + size_t(split) * it.units + rb) * C::kUnitRows +
+                           (lr - rb * C::kUnitRows)] = lse;
+            }
+            st_cluster_f32(pv_fin + uint32_t(r) * 4u, lt == 0.f ? 0.f : 1.f / lt);
+          } else {
+            const float lse = lt > 0.f ? (m_ref + log2f(lt)) * kLn2 : -INFINITY;
+            if (row_ok) p.part_lse[size_t(split) * rows_total + size_t(b) * R + lr] = lse;
+            st_cluster_f32(pv_fin + uint32_t(r) * 4u, lt > 0.f ? 1.f / lt : 0.f);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(pv_finbar);
         }
@@ -966,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t* cmd = reinterpret_cast<volatile uint32_t*>(gb + C::kOffCmd);
     if (producer) {
       // ---- producers: the CTA's value columns of the same tiles
-      if (!produce<kPair, C::kVBlocksCta, kRingV, false>(
+      if (!produce<kPair, Mode, C::kVBlocksCta, kRingV, false>(
               p, ri, sr, ntiles, ptid, sb + C::kOffV, bar(C::B_FULL), bar(C::B_EMPTY), srow,
               nullptr, 0u, abort_flag, &tmap_v, &tmap_2d, box3d != 0, 0u, raw0, cta_flags, hh) &&
           ptid == 0)
@@ -1180,6 +1340,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = reinterpret_cast<const float*>(gb + C::kOffFin)[r];
         uint8_t* stg = gb + C::kOffP;
         uint8_t* rowp = stg + r * kEpiRowBytes + 512 * half;
+        // Chunk calls keep partials in 32 bits (a bf16 partial would add a
+        // rounding as large as the output's own), in two passes of 128 columns
+        // through the same staging; a unit in one piece goes to out as bf16.
+        bool f32 = false;
+        if constexpr (kChunk) f32 = !direct;
+        if constexpr (kChunk) {
+          if (f32) {
+            float* dst = p.part_o +
+                         ((size_t(it.pslot0) + size_t(split) * it.units + rb) * C::kUnitRows +
+                          (lr - rb * C::kUnitRows)) * kDv + 256 * half;
+#pragma unroll 1
+            for (int h2 = 0; h2 < 2; ++h2) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32(tl + 128u * uint32_t(h2) + 32u * uint32_t(c), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<uint4*>(rowp + 128 * c + 16 * j) =
+                      make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              }
+              fence_proxy_async_cta();
+              if (row_ok) bulk_store_global(dst + 128 * h2, smem_u32(rowp), 512u);
+              bulk_commit();
+              bulk_wait_read<0>();   // read before the staging is filled again
+            }
+          }
+        }
+        if (!f32) {
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t v[32];
@@ -1202,11 +1394,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // each thread sends its own half row as soon as it is staged, and
         // waits only until the copy has read it (the writes complete before
         // the grid does)
-        if (row_ok)
-          bulk_store_global(p.part_o + (size_t(split) * rows_total + size_t(b) * R + lr) * kDv + 256 * half,
-                            smem_u32(rowp), 512u);
+        __nv_bfloat16* dst;
+        if constexpr (kChunk)
+          dst = p.out + (size_t(ri.q0) * p.H + lr) * kDv + 256 * half;
+        else
+          dst = p.part_o + (size_t(split) * rows_total + size_t(b) * R + lr) * kDv + 256 * half;
+        if (row_ok) bulk_store_global(dst, smem_u32(rowp), 512u);
         bulk_commit();
         bulk_wait_read<0>();
+        }
         if (lane == 0 && warp == 4) VA_TRACE_CTA(5, 1);
       } else if (ok && !fin) {
         fail();
@@ -1264,7 +1460,8 @@ int max_clusters() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, partial_tc_kernel<kPair>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, partial_tc_kernel<kPair, VerifyMode>, &cfg) !=
+      cudaSuccess) {
     n = 0;
     (void)cudaGetLastError();
   }
@@ -1315,13 +1512,13 @@ int tc_flag_blocks(int T, int H, bool pair) {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 cudaError_t init_partial_tc(int* max_pairs, int* max_quads) {
-  cudaError_t e = cudaFuncSetAttribute(partial_tc_kernel<false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(Cfg<false>::kSmemBytes));
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(partial_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           int(Cfg<true>::kSmemBytes));
-  if (e != cudaSuccess) return e;
+  constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  constexpr int kBytes1 = int(Cfg<false>::kSmemBytes), kBytes2 = int(Cfg<true>::kSmemBytes);
+  for (cudaError_t e : {cudaFuncSetAttribute(partial_tc_kernel<false, VerifyMode>, kSmem, kBytes1),
+                        cudaFuncSetAttribute(partial_tc_kernel<true, VerifyMode>, kSmem, kBytes2),
+                        cudaFuncSetAttribute(partial_tc_kernel<false, ChunkMode>, kSmem, kBytes1),
+                        cudaFuncSetAttribute(partial_tc_kernel<true, ChunkMode>, kSmem, kBytes2)})
+    if (e != cudaSuccess) return e;
   *max_pairs = max_clusters<false>();
   *max_quads = max_clusters<true>();
   if (!g_encode) {
@@ -1339,7 +1536,8 @@ cudaError_t init_partial_tc(int* max_pairs, int* max_quads) {
 // blocks: strides one row and 128 bytes), a box of `rows` keys x `blocks`
 // column blocks covering a CTA's share of a 64-key tile; 2-D (576 columns,
 // pool rows; blocks = 0), a box of one column block of `rows` keys.
-bool encode_pool_map(CUtensorMap* m, const Params& p, int blocks, int rows) {
+template <class P>
+bool encode_pool_map(CUtensorMap* m, const P& p, int blocks, int rows) {
   if (blocks > 0) {
     cuuint64_t dims[3] = {64u, cuuint64_t(p.num_slots), cuuint64_t(kKBlocks)};
     cuuint64_t strides[2] = {cuuint64_t(p.kv_stride) * 2u, 128u};
@@ -1360,32 +1558,41 @@ bool encode_pool_map(CUtensorMap* m, const Params& p, int blocks, int rows) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor map of the queries: 3-D (64 features, query rows B*T*H, column
+// Tensor map of the queries: 3-D (64 features, query rows, column
 // blocks: strides one 1152-byte row and 128 bytes); a box of 64 rows x 9
 // blocks is half a row block's Q.
-bool encode_q_map(CUtensorMap* m, const Params& p) {
-  cuuint64_t dims[3] = {64u, cuuint64_t(p.B) * cuuint64_t(p.rows_per_req), cuuint64_t(kKBlocks)};
+bool encode_q_map(CUtensorMap* m, const __nv_bfloat16* q, int64_t rows) {
+  cuuint64_t dims[3] = {64u, cuuint64_t(rows), cuuint64_t(kKBlocks)};
   cuuint64_t strides[2] = {cuuint64_t(kDqk) * 2u, 128u};
   cuuint32_t box[3] = {64u, 64u, uint32_t(kKBlocks)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(p.q), dims,
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(q), dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_partial_tc(const Params& p, int /*num_sms*/, cudaStream_t st) {
-  const bool pair = p.tc_pair != 0;
+namespace {
+
+// One launch of the kernel in either mode: `grid` counts clusters in x, row
+// blocks and requests in y and z.
+//  - Contiguous pools are read with TMA box loads; the maps are encoded on the
+//    host for this call's pool.  Paged calls do not use them.  Pair shares: a
+//    QK CTA's 32 keys of a tile (3-D box of 9 blocks, 2-D box per block where
+//    the ring wraps); a PV CTA's value blocks, two boxes of 2 blocks x 64 keys.
+//  - A programmatic dependent of the stream's previous kernel (programmatic
+//    stream serialization): after the draft-row append kernel the clusters run
+//    while it does (see the producers' griddepcontrol.wait); as the call's
+//    first kernel they may start while the stream's previous kernel finishes
+//    and wait for it before reading any input.
+template <class Mode>
+cudaError_t launch_tc(const typename Mode::P& p, dim3 grid, bool pair, int64_t q_rows,
+                      cudaStream_t st) {
   const int ctas = pair ? Cfg<true>::kCtas : Cfg<false>::kCtas;
-  const int unit = pair ? Cfg<true>::kUnitRows : Cfg<false>::kUnitRows;
-  // Contiguous pools are read with TMA box loads; the maps are encoded on the
-  // host for this call's pool.  Paged calls do not use them.  Pair shares: a
-  // QK CTA's 32 keys of a tile (3-D box of 9 blocks, 2-D box per block where
-  // the ring wraps); a PV CTA's value blocks, two boxes of 2 blocks x 64 keys.
   CUtensorMap tk, tv, t2, tq;
   memset(&tk, 0, sizeof tk);
   memset(&tv, 0, sizeof tv);
   memset(&t2, 0, sizeof t2);
-  if (!g_encode || !encode_q_map(&tq, p)) return cudaErrorNotSupported;
+  if (!g_encode || !encode_q_map(&tq, p.q, q_rows)) return cudaErrorNotSupported;
   int box3d = 0;
   if (p.kv_start) {
     const int krows = pair ? Cfg<true>::kSlotKeys : kTile;
@@ -1394,15 +1601,9 @@ cudaError_t launch_partial_tc(const Params& p, int /*num_sms*/, cudaStream_t st)
         encode_pool_map(&tv, p, pair ? 2 : kVBlocks, kTile))
       box3d = 1;
   }
-  // A programmatic dependent of the stream's previous kernel (programmatic
-  // stream serialization): after the draft-row append kernel the clusters
-  // run while it does (see the producers' griddepcontrol.wait); as the call's
-  // first kernel they may start while the stream's previous kernel finishes
-  // and wait for it before reading any input.
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(unsigned(ctas * p.nsplit), unsigned(ceil_div(p.rows_per_req, unit)),
-                     unsigned(p.B));
+  cfg.gridDim = dim3(unsigned(ctas) * grid.x, grid.y, grid.z);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = pair ? Cfg<true>::kSmemBytes : Cfg<false>::kSmemBytes;
   cfg.stream = st;
@@ -1415,8 +1616,23 @@ cudaError_t launch_partial_tc(const Params& p, int /*num_sms*/, cudaStream_t st)
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return pair ? cudaLaunchKernelEx(&cfg, partial_tc_kernel<true>, p, tk, tv, t2, tq, box3d)
-              : cudaLaunchKernelEx(&cfg, partial_tc_kernel<false>, p, tk, tv, t2, tq, box3d);
+  return pair ? cudaLaunchKernelEx(&cfg, partial_tc_kernel<true, Mode>, p, tk, tv, t2, tq, box3d)
+              : cudaLaunchKernelEx(&cfg, partial_tc_kernel<false, Mode>, p, tk, tv, t2, tq, box3d);
+}
+
+}  // namespace
+
+cudaError_t launch_partial_tc(const Params& p, int /*num_sms*/, cudaStream_t st) {
+  const bool pair = p.tc_pair != 0;
+  const int unit = pair ? Cfg<true>::kUnitRows : Cfg<false>::kUnitRows;
+  return launch_tc<VerifyMode>(p, dim3(unsigned(p.nsplit), unsigned(ceil_div(p.rows_per_req, unit)),
+                                       unsigned(p.B)),
+                               pair, int64_t(p.B) * p.rows_per_req, st);
+}
+
+cudaError_t launch_chunk_tc(const ChunkTcParams& p, int grid_items, bool pair, cudaStream_t st) {
+  return launch_tc<ChunkMode>(p, dim3(unsigned(grid_items), 1, 1), pair, int64_t(p.total_q) * p.H,
+                              st);
 }
 
 }  // namespace va
