@@ -15,6 +15,7 @@
 namespace va {
 cudaError_t init_partial_fma();
 cudaError_t init_partial_tc(int* max_pairs, int* max_quads);
+cudaError_t init_weights_tc();
 bool tc_supported(int B, int T, int H);
 bool tc_use_pair(int T, int H, int flags);
 int tc_auto_nsplit(int B, int T, int H, int clusters, bool pair);
@@ -225,12 +226,13 @@ VA_API int va_init(int device) {
   cudaError_t e1 = va::init_partial_fma();
   int pairs = 0, quads = 0;
   cudaError_t e2 = va::init_partial_tc(&pairs, &quads);
+  cudaError_t e3 = va::init_weights_tc();
   // the no-allocation scratch array: placed now, with the device current; a
   // failure here (no memory left for it) is not an error of va_init -- the
   // first verify_attn_paged_noalloc call on the device retries and reports it
   if (resolve_noalloc(device) != cudaSuccess) (void)cudaGetLastError();
   cudaSetDevice(prev);
-  if (e1 != cudaSuccess || e2 != cudaSuccess) return VA_ERR_CUDA;
+  if (e1 != cudaSuccess || e2 != cudaSuccess || e3 != cudaSuccess) return VA_ERR_CUDA;
   g_dev[device].num_sms = prop.multiProcessorCount;
   g_dev[device].tc_pairs = pairs > 0 ? pairs : prop.multiProcessorCount / 2;
   g_dev[device].tc_quads = quads > 0 ? quads : prop.multiProcessorCount / 4;

@@ -284,6 +284,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c
       : "memory");
 }
 
+// The same in a pair (cta_group::2): the box lands in this CTA's shared memory
+// and completes on a barrier of either CTA of the pair (address from mapa).
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, int c0, int c1,
+                                                 int c2, uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes."
+      "cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
+      : "memory");
+}
+
 // Bring a tensor map (a __grid_constant__ parameter) into the TMA unit's cache.
 __device__ __forceinline__ void tma_prefetch(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -4,10 +4,11 @@
 //                    exp(s_r - lse_r)
 // with s_r the scaled score and lse_r the row's log-sum-exp from the attention
 // call.  Which rows see a key is exactly what the attention call applied
-// (causal, window, sinks).
+// (causal, window, sinks).  The entry point and the CUDA-core path
+// (VA_PATH_FMA); the tensor-core path is in va_weights_tc.cu.
 #include <string.h>
 
-#include "va_chunk.cuh"
+#include "va_weights.cuh"
 
 #ifndef VA_API
 #define VA_API extern "C" __attribute__((visibility("default")))
@@ -41,14 +42,16 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fma_kernel(const Weigh
       const int j = int(k);
       const int64_t kr = chunk_key_row(c, r, j);
       float total = 0.f;
-      if (kr < 0) {
+      const int i0 = j > r.P ? j - r.P : 0;   // the first token that sees it, if any does
+      if (i0 >= r.n || (j >= c.sinks && j < window_first(c.window, r.P + i0))) {
+      } else if (kr < 0) {
         bits |= VA_STATUS_BAD_SLOT;
       } else {
         const uint32_t* k32 = reinterpret_cast<const uint32_t*>(c.kv + kr * c.kv_stride);
         uint32_t kv[9];
 #pragma unroll
         for (int x = 0; x < 9; ++x) kv[x] = k32[32 * x + lane];
-        for (int i = j > r.P ? j - r.P : 0; i < r.n; ++i) {
+        for (int i = i0; i < r.n; ++i) {
           if (j >= c.sinks && j < window_first(c.window, r.P + i)) break;   // nor any later token
           float token = 0.f;
           for (int h = 0; h < c.H; ++h) {
@@ -80,6 +83,23 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fma_kernel(const Weigh
   if (lane == 0 && bits) atomicOr(c.status, bits);
 }
 
+// List positions stay below 2^31 with a key tile's worth to spare.
+constexpr int64_t kEntriesMax = 0x7fffffff - 1024;
+
+struct WeightsLayout {
+  size_t flags, entry, cont, sums, total;
+};
+
+WeightsLayout weights_layout(int64_t num_entries) {
+  WeightsLayout L;
+  L.flags = kHeaderBytes;
+  L.entry = L.flags + align256(kWeightClusters * sizeof(uint32_t));
+  L.cont = L.entry + align256(kWeightClusters * sizeof(int32_t));
+  L.sums = L.cont + align256(size_t(kWeightClusters) * 256 * sizeof(float));
+  L.total = L.sums + align256(size_t(num_entries) * sizeof(float));
+  return L;
+}
+
 bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
 
 }  // namespace
@@ -89,9 +109,10 @@ VA_API size_t va_kv_weights_workspace_bytes(int B, int total_q, int H, int64_t n
                                             int flags) {
   if (B < 1 || B > 65535 || total_q < 0 || H < 1 || flags < VA_PATH_AUTO ||
       flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX || num_entries < 0 ||
-      num_entries > 0x7fffffff)
+      num_entries > va::kEntriesMax)
     return 0;
-  return va::kHeaderBytes;
+  if (flags == VA_PATH_FMA) return va::kHeaderBytes;
+  return va::weights_layout(num_entries).total;
 }
 
 VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_slots,
@@ -123,7 +144,7 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
   const int rc = chunk_check(c, true, sm_scale, flags, workspace);
   if (rc != VA_OK) return rc;
   if (!weights_out) return VA_ERR_NULL;
-  if (num_entries < 0 || num_entries > 0x7fffffff) return VA_ERR_SHAPE;
+  if (num_entries < 0 || num_entries > kEntriesMax) return VA_ERR_SHAPE;
   if (!aligned4(weights_in) || !aligned4(weights_out)) return VA_ERR_ALIGN;
   if (workspace_bytes < va_kv_weights_workspace_bytes(B, total_q, H, num_entries, flags))
     return VA_ERR_WORKSPACE;
@@ -135,6 +156,27 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
   p.win = weights_in;
   p.wout = weights_out;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (flags != VA_PATH_FMA) {
+    // two-SM products when the average request has more than 128 rows
+    const int busy = B < total_q ? B : total_q;
+    const bool pair = flags != VA_PATH_TC_1SM && int64_t(total_q) * H > 128 * int64_t(busy);
+    const WeightsLayout L = weights_layout(num_entries);
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    WeightTcParams t;
+    memset(&t, 0, sizeof t);
+    t.c = c;
+    t.win = weights_in;
+    t.wout = weights_out;
+    const int clusters = pair ? di.pairs : di.num_sms;
+    const int most = pair ? kWeightClusters / 2 : kWeightClusters;
+    t.clusters = clusters < most ? clusters : most;
+    t.tile_keys = pair ? 256 : 128;
+    t.cta_flags = reinterpret_cast<uint32_t*>(w + L.flags);
+    t.cont_entry = reinterpret_cast<int32_t*>(w + L.entry);
+    t.cont = reinterpret_cast<float*>(w + L.cont);
+    t.sums = reinterpret_cast<float*>(w + L.sums);
+    return launch_weights_tc(t, pair, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
+  }
   if (cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st) != cudaSuccess) return VA_ERR_LAUNCH;
   const int64_t want = (num_entries + kWeightThreads / 32 - 1) / (kWeightThreads / 32);
   const int64_t wave = int64_t(di.num_sms) * 8;
