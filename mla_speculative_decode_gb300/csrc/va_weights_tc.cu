@@ -83,9 +83,8 @@ struct WCfg {
   static constexpr uint32_t kOffFlags = 520;
   static constexpr uint32_t kOffSrow = 1024;    // int32 [2][128] pool rows of a key tile
   static constexpr uint32_t kOffLse = 2048;     // float [2][256] lse * log2(e) of a step's rows
-  static constexpr uint32_t kOffPos = 4096;     // int32 [2][256] their positions
-  static constexpr uint32_t kOffPart = 6144;    // float [128] the second half's sums
-  static constexpr uint32_t kOffK = 8192;
+  static constexpr uint32_t kOffPart = 4096;    // float [128] the second half's sums
+  static constexpr uint32_t kOffK = 5120;
   static constexpr uint32_t kOffQ = kOffK + kBlocks * kKSlot;
   static constexpr uint32_t kSmemBytes = kOffQ + kQSlots * kQSlot + 1024;
   static_assert(8 * kNumBars <= int(kOffTmemSlot), "barrier area");
@@ -476,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = q4 * 32 + lane;
     constexpr int kHalf = C::kTileRows / 2;
     float* lse = reinterpret_cast<float*>(gb + C::kOffLse);
-    int* pos = reinterpret_cast<int*>(gb + C::kOffPos);
     float* part = reinterpret_cast<float*>(gb + C::kOffPart);
     const uint32_t tl = tmem + (uint32_t(q4 * 32) << 16) + uint32_t(kHalf * half);
     const uint32_t sempty = kPair ? mapa(bar(C::B_SEMPTY), 0) : 0u;
@@ -488,31 +486,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int step = 0; w.left > 0; ++step) {
       const int bs = step & 1;
       const int R = w.r.n * w.p.H, row0 = w.rt * C::kTileRows;
-      // the step's rows: lse, and the position of each row's token; a row past
-      // the request's end, or one that saw nothing (lse -inf), hides every key
+      // the step's lse; +inf for a row that saw nothing (lse -inf): no weight
       bool clean = true;
       if (etid < C::kTileRows) {
         const int row = row0 + etid;
         float l = INFINITY;
-        int ps = -1;
         if (row < R) {
           const float x = w.p.lse[size_t(w.r.q0) * w.p.H + row];
-          if (x != -INFINITY) {
-            l = x * kLog2e;
-            ps = w.r.P + row / w.p.H;
-          }
+          if (x != -INFINITY) l = x * kLog2e;
         }
         lse[bs * 256 + etid] = l;
-        pos[bs * 256 + etid] = ps;
-        clean = ps >= 0;
+        clean = l != INFINITY;
       }
+      // The columns (rows of the step) that see this thread's key are one run
+      // [c_lo, c_hi): from its own token on, up to the last token whose window
+      // reaches it.  Most steps lie inside it for every key.
       const int k0 = w.kt * C::kTileKeys + hh * kKeys;
       const int j = k0 + r;
-      if (k0 + kKeys - 1 > w.r.P + row0 / w.p.H) clean = false;
-      if (window > 0 && k0 + kKeys > sinks) {
-        const int rz = (row0 + C::kTileRows < R ? row0 + C::kTileRows : R) - 1;
-        if (k0 < window_first(window, w.r.P + rz / w.p.H)) clean = false;
+      int c_lo, c_hi;
+      {
+        const int64_t lo = int64_t(j - w.r.P) * w.p.H - row0;
+        int64_t hi = R - row0;
+        if (window > 0 && j >= sinks) {
+          const int64_t x = (int64_t(j) + window - w.r.P) * w.p.H - row0;
+          hi = x < hi ? x : hi;
+        }
+        c_lo = lo < 0 ? 0 : lo > C::kTileRows ? C::kTileRows : int(lo);
+        c_hi = hi < 0 ? 0 : hi > C::kTileRows ? C::kTileRows : int(hi);
       }
+      if (c_lo > 0 || c_hi < C::kTileRows) clean = false;
       // what the step's end needs of this place
       const int N = w.N, tile0 = w.kt * C::kTileKeys, kt = w.kt, b = w.b;
       const int64_t base = w.r.base;
@@ -538,20 +540,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const float4 l = l4[c];
-              sum += ex2_approx(fmaf(__uint_as_float(sv[4 * c]), sc, -l.x)) +
-                     ex2_approx(fmaf(__uint_as_float(sv[4 * c + 1]), sc, -l.y)) +
+              sum += (ex2_approx(fmaf(__uint_as_float(sv[4 * c]), sc, -l.x)) +
+                      ex2_approx(fmaf(__uint_as_float(sv[4 * c + 1]), sc, -l.y))) +
                      (ex2_approx(fmaf(__uint_as_float(sv[4 * c + 2]), sc, -l.z)) +
                       ex2_approx(fmaf(__uint_as_float(sv[4 * c + 3]), sc, -l.w)));
             }
           } else {
-            const int* ps = pos + bs * 256 + kHalf * half + c0;
-            const float* lf = lse + bs * 256 + kHalf * half + c0;
+            // a score that is hidden, or of a row without weight, is not used
+            // at all, whatever it is
+            const int lo = c_lo - (kHalf * half + c0), hi = c_hi - (kHalf * half + c0);
+            auto term = [&](int c, float l) -> float {
+              return c >= lo && c < hi && l < INFINITY
+                         ? ex2_approx(fmaf(__uint_as_float(sv[c]), sc, -l))
+                         : (l != l && c >= lo && c < hi ? l : 0.f);
+            };
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int x = ps[c];
-              const bool see = j <= x && (window <= 0 || j > x - window || j < sinks);
-              // a hidden key's score is not used at all, whatever it is
-              sum += see ? ex2_approx(fmaf(__uint_as_float(sv[c]), sc, -lf[c])) : 0.f;
+            for (int c = 0; c < 8; ++c) {
+              const float4 l = l4[c];
+              sum += (term(4 * c, l.x) + term(4 * c + 1, l.y)) +
+                     (term(4 * c + 2, l.z) + term(4 * c + 3, l.w));
             }
           }
         }
