@@ -240,3 +240,11 @@ def test_chunk_weights_evict_verify_in_one_graph(va):
     ro, rl, _ = oracle.verify_attn(synth.as_u16(q2), synth.as_u16(pool), lists, indptr,
                                    np.full(B, budget, dtype=np.int32), bits, synth.SM_SCALE)
     _gpu.compare(vo, vl, ro, rl)
+
+
+@pytest.mark.parametrize("L,budget", [([30000], 25000), ([200000, 40000, 9000], 100000),
+                                      ([90000], 11000)])
+def test_in_place_with_more_kept_than_a_block_holds(va, L, budget):
+    for kind in ("floats", "ties"):
+        _run(va, L, 3, kind, budget, 4, 1024, seed=budget, inplace=True)
+    _run(va, L, 0, "equal", budget, 0, budget // 2, seed=budget, inplace=True)
