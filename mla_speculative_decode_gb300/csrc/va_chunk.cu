@@ -9,8 +9,9 @@
 // columns, value = the first 512) in one pass over the visible keys with a
 // running maximum and sum.
 //
-// Two paths: the tensor-core kernel of the verify calls in its chunk mode
-// (va_tc.cu), followed by chunk_finish_kernel, which merges the splits; and one
+// Two paths: the tensor cores -- a kernel for few rows per request
+// (va_decode_tc.cu) or that of the verify calls in its chunk mode (va_tc.cu) --
+// followed by chunk_finish_kernel, which merges the splits; and one
 // warp per row on CUDA cores (VA_PATH_FMA), an independent implementation that
 // the finish kernel also uses for the rare rows that the products may have
 // spoilt (see kFlagHiddenNonfinite).
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
       uint32_t f = 0u;
       for (int s = 0; s < x.ns; ++s)
         for (int c = 0; c < p.ctas; ++c)
-          f |= p.cta_flags[size_t(x.item + s * x.pstride) * p.ctas + c];
+          f |= p.cta_flags[size_t(x.item + s * x.istride) * p.ctas + c];
       const bool redo = f & kFlagHiddenNonfinite;
       // (the order of the list does not matter: a row is one CTA's alone)
       if (x.ns > 1 || redo) list[atomicAdd(&s_count, 1)] = redo ? ~u : u;
@@ -102,13 +103,15 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
           }
           continue;
         }
-        const size_t slot = size_t(x.pslot), step = size_t(x.pstride);
+        auto slot = [&](int s) -> size_t {
+          return size_t(s == 0 ? x.pslot : x.pslot1 + (s - 1) * x.pstride);
+        };
         const int ns = x.ns < kMaxNs ? x.ns : kMaxNs;
         __syncthreads();   // w and half of the row before are read
         if (tid < 32) {
           float m = -INFINITY;
           for (int s = lane; s < ns; s += 32) {
-            const float ls = p.part_lse[(slot + s * step) * U + r];
+            const float ls = p.part_lse[slot(s) * U + r];
             w[s] = ls;
             m = fmaxf(m, ls);
           }
@@ -125,12 +128,11 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
         }
         __syncthreads();
         const int col = tid & 127, group = tid >> 7;
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + (slot * U + r) * kDv) + col;
-        const size_t sstep = step * U * (kDv / 4);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + size_t(r) * kDv) + col;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int s = group; s < ns; s += 2) {
-          const float4 v4 = src[s * sstep];
+          const float4 v4 = src[slot(s) * U * (kDv / 4)];
           const float ws = w[s];
           acc.x = fmaf(ws, v4.x, acc.x);
           acc.y = fmaf(ws, v4.y, acc.y);
@@ -171,11 +173,12 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
 
 // Clusters of the tensor-core kernel that a GB300's 152 SMs hold at most; the
 // workspace is sized for them, so that sizing it takes no device call.
-constexpr int kMaxPairs = 76, kMaxQuads = 38;
+constexpr int kMaxSms = 152, kMaxPairs = 76, kMaxQuads = 38;
 // With many units, splits are cut so that about this many waves of clusters run.
 constexpr int kWaves = 3;
 
 struct ChunkPlan {
+  bool decode;       // va_decode_tc.cu
   bool pair;
   int unit_rows, ctas, max_clusters;
   int units_bound;   // units the batch can have
@@ -183,22 +186,26 @@ struct ChunkPlan {
   size_t off_units, off_flags, off_lse, off_o, total;
 };
 
-// Two-SM products when the average request has more than 128 rows.
+// The decode kernel when the average request has at most 64 rows, two-SM
+// products of the split kernel when it has more than 128.
 ChunkPlan chunk_plan(int B, int total_q, int H, int flags) {
   ChunkPlan c;
   const int64_t rows = int64_t(total_q) * H;
   const int busy = B < total_q ? B : total_q;   // requests with tokens, at most
+  c.decode = flags != VA_PATH_TC_1SM && rows <= 64 * int64_t(busy);
   c.pair = flags != VA_PATH_TC_1SM && rows > 128 * int64_t(busy);
-  c.unit_rows = c.pair ? 256 : 128;
-  c.ctas = c.pair ? 4 : 2;
-  c.max_clusters = c.pair ? kMaxQuads : kMaxPairs;
+  c.unit_rows = c.decode ? 64 : c.pair ? 256 : 128;
+  c.ctas = c.decode ? 1 : c.pair ? 4 : 2;
+  c.max_clusters = c.decode ? kMaxSms : c.pair ? kMaxQuads : kMaxPairs;
   c.units_bound = int((rows + c.unit_rows - 1) / c.unit_rows) + busy;
   c.one_wave = 2 * c.units_bound <= c.max_clusters;
   // items: one wave's clusters, or target + one per unit; partial slots: items
   // of requests in two or more splits, fewer than twice the target
   const size_t target = size_t(kWaves) * c.max_clusters;
-  const size_t items = c.one_wave ? size_t(c.max_clusters) : target + c.units_bound;
-  const size_t slots = c.one_wave ? size_t(c.max_clusters) : 2 * target;
+  // (the decode kernel: an item and two slots per CTA)
+  const size_t items = c.decode || c.one_wave ? size_t(c.max_clusters) : target + c.units_bound;
+  const size_t slots = c.decode ? 2 * size_t(c.max_clusters)
+                       : c.one_wave ? size_t(c.max_clusters) : 2 * target;
   c.off_units = kHeaderBytes;
   c.off_flags = c.off_units + align256(size_t(c.units_bound) * sizeof(ChunkUnit));
   c.off_lse = c.off_flags + align256(items * c.ctas * sizeof(uint32_t));
@@ -269,7 +276,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   ChunkTcParams t;
   memset(&t, 0, sizeof t);
   static_cast<ChunkParams&>(t) = p;
-  const int resident = c.pair ? di.quads : di.pairs;
+  const int resident = c.decode ? di.num_sms : c.pair ? di.quads : di.pairs;
   t.sched.unit_rows = c.unit_rows;
   t.sched.clusters = resident < c.max_clusters ? resident : c.max_clusters;
   t.sched.one_wave = c.one_wave ? 1 : 0;
@@ -281,7 +288,9 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   t.part_lse = reinterpret_cast<float*>(w + c.off_lse);
   t.part_o = reinterpret_cast<float*>(w + c.off_o);
   const int items = c.one_wave ? t.sched.clusters : t.sched.target + c.units_bound;
-  if (launch_chunk_tc(t, items, c.pair, st) != cudaSuccess) return VA_ERR_LAUNCH;
+  if ((c.decode ? launch_decode_tc(t, t.sched.clusters, st)
+                : launch_chunk_tc(t, items, c.pair, st)) != cudaSuccess)
+    return VA_ERR_LAUNCH;
   return launch_finish(t, di.num_sms, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }
 

@@ -337,8 +337,9 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
 struct alignas(16) ChunkUnit {
   int row0, rows;        // rows of out / lse
   int ns;                // splits that hold keys (1: already in out and lse)
-  int pslot, pstride;    // partial slot of split 0, and from split to split
-  int item;              // item of split 0 (then pstride apart)
+  int pslot;             // partial slot of split 0 ...
+  int pslot1, pstride;   // ... of split 1, and from there on
+  int item, istride;     // item of split 0, and from split to split
   int b, i0;             // request, row within it
 };
 
@@ -358,7 +359,9 @@ struct ChunkTcParams : ChunkParams {
 // computes the unit's rows again on CUDA cores.
 constexpr uint32_t kFlagHiddenNonfinite = 0x80000000u;
 
-// Tensor-core kernel (va_tc.cu).
+// Tensor-core kernels: va_decode_tc.cu for few rows per request (units of 64
+// rows, an item per CTA, two partial slots each), else va_tc.cu.
+cudaError_t launch_decode_tc(const ChunkTcParams& p, int ctas, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkTcParams& p, int grid_items, bool pair, cudaStream_t st);
 
 // Checks shared by the chunk calls (va_chunk.cu).

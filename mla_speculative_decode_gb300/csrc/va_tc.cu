@@ -646,8 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       u.rows = urows;
       u.ns = ns;
       u.pslot = it.pslot0 + rb;
+      u.pslot1 = u.pslot + it.units;
       u.pstride = it.units;
       u.item = item;
+      u.istride = it.units;
       u.b = b;
       u.i0 = urow;
       p.units[it.unit0 + rb] = u;
