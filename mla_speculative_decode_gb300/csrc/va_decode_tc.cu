@@ -45,6 +45,7 @@ constexpr int kMmaWarp = 15;
 constexpr int kThreads = 512;
 constexpr uint32_t kSoftmaxBar = 1, kProducerBar = 2;   // named barriers
 constexpr int kRows = 64, kTile = 64, kBlocks = kDqk / 64;
+constexpr int kGroups = 3;             // of three 64-column blocks: what is loaded and released as one
 constexpr uint32_t kSlot = kTile * 128u;               // one 64-column block of a tile
 constexpr uint32_t kTileBytes = kBlocks * kSlot;
 constexpr int kValidRing = 4;
@@ -54,9 +55,9 @@ constexpr long long kDrainCycles = 2000000ll;     // after an abort: boxes in fl
 constexpr float kRescaleLog2 = 8.f;
 
 // Barriers.
-constexpr int B_KFULL = 0;                     // [2] a key tile landed
-constexpr int B_KEMPTY = B_KFULL + 2;          // [2] both products of it are done
-constexpr int B_SFULL = B_KEMPTY + 2;          // [2]
+constexpr int B_KFULL = 0;                     // [2][kGroups] column blocks of a key tile landed
+constexpr int B_KEMPTY = B_KFULL + 2 * kGroups;   // [2][kGroups] both products of them are done
+constexpr int B_SFULL = B_KEMPTY + 2 * kGroups;   // [2]
 constexpr int B_SEMPTY = B_SFULL + 2;          // [2]
 constexpr int B_VREADY = B_SEMPTY + 2;         // [kValidRing] a tile's key-validity mask
 constexpr int B_PFULL = B_VREADY + kValidRing;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t cnt = 1;
-      if (i == B_KFULL || i == B_KFULL + 1) cnt = kProducers + 1;   // copies + producer 0
+      if (i >= B_KFULL && i < B_KFULL + 2 * kGroups) cnt = kProducers + 1;   // copies + producer 0
       if (i == B_SEMPTY || i == B_SEMPTY + 1 || i == B_PFULL || i == B_OFREE) cnt = kSoftmax;
       mbar_init(bar(i), cnt);
     }
@@ -276,18 +277,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (producer) {
     // ---- keys: 64 rows of a tile; a warp instruction copies 128 bytes of each of
-    // four rows (one column block), and the tile's 16 x 9 of them are dealt to
-    // the warps
+    // four rows (one column block).  The tile's rows are staged first; then, as
+    // each group of column blocks is released, the warps share its 3 x 16
+    // instructions.  After a wait gave up a warp stays in step, copying nothing.
     int* srow = reinterpret_cast<int*>(gb + kOffSrow);
     uint32_t* valid32 = reinterpret_cast<uint32_t*>(gb + kOffValid);
     const int pw = ptid >> 5;
     int rawrow = raw0;
     bool ok = true, bad_slot = false;
-    int box_step[2] = {-1, -1};   // the last step loaded by a box into each half
+    int box_step[2] = {-1, -1};   // the last step loaded by boxes into each half
     for (int s = 0; w.left > 0; ++s) {
       const int half = s & 1;
-      bool got = true;
-      if (ptid == 0 && s >= 2) got = wait(B_KEMPTY + half, uint32_t((s >> 1) - 1));
       const int tk0 = w.key();
       if (ptid < kTile) {
         const int row = rawrow >= 0 && int64_t(rawrow) < p.num_slots ? rawrow : -1;
@@ -296,56 +296,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t v = __ballot_sync(0xffffffffu, row >= 0);
         if (lane == 0) valid32[(s % kValidRing) * 2 + (ptid >> 5)] = v;
       }
-      if (!named_sync_and(kProducerBar, kProducers, got)) {
-        ok = false;
-        break;
-      }
+      named_sync(kProducerBar, kProducers);
       const int64_t row0 = p.kv_start ? w.r.base + tk0 : -1;
       const bool box = p.kv_start && w.t.whole(tk0) && tk0 + kTile <= w.r.nlist && row0 >= 0 &&
                        row0 + kTile <= p.num_slots && row0 + kTile <= 0x7fffffff;
       w.next();
       if (ptid < kTile && w.left > 0) rawrow = fetch(w);
-      const uint32_t dst0 = sb + kOffK + uint32_t(half) * kTileBytes;
       if (ptid == 0) {
         mbar_arrive(bar(B_VREADY + s % kValidRing));
         box_step[half] = box ? s : -1;
-        if (box) {
-          mbar_arrive_expect_tx(bar(B_KFULL + half), kTileBytes);
-          tma_load_3d(dst0, &tmap_k, 0, int(row0), 0, bar(B_KFULL + half));
-        } else {
-          mbar_arrive(bar(B_KFULL + half));
-        }
       }
-      if (!box) {
-#pragma unroll 7
-        for (int u = pw; u < kTile / 4 * kBlocks; u += kProducers / 32) {
-          const int quad = u / kBlocks, c = u - quad * kBlocks;
-          const int key = 4 * quad + (lane >> 3);
-          const int row = srow[half * kTile + key];
-          const __nv_bfloat16* src =
-              p.kv + (row >= 0 ? int64_t(row) * p.kv_stride : 0) + 64 * c + (lane & 7) * 8;
-          cp_async16(dst0 + uint32_t(c) * kSlot + uint32_t(key) * 128u +
-                         uint32_t(((lane & 7) ^ (key & 7)) * 16),
-                     src, row >= 0 ? 16u : 0u);
+      const uint32_t dst0 = sb + kOffK + uint32_t(half) * kTileBytes;
+#pragma unroll 1
+      for (int g = 0; g < kGroups; ++g) {
+        const int full = B_KFULL + half * kGroups + g;
+        if (s >= 2 && ok) {
+          bool got = true;
+          if (lane == 0) got = wait(B_KEMPTY + half * kGroups + g, uint32_t((s >> 1) - 1));
+          ok = __all_sync(0xffffffffu, got);
+          if (!ok && lane == 0) fail();
         }
+        if (ptid == 0) {
+          if (box && ok) {
+            mbar_arrive_expect_tx(bar(full), 3 * kSlot);
+            tma_load_3d(dst0 + uint32_t(3 * g) * kSlot, &tmap_k, 0, int(row0), 3 * g, bar(full));
+          } else {
+            mbar_arrive(bar(full));
+          }
+        }
+        if (!box && ok) {
+#pragma unroll
+          for (int x = 0; x < 7; ++x) {
+            const int u = pw + x * (kProducers / 32);   // block of the group x four keys
+            if (u < 3 * kTile / 4) {
+              const int c = 3 * g + (u >> 4);
+              const int key = 4 * (u & 15) + (lane >> 3);
+              const int row = srow[half * kTile + key];
+              const __nv_bfloat16* src =
+                  p.kv + (row >= 0 ? int64_t(row) * p.kv_stride : 0) + 64 * c + (lane & 7) * 8;
+              cp_async16(dst0 + uint32_t(c) * kSlot + uint32_t(key) * 128u +
+                             uint32_t(((lane & 7) ^ (key & 7)) * 16),
+                         src, row >= 0 ? 16u : 0u);
+            }
+          }
+        }
+        cp_async_arrive_noinc(bar(full));
       }
-      cp_async_arrive_noinc(bar(B_KFULL + half));
     }
     if (bad_slot) atomicOr(cta_flags, VA_STATUS_BAD_SLOT);
     cp_async_wait_all();
     if (ptid == 0) {
-      if (!ok) fail();
       (void)mbar_wait(bar(B_FIN), 0, nullptr, kWaitCycles);
       // after an abort, boxes still in flight land before the CTA can leave
       if (*abort_flag)
-        for (int h = 0; h < 2; ++h)
-          if (box_step[h] >= 0)
-            (void)mbar_wait(bar(B_KFULL + h), uint32_t(box_step[h] >> 1) & 1u, nullptr, kWaitCycles);
+        for (int i = 0; i < 2 * kGroups; ++i)
+          if (box_step[i / kGroups] >= 0)
+            (void)mbar_wait(bar(B_KFULL + i), uint32_t(box_step[i / kGroups] >> 1) & 1u, nullptr,
+                            kDrainCycles);
     }
   } else if (warp == kMmaWarp) {
     // ---- products.  The second product of a tile follows the first of the next
-    // one, so that the softmax of a tile runs under that; at a unit's end it
-    // goes first, as the next unit's queries are still to come.
+    // one, so that the softmax of a tile runs under that, unless the next tile
+    // has not landed yet, or needs another unit's queries.
     //
     // Queries: one box of 64 rows per unit, as soon as the last product that
     // reads the unit before is done (rows past the request's end are another's,
@@ -393,8 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kTile / 16; ++k)
           mma_ss_warp(tmem + kTmemO + uint32_t(64 * m), ad + uint64_t((uint32_t(k) * 2048u) >> 4),
                       bd + uint64_t((uint32_t(k) * 32u) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
+        // blocks 0-2, 3-5 and 6-8 are done with after value blocks 0-3, 4-5, 6-7
+        if (m > 0) mma_commit_warp(bar(B_KEMPTY + (s & 1) * kGroups + m - 1));
       }
-      mma_commit_warp(bar(B_KEMPTY + (s & 1)));
       mma_commit_warp(bar(B_PFREE));
       if (last) {
         mma_commit_warp(bar(B_OFULL));
@@ -411,13 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && w.left > 0) {
       const bool last = w.last_tile();
       const int n16 = (w.rows() + 15) & ~15;
-      if (first && pending) {
+      const int full = B_KFULL + (s & 1) * kGroups;
+      if (pending && (first || !__all_sync(0xffffffffu,
+                                           mbar_test(bar(full), uint32_t(s >> 1) & 1u)))) {
         ok = second(s - 1, pend_n, pend_first, pend_last);
         pending = false;
         if (!ok) break;
       }
-      bool got = wait(B_KFULL + (s & 1), uint32_t(s >> 1)) &&
-                 (s < 2 || wait(B_SEMPTY + (s & 1), uint32_t((s >> 1) - 1)));
+      bool got = s < 2 || wait(B_SEMPTY + (s & 1), uint32_t((s >> 1) - 1));
       if (first) {
         got = got && wait(B_QFULL, uint32_t(qload));
         ++qload;
@@ -426,10 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      fence_proxy_async_cta();   // the producers' copies, seen by the tensor core
-      tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kBlocks; ++c) {
+        if (c % 3 == 0) {
+          ok = ok && __all_sync(0xffffffffu, wait(full + c / 3, uint32_t(s >> 1)));
+          if (!ok) break;
+          fence_proxy_async_cta();   // the producers' copies, seen by the tensor core
+          tc_fence_after();
+        }
         const uint64_t ad = smem_desc(sb + kOffQ + uint32_t(c) * kSlot, 16, 1024, kSwizzle128B);
         const uint64_t bd = smem_desc(sb + kOffK + uint32_t(s & 1) * kTileBytes + uint32_t(c) * kSlot,
                                       16, 1024, kSwizzle128B);
@@ -438,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss_warp(tmem + kTmemS + uint32_t(64 * (s & 1)), ad + uint64_t(2 * kk),
                       bd + uint64_t(2 * kk), idesc_s, (c | kk) != 0 ? 1u : 0u);
       }
+      if (!ok) break;
       mma_commit_warp(bar(B_SFULL + (s & 1)));
       if (last) mma_commit_warp(bar(B_QEMPTY));
       if (pending && !second(s - 1, pend_n, pend_first, pend_last)) {
@@ -519,24 +538,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c)
               hidden_nonfinite |= (((held & ~v32) >> c) & 1u) && (sv[c] & 0x7f800000u) == 0x7f800000u;
           }
+          if (__all_sync(0xffffffffu, v32 == 0xffffffffu || !row_lane)) {   // nothing is hidden
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            x[c] = ((v32 >> c) & 1u) ? __uint_as_float(sv[c]) * p.scale_log2 : -INFINITY;
-            mth = fmaxf(mth, x[c]);
+            for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sv[c]) * p.scale_log2;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              x[c] = ((v32 >> c) & 1u) ? __uint_as_float(sv[c]) * p.scale_log2 : -INFINITY;
           }
+          float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int c = 4; c < 32; ++c) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
+          if (row_ok) mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         }
         if (row_lane) mx[half * kRows + r] = mth;
-        if (!named_sync_and(kSoftmaxBar, kSoftmax, wok)) {
-          if (tid == 0) fail();
-          ok = false;
-          break;
-        }
-        const float mt = fmaxf(mx[r], mx[kRows + r]);
+        // One barrier per tile: the halves' maxima are in place, and whether any
+        // row's reference moves (either half's maximum alone decides that).
+        const bool calm = wok && !(mth > m_ref + kRescaleLog2);
         float alpha = 1.f;
-        if (mt > m_ref + kRescaleLog2) {
-          alpha = ex2_approx(m_ref - mt);   // 0 when nothing was seen before
-          l *= alpha;
-          m_ref = mt;
+        if (!named_sync_and(kSoftmaxBar, kSoftmax, calm)) {
+          if (!named_sync_and(kSoftmaxBar, kSoftmax, wok)) {
+            if (tid == 0) fail();
+            ok = false;
+            break;
+          }
+          const float mt = fmaxf(mx[r], mx[kRows + r]);
+          if (row_lane && mt > m_ref + kRescaleLog2) {
+            alpha = ex2_approx(m_ref - mt);   // 0 when nothing was seen before
+            l *= alpha;
+            m_ref = mt;
+          }
+          if (half == 0 && row_lane) alpha_s[r] = alpha;
+          const bool pfree = s == 0 || wait(B_PFREE, uint32_t(s - 1));   // O is final
+          if (!named_sync_and(kSoftmaxBar, kSoftmax, __all_sync(0xffffffffu, pfree))) {
+            if (tid == 0) fail();
+            ok = false;
+            break;
+          }
+          if (!fresh) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {   // 32 rows (columns of O) of one of two blocks of values
+              const uint32_t at = lanes + kTmemO + uint32_t(64 * (2 * half + (c >> 1)) + 32 * (c & 1));
+              uint32_t v[32];
+              tmem_ld32(at, v);
+              tmem_wait_ld();
+              const float* a = alpha_s + 32 * (c & 1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a[e]);
+              tmem_st32(at, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
         }
         const float mr = m_ref == -INFINITY ? 0.f : m_ref;
         uint32_t pk[16];
@@ -549,33 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[c] = *reinterpret_cast<const uint32_t*>(&h);
         }
         l += lt;
-        // P's buffer is free, and O final, once the tile before has been
-        // multiplied; rows whose reference moved then rescale their columns of O
-        const bool pfree = s == 0 || wait(B_PFREE, uint32_t(s - 1));
-        if (half == 0 && row_lane) alpha_s[r] = alpha;
-        const bool keep = fresh || alpha == 1.f || !row_lane;
-        const bool pok = __all_sync(0xffffffffu, pfree);
-        if (!named_sync_and(kSoftmaxBar, kSoftmax, pok)) {
-          if (tid == 0) fail();
-          ok = false;
-          break;
-        }
-        if (!named_sync_and(kSoftmaxBar, kSoftmax, keep)) {
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {   // 32 rows (columns of O) of one of two blocks of values
-            const uint32_t at = lanes + kTmemO + uint32_t(64 * (2 * half + (c >> 1)) + 32 * (c & 1));
-            uint32_t v[32];
-            tmem_ld32(at, v);
-            tmem_wait_ld();
-            const float* a = alpha_s + 32 * (c & 1);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a[e]);
-            tmem_st32(at, v);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-        }
+        // P's buffer is free once the tile before has been multiplied (should
+        // this wait give up, the next tile's end the piece for everyone)
+        if (s > 0 && !wait(B_PFREE, uint32_t(s - 1))) fail();
         fresh = false;
         // this row's 32 keys (K-major, 128-byte swizzle)
         if (row_lane) {
@@ -657,10 +687,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-bool encode(CUtensorMap* m, const __nv_bfloat16* base, int64_t rows, int64_t stride) {
+// Rows of 576 features as column blocks of 64: a box of 64 rows x `blocks`.
+bool encode(CUtensorMap* m, const __nv_bfloat16* base, int64_t rows, int64_t stride, int blocks) {
   cuuint64_t dims[3] = {64u, cuuint64_t(rows), cuuint64_t(kBlocks)};
   cuuint64_t strides[2] = {cuuint64_t(stride) * 2u, 128u};
-  cuuint32_t box[3] = {64u, 64u, uint32_t(kBlocks)};
+  cuuint32_t box[3] = {64u, 64u, uint32_t(blocks)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(base), dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -679,8 +710,8 @@ cudaError_t launch_decode_tc(const ChunkTcParams& p, int ctas, cudaStream_t st) 
   CUtensorMap tk, tq;
   memset(&tk, 0, sizeof tk);
   memset(&tq, 0, sizeof tq);
-  if (!g_encode || !encode(&tq, p.q, int64_t(p.total_q) * p.H, kDqk)) return cudaErrorNotSupported;
-  if (p.kv_start && !encode(&tk, p.kv, p.num_slots, p.kv_stride)) return cudaErrorNotSupported;
+  if (!g_encode || !encode(&tq, p.q, int64_t(p.total_q) * p.H, kDqk, kBlocks)) return cudaErrorNotSupported;
+  if (p.kv_start && !encode(&tk, p.kv, p.num_slots, p.kv_stride, kBlocks / kGroups)) return cudaErrorNotSupported;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
