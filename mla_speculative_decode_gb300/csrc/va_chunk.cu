@@ -53,114 +53,152 @@ __global__ void __launch_bounds__(kRowThreads) chunk_fma_kernel(const ChunkParam
 
 // Merge of the splits (and the call's status word).  Split s of a row left its
 // normalised partial o_s and lse_s; with L = ln sum_s exp(lse_s) the row is
-// sum_s exp(lse_s - L) o_s, in a fixed order.  The batch's rows are dealt to the
-// CTAs in turn; a CTA looks at 256 units at a time, a thread each, for units in
-// more than one split (or flagged), and then takes its rows of those.  A thread
-// holds four columns of every other split.  Bound by the partials' bytes (2 KB
-// per row and split, from L2) and, with few rows, by three dependent loads.
+// sum_s exp(lse_s - L) o_s, in a fixed order.  A row is taken by one warp, or,
+// when there are too few rows to fill the SMs that way, by the kW = 8 warps of a
+// CTA, each with every eighth split; a lane holds 16 of the 512 columns.  Rows of
+// units in one split are final already and only passed over.  Bound by the
+// partials' bytes (2 KB per row and split, mostly from L2) and, with few rows, by
+// the latency of the unit's entry, the lse values and the partials.  (Rows dealt
+// out before looking whether their unit needs anything took 87 us for the 278k
+// rows of three prompts, all of them final.)
 constexpr int kFinishThreads = 256;
+constexpr int kFinishWarps = kFinishThreads / 32;
 constexpr int kMaxNs = 512;   // splits of a unit: at most the launch's target + 1
 
+template <int kW>
 __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const ChunkTcParams p) {
-  __shared__ float w[kMaxNs];
-  __shared__ float4 half[kDv / 4];
-  __shared__ int list[kFinishThreads];
-  __shared__ int s_count;
-  __shared__ uint32_t s_bits;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int G = gridDim.x;
+  static_assert(kW == 1 || kW == kFinishWarps, "a warp or a CTA per row");
+  __shared__ float weight[kFinishWarps][kMaxNs];
+  __shared__ ChunkUnit list[kFinishThreads];   // units to merge (b < 0: ~b, to compute again)
+  __shared__ int warp_count[kFinishWarps];
+  __shared__ float4 sums[kW == 1 ? 1 : kFinishWarps][kDv / 4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();                // the split kernel's results are complete
   griddep_launch_dependents();   // the next kernel may start its set-up
-  const int total_units = p.totals[0];
   const int U = p.sched.unit_rows;
-  for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    const int u = u0 + tid;
-    if (u < total_units) {
-      const ChunkUnit x = p.units[u];
-      uint32_t f = 0u;
-      for (int s = 0; s < x.ns; ++s)
-        for (int c = 0; c < p.ctas; ++c)
-          f |= p.cta_flags[size_t(x.item + s * x.istride) * p.ctas + c];
-      const bool redo = f & kFlagHiddenNonfinite;
-      // (the order of the list does not matter: a row is one CTA's alone)
-      if (x.ns > 1 || redo) list[atomicAdd(&s_count, 1)] = redo ? ~u : u;
-    }
-    __syncthreads();
-    const int count = s_count;
-    for (int k = 0; k < count; ++k) {
-      const bool redo = list[k] < 0;
-      const int v = redo ? ~list[k] : list[k];
-      const ChunkUnit x = p.units[v];
-      const int turn = int((int64_t(v) * U) % G);
-      for (int r = (blockIdx.x - turn + G) % G; r < x.rows; r += G) {
-        if (redo) {
-          if (tid < 32) {
-            const ChunkReq rq = chunk_req(p, x.b);
-            bool bad = false;
-            chunk_row(p, rq, (x.i0 + r) / p.H, (x.i0 + r) % p.H, lane, &bad);
-          }
-          continue;
-        }
-        auto slot = [&](int s) -> size_t {
-          return size_t(s == 0 ? x.pslot : x.pslot1 + (s - 1) * x.pstride);
-        };
-        const int ns = x.ns < kMaxNs ? x.ns : kMaxNs;
-        __syncthreads();   // w and half of the row before are read
-        if (tid < 32) {
-          float m = -INFINITY;
-          for (int s = lane; s < ns; s += 32) {
-            const float ls = p.part_lse[slot(s) * U + r];
-            w[s] = ls;
-            m = fmaxf(m, ls);
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          float z = 0.f;
-          for (int s = lane; s < ns; s += 32)
-            if (w[s] != -INFINITY) z += expf(w[s] - m);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          const float L = z == 0.f ? -INFINITY : m + logf(z);
-          for (int s = lane; s < ns; s += 32) w[s] = w[s] == -INFINITY ? 0.f : expf(w[s] - L);
-          if (lane == 0) p.lse[x.row0 + r] = L;
-        }
-        __syncthreads();
-        const int col = tid & 127, group = tid >> 7;
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + size_t(r) * kDv) + col;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int total_units = p.totals[0];
+  constexpr int kRowsPerCta = kFinishWarps / kW;
+  float* w = weight[warp];
+  // every CTA's status bits; which units a hidden key may have spoilt is looked
+  // up only when there is one
+  uint32_t bits = 0u;
+  {
+    const int n = p.totals[1] * p.ctas;
 #pragma unroll 4
-        for (int s = group; s < ns; s += 2) {
-          const float4 v4 = src[slot(s) * U * (kDv / 4)];
-          const float ws = w[s];
-          acc.x = fmaf(ws, v4.x, acc.x);
-          acc.y = fmaf(ws, v4.y, acc.y);
-          acc.z = fmaf(ws, v4.z, acc.z);
-          acc.w = fmaf(ws, v4.w, acc.w);
-        }
-        if (group) half[col] = acc;
-        __syncthreads();
-        if (!group) {
-          const float4 h = half[col];
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x + h.x, acc.y + h.y);
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z + h.z, acc.w + h.w);
-          uint2 o;
-          o.x = *reinterpret_cast<const uint32_t*>(&lo);
-          o.y = *reinterpret_cast<const uint32_t*>(&hi);
-          reinterpret_cast<uint2*>(p.out + size_t(x.row0 + r) * kDv)[col] = o;
-        }
+    for (int i = tid; i < n; i += kFinishThreads) bits |= p.cta_flags[i];
+  }
+  const bool hidden = __syncthreads_or((bits & kFlagHiddenNonfinite) != 0u);
+  for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
+  // which of 256 units need work: listed in the same order by every CTA
+  ChunkUnit unit;
+  unit.ns = 1;
+  uint32_t f = 0u;
+  if (u0 + tid < total_units) {
+    unit = p.units[u0 + tid];
+    if (hidden)
+      for (int s = 0; s < unit.ns; ++s)
+        for (int c = 0; c < p.ctas; ++c)
+          f |= p.cta_flags[size_t(unit.item + s * unit.istride) * p.ctas + c];
+    if (f & kFlagHiddenNonfinite) unit.b = ~unit.b;
+  }
+  const bool need = unit.ns > 1 || (f & kFlagHiddenNonfinite);
+  const uint32_t ballot = __ballot_sync(0xffffffffu, need);
+  if (lane == 0) warp_count[warp] = __popc(ballot);
+  __syncthreads();
+  int at = __popc(ballot & ((1u << lane) - 1u)), count = 0;
+#pragma unroll
+  for (int k = 0; k < kFinishWarps; ++k) {
+    at += k < warp ? warp_count[k] : 0;
+    count += warp_count[k];
+  }
+  if (need) list[at] = unit;
+  __syncthreads();
+  for (int id = int(blockIdx.x) * kRowsPerCta + (kW == 1 ? warp : 0); id < count * U;
+       id += int(gridDim.x) * kRowsPerCta) {
+    const ChunkUnit& x = list[id / U];
+    const int r = id % U;
+    if (r >= x.rows) continue;
+    if (x.b < 0) {   // a hidden key may have spoilt the unit's rows
+      if (kW == 1 || warp == 0) {
+        bool bad = false;
+        chunk_row(p, chunk_req(p, ~x.b), (x.i0 + r) / p.H, (x.i0 + r) % p.H, lane, &bad);
+      }
+      continue;
+    }
+    const int ns = x.ns < kMaxNs ? x.ns : kMaxNs;
+    auto slot = [&](int s) -> size_t {
+      return size_t(s == 0 ? x.pslot : x.pslot1 + (s - 1) * x.pstride) * U + r;
+    };
+    float m = -INFINITY;
+    for (int s = lane; s < ns; s += 32) {
+      const float ls = p.part_lse[slot(s)];
+      w[s] = ls;
+      m = fmaxf(m, ls);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float z = 0.f;
+    for (int s = lane; s < ns; s += 32)
+      if (w[s] != -INFINITY) z += expf(w[s] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const float L = z == 0.f ? -INFINITY : m + logf(z);
+    for (int s = lane; s < ns; s += 32) w[s] = w[s] == -INFINITY ? 0.f : expf(w[s] - L);
+    __syncwarp();
+    if (lane == 0 && (kW == 1 || warp == 0)) p.lse[x.row0 + r] = L;
+    // columns 4 * lane + 128 q .. + 3
+    float4 acc[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = kW == 1 ? 0 : warp; s < ns; s += kW) {
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(s) * kDv) + lane;
+      const float ws = w[s];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 v = src[32 * q];
+        acc[q].x = fmaf(ws, v.x, acc[q].x);
+        acc[q].y = fmaf(ws, v.y, acc[q].y);
+        acc[q].z = fmaf(ws, v.z, acc[q].z);
+        acc[q].w = fmaf(ws, v.w, acc[q].w);
       }
     }
-    __syncthreads();
+    __syncwarp();   // w is read
+    uint2* out = reinterpret_cast<uint2*>(p.out + size_t(x.row0 + r) * kDv);
+    auto pack = [](float4 v) -> uint2 {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    };
+    if constexpr (kW == 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) out[32 * q + lane] = pack(acc[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sums[warp][32 * q + lane] = acc[q];
+      __syncthreads();
+      if (tid < kDv / 4) {
+        float4 t = sums[0][tid];
+#pragma unroll
+        for (int k = 1; k < kW; ++k) {
+          const float4 v = sums[k][tid];
+          t.x += v.x;
+          t.y += v.y;
+          t.z += v.z;
+          t.w += v.w;
+        }
+        out[tid] = pack(t);
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();   // the list is read
   }
   // the status word: every CTA's bits, and requests whose bounds were clamped
   if (blockIdx.x == 0) {
+    __shared__ uint32_t s_bits;
     if (tid == 0) s_bits = 0u;
     __syncthreads();
-    uint32_t bits = 0u;
-    const int n = p.totals[1] * p.ctas;
-    for (int i = tid; i < n; i += kFinishThreads) bits |= p.cta_flags[i] & ~kFlagHiddenNonfinite;
+    bits &= ~kFlagHiddenNonfinite;
     for (int b = tid; b < p.B; b += kFinishThreads)
       if (chunk_req(p, b).bad) bits |= VA_STATUS_BAD_INDPTR;
     if (bits) atomicOr(&s_bits, bits);
@@ -214,20 +252,25 @@ ChunkPlan chunk_plan(int B, int total_q, int H, int flags) {
   return c;
 }
 
-cudaError_t launch_finish(const ChunkTcParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_finish(const ChunkTcParams& p, int units_bound, int num_sms, cudaStream_t st) {
+  const int64_t wave = int64_t(num_sms) * 8;   // CTAs
   const int64_t rows = int64_t(p.total_q) * p.H;
-  const int64_t wave = int64_t(num_sms) * 8;
+  // a CTA per row while one wave of CTAs covers the rows, else a warp per row
+  const bool cta_rows = rows <= wave;
+  const int64_t ids = int64_t(units_bound) * p.sched.unit_rows;   // rows, padded to units
+  const int64_t want = cta_rows ? ids : (ids + kFinishWarps - 1) / kFinishWarps;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(unsigned(rows < wave ? rows : wave), 1, 1);
+  cfg.gridDim = dim3(unsigned(want < wave ? want : wave), 1, 1);
   cfg.blockDim = dim3(kFinishThreads, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_finish_kernel, p);
+  return cta_rows ? cudaLaunchKernelEx(&cfg, chunk_finish_kernel<kFinishWarps>, p)
+                  : cudaLaunchKernelEx(&cfg, chunk_finish_kernel<1>, p);
 }
 
 }  // namespace
@@ -291,7 +334,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   if ((c.decode ? launch_decode_tc(t, t.sched.clusters, st)
                 : launch_chunk_tc(t, items, c.pair, st)) != cudaSuccess)
     return VA_ERR_LAUNCH;
-  return launch_finish(t, di.num_sms, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
+  return launch_finish(t, c.units_bound, di.num_sms, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -355,9 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             kDrainCycles);
     }
   } else if (warp == kMmaWarp) {
-    // ---- products.  The second product of a tile follows the first of the next
-    // one, so that the softmax of a tile runs under that, unless the next tile
-    // has not landed yet, or needs another unit's queries.
+    // ---- products.  The second product of a tile goes as soon as its P is there
+    // -- it is what frees the tile's shared memory -- and the first product of the
+    // next tile group by group as it lands, whichever comes first; at a unit's end
+    // the second goes first, as the next unit's queries are still to come.
     //
     // Queries: one box of 64 rows per unit, as soon as the last product that
     // reads the unit before is done (rows past the request's end are another's,
@@ -494,6 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* mx = reinterpret_cast<float*>(gb + kOffMx);
     float* alpha_s = reinterpret_cast<float*>(gb + kOffAlpha);
     volatile uint64_t* valid_ring = reinterpret_cast<volatile uint64_t*>(gb + kOffValid);
+    const bool raw_scores = p.scale_log2 > 0.f;
+    const float sc = raw_scores ? p.scale_log2 : 1.f;
     bool ok = true, hidden_nonfinite = false;
     int s = 0, piece = 0;
     while (w.left > 0 && ok) {
@@ -515,17 +518,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         more = !w.last_tile();
         ends = w.k + 1 == w.t.ntiles;
         w.next();
-        const bool got = wait(B_SFULL + (s & 1), uint32_t(s >> 1)) &&
-                         wait(B_VREADY + s % kValidRing, uint32_t(s / kValidRing));
-        const bool wok = __all_sync(0xffffffffu, got);
+        // which of this row's 32 keys it sees, while the scores are on their way
         uint64_t vis = ~0ull;
         if (tk0 + kTile > pos_a + 1 || (tk0 < first_z && tk0 + kTile > p.sinks))
           vis = low_bits(pos + 1 - tk0) & (~low_bits(first - tk0) | low_bits(p.sinks - tk0));
+        bool got = wait(B_VREADY + s % kValidRing, uint32_t(s / kValidRing));
+        const uint32_t held = got ? uint32_t(valid_ring[s % kValidRing] >> (32 * half)) : 0u;
+        const uint32_t v32 = row_ok ? uint32_t(vis >> (32 * half)) & held : 0u;
+        const bool all_seen = __all_sync(0xffffffffu, v32 == 0xffffffffu || !row_lane);
+        got = got && wait(B_SFULL + (s & 1), uint32_t(s >> 1));
+        const bool wok = __all_sync(0xffffffffu, got);
         float x[32];
         float mth = -INFINITY;
         if (wok) {
-          const uint32_t held = uint32_t(valid_ring[s % kValidRing] >> (32 * half));
-          const uint32_t v32 = row_ok ? uint32_t(vis >> (32 * half)) & held : 0u;
           tc_fence_after();
           uint32_t sv[32];
           tmem_ld32(lanes + kTmemS + uint32_t(64 * (s & 1) + 32 * half), sv);
@@ -538,18 +543,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c)
               hidden_nonfinite |= (((held & ~v32) >> c) & 1u) && (sv[c] & 0x7f800000u) == 0x7f800000u;
           }
-          if (__all_sync(0xffffffffu, v32 == 0xffffffffu || !row_lane)) {   // nothing is hidden
+          // With a positive scale (the usual case) the scores stay raw, their
+          // maximum is scaled, and each exponent is one multiply-add; otherwise
+          // they are scaled here.
+          if (all_seen && raw_scores) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sv[c]) * p.scale_log2;
+            for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sv[c]);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              x[c] = ((v32 >> c) & 1u) ? __uint_as_float(sv[c]) * p.scale_log2 : -INFINITY;
+              x[c] = ((v32 >> c) & 1u) ? __uint_as_float(sv[c]) * (raw_scores ? 1.f : p.scale_log2)
+                                       : -INFINITY;
           }
           float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
           for (int c = 4; c < 32; ++c) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
-          if (row_ok) mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          if (row_ok) mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
         }
         if (row_lane) mx[half * kRows + r] = mth;
         // One barrier per tile: the halves' maxima are in place, and whether any
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lt = 0.f;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float a = ex2_approx(x[2 * c] - mr), b = ex2_approx(x[2 * c + 1] - mr);
+          const float a = ex2_approx(fmaf(x[2 * c], sc, -mr)), b = ex2_approx(fmaf(x[2 * c + 1], sc, -mr));
           lt += a + b;
           const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
           pk[c] = *reinterpret_cast<const uint32_t*>(&h);
