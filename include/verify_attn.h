@@ -463,9 +463,14 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *   1 <= B <= 65535, 1 <= H, 0 <= total_q, total_q * H <= VA_CHUNK_ROWS_MAX.
  *   window, sinks  >= 0; host values, the same for every request.
  *   flags          VA_PATH_*.
- *   workspace      device, >= va_chunk_workspace_bytes(B, total_q, H, flags)
- *                  bytes, 256-byte aligned; first 4 bytes: the status word,
- *                  rewritten by every call.
+ *   num_entries    entries of slot_idx (lists that leave them are clamped; 0
+ *                  for the contiguous form's workspace).
+ *   workspace      device, >= va_chunk_workspace_bytes(B, total_q, H,
+ *                  num_entries, flags) bytes, 256-byte aligned; first 4 bytes:
+ *                  the status word, rewritten by every call.  It includes room
+ *                  for the listed rows (1152 bytes per entry) when the average
+ *                  request brings 1024 query rows (tokens x heads) or more: the
+ *                  call then first packs them side by side.
  *   out            bf16 [total_q, H, 512], 16-byte aligned; lse float
  *                  [total_q, H] (natural log).  A token none of whose keys has
  *                  a valid pool row gets out 0 and lse -inf.
@@ -477,12 +482,13 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  * infinities included, does not change that token's result.
  */
 #define VA_CHUNK_ROWS_MAX (1 << 24)
-size_t va_chunk_workspace_bytes(int B, int total_q, int H, int flags);
+size_t va_chunk_workspace_bytes(int B, int total_q, int H, int64_t num_entries, int flags);
 int va_chunk_attn_paged(const void *q, const void *kv_pool, int64_t num_slots,
                         int64_t kv_row_stride, const int32_t *slot_idx, const int32_t *kv_indptr,
-                        const int32_t *prefix_len, const int32_t *q_indptr, int B, int total_q,
-                        int H, float sm_scale, int window, int sinks, int flags, void *workspace,
-                        size_t workspace_bytes, void *out, float *lse, va_stream_t stream);
+                        const int32_t *prefix_len, const int32_t *q_indptr, int64_t num_entries,
+                        int B, int total_q, int H, float sm_scale, int window, int sinks,
+                        int flags, void *workspace, size_t workspace_bytes, void *out, float *lse,
+                        va_stream_t stream);
 int va_chunk_attn_contiguous(const void *q, const void *kv_pool, int64_t num_slots,
                              int64_t kv_row_stride, const int64_t *kv_start,
                              const int32_t *prefix_len, const int32_t *q_indptr, int B,

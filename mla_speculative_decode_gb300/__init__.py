@@ -92,10 +92,10 @@ def load() -> ctypes.CDLL:
     lib.va_kv_append_contiguous.restype = i32
     lib.va_kv_compact_accepted.argtypes = [P, i64, i64, P, P, P, P, P, i32, i32, P, P]
     lib.va_kv_compact_accepted.restype = i32
-    lib.va_chunk_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.va_chunk_workspace_bytes.argtypes = [i32, i32, i32, i64, i32]
     lib.va_chunk_workspace_bytes.restype = sz
-    lib.va_chunk_attn_paged.argtypes = [P, P, i64, i64, P, P, P, P, i32, i32, i32, f32, i32, i32,
-                                        i32, P, sz, P, P, P]
+    lib.va_chunk_attn_paged.argtypes = [P, P, i64, i64, P, P, P, P, i64, i32, i32, i32, f32, i32,
+                                        i32, i32, P, sz, P, P, P]
     lib.va_chunk_attn_paged.restype = i32
     lib.va_chunk_attn_contiguous.argtypes = [P, P, i64, i64, P, P, P, i32, i32, i32, f32, i32, i32,
                                              i32, P, sz, P, P, P]
@@ -648,13 +648,15 @@ def _prepare_chunk(name, q, kv_pool, keys, dims, prefix_len, q_indptr, sm_scale,
                    flags, workspace, out, lse, stream) -> BoundCall:
     B, total_q, H = dims
     init(q.device.index)
-    workspace = _workspace(workspace, load().va_chunk_workspace_bytes(B, total_q, H, flags),
+    n = keys[0].numel() if len(keys) == 2 else 0     # entries of a paged call's lists
+    workspace = _workspace(workspace, load().va_chunk_workspace_bytes(B, total_q, H, n, flags),
                            q.device, "va_chunk_workspace_bytes")
     out, lse = _outputs(total_q, H, q.device, out, lse)
     _same_device(q.device, out=out, lse=lse)
     args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), *(_ptr(k) for k in keys),
-            _ptr(prefix_len), _ptr(q_indptr), B, total_q, H, float(sm_scale), int(window),
-            int(sinks), int(flags), _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse))
+            _ptr(prefix_len), _ptr(q_indptr), *([n] if len(keys) == 2 else []), B, total_q, H,
+            float(sm_scale), int(window), int(sinks), int(flags), _ptr(workspace),
+            workspace.numel(), _ptr(out), _ptr(lse))
     return BoundCall(name, args, (out, lse),
                      (workspace, q, kv_pool, keys, prefix_len, q_indptr, out, lse),
                      q.device.index, stream)

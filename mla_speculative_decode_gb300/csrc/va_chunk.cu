@@ -212,21 +212,26 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
 // Clusters of the tensor-core kernel that a GB300's 152 SMs hold at most; the
 // workspace is sized for them, so that sizing it takes no device call.
 constexpr int kMaxSms = 152, kMaxPairs = 76, kMaxQuads = 38;
-// With many units, splits are cut so that about this many waves of clusters run.
-constexpr int kWaves = 3;
+// Paged rows are packed side by side first when the average request has at least
+// this many query rows (and the lists are not enormous): its units then read
+// their keys with TMA boxes (0.95 us a tile) instead of gathering them (1.45 us),
+// which pays for the copy (0.5 ns a key) from about three units of 256 rows on.
+constexpr int kPackRows = 1024;
+constexpr int64_t kPackEntriesMax = int64_t(1) << 21;
 
 struct ChunkPlan {
   bool decode;       // va_decode_tc.cu
   bool pair;
   int unit_rows, ctas, max_clusters;
   int units_bound;   // units the batch can have
-  bool one_wave;
-  size_t off_units, off_flags, off_lse, off_o, total;
+  int max_waves;     // waves of clusters in the grid
+  bool pack;
+  size_t off_units, off_flags, off_lse, off_o, off_pack, total;
 };
 
 // The decode kernel when the average request has at most 64 rows, two-SM
 // products of the split kernel when it has more than 128.
-ChunkPlan chunk_plan(int B, int total_q, int H, int flags) {
+ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) {
   ChunkPlan c;
   const int64_t rows = int64_t(total_q) * H;
   const int busy = B < total_q ? B : total_q;   // requests with tokens, at most
@@ -236,20 +241,86 @@ ChunkPlan chunk_plan(int B, int total_q, int H, int flags) {
   c.ctas = c.decode ? 1 : c.pair ? 4 : 2;
   c.max_clusters = c.decode ? kMaxSms : c.pair ? kMaxQuads : kMaxPairs;
   c.units_bound = int((rows + c.unit_rows - 1) / c.unit_rows) + busy;
-  c.one_wave = 2 * c.units_bound <= c.max_clusters;
-  // items: one wave's clusters, or target + one per unit; partial slots: items
-  // of requests in two or more splits, fewer than twice the target
-  const size_t target = size_t(kWaves) * c.max_clusters;
-  // (the decode kernel: an item and two slots per CTA)
-  const size_t items = c.decode || c.one_wave ? size_t(c.max_clusters) : target + c.units_bound;
-  const size_t slots = c.decode ? 2 * size_t(c.max_clusters)
-                       : c.one_wave ? size_t(c.max_clusters) : 2 * target;
+  // (fewer clusters than the most may be resident: the waves are counted for
+  // three quarters of them at least, see launch)
+  const int waves = (c.units_bound + c.max_clusters * 3 / 4 - 1) / (c.max_clusters * 3 / 4);
+  c.max_waves = waves > kSplitWaves ? waves : kSplitWaves;
+  // the decode kernel: an item and two slots per CTA
+  const size_t items = c.decode ? size_t(c.max_clusters) : size_t(c.max_waves) * c.max_clusters;
+  const size_t slots = size_t(c.decode ? 2 : kSplitWaves) * c.max_clusters;
+  c.pack = c.pair && rows >= kPackRows * int64_t(busy) && num_entries > 0 &&
+           num_entries <= kPackEntriesMax;
   c.off_units = kHeaderBytes;
   c.off_flags = c.off_units + align256(size_t(c.units_bound) * sizeof(ChunkUnit));
   c.off_lse = c.off_flags + align256(items * c.ctas * sizeof(uint32_t));
   c.off_o = c.off_lse + align256(slots * c.unit_rows * sizeof(float));
-  c.total = c.off_o + slots * c.unit_rows * kDv * sizeof(float);
+  c.off_pack = c.off_o + align256(slots * c.unit_rows * kDv * sizeof(float));
+  c.total = c.off_pack + (c.pack ? size_t(num_entries) * kDqk * sizeof(__nv_bfloat16) : 0);
   return c;
+}
+
+// Every listed row that some token sees, copied to its list position in `packed`
+// (zeros for a key without a row).  A warp takes 32 consecutive entries: a lane
+// finds the pool row of one, then the warp copies four rows at a time, all loads
+// before the stores.  Bound by HBM: 1152 B read and written per key.
+constexpr int kPackThreads = 256;
+
+__global__ void __launch_bounds__(kPackThreads) chunk_pack_kernel(const ChunkParams p) {
+  griddep_wait();                // the stream's previous kernel has completed
+  griddep_launch_dependents();   // the attention kernel may start its set-up
+  const int lane = threadIdx.x & 31;
+  const int64_t e0 = (int64_t(blockIdx.x) * kPackThreads + threadIdx.x) - lane;
+  const int64_t e = e0 + lane;
+  int64_t row = -2;   // -2: nobody sees it, -1: no row
+  if (e < p.num_entries) {
+    int lo = 0, hi = p.B;   // the last list that begins at or before e
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.kv_indptr[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    const ChunkReq r = chunk_req(p, lo);
+    const int64_t j = e - r.base;
+    if (r.n > 0 && j >= 0 && j < r.P + r.n && j < r.nlist &&
+        (j >= window_first(p.window, r.P) || j < p.sinks))
+      row = chunk_key_row(p, r, int(j));
+  }
+  uint4* dst = reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.packed) + e0 * kDqk);
+  constexpr int kChunks = kDqk / 8;   // 72 chunks of 16 bytes
+  for (int k = 0; k < 32; k += 4) {
+    uint4 v[4][3];
+    int64_t src[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      src[x] = __shfl_sync(0xffffffffu, row, k + x);
+      const uint4* s = reinterpret_cast<const uint4*>(p.kv + (src[x] > 0 ? src[x] : 0) * p.kv_stride);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) {
+        v[x][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (src[x] >= 0 && lane + 32 * c < kChunks) v[x][c] = s[lane + 32 * c];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
+        if (src[x] >= -1 && lane + 32 * c < kChunks)
+          dst[size_t(k + x) * kChunks + lane + 32 * c] = v[x][c];
+  }
+}
+
+cudaError_t launch_pack(const ChunkParams& p, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(unsigned((p.num_entries + kPackThreads - 1) / kPackThreads), 1, 1);
+  cfg.blockDim = dim3(kPackThreads, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_pack_kernel, p);
 }
 
 cudaError_t launch_finish(const ChunkTcParams& p, int units_bound, int num_sms, cudaStream_t st) {
@@ -298,11 +369,12 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   if (rc != VA_OK) return rc;
   if (p.total_q > 0 && !p.out) return VA_ERR_NULL;
   if (!aligned(p.out, 16)) return VA_ERR_ALIGN;
-  if (ws_bytes < va_chunk_workspace_bytes(p.B, p.total_q, p.H, flags)) return VA_ERR_WORKSPACE;
+  if (p.num_entries < 0 || p.num_entries > 0x7fffffff) return VA_ERR_SHAPE;
+  if (ws_bytes < va_chunk_workspace_bytes(p.B, p.total_q, p.H, p.num_entries, flags))
+    return VA_ERR_WORKSPACE;
   DeviceInfo di;
   const int rd = device_info(&di);
   if (rd != VA_OK) return rd;
-  p.num_entries = 0x7fffffff;
   p.scale_log2 = sm_scale * kLog2e;
   p.status = static_cast<uint32_t*>(ws);
   const int64_t rows = int64_t(p.total_q) * p.H;
@@ -314,7 +386,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
     chunk_fma_kernel<<<unsigned(want < wave ? want : wave), kRowThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
   }
-  const ChunkPlan c = chunk_plan(p.B, p.total_q, p.H, flags);
+  const ChunkPlan c = chunk_plan(p.B, p.total_q, p.H, p.num_entries, flags);
   uint8_t* w = static_cast<uint8_t*>(ws);
   ChunkTcParams t;
   memset(&t, 0, sizeof t);
@@ -322,15 +394,19 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   const int resident = c.decode ? di.num_sms : c.pair ? di.quads : di.pairs;
   t.sched.unit_rows = c.unit_rows;
   t.sched.clusters = resident < c.max_clusters ? resident : c.max_clusters;
-  t.sched.one_wave = c.one_wave ? 1 : 0;
-  t.sched.target = kWaves * t.sched.clusters;
+  if (!c.decode && t.sched.clusters < c.max_clusters * 3 / 4) return VA_ERR_UNSUPPORTED;
+  t.sched.max_waves = c.max_waves;
   t.ctas = c.ctas;
   t.totals = reinterpret_cast<int32_t*>(w) + 4;
   t.units = reinterpret_cast<ChunkUnit*>(w + c.off_units);
   t.cta_flags = reinterpret_cast<uint32_t*>(w + c.off_flags);
   t.part_lse = reinterpret_cast<float*>(w + c.off_lse);
   t.part_o = reinterpret_cast<float*>(w + c.off_o);
-  const int items = c.one_wave ? t.sched.clusters : t.sched.target + c.units_bound;
+  const int items = c.max_waves * t.sched.clusters;
+  if (c.pack) {
+    t.packed = reinterpret_cast<const __nv_bfloat16*>(w + c.off_pack);
+    if (launch_pack(t, st) != cudaSuccess) return VA_ERR_LAUNCH;
+  }
   if ((c.decode ? launch_decode_tc(t, t.sched.clusters, st)
                 : launch_chunk_tc(t, items, c.pair, st)) != cudaSuccess)
     return VA_ERR_LAUNCH;
@@ -340,20 +416,21 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
 }  // namespace
 }  // namespace va
 
-VA_API size_t va_chunk_workspace_bytes(int B, int total_q, int H, int flags) {
-  if (B < 1 || B > 65535 || total_q < 0 || H < 1 || flags < VA_PATH_AUTO ||
+VA_API size_t va_chunk_workspace_bytes(int B, int total_q, int H, int64_t num_entries,
+                                       int flags) {
+  if (num_entries < 0 || num_entries > 0x7fffffff || B < 1 || B > 65535 || total_q < 0 || H < 1 || flags < VA_PATH_AUTO ||
       flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX)
     return 0;
   if (total_q == 0 || flags == VA_PATH_FMA) return va::kHeaderBytes;
-  return va::chunk_plan(B, total_q, H, flags).total;
+  return va::chunk_plan(B, total_q, H, num_entries, flags).total;
 }
 
 VA_API int va_chunk_attn_paged(const void* q, const void* kv_pool, int64_t num_slots,
                                int64_t kv_row_stride, const int32_t* slot_idx,
                                const int32_t* kv_indptr, const int32_t* prefix_len,
-                               const int32_t* q_indptr, int B, int total_q, int H, float sm_scale,
-                               int window, int sinks, int flags, void* workspace,
-                               size_t workspace_bytes, void* out, float* lse,
+                               const int32_t* q_indptr, int64_t num_entries, int B, int total_q,
+                               int H, float sm_scale, int window, int sinks, int flags,
+                               void* workspace, size_t workspace_bytes, void* out, float* lse,
                                va_stream_t stream) {
   va::ChunkParams p;
   memset(&p, 0, sizeof p);
@@ -365,6 +442,7 @@ VA_API int va_chunk_attn_paged(const void* q, const void* kv_pool, int64_t num_s
   p.kv_indptr = kv_indptr;
   p.prefix_len = prefix_len;
   p.q_indptr = q_indptr;
+  p.num_entries = num_entries;
   p.B = B;
   p.total_q = total_q;
   p.H = H;

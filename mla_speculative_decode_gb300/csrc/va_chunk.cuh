@@ -9,9 +9,14 @@
 
 namespace va {
 
-// With many units a split takes at least this many tiles: a cluster's set-up,
-// fill and write-out cost about as much as ten tiles.
-constexpr int kMinSplitTiles = 8;
+// What a cluster of the split kernel costs besides its tiles (set-up, fill,
+// drain and write-out, about 11 us), in tiles; and the most waves of clusters that
+// units are split for.  (A batch that needs more waves than that for its units
+// alone is split only as far as its last wave has room.  So at most kSplitWaves
+// waves' items are parts of split units, or 2 waves' when the units alone need
+// more: that bounds the partials.)
+constexpr int kFixedTiles = 10;
+constexpr int kSplitWaves = 7;
 
 // Arguments of a chunk call (va_chunk_attn_*, va_kv_weights_paged), by value.
 // Request b's new tokens are query tokens q_indptr[b] .. q_indptr[b+1] - 1; its
@@ -22,6 +27,7 @@ struct ChunkParams {
   int64_t num_slots;
   int64_t kv_stride;           // elements
   const int32_t* slot_idx;     // paged
+  const __nv_bfloat16* packed; // paged, optional: [num_entries, 576] the listed rows side by side
   const int32_t* kv_indptr;    // paged: [B+1]
   const int64_t* kv_start;     // contiguous: [B] (NULL when paged)
   const int32_t* prefix_len;   // [B]
@@ -217,8 +223,7 @@ __device__ inline ChunkTiles chunk_tiles(const ChunkParams& p, const ChunkReq& r
 struct ChunkSched {
   int unit_rows;   // 128, or 256 with two-SM products
   int clusters;    // clusters resident at once
-  int one_wave;    // few units: at most `clusters` items, else about `target`
-  int target;
+  int max_waves;   // waves of clusters that the grid holds
 };
 
 struct ChunkItem {
@@ -246,12 +251,14 @@ __device__ inline void chunk_work(const ChunkParams& p, const ChunkSched& s, int
 }
 
 // Item `item` of the batch; a whole warp takes part, lane l looking at requests
-// l, l + 32, ...  With W = the sum of units x tiles, a split takes `chunk`
-// tiles: about W / target of them, or, when one wave of clusters is to hold
-// everything, the smallest such count (grown by eighths from W / clusters) whose
-// items fit.  A request with t tiles gets ns = ceil(t / chunk) splits; items run
-// split by split, and within a split from the last unit (the most keys) to the
-// first, so that units that read the same keys run together.
+// l, l + 32, ...  A split takes at most `chunk` tiles, so a request with t tiles
+// gets ns = ceil(t / chunk) splits and units * ns items.  For each number k of
+// waves of clusters that could hold the batch, the smallest chunk whose items fit
+// is found (grown by eighths from the average), and the k with the least
+// k * (chunk + kFixedTiles) is taken: k rounds of a split's tiles and of what a
+// cluster costs besides.  Items run split by split, and within a split from the
+// last unit (the most keys) to the first, so that units that read the same keys
+// run together.
 __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s, int item,
                                        int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
@@ -265,27 +272,40 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(kAll, work, o);
-  int chunk;
-  if (s.one_wave) {
-    chunk = int((work + s.clusters - 1) / s.clusters);
-    if (chunk < 1) chunk = 1;
-    // (one split per unit always fits: a launch in one wave has at most half
-    // as many units as clusters)
-    for (;;) {
-      int n = 0;
+  int all_units = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    int u = u0, t = t0;
+    if (b >= 32) chunk_work(p, s, b, &u, &t);
+    all_units += u;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all_units += __shfl_xor_sync(kAll, all_units, o);
+  // (one split per unit fits the grid whatever the lengths: its waves hold all
+  // units that the batch can have)
+  int chunk = 0x3fffffff;
+  int64_t best = INT64_MAX;
+  const int k0 = (all_units + s.clusters - 1) / s.clusters;
+  for (int k = k0 < 1 ? 1 : k0;
+       k <= s.max_waves && (k <= kSplitWaves || best == INT64_MAX); ++k) {
+    int64_t c = (work + int64_t(k) * s.clusters - 1) / (int64_t(k) * s.clusters);
+    if (c < 1) c = 1;
+    if (k * (c + kFixedTiles) >= best) continue;   // could not be better even if it fitted
+    for (int n = INT32_MAX; c < 0x3fffffff; c += c / 8 + 1) {
+      n = 0;
       for (int b = lane; b < p.B; b += 32) {
         int u = u0, t = t0;
         if (b >= 32) chunk_work(p, s, b, &u, &t);
-        n += u * ((t + chunk - 1) / chunk);
+        n += u * int((t + c - 1) / c);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
-      if (n <= s.clusters || chunk > (1 << 26)) break;
-      chunk += chunk / 8 + 1;
+      if (n <= k * s.clusters) break;
     }
-  } else {
-    const int64_t c = (work + s.target - 1) / s.target;
-    chunk = c < kMinSplitTiles ? kMinSplitTiles : int(c);
+    if (k * (c + kFixedTiles) < best) {
+      best = k * (c + kFixedTiles);
+      chunk = int(c);
+    }
+    if (c <= kFixedTiles) break;   // shorter splits only add to what clusters cost
   }
   ChunkItem it;
   it.live = false;

@@ -15,8 +15,8 @@ def lib():
 
 
 CHUNK = dict(q=A16, kv=A16, num_slots=4096, stride=576, slot=A16, indptr=A16, prefix=A16,
-             qind=A16, B=2, total_q=5, H=8, scale=0.07, window=0, sinks=0, flags=0, ws=A256,
-             ws_bytes=1 << 40, out=A16, lse=A16, stream=None)
+             qind=A16, n=1000, B=2, total_q=5, H=8, scale=0.07, window=0, sinks=0, flags=0,
+             ws=A256, ws_bytes=1 << 40, out=A16, lse=A16, stream=None)
 
 
 def _paged(lib, **over):
@@ -26,6 +26,7 @@ def _paged(lib, **over):
 def _contiguous(lib, **over):
     a = CHUNK | dict(slot=A16) | over
     a.pop("indptr")
+    a.pop("n")
     return lib.va_chunk_attn_contiguous(*a.values())
 
 
@@ -44,7 +45,8 @@ COMMON = [
 
 
 @pytest.mark.parametrize("over,code", COMMON + [(dict(indptr=None), -1),
-                                                (dict(indptr=A16 + 2), -3)])
+                                                (dict(indptr=A16 + 2), -3), (dict(n=-1), -2),
+                                                (dict(n=1 << 31), -2)])
 def test_paged_chunk_errors(lib, over, code):
     assert _paged(lib, **over) == code
 
@@ -64,12 +66,16 @@ def test_good_chunk_calls_end_at_the_device_check(lib):
 
 def test_chunk_workspace_bytes(lib):
     f = lib.va_chunk_workspace_bytes
-    for bad in ((0, 1, 1, 0), (65536, 1, 1, 0), (1, -1, 1, 0), (1, 1, 0, 0), (1, 1 << 24, 2, 0),
-                (1, 1, 1, 4), (1, 1, 1, -1)):
+    for bad in ((0, 1, 1, 0, 0), (65536, 1, 1, 0, 0), (1, -1, 1, 0, 0), (1, 1, 0, 0, 0),
+                (1, 1 << 24, 2, 0, 0), (1, 1, 1, 0, 4), (1, 1, 1, 0, -1), (1, 1, 1, -1, 0),
+                (1, 1, 1, 1 << 31, 0)):
         assert f(*bad) == 0
     for B, total_q, H in ((1, 0, 1), (1, 1, 1), (8, 4096, 64), (65535, 1, 1), (1, 1 << 17, 128)):
         for flags in range(4):
-            assert 256 <= f(B, total_q, H, flags) < 1 << 32
+            assert 256 <= f(B, total_q, H, 0, flags) < 1 << 32
+    # many rows per request: the listed rows are packed first
+    assert f(1, 512, 64, 20000, 0) - f(1, 512, 64, 0, 0) == 20000 * 1152
+    assert f(1, 15, 64, 20000, 0) == f(1, 15, 64, 0, 0)
 
 
 WEIGHTS = dict(q=A16, kv=A16, num_slots=4096, stride=576, slot=A16, indptr=A16, prefix=A16,

@@ -246,3 +246,61 @@ def test_refusals(va):
     with pytest.raises(va.VaError) as e:
         va.chunk_attn_paged(*a, **ok, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.code == -4
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5), (33, 70)])
+def test_many_rows_per_request_read_packed_lists(va, window, sinks):
+    """1024 query rows and more per request: the call packs the listed rows
+    first (invisible ones not at all, ones without a row as zeros that count for
+    nothing)."""
+    c = _chunk.make([400, 0, 130], [40, 33, 1], 64, seed=40 + window, stride=584, list_gap=3,
+                    q_before=1, q_behind=2)
+    for b, j in ((0, 7), (0, 410), (1, 2), (2, 0)):
+        c.slot_idx[int(c.kv_indptr[b]) + j] = -1 if j % 2 else c.pool.shape[0] + j
+        c.key_rows[b][j] = -1
+    call = _chunk.call(va, c, window=window, sinks=sinks, prepare=True)
+    assert call.workspace.numel() > va.load().va_chunk_workspace_bytes(3, c.q.shape[0], 64, 0, 0)
+    out, lse = call()
+    _chunk.check(c, out, lse, window=window, sinks=sinks)
+    own = slice(1, -2)                   # rows no request owns hold whatever they held
+    first = out[own].clone()
+    assert va.read_status(call.workspace) == va.STATUS_BAD_SLOT
+    call()
+    assert torch.equal(out[own], first)
+
+
+def test_packed_lists_with_nan_where_nothing_may_look(va):
+    P, n, H = [300], [60], 32
+    c = _chunk.make(P, n, H, seed=50)
+    for j in (305, 340, 359, 100, 3):
+        c.pool[int(c.key_rows[0][j])] = float("nan")
+    for window, sinks in ((0, 0), (90, 2), (150, 8)):
+        out, lse = _chunk.call(va, c, window=window, sinks=sinks)
+        ref = _chunk.reference(c, window=window, sinks=sinks)
+        fin = np.isfinite(ref[1])
+        np.testing.assert_array_equal(np.isfinite(lse.cpu().numpy()), fin)
+        np.testing.assert_array_equal(np.isfinite(out.float().cpu().numpy()).all(-1), fin)
+        spread = _chunk.reference(_chunk.make(P, n, H, seed=50), window=window, sinks=sinks)[3]
+        err = np.abs(out.float().cpu().numpy() - ref[0])[fin]
+        assert np.all(err <= _chunk.out_bound(ref[0], ref[2], spread, 400)[fin])
+
+
+@pytest.mark.parametrize("P,n,H", [([2000], [64], 16), ([5000, 0], [40, 3], 64),
+                                   ([0], [700], 8), ([9000], [1], 128), ([64] * 40, [2] * 40, 8),
+                                   ([700] * 70, [3] * 70, 64)])
+@pytest.mark.parametrize("layout", ["paged", "contiguous"])
+def test_longer_batches(va, P, n, H, layout):
+    """More units, splits and waves than the small cases have; rows sampled."""
+    c = _chunk.make(P, n, H, seed=60, layout=layout)
+    out, lse = _chunk.call(va, c)
+    fma_out, fma_lse = _chunk.call(va, c, flags=1)     # the CUDA-core path, on every row
+    assert float((lse - fma_lse).abs().max()) < 1e-4
+    d = (out.float() - fma_out.float()).abs()
+    assert float((d - 2 * 2.0 ** -8 * fma_out.float().abs()).max()) < 2e-2
+    for b in sorted({0, len(P) - 1}):                  # and against the oracle, whole requests
+        t = slice(int(c.q_indptr[b]), min(int(c.q_indptr[b + 1]), int(c.q_indptr[b]) + 4))
+        sub = _chunk.Chunk(P=[P[b]], n=[t.stop - t.start], H=H, q=c.q[t], pool=c.pool,
+                           key_rows=[c.key_rows[b]], slot_idx=c.slot_idx, kv_indptr=c.kv_indptr,
+                           prefix_len=c.prefix_len,
+                           q_indptr=torch.tensor([0, t.stop - t.start], dtype=torch.int32))
+        _chunk.check(sub, out[t], lse[t])
