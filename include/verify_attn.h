@@ -460,7 +460,8 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *   total_q        query tokens in q, out and lse.  Rows that no request owns
  *                  (before q_indptr[0], behind q_indptr[B]) are left as they
  *                  were, so a captured call can serve smaller batches.
- *   1 <= B <= 65535, 1 <= H, 0 <= total_q, total_q * H <= VA_CHUNK_ROWS_MAX.
+ *   1 <= B <= 65535, 1 <= H, 0 <= total_q, total_q * H <= VA_CHUNK_ROWS_MAX,
+ *   num_slots <= 0x7fffff00.
  *   window, sinks  >= 0; host values, the same for every request.
  *   flags          VA_PATH_*.
  *   num_entries    entries of slot_idx (lists that leave them are clamped; 0

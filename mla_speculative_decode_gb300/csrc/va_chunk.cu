@@ -10,8 +10,8 @@
 // running maximum and sum.
 //
 // Two paths: the tensor cores -- a kernel for few rows per request
-// (va_decode_tc.cu) or that of the verify calls in its chunk mode (va_tc.cu) --
-// followed by chunk_finish_kernel, which merges the splits; and one
+// (va_decode_tc.cu), one for many (va_prefill_tc.cu), and between them that of the
+// verify calls in its chunk mode (va_tc.cu) -- followed by chunk_finish_kernel, which merges the splits; and one
 // warp per row on CUDA cores (VA_PATH_FMA), an independent implementation that
 // the finish kernel also uses for the rare rows that the products may have
 // spoilt (see kFlagHiddenNonfinite).
@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
     const int n = p.totals[1] * p.ctas;
 #pragma unroll 4
     for (int i = tid; i < n; i += kFinishThreads) bits |= p.cta_flags[i];
+    if (blockIdx.x == 0)
+      for (int i = tid; i < p.pack_blocks; i += kFinishThreads) bits |= p.pack_flags[i];
   }
   const bool hidden = __syncthreads_or((bits & kFlagHiddenNonfinite) != 0u);
   for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
@@ -212,27 +214,31 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
 // Clusters of the tensor-core kernel that a GB300's 152 SMs hold at most; the
 // workspace is sized for them, so that sizing it takes no device call.
 constexpr int kMaxSms = 152, kMaxPairs = 76, kMaxQuads = 38;
-// Paged rows are packed side by side first when the average request has at least
-// this many query rows (and the lists are not enormous): its units then read
-// their keys with TMA boxes (0.95 us a tile) instead of gathering them (1.45 us),
-// which pays for the copy (0.5 ns a key) from about three units of 256 rows on.
-constexpr int kPackRows = 1024;
+// The prefill kernel (va_prefill_tc.cu) from this many query rows per request, on
+// the average, on: paged rows are packed side by side for it (0.5 ns a key), which
+// pays when they are read by about three units of 256 rows instead of gathered by
+// them (a tile costs 0.95 us with boxes, 1.45 us gathered).  Enormous lists, whose
+// copy would, are left to the split kernel.
+constexpr int kPrefillRows = 1024;
 constexpr int64_t kPackEntriesMax = int64_t(1) << 21;
 
 struct ChunkPlan {
   bool decode;       // va_decode_tc.cu
+  bool prefill;      // va_prefill_tc.cu
   bool pair;
   int unit_rows, ctas, max_clusters;
   int units_bound;   // units the batch can have
   int max_waves;     // waves of clusters in the grid
-  bool pack;
-  size_t off_units, off_flags, off_lse, off_o, off_pack, total;
+  int pack_blocks;
+  size_t off_units, off_flags, off_lse, off_o, off_pack_flags, off_valid, off_tails, off_pack, total;
 };
 
-// The decode kernel when the average request has at most 64 rows, two-SM
-// products of the split kernel when it has more than 128.
+// The decode kernel when the average request has at most 64 rows, the prefill
+// kernel when it has at least kPrefillRows; between them the split kernel, with
+// two-SM products when it has more than 128.
 ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) {
   ChunkPlan c;
+  memset(&c, 0, sizeof c);
   const int64_t rows = int64_t(total_q) * H;
   const int busy = B < total_q ? B : total_q;   // requests with tokens, at most
   c.decode = flags != VA_PATH_TC_1SM && rows <= 64 * int64_t(busy);
@@ -245,49 +251,45 @@ ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) 
   // three quarters of them at least, see launch)
   const int waves = (c.units_bound + c.max_clusters * 3 / 4 - 1) / (c.max_clusters * 3 / 4);
   c.max_waves = waves > kSplitWaves ? waves : kSplitWaves;
-  // the decode kernel: an item and two slots per CTA
-  const size_t items = c.decode ? size_t(c.max_clusters) : size_t(c.max_waves) * c.max_clusters;
-  const size_t slots = size_t(c.decode ? 2 : kSplitWaves) * c.max_clusters;
-  c.pack = c.pair && rows >= kPackRows * int64_t(busy) && num_entries > 0 &&
-           num_entries <= kPackEntriesMax;
+  c.prefill = c.pair && rows >= kPrefillRows * int64_t(busy) && num_entries <= kPackEntriesMax;
+  // the decode and prefill kernels: an item and two slots per CTA or cluster
+  const bool even = c.decode || c.prefill;
+  const size_t items = even ? size_t(c.max_clusters) : size_t(c.max_waves) * c.max_clusters;
+  const size_t slots = size_t(even ? 2 : kSplitWaves) * c.max_clusters;
   c.off_units = kHeaderBytes;
   c.off_flags = c.off_units + align256(size_t(c.units_bound) * sizeof(ChunkUnit));
   c.off_lse = c.off_flags + align256(items * c.ctas * sizeof(uint32_t));
   c.off_o = c.off_lse + align256(slots * c.unit_rows * sizeof(float));
-  c.off_pack = c.off_o + align256(slots * c.unit_rows * kDv * sizeof(float));
-  c.total = c.off_pack + (c.pack ? size_t(num_entries) * kDqk * sizeof(__nv_bfloat16) : 0);
+  c.off_pack_flags = c.off_o + align256(slots * c.unit_rows * kDv * sizeof(float));
+  c.total = c.off_pack_flags;
+  if (c.prefill) {
+    constexpr size_t kRowBytes = kDqk * sizeof(__nv_bfloat16);
+    c.pack_blocks = int((num_entries + 255) / 256);
+    // (entries rounded up to whole blocks; two words more for the last tile's bits)
+    c.off_valid = c.off_pack_flags + align256(size_t(c.pack_blocks) * sizeof(uint32_t));
+    c.off_tails = c.off_valid + align256((size_t(c.pack_blocks) * 8 + 4) * sizeof(uint32_t));
+    c.off_pack = c.off_tails + align256(size_t(B) * 64 * kRowBytes);
+    c.total = c.off_pack + size_t(num_entries) * kRowBytes;
+  }
   return c;
 }
 
-// Every listed row that some token sees, copied to its list position in `packed`
-// (zeros for a key without a row).  A warp takes 32 consecutive entries: a lane
-// finds the pool row of one, then the warp copies four rows at a time, all loads
-// before the stores.  Bound by HBM: 1152 B read and written per key.
+// What va_prefill_tc.cu reads, laid out for its boxes.  The first `pack_blocks`
+// blocks (paged calls): every listed row that lies in a tile some token sees, at
+// its list position in `packed` (zeros for a key without a row), and a bit per
+// entry that has one.  Then a block per request: its last tile, when that is not
+// whole, with zeros behind the request's last key.  A warp takes 32 entries (or 8
+// rows of a tail): a lane finds the pool row of one, then the warp copies four rows
+// at a time, all loads before the stores.  Bound by HBM: 1152 B read and written
+// per key.
 constexpr int kPackThreads = 256;
 
-__global__ void __launch_bounds__(kPackThreads) chunk_pack_kernel(const ChunkParams p) {
-  griddep_wait();                // the stream's previous kernel has completed
-  griddep_launch_dependents();   // the attention kernel may start its set-up
-  const int lane = threadIdx.x & 31;
-  const int64_t e0 = (int64_t(blockIdx.x) * kPackThreads + threadIdx.x) - lane;
-  const int64_t e = e0 + lane;
-  int64_t row = -2;   // -2: nobody sees it, -1: no row
-  if (e < p.num_entries) {
-    int lo = 0, hi = p.B;   // the last list that begins at or before e
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.kv_indptr[mid] <= e) lo = mid;
-      else hi = mid;
-    }
-    const ChunkReq r = chunk_req(p, lo);
-    const int64_t j = e - r.base;
-    if (r.n > 0 && j >= 0 && j < r.P + r.n && j < r.nlist &&
-        (j >= window_first(p.window, r.P) || j < p.sinks))
-      row = chunk_key_row(p, r, int(j));
-  }
-  uint4* dst = reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.packed) + e0 * kDqk);
+// Rows k .. k + 3 of the warp's: lane x holds row x's pool row (-1: zeros, -2: no
+// copy); row x goes to dst + x rows.
+__device__ __forceinline__ void copy_rows(const ChunkParams& p, int64_t row, int count, uint4* dst,
+                                          int lane) {
   constexpr int kChunks = kDqk / 8;   // 72 chunks of 16 bytes
-  for (int k = 0; k < 32; k += 4) {
+  for (int k = 0; k < count; k += 4) {
     uint4 v[4][3];
     int64_t src[4];
 #pragma unroll
@@ -309,13 +311,56 @@ __global__ void __launch_bounds__(kPackThreads) chunk_pack_kernel(const ChunkPar
   }
 }
 
-cudaError_t launch_pack(const ChunkParams& p, cudaStream_t st) {
+__global__ void __launch_bounds__(kPackThreads) chunk_pack_kernel(const ChunkTcParams p) {
+  griddep_wait();                // the stream's previous kernel has completed
+  griddep_launch_dependents();   // the attention kernel may start its set-up
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (int(blockIdx.x) >= p.pack_blocks) {
+    const int b = int(blockIdx.x) - p.pack_blocks;
+    const ChunkReq r = chunk_req(p, b);
+    const int N = r.nlist < r.P + r.n ? r.nlist : r.P + r.n;
+    if (N % 64 == 0 || r.n == 0) return;
+    const int i0 = 8 * warp, j = N / 64 * 64 + i0 + lane;
+    const int64_t row = lane < 8 && j < N ? chunk_key_row(p, r, j) : -1;
+    copy_rows(p, row, 8,
+              reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.tails) +
+                                       (size_t(b) * 64 + i0) * kDqk), lane);
+    return;
+  }
+  const int64_t e = int64_t(blockIdx.x) * kPackThreads + tid, e0 = e - lane;
+  int64_t row = -2;
+  bool bad = false;
+  if (e < p.num_entries) {
+    int lo = 0, hi = p.B;   // the last list that begins at or before e
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.kv_indptr[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    const ChunkReq r = chunk_req(p, lo);
+    const int64_t j = e - r.base;
+    const int first = window_first(p.window, r.P);
+    if (r.n > 0 && j >= 0 && j < r.P + r.n && j < r.nlist &&
+        (j >= (first & ~63) || j < (int64_t(p.sinks) + 63) / 64 * 64)) {
+      row = chunk_key_row(p, r, int(j));
+      bad = row < 0 && (j >= first || j < p.sinks);
+    }
+  }
+  const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+  if (lane == 0) const_cast<uint32_t*>(p.valid)[e0 >> 5] = have;
+  const bool any_bad = __syncthreads_or(bad);
+  if (tid == 0) p.pack_flags[blockIdx.x] = any_bad ? VA_STATUS_BAD_SLOT : 0u;
+  copy_rows(p, row, 32, reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.packed) + e0 * kDqk),
+            lane);
+}
+
+cudaError_t launch_pack(const ChunkTcParams& p, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(unsigned((p.num_entries + kPackThreads - 1) / kPackThreads), 1, 1);
+  cfg.gridDim = dim3(unsigned(p.pack_blocks + p.B), 1, 1);
   cfg.blockDim = dim3(kPackThreads, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
@@ -370,6 +415,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   if (p.total_q > 0 && !p.out) return VA_ERR_NULL;
   if (!aligned(p.out, 16)) return VA_ERR_ALIGN;
   if (p.num_entries < 0 || p.num_entries > 0x7fffffff) return VA_ERR_SHAPE;
+  if (p.num_slots > 0x7fffff00) return VA_ERR_SHAPE;   // rows are named by 32-bit coordinates
   if (ws_bytes < va_chunk_workspace_bytes(p.B, p.total_q, p.H, p.num_entries, flags))
     return VA_ERR_WORKSPACE;
   DeviceInfo di;
@@ -378,7 +424,8 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   p.scale_log2 = sm_scale * kLog2e;
   p.status = static_cast<uint32_t*>(ws);
   const int64_t rows = int64_t(p.total_q) * p.H;
-  if (flags == VA_PATH_FMA || rows == 0) {
+  // (no entries at all: no keys, and nothing to lay out for the tensor cores)
+  if (flags == VA_PATH_FMA || rows == 0 || (!p.kv_start && p.num_entries == 0)) {
     if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return VA_ERR_LAUNCH;
     if (rows == 0) return VA_OK;
     const int64_t want = (rows + kRowThreads / 32 - 1) / (kRowThreads / 32);
@@ -395,21 +442,32 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   t.sched.unit_rows = c.unit_rows;
   t.sched.clusters = resident < c.max_clusters ? resident : c.max_clusters;
   if (!c.decode && t.sched.clusters < c.max_clusters * 3 / 4) return VA_ERR_UNSUPPORTED;
-  t.sched.max_waves = c.max_waves;
   t.ctas = c.ctas;
   t.totals = reinterpret_cast<int32_t*>(w) + 4;
   t.units = reinterpret_cast<ChunkUnit*>(w + c.off_units);
   t.cta_flags = reinterpret_cast<uint32_t*>(w + c.off_flags);
   t.part_lse = reinterpret_cast<float*>(w + c.off_lse);
   t.part_o = reinterpret_cast<float*>(w + c.off_o);
-  const int items = c.max_waves * t.sched.clusters;
-  if (c.pack) {
-    t.packed = reinterpret_cast<const __nv_bfloat16*>(w + c.off_pack);
+  cudaError_t e;
+  if (c.prefill) {
+    t.tails = reinterpret_cast<const __nv_bfloat16*>(w + c.off_tails);
+    if (!p.kv_start) {
+      t.packed = reinterpret_cast<const __nv_bfloat16*>(w + c.off_pack);
+      t.valid = reinterpret_cast<const uint32_t*>(w + c.off_valid);
+      t.pack_flags = reinterpret_cast<uint32_t*>(w + c.off_pack_flags);
+      t.pack_blocks = c.pack_blocks;
+    }
     if (launch_pack(t, st) != cudaSuccess) return VA_ERR_LAUNCH;
+    e = launch_prefill_tc(t, t.sched.clusters, st);
+  } else if (c.decode) {
+    e = launch_decode_tc(t, t.sched.clusters, st);
+  } else {
+    // (at most max_waves * max_clusters items, which the workspace is sized for)
+    const int waves = (c.units_bound + t.sched.clusters - 1) / t.sched.clusters;
+    t.sched.max_waves = waves > kSplitWaves ? waves : kSplitWaves;
+    e = launch_chunk_tc(t, t.sched.max_waves * t.sched.clusters, c.pair, st);
   }
-  if ((c.decode ? launch_decode_tc(t, t.sched.clusters, st)
-                : launch_chunk_tc(t, items, c.pair, st)) != cudaSuccess)
-    return VA_ERR_LAUNCH;
+  if (e != cudaSuccess) return VA_ERR_LAUNCH;
   return launch_finish(t, c.units_bound, di.num_sms, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }
 

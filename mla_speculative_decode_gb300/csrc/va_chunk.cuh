@@ -27,7 +27,6 @@ struct ChunkParams {
   int64_t num_slots;
   int64_t kv_stride;           // elements
   const int32_t* slot_idx;     // paged
-  const __nv_bfloat16* packed; // paged, optional: [num_entries, 576] the listed rows side by side
   const int32_t* kv_indptr;    // paged: [B+1]
   const int64_t* kv_start;     // contiguous: [B] (NULL when paged)
   const int32_t* prefix_len;   // [B]
@@ -204,6 +203,11 @@ struct ChunkTiles {
   }
 };
 
+// The n lowest bits of a 64-bit mask (any n).
+__device__ __forceinline__ uint64_t low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 // All tiles of rows [row0, row0 + rows) of a request (rows >= 1).
 __device__ inline ChunkTiles chunk_tiles(const ChunkParams& p, const ChunkReq& r, int row0,
                                          int rows) {
@@ -352,6 +356,177 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
   return it;
 }
 
+// A place in the row of steps: the tiles of all units (kRows query rows each) of
+// the batch, request by request, unit by unit.  A launch cuts the row into equal
+// runs, one for each of its CTAs or clusters; every role of those walks its run
+// with one of these, so that they agree without talking.
+template <int kRows>
+struct ChunkRun {
+  const ChunkParams& p;
+  ChunkReq r;
+  ChunkTiles t;        // all tiles of the unit
+  int b, unit, units, unit0;   // request, unit within it, its units, units before it
+  int k;               // tile within the unit
+  int64_t left;        // steps left, this one included
+  int64_t g, total;    // index of this step in the batch; steps of the batch
+  int runs;            // CTAs that have a run
+
+  __device__ explicit ChunkRun(const ChunkParams& p_) : p(p_) {}
+  __device__ int rows() const {
+    const int n = r.n * p.H - unit * kRows;
+    return n < kRows ? n : kRows;
+  }
+  __device__ void load(int b_) {
+    b = b_;
+    r = chunk_req(p, b);
+    units = (r.n * p.H + kRows - 1) / kRows;
+    unit = 0;
+  }
+  __device__ void tiles() { t = chunk_tiles(p, r, unit * kRows, rows()); }
+  __device__ int key() const { return t.tile_key(k); }
+  __device__ bool last_tile() const { return k + 1 == t.ntiles || left == 1; }
+  // The next step (only while left > 1).
+  __device__ void next() {
+    ++g;
+    if (--left <= 0) return;
+    if (++k < t.ntiles) return;
+    k = 0;
+    if (++unit >= units) {
+      unit0 += units;
+      do load(b + 1);
+      while (units == 0 && b + 1 < p.B);
+    }
+    tiles();
+  }
+  // The steps of this unit that lie in the run from here on, and the step after
+  // them.
+  __device__ int piece() const { return int(t.ntiles - k < left ? t.ntiles - k : left); }
+  __device__ void next_piece() {
+    const int n = piece() - 1;
+    k += n;
+    g += n;
+    left -= n;
+    next();
+  }
+  // First step of run c, and the run that step x is in.
+  __device__ int64_t begin(int c) const { return total * c / runs; }
+  __device__ int owner(int64_t x) const {
+    int c = int(x * runs / total);
+    while (c + 1 < runs && begin(c + 1) <= x) ++c;
+    while (c > 0 && begin(c) > x) --c;
+    return c;
+  }
+};
+
+// Steps and units of requests b0 + lane: a lane counts a request of at most two
+// units by itself, the warp together one of more.
+template <int kRows>
+__device__ int64_t count_steps(ChunkRun<kRows>& w, int b0, int lane, int* units) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  int64_t mine = 0;
+  *units = 0;
+  if (b0 + lane < w.p.B) {
+    w.load(b0 + lane);
+    *units = w.units;
+    if (w.units <= 2)
+      for (; w.unit < w.units; ++w.unit) {
+        w.tiles();
+        mine += w.t.ntiles;
+      }
+  }
+  for (uint32_t many = __ballot_sync(kAll, *units > 2); many; many &= many - 1) {
+    const int src = __ffs(int(many)) - 1;
+    w.load(b0 + src);
+    int64_t n = 0;
+    for (w.unit = lane; w.unit < w.units; w.unit += 32) {
+      w.tiles();
+      n += w.t.ntiles;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+    if (lane == src) mine = n;
+  }
+  return mine;
+}
+
+// Run c's place and length (left = 0: none), of at most `grid` runs; returns the
+// batch's units in total.  A whole warp takes part.
+template <int kRows>
+__device__ int find_run(ChunkRun<kRows>& w, int c, int grid, int lane) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  int64_t total = 0, s0 = 0;
+  int all_units = 0, n0 = 0;
+  for (int b0 = 0; b0 < w.p.B; b0 += 32) {
+    int n;
+    const int64_t s = count_steps(w, b0, lane, &n);
+    if (b0 == 0) { s0 = s; n0 = n; }
+    total += s;
+    all_units += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(kAll, total, o);
+    all_units += __shfl_xor_sync(kAll, all_units, o);
+  }
+  w.total = total;
+  w.runs = total < grid ? int(total) : grid;
+  w.left = 0;
+  if (c >= w.runs) return all_units;
+  w.g = w.begin(c);
+  w.left = w.begin(c + 1) - w.g;
+  int64_t before = 0;
+  int units = 0;
+  for (int b0 = 0; b0 < w.p.B; b0 += 32) {
+    int64_t s = s0;
+    int n = n0;
+    if (b0 > 0) s = count_steps(w, b0, lane, &n);
+    int64_t sum = s;
+    int nsum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(kAll, sum, o);
+      const int y = __shfl_up_sync(kAll, nsum, o);
+      if (lane >= o) { sum += x; nsum += y; }
+    }
+    const uint32_t mine = __ballot_sync(kAll, w.g >= before + sum - s && w.g < before + sum);
+    if (mine) {
+      const int src = __ffs(int(mine)) - 1;
+      int64_t at = w.g - before - __shfl_sync(kAll, sum - s, src);   // steps into the request
+      w.unit0 = units + __shfl_sync(kAll, nsum - n, src);
+      w.load(b0 + src);
+      for (int u0 = 0;; u0 += 32) {   // 32 units at a time
+        int64_t t = 0;
+        w.unit = u0 + lane;
+        if (w.unit < w.units) {
+          w.tiles();
+          t = w.t.ntiles;
+        }
+        int64_t cum = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t x = __shfl_up_sync(kAll, cum, o);
+          if (lane >= o) cum += x;
+        }
+        const uint32_t in = __ballot_sync(kAll, at >= cum - t && at < cum);
+        if (in) {
+          const int u = __ffs(int(in)) - 1;
+          w.k = int(at - __shfl_sync(kAll, cum - t, u));
+          w.unit = u0 + u;
+          w.tiles();
+          return all_units;
+        }
+        at -= __shfl_sync(kAll, cum, 31);
+        if (u0 + 32 >= w.units) break;   // (cannot be: the step lies in this request)
+      }
+      break;
+    }
+    before += __shfl_sync(kAll, sum, 31);
+    units += __shfl_sync(kAll, nsum, 31);
+  }
+  w.left = 0;
+  return all_units;
+}
+
 // One unit's entry in the workspace, written by its first split's cluster for
 // the kernel that merges the splits.
 struct alignas(16) ChunkUnit {
@@ -370,6 +545,12 @@ struct ChunkTcParams : ChunkParams {
   int32_t* totals;       // [2]: units, items (written by item 0)
   ChunkUnit* units;
   uint32_t* cta_flags;   // [items][ctas] status bits of each CTA
+  // many rows per request (va_prefill_tc.cu):
+  const __nv_bfloat16* packed;  // paged: [num_entries, 576] the listed rows side by side
+  const uint32_t* valid;        // paged: bit e set when entry e has a pool row
+  const __nv_bfloat16* tails;   // [B * 64, 576]: each request's last, partial tile, zeros behind it
+  uint32_t* pack_flags;         // [pack_blocks] status bits of the packing
+  int pack_blocks;
   float* part_lse;       // [slots][unit_rows]
   float* part_o;         // [slots][unit_rows][512], normalised by the split's row sum
 };
@@ -382,6 +563,9 @@ constexpr uint32_t kFlagHiddenNonfinite = 0x80000000u;
 // Tensor-core kernels: va_decode_tc.cu for few rows per request (units of 64
 // rows, an item per CTA, two partial slots each), else va_tc.cu.
 cudaError_t launch_decode_tc(const ChunkTcParams& p, int ctas, cudaStream_t st);
+// va_prefill_tc.cu: many rows per request (units of 256 rows, an item per
+// cluster, two partial slots each), keys side by side.
+cudaError_t launch_prefill_tc(const ChunkTcParams& p, int clusters, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkTcParams& p, int grid_items, bool pair, cudaStream_t st);
 
 // Checks shared by the chunk calls (va_chunk.cu).

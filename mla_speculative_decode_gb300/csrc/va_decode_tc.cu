@@ -54,6 +54,8 @@ constexpr long long kWaitCycles = 4000000000ll;   // wait bound in SM cycles (~2
 constexpr long long kDrainCycles = 2000000ll;     // after an abort: boxes in flight land
 constexpr float kRescaleLog2 = 8.f;
 
+using Run = ChunkRun<kRows>;
+
 // Barriers.
 constexpr int B_KFULL = 0;                     // [2][kGroups] column blocks of a key tile landed
 constexpr int B_KEMPTY = B_KFULL + 2 * kGroups;   // [2][kGroups] both products of them are done
@@ -82,132 +84,6 @@ constexpr uint32_t kEnd = kOffP + kRows * 128u;
 constexpr uint32_t kSmemBytes = kEnd + 1024;
 static_assert(8 * kNumBars <= int(kOffTmemSlot) && kOffValid + 8 * kValidRing <= kOffSrow, "header");
 static_assert(kOffK % 1024 == 0 && kSmemBytes <= 232448, "shared memory budget");
-
-// A place in the row of steps (unit by unit, tile by tile).  Every role walks
-// its CTA's run with one of these.
-struct Run {
-  const ChunkParams& p;
-  ChunkReq r;
-  ChunkTiles t;        // all tiles of the unit
-  int b, unit, units, unit0;   // request, unit within it, its units, units before it
-  int k;               // tile within the unit
-  int64_t left;        // steps left, this one included
-  int64_t g, total;    // index of this step in the batch; steps of the batch
-  int ctas;            // CTAs that have a run
-
-  __device__ explicit Run(const ChunkParams& p_) : p(p_) {}
-  __device__ int rows() const {
-    const int n = r.n * p.H - unit * kRows;
-    return n < kRows ? n : kRows;
-  }
-  __device__ void load(int b_) {
-    b = b_;
-    r = chunk_req(p, b);
-    units = (r.n * p.H + kRows - 1) / kRows;
-    unit = 0;
-  }
-  __device__ void tiles() { t = chunk_tiles(p, r, unit * kRows, rows()); }
-  __device__ int64_t steps() {
-    int64_t n = 0;
-    for (unit = 0; unit < units; ++unit) {
-      tiles();
-      n += t.ntiles;
-    }
-    return n;
-  }
-  __device__ int key() const { return t.tile_key(k); }
-  __device__ bool last_tile() const { return k + 1 == t.ntiles || left == 1; }
-  // The next step (only while left > 1).
-  __device__ void next() {
-    ++g;
-    if (--left <= 0) return;
-    if (++k < t.ntiles) return;
-    k = 0;
-    if (++unit >= units) {
-      unit0 += units;
-      do load(b + 1);
-      while (units == 0 && b + 1 < p.B);
-    }
-    tiles();
-  }
-  // First step of CTA c's run, and the CTA that owns step x.
-  __device__ int64_t begin(int c) const { return total * c / ctas; }
-  __device__ int owner(int64_t x) const {
-    int c = int(x * ctas / total);
-    while (c + 1 < ctas && begin(c + 1) <= x) ++c;
-    while (c > 0 && begin(c) > x) --c;
-    return c;
-  }
-};
-
-// CTA c's run (left = 0: none), and the batch's units in total.  Whole warps.
-__device__ int find_run(Run& w, int c, int grid, int lane) {
-  constexpr uint32_t kAll = 0xffffffffu;
-  int64_t total = 0, s0 = 0;
-  int all_units = 0, n0 = 0;
-  for (int b = lane; b < w.p.B; b += 32) {
-    w.load(b);
-    const int64_t s = w.steps();
-    if (b < 32) { s0 = s; n0 = w.units; }
-    total += s;
-    all_units += w.units;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(kAll, total, o);
-    all_units += __shfl_xor_sync(kAll, all_units, o);
-  }
-  w.total = total;
-  w.ctas = total < grid ? int(total) : grid;
-  w.left = 0;
-  if (c >= w.ctas) return all_units;
-  w.g = w.begin(c);
-  w.left = w.begin(c + 1) - w.g;
-  int64_t before = 0;
-  int units = 0;
-  for (int b0 = 0; b0 < w.p.B; b0 += 32) {
-    int64_t s = s0;
-    int n = n0;
-    if (b0 > 0) {
-      s = 0;
-      n = 0;
-      if (b0 + lane < w.p.B) {
-        w.load(b0 + lane);
-        s = w.steps();
-        n = w.units;
-      }
-    }
-    int64_t sum = s;
-    int nsum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(kAll, sum, o);
-      const int y = __shfl_up_sync(kAll, nsum, o);
-      if (lane >= o) { sum += x; nsum += y; }
-    }
-    const uint32_t mine = __ballot_sync(kAll, w.g >= before + sum - s && w.g < before + sum);
-    if (mine) {
-      const int src = __ffs(int(mine)) - 1;
-      int64_t at = w.g - before - __shfl_sync(kAll, sum - s, src);
-      w.unit0 = units + __shfl_sync(kAll, nsum - n, src);
-      w.load(b0 + src);
-      for (w.tiles(); at >= w.t.ntiles; w.tiles()) {
-        at -= w.t.ntiles;
-        ++w.unit;
-      }
-      w.k = int(at);
-      return all_units;
-    }
-    before += __shfl_sync(kAll, sum, 31);
-    units += __shfl_sync(kAll, nsum, 31);
-  }
-  w.left = 0;
-  return all_units;
-}
-
-__device__ __forceinline__ uint64_t low_bits(int n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
 
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const __grid_constant__ ChunkTcParams p, const __grid_constant__ CUtensorMap tmap_k,

@@ -18,6 +18,7 @@ cudaError_t init_partial_tc(int* max_pairs, int* max_quads);
 cudaError_t init_weights_tc();
 cudaError_t init_evict();
 cudaError_t init_decode_tc();
+cudaError_t init_prefill_tc();
 bool tc_supported(int B, int T, int H);
 bool tc_use_pair(int T, int H, int flags);
 int tc_auto_nsplit(int B, int T, int H, int clusters, bool pair);
@@ -231,6 +232,7 @@ VA_API int va_init(int device) {
   cudaError_t e3 = va::init_weights_tc();
   if (e3 == cudaSuccess) e3 = va::init_evict();
   if (e3 == cudaSuccess) e3 = va::init_decode_tc();
+  if (e3 == cudaSuccess) e3 = va::init_prefill_tc();
   // the no-allocation scratch array: placed now, with the device current; a
   // failure here (no memory left for it) is not an error of va_init -- the
   // first verify_attn_paged_noalloc call on the device retries and reports it

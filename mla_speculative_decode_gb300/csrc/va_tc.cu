@@ -291,11 +291,6 @@ struct ChunkMode {
   using Range = ChunkTiles;
 };
 
-// The n lowest bits of a 64-bit mask (any n).
-__device__ __forceinline__ uint64_t low_bits(int n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
-
 // Raw pool row of key j of the split as stored in the slot list (contiguous
 // pools: the row itself; segmented lists: the draft list past the prefix), or
 // -1 when no row of the unit sees key j or the list ends before it.  The value is only range-checked
@@ -441,12 +436,9 @@ __device__ __forceinline__ bool produce(const typename Mode::P& p, const typenam
     // the append (in the kernel before this one) has completed
     if constexpr (!Mode::kChunk)
       if (p.draft_kv && tk0 + kTile > ri.P) griddep_wait();
-    const int64_t row0 = ri.base + tk0;
-    int64_t box_rows = p.kv_start ? p.num_slots : 0;
-    if constexpr (Mode::kChunk)   // paged rows that were packed in list order
-      if (p.packed) box_rows = p.num_entries;
-    bool boxes = box_rows > 0 && sr.whole(tk0) && tk0 + kTile <= ri.nlist &&
-                 row0 >= 0 && row0 + kTile <= box_rows && row0 + kTile <= 0x7fffffff;
+    const int64_t row0 = p.kv_start ? ri.base + tk0 : -1;
+    bool boxes = p.kv_start != nullptr && sr.whole(tk0) && tk0 + kTile <= ri.nlist &&
+                 row0 >= 0 && row0 + kTile <= p.num_slots && row0 + kTile <= 0x7fffffff;
     if (kPair && !kMask && !box3d) boxes = false;   // the PV pair share needs the 3-D map
     if (kMask && ptid == 0) mbar_arrive(vready0 + 8u * uint32_t(t % C::kValidRing));
     if (ptid == 0) {
@@ -590,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the maps' descriptors are fetched while the request's bounds load
   if (tid == 0) {
     if (qk) tma_prefetch(&tmap_q);
-    if (box3d) {
+    if (p.kv_start) {
       tma_prefetch(qk ? &tmap_k : &tmap_v);
       tma_prefetch(&tmap_2d);
     }
@@ -1541,11 +1533,8 @@ cudaError_t init_partial_tc(int* max_pairs, int* max_quads) {
 // blocks: strides one row and 128 bytes), a box of `rows` keys x `blocks`
 // column blocks covering a CTA's share of a 64-key tile; 2-D (576 columns,
 // pool rows; blocks = 0), a box of one column block of `rows` keys.
-struct PoolRows {
-  const __nv_bfloat16* kv;
-  int64_t num_slots, kv_stride;
-};
-bool encode_pool_map(CUtensorMap* m, const PoolRows& p, int blocks, int rows) {
+template <class P>
+bool encode_pool_map(CUtensorMap* m, const P& p, int blocks, int rows) {
   if (blocks > 0) {
     cuuint64_t dims[3] = {64u, cuuint64_t(p.num_slots), cuuint64_t(kKBlocks)};
     cuuint64_t strides[2] = {cuuint64_t(p.kv_stride) * 2u, 128u};
@@ -1602,18 +1591,11 @@ cudaError_t launch_tc(const typename Mode::P& p, dim3 grid, bool pair, int64_t q
   memset(&t2, 0, sizeof t2);
   if (!g_encode || !encode_q_map(&tq, p.q, q_rows)) return cudaErrorNotSupported;
   int box3d = 0;
-  PoolRows pool{p.kv, p.num_slots, p.kv_stride};
-  bool contiguous = p.kv_start != nullptr;
-  if constexpr (Mode::kChunk)
-    if (p.packed) {
-      pool = PoolRows{p.packed, p.num_entries, kDqk};
-      contiguous = true;
-    }
-  if (contiguous) {
+  if (p.kv_start) {
     const int krows = pair ? Cfg<true>::kSlotKeys : kTile;
-    if (!encode_pool_map(&t2, pool, 0, krows)) return cudaErrorNotSupported;
-    if (encode_pool_map(&tk, pool, kKBlocks, krows) &&
-        encode_pool_map(&tv, pool, pair ? 2 : kVBlocks, kTile))
+    if (!encode_pool_map(&t2, p, 0, krows)) return cudaErrorNotSupported;
+    if (encode_pool_map(&tk, p, kKBlocks, krows) &&
+        encode_pool_map(&tv, p, pair ? 2 : kVBlocks, kTile))
       box3d = 1;
   }
   cudaLaunchConfig_t cfg;

@@ -74,7 +74,7 @@ def test_chunk_workspace_bytes(lib):
         for flags in range(4):
             assert 256 <= f(B, total_q, H, 0, flags) < 1 << 32
     # many rows per request: the listed rows are packed first
-    assert f(1, 512, 64, 20000, 0) - f(1, 512, 64, 0, 0) == 20000 * 1152
+    assert 0 <= f(1, 512, 64, 20000, 0) - f(1, 512, 64, 0, 0) - 20000 * 1152 < 1 << 16
     assert f(1, 15, 64, 20000, 0) == f(1, 15, 64, 0, 0)
 
 
