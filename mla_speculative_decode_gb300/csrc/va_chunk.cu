@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
 #pragma unroll 4
     for (int i = tid; i < n; i += kFinishThreads) bits |= p.cta_flags[i];
     if (blockIdx.x == 0)
-      for (int i = tid; i < p.pack_blocks; i += kFinishThreads) bits |= p.pack_flags[i];
+      for (int i = tid; i < p.pack_blocks; i += kFinishThreads) bits |= p.pack_flags[i] & ~kPackMissing;
   }
   const bool hidden = __syncthreads_or((bits & kFlagHiddenNonfinite) != 0u);
   for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
@@ -348,8 +348,9 @@ __global__ void __launch_bounds__(kPackThreads) chunk_pack_kernel(const ChunkTcP
   }
   const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
   if (lane == 0) const_cast<uint32_t*>(p.valid)[e0 >> 5] = have;
-  const bool any_bad = __syncthreads_or(bad);
-  if (tid == 0) p.pack_flags[blockIdx.x] = any_bad ? VA_STATUS_BAD_SLOT : 0u;
+  const bool any_bad = __syncthreads_or(bad), missing = __syncthreads_or(row == -1);
+  if (tid == 0)
+    p.pack_flags[blockIdx.x] = (any_bad ? VA_STATUS_BAD_SLOT : 0u) | (missing ? kPackMissing : 0u);
   copy_rows(p, row, 32, reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.packed) + e0 * kDqk),
             lane);
 }

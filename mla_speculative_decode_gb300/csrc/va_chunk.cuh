@@ -560,6 +560,10 @@ struct ChunkTcParams : ChunkParams {
 // computes the unit's rows again on CUDA cores.
 constexpr uint32_t kFlagHiddenNonfinite = 0x80000000u;
 
+// Bit of a packing block's status word: one of its entries that were copied has no
+// pool row.
+constexpr uint32_t kPackMissing = 0x80000000u;
+
 // Tensor-core kernels: va_decode_tc.cu for few rows per request (units of 64
 // rows, an item per CTA, two partial slots each), else va_tc.cu.
 cudaError_t launch_decode_tc(const ChunkTcParams& p, int ctas, cudaStream_t st);

@@ -290,11 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- products S[T % 2] = Q K^T, issued by the even rank for both
       if (even) {
         constexpr uint32_t idesc = idesc_bf16(kUnitRows, kTile, 0, 0);
-        bool ok = true, first = true;
-        int f = 0, u = 0;
-        for (int T = 0; w.left > 0; ++T, ++f) {
+        bool ok = true;
+        int f = 0, u = 0, n = 0;   // ring entry, unit, tiles left of the unit's piece
+        for (int T = 0; n > 0 || w.left > 0; ++T, ++f, --n) {
           bool got = true;
-          if (first) {
+          if (n == 0) {
+            n = w.piece();
+            w.next_piece();
             got = wait(B_QREADY, u) && wait_far(B_QREADYP, u);
             ++u;
             f += kQSlots;
@@ -319,8 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (c | kk) != 0 ? 1u : 0u);
           mma2_commit_mc_warp(bar(B_SFULL + bs), kQkMask);
           mma2_commit_mc_warp(bar(B_EMPTY + s), kQkMask);
-          first = w.last_tile();
-          w.next();
         }
         if (!ok && lane == 0) fail();
         mma2_commit_mc_warp(bar(B_MMAFIN), kQkMask);
@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sc = raw_scores ? p.scale_log2 : 1.f;
       bool ok = true, issuer_ok = true, hidden_nonfinite = false, bad_slot = false;
       int T = 0, f = 0;
+      int last_b = -1;          // request of the piece before,
+      bool all_valid = false;   // and whether every key of it has a row
       for (int u = 0; ok && w.left > 0; ++u) {
         // one piece: the tiles of this unit that lie in the run
         const int rows = w.rows() - hh * kRows;            // of this CTA
@@ -359,6 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int N = w.r.nlist < w.r.P + w.r.n ? w.r.nlist : w.r.P + w.r.n;
         const bool direct = w.k == 0 && w.piece() == w.t.ntiles;
         const size_t slot = size_t(2 * cluster + (w.g > w.begin(cluster) ? 1 : 0));
+        if (w.b != last_b) {
+          last_b = w.b;
+          bool all = true;
+          if (p.valid) {   // any key of the blocks that the list touches without one
+            for (int64_t k = base / 256 + (tid - 128); k * 256 < base + N; k += kSoftmax)
+              all = all && !(p.pack_flags[k] & kPackMissing);
+          } else {
+            all = base >= 0 && base + N <= p.num_slots;
+          }
+          all_valid = named_sync_and(kRowBar, kSoftmax, all);
+        }
         // The unit's queries: this warp's quarter of the rows, column blocks 0-4
         // or 5-8, into tensor memory.  (The products of the unit before are done:
         // its last scores have been read.)
@@ -397,32 +410,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           f += kQSlots;
         }
         float m_ref = -INFINITY, l = 0.f;
-        for (bool more = true; more; ++T, ++f) {
+        ChunkTiles tiles = w.t;   // (the tile's index is all that moves)
+        const int n = w.piece();
+        tiles.t0 = w.k;
+        w.next_piece();
+        for (int i = 0; i < n; ++i, ++T, ++f) {
           const int bs = T & 1, pb = T % kPBufs;
-          const int tk0 = w.key();
-          more = !w.last_tile();
-          // which of the half's 32 keys have a row, and which of them this row sees
-          uint32_t valid = 0u;
-          if (p.valid) {
-            const int n = N - (tk0 + 32 * half);   // of them in the list
-            const int64_t e = base + tk0 + 32 * half;
-            if (n > 0)
-              valid = __funnelshift_r(__ldg(p.valid + (e >> 5)), __ldg(p.valid + (e >> 5) + 1),
-                                      uint32_t(e) & 31u) & uint32_t(low_bits(n));
-          } else {
-            const int64_t a = base + tk0 + 32 * half;   // pool row of the first
-            const int64_t lo = -a, hi = p.num_slots - a;
-            const uint64_t in = low_bits(hi > 64 ? 64 : int(hi < 0 ? 0 : hi)) &
-                                ~low_bits(lo > 64 ? 64 : int(lo < 0 ? 0 : lo));
-            valid = uint32_t(in);
-            const uint64_t seen = low_bits(k1 - tk0) & (~low_bits(first_a - tk0) | low_bits(p.sinks - tk0));
-            bad_slot |= (uint32_t(seen >> (32 * half)) & ~valid) != 0u;
+          const int tk0 = tiles.tile_key(i);
+          // Which of the half's 32 keys this row sees.  Most tiles lie inside for
+          // every row of the unit, with a row behind every key.
+          const bool inside = tk0 + kTile <= pos_a + 1 && (tk0 >= first_z || tk0 + kTile <= p.sinks);
+          uint32_t v32 = 0xffffffffu;
+          if (!all_valid || !inside) {
+            uint32_t valid = 0u;
+            if (p.valid) {
+              const int c = N - (tk0 + 32 * half);   // of them in the list
+              const int64_t e = base + tk0 + 32 * half;
+              if (c > 0)
+                valid = __funnelshift_r(__ldg(p.valid + (e >> 5)), __ldg(p.valid + (e >> 5) + 1),
+                                        uint32_t(e) & 31u) & uint32_t(low_bits(c));
+            } else {
+              const int64_t a = base + tk0 + 32 * half;   // pool row of the first
+              const int64_t lo = -a, hi = p.num_slots - a;
+              valid = uint32_t(low_bits(hi > 64 ? 64 : int(hi < 0 ? 0 : hi)) &
+                               ~low_bits(lo > 64 ? 64 : int(lo < 0 ? 0 : lo)));
+              const uint64_t seen =
+                  low_bits(k1 - tk0) & (~low_bits(first_a - tk0) | low_bits(p.sinks - tk0));
+              bad_slot |= (uint32_t(seen >> (32 * half)) & ~valid) != 0u;
+            }
+            const uint64_t vis =
+                low_bits(pos + 1 - tk0) & (~low_bits(first - tk0) | low_bits(p.sinks - tk0));
+            v32 = uint32_t(vis >> (32 * half)) & valid;
           }
-          uint64_t vis = ~0ull;
-          if (tk0 + kTile > pos_a + 1 || (tk0 < first_z && tk0 + kTile > p.sinks))
-            vis = low_bits(pos + 1 - tk0) & (~low_bits(first - tk0) | low_bits(p.sinks - tk0));
-          const uint32_t v32 = row_ok ? uint32_t(vis >> (32 * half)) & valid : 0u;
-          w.next();
           const bool wok = __all_sync(0xffffffffu, wait(B_SFULL + bs, T >> 1));
           float x[32];
           float mth = -INFINITY;
@@ -458,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
             for (int c = 4; c < 32; ++c) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
-            mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+            // (a row past the unit's is not written, and must not move anything)
+            if (row_ok) mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
           }
           mx[half * kRows + r] = mth;
           if (issuer) bulk_wait_read<1>();   // staging buffer bs: the copy two tiles back has read it
@@ -579,9 +599,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         for (int t = 0; t < kPBufs && t < steps; ++t) mbar_arrive_expect_tx(bar(B_PFULL + t), kPPayload);
       __syncwarp();
-      bool ok = true, first = true;
-      int u = 0, nresc = 0;
-      for (int T = 0; w.left > 0; ++T) {
+      bool ok = true, first = false;
+      int u = 0, nresc = 0, n = 0;   // units begun, rescales, tiles left of the unit's piece
+      for (int T = 0; n > 0 || w.left > 0; ++T) {
+        first = n == 0;
+        if (first) {
+          n = w.piece();
+          w.next_piece();
+        }
         const int pb = T % kPBufs, s = T % kVRing;
         const bool got = (!first || u == 0 || wait_far(B_OFREE, u - 1)) &&
                          wait_far(B_VFULL + s, T / kVRing) && wait_far(B_PFULL + pb, T / kPBufs) &&
@@ -627,9 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0 && T + kPBufs < steps) mbar_arrive_expect_tx(bar(B_PFULL + pb), kPPayload);
         __syncwarp();
         mma2_commit_mc_warp(bar(B_PFREE + pb), kQkMask);
-        first = w.last_tile();
-        w.next();
-        if (first) {   // the unit's last product here: its rows may be written out
+        if (--n == 0) {   // the unit's last product here: its rows may be written out
           mma2_commit_mc_warp(bar(B_OFULL), kPvMask);
           command(kCmdUnit);
           ++u;
