@@ -357,19 +357,20 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
 }
 
 // A place in the row of steps: the tiles of all units (kRows query rows each) of
-// the batch, request by request, unit by unit.  A launch cuts the row into equal
-// runs, one for each of its CTAs or clusters; every role of those walks its run
-// with one of these, so that they agree without talking.
-template <int kRows>
+// the batch, request by request, unit by unit, each unit's preceded by kCost places
+// for what a unit costs besides its tiles.  A launch cuts the row into equal runs,
+// one for each of its CTAs or clusters; every role of those walks its run with one
+// of these, so that they agree without talking.
+template <int kRows, int kCost>
 struct ChunkRun {
   const ChunkParams& p;
   ChunkReq r;
   ChunkTiles t;        // all tiles of the unit
   int b, unit, units, unit0;   // request, unit within it, its units, units before it
   int k;               // tile within the unit
-  int64_t left;        // steps left, this one included
-  int64_t g, total;    // index of this step in the batch; steps of the batch
-  int runs;            // CTAs that have a run
+  int64_t g, end;      // place of this step in the row; of the run's end
+  int64_t total;       // places of the batch
+  int runs;            // runs it is cut into
 
   __device__ explicit ChunkRun(const ChunkParams& p_) : p(p_) {}
   __device__ int rows() const {
@@ -384,12 +385,14 @@ struct ChunkRun {
   }
   __device__ void tiles() { t = chunk_tiles(p, r, unit * kRows, rows()); }
   __device__ int key() const { return t.tile_key(k); }
-  __device__ bool last_tile() const { return k + 1 == t.ntiles || left == 1; }
-  // The next step (only while left > 1).
+  __device__ bool more() const { return g < end; }
+  __device__ bool last_tile() const { return k + 1 == t.ntiles || g + 1 >= end; }
+  // The next step of the run, if there is one (see more).
   __device__ void next() {
-    ++g;
-    if (--left <= 0) return;
+    if (++g >= end) return;
     if (++k < t.ntiles) return;
+    g += kCost;
+    if (g >= end) return;
     k = 0;
     if (++unit >= units) {
       unit0 += units;
@@ -400,15 +403,14 @@ struct ChunkRun {
   }
   // The steps of this unit that lie in the run from here on, and the step after
   // them.
-  __device__ int piece() const { return int(t.ntiles - k < left ? t.ntiles - k : left); }
+  __device__ int piece() const { return int(t.ntiles - k < end - g ? t.ntiles - k : end - g); }
   __device__ void next_piece() {
     const int n = piece() - 1;
     k += n;
     g += n;
-    left -= n;
     next();
   }
-  // First step of run c, and the run that step x is in.
+  // First place of run c, and the run that place x is in.
   __device__ int64_t begin(int c) const { return total * c / runs; }
   __device__ int owner(int64_t x) const {
     int c = int(x * runs / total);
@@ -418,10 +420,10 @@ struct ChunkRun {
   }
 };
 
-// Steps and units of requests b0 + lane: a lane counts a request of at most two
+// Places and units of requests b0 + lane: a lane counts a request of at most two
 // units by itself, the warp together one of more.
-template <int kRows>
-__device__ int64_t count_steps(ChunkRun<kRows>& w, int b0, int lane, int* units) {
+template <int kRows, int kCost>
+__device__ int64_t count_steps(ChunkRun<kRows, kCost>& w, int b0, int lane, int* units) {
   constexpr uint32_t kAll = 0xffffffffu;
   int64_t mine = 0;
   *units = 0;
@@ -446,13 +448,13 @@ __device__ int64_t count_steps(ChunkRun<kRows>& w, int b0, int lane, int* units)
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
     if (lane == src) mine = n;
   }
-  return mine;
+  return mine + int64_t(*units) * kCost;
 }
 
-// Run c's place and length (left = 0: none), of at most `grid` runs; returns the
+// Run c's first step and end (see more), of at most `grid` runs; returns the
 // batch's units in total.  A whole warp takes part.
-template <int kRows>
-__device__ int find_run(ChunkRun<kRows>& w, int c, int grid, int lane) {
+template <int kRows, int kCost>
+__device__ int find_run(ChunkRun<kRows, kCost>& w, int c, int grid, int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
   int64_t total = 0, s0 = 0;
   int all_units = 0, n0 = 0;
@@ -470,10 +472,10 @@ __device__ int find_run(ChunkRun<kRows>& w, int c, int grid, int lane) {
   }
   w.total = total;
   w.runs = total < grid ? int(total) : grid;
-  w.left = 0;
+  w.g = w.end = 0;
   if (c >= w.runs) return all_units;
   w.g = w.begin(c);
-  w.left = w.begin(c + 1) - w.g;
+  w.end = w.begin(c + 1);
   int64_t before = 0;
   int units = 0;
   for (int b0 = 0; b0 < w.p.B; b0 += 32) {
@@ -499,7 +501,7 @@ __device__ int find_run(ChunkRun<kRows>& w, int c, int grid, int lane) {
         w.unit = u0 + lane;
         if (w.unit < w.units) {
           w.tiles();
-          t = w.t.ntiles;
+          t = w.t.ntiles + kCost;
         }
         int64_t cum = t;
 #pragma unroll
@@ -510,7 +512,10 @@ __device__ int find_run(ChunkRun<kRows>& w, int c, int grid, int lane) {
         const uint32_t in = __ballot_sync(kAll, at >= cum - t && at < cum);
         if (in) {
           const int u = __ffs(int(in)) - 1;
-          w.k = int(at - __shfl_sync(kAll, cum - t, u));
+          // (a run that begins in a unit's cost begins with its first tile)
+          const int k = int(at - __shfl_sync(kAll, cum - t, u)) - kCost;
+          w.k = k < 0 ? 0 : k;
+          w.g += k < 0 ? -k : 0;
           w.unit = u0 + u;
           w.tiles();
           return all_units;
@@ -523,7 +528,7 @@ __device__ int find_run(ChunkRun<kRows>& w, int c, int grid, int lane) {
     before += __shfl_sync(kAll, sum, 31);
     units += __shfl_sync(kAll, nsum, 31);
   }
-  w.left = 0;
+  w.g = w.end;
   return all_units;
 }
 

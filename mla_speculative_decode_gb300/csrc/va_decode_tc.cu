@@ -54,7 +54,8 @@ constexpr long long kWaitCycles = 4000000000ll;   // wait bound in SM cycles (~2
 constexpr long long kDrainCycles = 2000000ll;     // after an abort: boxes in flight land
 constexpr float kRescaleLog2 = 8.f;
 
-using Run = ChunkRun<kRows>;
+// (a unit costs about one tile besides its own: queries in, rows out)
+using Run = ChunkRun<kRows, 1>;
 
 // Barriers.
 constexpr int B_KFULL = 0;                     // [2][kGroups] column blocks of a key tile landed
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.totals[0] = all_units;
     p.totals[1] = int(gridDim.x);
   }
-  if (w.left == 0) {
+  if (!w.more()) {
     if (tid == 0) p.cta_flags[cta] = 0u;
     return;
   }
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int rawrow = raw0;
     bool ok = true, bad_slot = false;
     int box_step[2] = {-1, -1};   // the last step loaded by boxes into each half
-    for (int s = 0; w.left > 0; ++s) {
+    for (int s = 0; w.more(); ++s) {
       const int half = s & 1;
       const int tk0 = w.key();
       if (ptid < kTile) {
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool box = p.kv_start && w.t.whole(tk0) && tk0 + kTile <= w.r.nlist && row0 >= 0 &&
                        row0 + kTile <= p.num_slots && row0 + kTile <= 0x7fffffff;
       w.next();
-      if (ptid < kTile && w.left > 0) rawrow = fetch(w);
+      if (ptid < kTile && w.more()) rawrow = fetch(w);
       if (ptid == 0) {
         mbar_arrive(bar(B_VREADY + s % kValidRing));
         box_step[half] = box ? s : -1;
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool pending = false, pend_first = false, pend_last = false;
     int pend_n = 0;
     bool first = true;
-    while (ok && w.left > 0) {
+    while (ok && w.more()) {
       const bool last = w.last_tile();
       const int n16 = (w.rows() + 15) & ~15;
       const int full = B_KFULL + (s & 1) * kGroups;
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       first = last;
       ++s;
       w.next();
-      if (last && w.left > 0) {
+      if (last && w.more()) {
         if (!__all_sync(0xffffffffu, wait(B_QEMPTY, uint32_t(qload - 1)))) {
           ok = false;
           break;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = raw_scores ? p.scale_log2 : 1.f;
     bool ok = true, hidden_nonfinite = false;
     int s = 0, piece = 0;
-    while (w.left > 0 && ok) {
+    while (w.more() && ok) {
       // one piece: the tiles of this unit that lie in the run
       const int rows = w.rows();
       const bool row_ok = row_lane && r < rows;

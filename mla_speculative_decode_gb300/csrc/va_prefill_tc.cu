@@ -72,7 +72,10 @@ constexpr long long kWaitCycles = 4000000000ll;   // wait bound in SM cycles (~2
 constexpr long long kDrainCycles = 2000000ll;     // after an abort: boxes in flight land
 constexpr float kRescaleLog2 = 8.f;
 
-using Run = ChunkRun<kUnitRows>;
+// What a unit costs besides its tiles, in tiles: queries into tensor memory, the
+// pipeline's fill, rows out of it.
+constexpr int kUnitCost = 3;
+using Run = ChunkRun<kUnitRows, kUnitCost>;
 
 // Barriers: one layout in all four CTAs, QK and PV sides side by side.
 constexpr int B_FULL = 0;                      // [kRing] QK: slot landed
@@ -114,7 +117,7 @@ static_assert(8 * kNumBars <= int(kOffTmemSlot), "barrier area");
 static_assert(kOffStage % 1024 == 0 && kOffV % 1024 == 0 && kSmemBytes <= 232448, "layout");
 
 struct RunPlace {
-  int64_t left, g, total;
+  int64_t g, end, total;
   int b, unit, unit0, k, runs;
 };
 static_assert(kOffRun + sizeof(RunPlace) <= kOffPeerAny, "header");
@@ -144,6 +147,13 @@ __device__ __forceinline__ TileAt tile_at(const ChunkTcParams& p, const Run& w) 
   t.tail = tk0 < N && tk0 + kTile > N;
   t.row = t.tail ? w.b * kTile : int(tk0 >= N || row < -kTile || row > rows ? rows : row);
   return t;
+}
+
+// Tiles of the rest of a run.
+__device__ int64_t tiles_of(Run w) {
+  int64_t n = 0;
+  for (; w.more(); w.next_piece()) n += w.piece();
+  return n;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     const int units = find_run(w, cluster, int(gridDim.x) / kCtas, lane);
     if (lane == 0) {
-      *place = RunPlace{w.left, w.g, w.total, w.b, w.unit, w.unit0, w.k, w.runs};
+      *place = RunPlace{w.g, w.end, w.total, w.b, w.unit, w.unit0, w.k, w.runs};
       if (blockIdx.x == 0) {
         p.totals[0] = units;
         p.totals[1] = int(gridDim.x) / kCtas;
@@ -208,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (place->left == 0) {   // every CTA of the cluster leaves together
+  if (place->g >= place->end) {   // every CTA of the cluster leaves together
     if (tid == 0) p.cta_flags[blockIdx.x] = 0u;
     return;
   }
@@ -218,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.tiles();
     w.unit0 = place->unit0;
     w.k = place->k;
-    w.left = place->left;
     w.g = place->g;
+    w.end = place->end;
     w.total = place->total;
     w.runs = place->runs;
   }
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int f = 0;   // ring entry
         bool first = true;
         const uint32_t lead_full = mapa(bar(B_FULL), lead);
-        for (; ok && w.left > 0; w.next()) {
+        for (; ok && w.more(); w.next()) {
           if (first) {
             const int row = w.r.q0 * p.H + w.unit * kUnitRows + hh * kRows;
             for (int i = 0; ok && i < kQSlots; ++i, ++f) {
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc = idesc_bf16(kUnitRows, kTile, 0, 0);
         bool ok = true;
         int f = 0, u = 0, n = 0;   // ring entry, unit, tiles left of the unit's piece
-        for (int T = 0; n > 0 || w.left > 0; ++T, ++f, --n) {
+        for (int T = 0; n > 0 || w.more(); ++T, ++f, --n) {
           bool got = true;
           if (n == 0) {
             n = w.piece();
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int T = 0, f = 0;
       int last_b = -1;          // request of the piece before,
       bool all_valid = false;   // and whether every key of it has a row
-      for (int u = 0; ok && w.left > 0; ++u) {
+      for (int u = 0; ok && w.more(); ++u) {
         // one piece: the tiles of this unit that lie in the run
         const int rows = w.rows() - hh * kRows;            // of this CTA
         const bool row_ok = r < rows;
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         bool ok = true;
         const uint32_t lead_full = mapa(bar(B_VFULL), lead);
-        for (int T = 0; w.left > 0; ++T, w.next()) {
+        for (int T = 0; w.more(); ++T, w.next()) {
           const int s = T % kVRing;
           if (T >= kVRing && !wait(B_VEMPTY + s, T / kVRing - 1)) {
             ok = false;
@@ -595,13 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // a P buffer's barrier expects one arrival, ours, that carries the bytes of
       // the QK CTA's copy into it
-      const int64_t steps = w.left;
+      const int64_t steps = tiles_of(w);
       if (lane == 0)
         for (int t = 0; t < kPBufs && t < steps; ++t) mbar_arrive_expect_tx(bar(B_PFULL + t), kPPayload);
       __syncwarp();
       bool ok = true, first = false;
       int u = 0, nresc = 0, n = 0;   // units begun, rescales, tiles left of the unit's piece
-      for (int T = 0; n > 0 || w.left > 0; ++T) {
+      for (int T = 0; n > 0 || w.more(); ++T) {
         first = n == 0;
         if (first) {
           n = w.piece();
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- odd rank: forwards its P buffers' arrivals, and whether their rows
       // rescale, to the even rank, and re-arms them
       const uint32_t pfullp = mapa(bar(B_PFULLP), mate), peer_any = mapa(sb + kOffPeerAny, mate);
-      const int64_t steps = w.left;
+      const int64_t steps = tiles_of(w);
       if (lane == 0)
         for (int t = 0; t < kPBufs && t < steps; ++t) mbar_arrive_expect_tx(bar(B_PFULL + t), kPPayload);
       __syncwarp();
