@@ -74,12 +74,16 @@ constexpr float kRescaleLog2 = 8.f;
 
 // What a unit costs besides its tiles, in tiles: queries into tensor memory, the
 // pipeline's fill, rows out of it.
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 5;
 using Run = ChunkRun<kUnitRows, kUnitCost>;
 
 // Barriers: one layout in all four CTAs, QK and PV sides side by side.
-constexpr int B_FULL = 0;                      // [kRing] QK: slot landed
-constexpr int B_EMPTY = B_FULL + kRing;        // [kRing] QK: slot read
+// (Keys and queries land on barriers of their own although they share the slots:
+// an odd rank that is ahead may have its keys on the way into a slot whose
+// queries the even rank is still waiting for.)
+constexpr int B_KFULL = 0;                     // [kRing] QK, even rank: both CTAs' keys in a slot
+constexpr int B_QFULL = B_KFULL + kRing;       // [kQSlots] QK: a quarter of the CTA's queries
+constexpr int B_EMPTY = B_QFULL + kQSlots;     // [kRing] QK: slot read
 constexpr int B_SFULL = B_EMPTY + kRing;       // [2]
 constexpr int B_SEMPTY = B_SFULL + 2;          // [2]
 constexpr int B_QREADY = B_SEMPTY + 2;         // a unit's queries in tensor memory
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int f = 0;   // ring entry
         bool first = true;
-        const uint32_t lead_full = mapa(bar(B_FULL), lead);
+        const uint32_t lead_full = mapa(bar(B_KFULL), lead);
         for (; ok && w.more(); w.next()) {
           if (first) {
             const int row = w.r.q0 * p.H + w.unit * kUnitRows + hh * kRows;
@@ -256,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int s = f % kRing;
               ok = f < kRing || wait(B_EMPTY + s, f / kRing - 1);
               if (!ok) break;
-              mbar_arrive_expect_tx(bar(B_FULL + s), kSlotBytes);
+              mbar_arrive_expect_tx(bar(B_QFULL + i), kSlotBytes);
               tma_load_3d(sb + kOffK + uint32_t(s) * kSlotBytes, &maps.q, 0, row + kSlotRows * i, 0,
-                          bar(B_FULL + s));
+                          bar(B_QFULL + i));
             }
             if (even && w.k == 0) {   // the unit's entry, for the merge
               ChunkUnit u;
@@ -281,10 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = f % kRing;
           ok = f < kRing || wait(B_EMPTY + s, f / kRing - 1);
           if (!ok) break;
-          // both CTAs' keys land on the even rank's barrier; the odd one only
-          // keeps its own in step
-          if (even) mbar_arrive_expect_tx(bar(B_FULL + s), 2 * kSlotBytes);
-          else mbar_arrive(bar(B_FULL + s));
+          // both CTAs' keys land on the even rank's barrier
+          if (even) mbar_arrive_expect_tx(bar(B_KFULL + s), 2 * kSlotBytes);
           const TileAt t = tile_at(p, w);
           tma_load_3d_pair(sb + kOffK + uint32_t(s) * kSlotBytes, t.tail ? &maps.kt : &maps.k, 0,
                            t.row + kSlotRows * hh, 0, lead_full + 8u * uint32_t(s));
@@ -302,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc = idesc_bf16(kUnitRows, kTile, 0, 0);
         bool ok = true;
         int f = 0, u = 0, n = 0;   // ring entry, unit, tiles left of the unit's piece
+        uint32_t kphase = 0;       // bit s: parity of slot s's next keys
         for (int T = 0; n > 0 || w.more(); ++T, ++f, --n) {
           bool got = true;
           if (n == 0) {
@@ -312,12 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             f += kQSlots;
           }
           const int s = f % kRing, bs = T & 1;
-          got = got && wait_far(B_FULL + s, f / kRing) &&
+          got = got && wait_far(B_KFULL + s, int(kphase >> s & 1u)) &&
                 (T < 2 || wait_far(B_SEMPTY + bs, (T >> 1) - 1));
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
             break;
           }
+          kphase ^= 1u << s;
           fence_proxy_async_cta();
           tc_fence_after();
           const uint32_t d = tmem + kTmemS + 64u * uint32_t(bs);
@@ -386,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // or 5-8, into tensor memory.  (The products of the unit before are done:
         // its last scores have been read.)
         {
-          const int e = f + q4, s = e % kRing;
-          const bool got = __all_sync(0xffffffffu, wait(B_FULL + s, e / kRing));
+          const int s = (f + q4) % kRing;
+          const bool got = __all_sync(0xffffffffu, wait(B_QFULL + q4, u));
           if (got) {
             const uint32_t row_addr = sb + kOffK + uint32_t(s) * kSlotBytes + uint32_t(lane) * 128u;
 #pragma unroll 1

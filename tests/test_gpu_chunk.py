@@ -304,3 +304,24 @@ def test_longer_batches(va, P, n, H, layout):
                            prefix_len=c.prefix_len,
                            q_indptr=torch.tensor([0, t.stop - t.start], dtype=torch.int32))
         _chunk.check(sub, out[t], lse[t])
+
+
+@pytest.mark.parametrize("P,n,H,window", [([0, 0, 0], [700, 333, 1000], 64, 0),
+                                          ([3000, 100], [90, 257], 64, 200), ([4000], [64], 128, 0),
+                                          ([900] * 24, [1] * 24, 64, 0)])
+def test_calls_back_to_back_give_the_same_bits(va, P, n, H, window):
+    """Many calls in a row, nothing waited for between them: each one's rows are
+    the first one's, bit for bit."""
+    c = _chunk.make(P, n, H, seed=70, layout="contiguous" if n[0] == 700 else "paged")
+    call = _chunk.call(va, c, window=window, prepare=True)
+    out, lse = call()
+    first = out.clone(), lse.clone()
+    assert bool(torch.isfinite(first[1]).all())
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(60):
+        out.fill_(9.0)
+        for _ in range(4):
+            call()
+        differ += (out != first[0]).sum() + (lse != first[1]).sum()
+    assert int(differ) == 0
+    assert va.read_status(call.workspace) == 0
