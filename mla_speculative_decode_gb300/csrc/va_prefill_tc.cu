@@ -43,7 +43,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kThreads = 384;          // warps: 0 boxes, 1 products, 2-3 idle, 4-11 rows
+constexpr int kThreads = 384;          // warps: 0 boxes, 1 products, 2 P copies, 4-11 rows
 constexpr int kCtas = 4;
 constexpr int kRows = 128;             // of a CTA; a unit has two CTAs' worth
 constexpr int kUnitRows = 2 * kRows;
@@ -99,14 +99,17 @@ constexpr int B_ODONE = B_OCORR + 1;           // PV: products before a rescale 
 constexpr int B_OFULL = B_ODONE + 1;           // PV: a unit's products done
 constexpr int B_OFREE = B_OFULL + 1;           // PV: its O has been read
 constexpr int B_FIN = B_OFREE + 1;             // [kFinRing] PV: row sums from QK
-constexpr int B_MMAFIN = B_FIN + kFinRing;
+constexpr int B_STGFULL = B_FIN + kFinRing;    // [2] QK: a P staging buffer written
+constexpr int B_STGFREE = B_STGFULL + 2;       // [2] QK: read by its copy
+constexpr int B_MMAFIN = B_STGFREE + 2;
 constexpr int kNumBars = B_MMAFIN + 1;
 
 // Shared layout (offsets from a 1024-byte aligned base).
 constexpr uint32_t kOffTmemSlot = 512, kOffAbort = 516, kOffCmd = 520, kOffFlags = 524;
 constexpr uint32_t kOffRun = 544;              // RunPlace
 constexpr uint32_t kOffPeerAny = 640;          // PV, even rank: uint32 [kPBufs]
-constexpr uint32_t kOffMx = 1024;              // QK: float [2][128]
+constexpr uint32_t kOffMx = 1024;              // QK: float [2][2][128] half maxima, by tile parity
+constexpr uint32_t kOffSum = 3072;             // QK: float [2][128] half sums
 constexpr uint32_t kOffFin = 2048;             // PV: float [kFinRing][128] 1 / row sum
 constexpr uint32_t kOffK = 4096;               // QK: ring
 constexpr uint32_t kOffStage = kOffK + kRing * kSlotBytes;   // QK: P staging [2]
@@ -196,8 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t cnt = 1;
       // the odd rank's eight row warps add one arrival each
-      if (i == B_SEMPTY || i == B_SEMPTY + 1 || i == B_OCORR || i == B_OFREE)
-        cnt = kSoftmax + kSoftmax / 32;
+      if (i == B_OCORR || i == B_OFREE) cnt = kSoftmax + kSoftmax / 32;
+      if (i == B_SEMPTY || i == B_SEMPTY + 1) cnt = 2 * kSoftmax / 32;
+      if (i == B_STGFULL || i == B_STGFULL + 1) cnt = kSoftmax / 32;
       if (i == B_QREADY) cnt = kSoftmax;
       if (i == B_QREADYP) cnt = kSoftmax / 32;
       if (i >= B_FIN && i < B_FIN + kFinRing) cnt = 4;   // the first four row warps
@@ -342,21 +346,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // products read both CTAs' memories until their last commit
       (void)mbar_wait<true>(bar(B_MMAFIN), 0, nullptr, kWaitCycles);
       __syncwarp();
+    } else if (warp == 2) {
+      // ---- P to the PV CTA of the same rows, a copy per tile
+      if (lane == 0) {
+        const uint32_t pv_p = mapa(sb + kOffP, other), pv_pfull = mapa(bar(B_PFULL), other);
+        const int64_t steps = tiles_of(w);
+        bool ok = true;
+        int T = 0;
+        for (; T < steps; ++T) {
+          const int bs = T & 1, pb = T % kPBufs;
+          ok = wait(B_STGFULL + bs, T >> 1) && (T < kPBufs || wait_far(B_PFREE + pb, T / kPBufs - 1));
+          if (!ok) break;
+          bulk_copy_to_cluster(pv_p + uint32_t(pb) * kPBufBytes,
+                               sb + kOffStage + uint32_t(bs) * kPBufBytes, kPPayload,
+                               pv_pfull + 8u * uint32_t(pb));
+          bulk_commit();
+          bulk_wait_read<0>();
+          mbar_arrive(bar(B_STGFREE + bs));
+        }
+        // the PV CTAs' last releases land before this shared memory goes away
+        for (int t = T > kPBufs ? T - kPBufs : 0; ok && t < T; ++t)
+          ok = wait_far(B_PFREE + t % kPBufs, t / kPBufs);
+        if (!ok) fail();
+      }
+      __syncwarp();
     } else if (warp >= 4) {
       // ---- softmax: warpgroup `half` owns 32 of a tile's 64 keys for row r
       const int r = q4 * 32 + lane;
       const uint32_t tl = tmem + (uint32_t(q4 * 32) << 16);
       const bool issuer = tid == 128;
-      float* mx = reinterpret_cast<float*>(gb + kOffMx);
-      const uint32_t pv_p = mapa(sb + kOffP, other);
-      const uint32_t pv_pfull = mapa(bar(B_PFULL), other);
+      float* sum_s = reinterpret_cast<float*>(gb + kOffSum);
       const uint32_t pv_fin = mapa(sb + kOffFin, other);
       const uint32_t pv_finbar = mapa(bar(B_FIN), other);
       const uint32_t sempty_lead = mapa(bar(B_SEMPTY), lead);
       const uint32_t qready_lead = mapa(bar(B_QREADYP), lead);
       const bool raw_scores = p.scale_log2 > 0.f;
       const float sc = raw_scores ? p.scale_log2 : 1.f;
-      bool ok = true, issuer_ok = true, hidden_nonfinite = false, bad_slot = false;
+      bool ok = true, hidden_nonfinite = false, bad_slot = false;
       int T = 0, f = 0;
       int last_b = -1;          // request of the piece before,
       bool all_valid = false;   // and whether every key of it has a row
@@ -428,14 +454,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = w.piece();
         tiles.t0 = w.k;
         w.next_piece();
+        // Tiles that lie inside for every row of the unit, with a row behind every
+        // key: [0, in_a) among the sinks and [in_b, in_c) of the window (counted from
+        // the piece's first).
+        int in_a = 0, in_b = 0, in_c = 0;
+        if (all_valid) {
+          const int seen = (pos_a + 1) / kTile;      // tiles of the list that all rows reach
+          const int whole = p.sinks / kTile < seen ? p.sinks / kTile : seen;
+          in_a = (tiles.nst < whole ? tiles.nst : whole) - tiles.t0;
+          // list tile x >= wt is the unit's tile x - wt + nst
+          const int from = (first_z + kTile - 1) / kTile;
+          in_b = (from > tiles.wt ? from : tiles.wt) - tiles.wt + tiles.nst - tiles.t0;
+          in_c = seen - tiles.wt + tiles.nst - tiles.t0;
+        }
         for (int i = 0; i < n; ++i, ++T, ++f) {
-          const int bs = T & 1, pb = T % kPBufs;
-          const int tk0 = tiles.tile_key(i);
-          // Which of the half's 32 keys this row sees.  Most tiles lie inside for
-          // every row of the unit, with a row behind every key.
-          const bool inside = tk0 + kTile <= pos_a + 1 && (tk0 >= first_z || tk0 + kTile <= p.sinks);
-          uint32_t v32 = 0xffffffffu;
-          if (!all_valid || !inside) {
+          const int bs = T & 1;
+          float* mx = reinterpret_cast<float*>(gb + kOffMx) + bs * 2 * kRows;
+          uint32_t v32 = 0xffffffffu;   // which of the half's 32 keys this row sees
+          if (!(i < in_a || (i >= in_b && i < in_c))) {
+            const int tk0 = tiles.tile_key(i);
             uint32_t valid = 0u;
             if (p.valid) {
               const int c = N - (tk0 + 32 * half);   // of them in the list
@@ -465,11 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tl + kTmemS + 64u * uint32_t(bs) + 32u * uint32_t(half), sv);
             tmem_wait_ld();
             tc_fence_before();
-            if (even) {
-              mbar_arrive(bar(B_SEMPTY + bs));
-            } else {
-              __syncwarp();
-              if (lane == 0) mbar_arrive_remote_relaxed(sempty_lead + 8u * uint32_t(bs));
+            __syncwarp();
+            if (lane == 0) {
+              if (even) mbar_arrive(bar(B_SEMPTY + bs));
+              else mbar_arrive_remote_relaxed(sempty_lead + 8u * uint32_t(bs));
             }
             // With a positive scale (the usual case) the scores stay raw, their
             // maximum is scaled, and each exponent is one multiply-add.
@@ -495,8 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (row_ok) mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
           }
           mx[half * kRows + r] = mth;
-          if (issuer) bulk_wait_read<1>();   // staging buffer bs: the copy two tiles back has read it
-          if (!named_sync_and(kRowBar, kSoftmax, wok && issuer_ok)) {
+          if (!named_sync_and(kRowBar, kSoftmax, wok)) {
             if (issuer) fail();
             ok = false;
             break;
@@ -516,6 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[c] = pack_bf16(ex2_approx(fmaf(x[2 * c], sc, -mr)),
                               ex2_approx(fmaf(x[2 * c + 1], sc, -mr)), lt);
           l += lt;
+          // the copy two tiles back has read the staging buffer (should the wait
+          // give up, the next barrier ends the run for everyone)
+          if (T >= 2 && !wait(B_STGFREE + bs, (T >> 1) - 1)) fail();
           uint8_t* stg = gb + kOffStage + uint32_t(bs) * kPBufBytes;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -527,22 +565,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) reinterpret_cast<uint32_t*>(stg + kPFlags)[q4] = moved ? 1u : 0u;
           }
           fence_proxy_async_cta();   // staging writes, read by the bulk copy
-          named_sync(kRowBar, kSoftmax);
-          if (issuer) {
-            issuer_ok = T < kPBufs || wait_far(B_PFREE + pb, T / kPBufs - 1);
-            if (issuer_ok) {
-              bulk_copy_to_cluster(pv_p + uint32_t(pb) * kPBufBytes, smem_u32(stg), kPPayload,
-                                   pv_pfull + 8u * uint32_t(pb));
-              bulk_commit();
-            }
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_STGFULL + bs));
         }
         if (!ok) break;
         // row sums: the two warpgroups' partial sums share the reference
-        mx[half * kRows + r] = l;
+        sum_s[half * kRows + r] = l;
         named_sync(kRowBar, kSoftmax);
         if (half == 0) {
-          const float lt = mx[r] + mx[kRows + r];
+          const float lt = sum_s[r] + sum_s[kRows + r];
           const float lse = lt == 0.f ? -INFINITY : (m_ref + log2f(lt)) * kLn2;
           if (row_ok) {
             if (direct) p.lse[grow + r] = lse;
@@ -555,17 +586,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (bad_slot) atomicOr(cta_flags, VA_STATUS_BAD_SLOT);
       if (hidden_nonfinite) atomicOr(cta_flags, kFlagHiddenNonfinite);
-      if (issuer) {
-        // the last copies have read the staging buffers, and the PV CTAs' last
-        // releases have landed, before this shared memory goes away
-        bulk_wait_read<0>();
-        if (!issuer_ok) fail();
-        if (ok)
-          for (int t = T > kPBufs ? T - kPBufs : 0; t < T; ++t)
-            if (!mbar_wait<true>(bar(B_PFREE + t % kPBufs), uint32_t(t / kPBufs) & 1u, abort_flag,
-                                 kWaitCycles))
-              fail();
-      }
     }
   } else {
     // ================================================================ PV CTA
