@@ -25,6 +25,18 @@
 //  - The QK SMs' ring holds five slots of 36 KB: a slot takes an SM's 32 keys of a
 //    tile, or a quarter of its 128 query rows, which pass through the ring like
 //    tiles on their way to tensor memory.
+//  - The two softmax warpgroups take alternate tiles, a thread a row of 64 keys, so
+//    a tile's scores, exponentials and probabilities have two tiles' time.  Only the
+//    row's reference maximum goes from tile to tile.  (Sharing every tile, 32 keys a
+//    thread, a tile's chain of load, maximum, barrier, exponentials and hand-over
+//    took 1600 cycles, longer than its products.)  And one thread issues a tile's
+//    products in one go: with an election per product they went out every 37 to 41
+//    cycles, where the tensor cores need 32.  Either change alone gained 0 to 4%,
+//    both 15%.
+//
+// A request of 512 tokens, 64 heads, with 16k keys in front: 778 us, 78% of the
+// cuBLAS rate; per tile about 1590 cycles, of which the QK SMs' tensor cores work
+// 1152.
 //
 // Every wait is bounded; a role that gives up sets VA_STATUS_TIMEOUT and its CTA
 // drains its copies and products before it leaves.
@@ -101,15 +113,16 @@ constexpr int B_OFREE = B_OFULL + 1;           // PV: its O has been read
 constexpr int B_FIN = B_OFREE + 1;             // [kFinRing] PV: row sums from QK
 constexpr int B_STGFULL = B_FIN + kFinRing;    // [2] QK: a P staging buffer written
 constexpr int B_STGFREE = B_STGFULL + 2;       // [2] QK: read by its copy
-constexpr int B_MMAFIN = B_STGFREE + 2;
+constexpr int B_REF = B_STGFREE + 2;           // [2][4] QK: a tile's references, by quadrant
+constexpr int B_MMAFIN = B_REF + 8;
 constexpr int kNumBars = B_MMAFIN + 1;
 
 // Shared layout (offsets from a 1024-byte aligned base).
 constexpr uint32_t kOffTmemSlot = 512, kOffAbort = 516, kOffCmd = 520, kOffFlags = 524;
 constexpr uint32_t kOffRun = 544;              // RunPlace
 constexpr uint32_t kOffPeerAny = 640;          // PV, even rank: uint32 [kPBufs]
-constexpr uint32_t kOffMx = 1024;              // QK: float [2][2][128] half maxima, by tile parity
-constexpr uint32_t kOffSum = 3072;             // QK: float [2][128] half sums
+constexpr uint32_t kOffRef = 1024;             // QK: float [2][128] reference maxima, by tile parity
+constexpr uint32_t kOffSum = 2048;             // QK: float [2][2][128] partial sums, their references
 constexpr uint32_t kOffFin = 2048;             // PV: float [kFinRing][128] 1 / row sum
 constexpr uint32_t kOffK = 4096;               // QK: ring
 constexpr uint32_t kOffStage = kOffK + kRing * kSlotBytes;   // QK: P staging [2]
@@ -200,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t cnt = 1;
       // the odd rank's eight row warps add one arrival each
       if (i == B_OCORR || i == B_OFREE) cnt = kSoftmax + kSoftmax / 32;
-      if (i == B_SEMPTY || i == B_SEMPTY + 1) cnt = 2 * kSoftmax / 32;
-      if (i == B_STGFULL || i == B_STGFULL + 1) cnt = kSoftmax / 32;
+      // a tile's four softmax warps, of both CTAs of the pair or of one
+      if (i == B_SEMPTY || i == B_SEMPTY + 1) cnt = 8;
+      if (i == B_STGFULL || i == B_STGFULL + 1) cnt = 4;
       if (i == B_QREADY) cnt = kSoftmax;
       if (i == B_QREADYP) cnt = kSoftmax / 32;
       if (i >= B_FIN && i < B_FIN + kFinRing) cnt = 4;   // the first four row warps
@@ -330,15 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem + kTmemS + 64u * uint32_t(bs);
           const uint64_t b0 = smem_desc(sb + kOffK + uint32_t(s) * kSlotBytes, 16, 1024, kSwizzle128B);
+          if (elect_one()) {
 #pragma unroll
-          for (int c = 0; c < kBlocks; ++c)
+            for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma2_ts_warp(d, tmem + kTmemQ + 8u * uint32_t(4 * c + kk),
-                           b0 + uint64_t((uint32_t(c) * kBlockBytes + uint32_t(kk) * 32u) >> 4), idesc,
-                           (c | kk) != 0 ? 1u : 0u);
-          mma2_commit_mc_warp(bar(B_SFULL + bs), kQkMask);
-          mma2_commit_mc_warp(bar(B_EMPTY + s), kQkMask);
+              for (int kk = 0; kk < 4; ++kk)
+                mma2_ts(d, tmem + kTmemQ + 8u * uint32_t(4 * c + kk),
+                        b0 + uint64_t((uint32_t(c) * kBlockBytes + uint32_t(kk) * 32u) >> 4), idesc,
+                        (c | kk) != 0 ? 1u : 0u);
+            mma2_commit_mc(bar(B_SFULL + bs), kQkMask);
+            mma2_commit_mc(bar(B_EMPTY + s), kQkMask);
+          }
+          __syncwarp();
         }
         if (!ok && lane == 0) fail();
         mma2_commit_mc_warp(bar(B_MMAFIN), kQkMask);
@@ -371,10 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp >= 4) {
-      // ---- softmax: warpgroup `half` owns 32 of a tile's 64 keys for row r
+      // ---- softmax: the warpgroups take alternate tiles, a thread a row's 64
+      // keys.  A row's reference maximum goes from tile to tile, so from warp to warp
+      // of a quadrant, through shared memory; everything else of a tile -- its
+      // scores, exponentials and probabilities -- has two tiles' time.  Each
+      // warpgroup keeps its own part of a row's sum, to the reference of its last
+      // tile.
+      const int wg = half;
       const int r = q4 * 32 + lane;
       const uint32_t tl = tmem + (uint32_t(q4 * 32) << 16);
-      const bool issuer = tid == 128;
+      float* ref_s = reinterpret_cast<float*>(gb + kOffRef);
       float* sum_s = reinterpret_cast<float*>(gb + kOffSum);
       const uint32_t pv_fin = mapa(sb + kOffFin, other);
       const uint32_t pv_finbar = mapa(bar(B_FIN), other);
@@ -386,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int T = 0, f = 0;
       int last_b = -1;          // request of the piece before,
       bool all_valid = false;   // and whether every key of it has a row
-      for (int u = 0; ok && w.more(); ++u) {
+      for (int u = 0; w.more(); ++u) {
         // one piece: the tiles of this unit that lie in the run
         const int rows = w.rows() - hh * kRows;            // of this CTA
         const bool row_ok = r < rows;
@@ -413,12 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           all_valid = named_sync_and(kRowBar, kSoftmax, all);
         }
         // The unit's queries: this warp's quarter of the rows, column blocks 0-4
-        // or 5-8, into tensor memory.  (The products of the unit before are done:
-        // its last scores have been read.)
+        // or 5-8, into tensor memory, once the products of the unit before are done
+        // (its last scores are complete).
         {
           const int s = (f + q4) % kRing;
-          const bool got = __all_sync(0xffffffffu, wait(B_QFULL + q4, u));
+          const bool got = __all_sync(
+              0xffffffffu, wait(B_QFULL + q4, u) &&
+                               (T == 0 || wait(B_SFULL + ((T - 1) & 1), (T - 1) >> 1)));
           if (got) {
+            tc_fence_after();
             const uint32_t row_addr = sb + kOffK + uint32_t(s) * kSlotBytes + uint32_t(lane) * 128u;
 #pragma unroll 1
             for (int c = half ? 5 : 0; c < (half ? 9 : 5); ++c) {
@@ -435,11 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           if (!named_sync_and(kRowBar, kSoftmax, got)) {
-            if (issuer) fail();
-            ok = false;
+            if (tid == 128) fail();
             break;
           }
-          if (issuer)
+          if (tid == 128)
             for (int i = 0; i < kQSlots; ++i) mbar_arrive(bar(B_EMPTY + (f + i) % kRing));
           if (even) {
             mbar_arrive(bar(B_QREADY));
@@ -449,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           f += kQSlots;
         }
-        float m_ref = -INFINITY, l = 0.f;
+        float m_ref = -INFINITY, l = 0.f;   // of this warpgroup's last tile
         ChunkTiles tiles = w.t;   // (the tile's index is all that moves)
         const int n = w.piece();
         tiles.t0 = w.k;
@@ -467,114 +492,134 @@ __global__ void __launch_bounds__(kThreads, 1)
           in_b = (from > tiles.wt ? from : tiles.wt) - tiles.wt + tiles.nst - tiles.t0;
           in_c = seen - tiles.wt + tiles.nst - tiles.t0;
         }
-        for (int i = 0; i < n; ++i, ++T, ++f) {
-          const int bs = T & 1;
-          float* mx = reinterpret_cast<float*>(gb + kOffMx) + bs * 2 * kRows;
-          uint32_t v32 = 0xffffffffu;   // which of the half's 32 keys this row sees
-          if (!(i < in_a || (i >= in_b && i < in_c))) {
+        // (after a wait gave up a warp goes on to the unit's end, where all agree)
+        for (int i = (T & 1) == wg ? 0 : 1; ok && i < n; i += 2) {
+          const int t = T + i, bs = wg;
+          const bool inside = i < in_a || (i >= in_b && i < in_c);
+          uint64_t v64 = ~0ull;   // which of the tile's 64 keys this row sees
+          if (!inside) {
             const int tk0 = tiles.tile_key(i);
-            uint32_t valid = 0u;
+            uint64_t valid = 0ull;
             if (p.valid) {
-              const int c = N - (tk0 + 32 * half);   // of them in the list
-              const int64_t e = base + tk0 + 32 * half;
-              if (c > 0)
-                valid = __funnelshift_r(__ldg(p.valid + (e >> 5)), __ldg(p.valid + (e >> 5) + 1),
-                                        uint32_t(e) & 31u) & uint32_t(low_bits(c));
+              const int c = N - tk0;   // of them in the list
+              const int64_t e = base + tk0;
+              if (c > 0) {
+                const uint32_t* v = p.valid + (e >> 5);
+                const uint32_t x0 = __ldg(v), x1 = __ldg(v + 1), x2 = __ldg(v + 2);
+                valid = (uint64_t(__funnelshift_r(x1, x2, uint32_t(e) & 31u)) << 32 |
+                         __funnelshift_r(x0, x1, uint32_t(e) & 31u)) & low_bits(c);
+              }
             } else {
-              const int64_t a = base + tk0 + 32 * half;   // pool row of the first
+              const int64_t a = base + tk0;   // pool row of the first
               const int64_t lo = -a, hi = p.num_slots - a;
-              valid = uint32_t(low_bits(hi > 64 ? 64 : int(hi < 0 ? 0 : hi)) &
-                               ~low_bits(lo > 64 ? 64 : int(lo < 0 ? 0 : lo)));
+              valid = low_bits(hi > 64 ? 64 : int(hi < 0 ? 0 : hi)) &
+                      ~low_bits(lo > 64 ? 64 : int(lo < 0 ? 0 : lo));
               const uint64_t seen =
                   low_bits(k1 - tk0) & (~low_bits(first_a - tk0) | low_bits(p.sinks - tk0));
-              bad_slot |= (uint32_t(seen >> (32 * half)) & ~valid) != 0u;
+              bad_slot |= (seen & ~valid) != 0ull;
             }
             const uint64_t vis =
                 low_bits(pos + 1 - tk0) & (~low_bits(first - tk0) | low_bits(p.sinks - tk0));
-            v32 = uint32_t(vis >> (32 * half)) & valid;
+            v64 = vis & valid;
           }
-          const bool wok = __all_sync(0xffffffffu, wait(B_SFULL + bs, T >> 1));
-          float x[32];
-          float mth = -INFINITY;
-          if (wok) {
-            tc_fence_after();
-            uint32_t sv[32];
-            tmem_ld32(tl + kTmemS + 64u * uint32_t(bs) + 32u * uint32_t(half), sv);
+          ok = __all_sync(0xffffffffu, wait(B_SFULL + bs, t >> 1));
+          if (!ok) break;
+          float x[64];
+          tc_fence_after();
+          {
+            uint32_t a[32], b[32];
+            tmem_ld32(tl + kTmemS + 64u * uint32_t(bs), a);
+            tmem_ld32(tl + kTmemS + 64u * uint32_t(bs) + 32u, b);
             tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (even) mbar_arrive(bar(B_SEMPTY + bs));
-              else mbar_arrive_remote_relaxed(sempty_lead + 8u * uint32_t(bs));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              x[c] = __uint_as_float(a[c]);
+              x[32 + c] = __uint_as_float(b[c]);
             }
-            // With a positive scale (the usual case) the scores stay raw, their
-            // maximum is scaled, and each exponent is one multiply-add.
-            if (v32 == 0xffffffffu && raw_scores) {
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (even) mbar_arrive(bar(B_SEMPTY + bs));
+            else mbar_arrive_remote_relaxed(sempty_lead + 8u * uint32_t(bs));
+          }
+          // With a positive scale (the usual case) the scores stay raw, their
+          // maximum is scaled, and each exponent is one multiply-add.
+          if (v64 != ~0ull || !raw_scores) {
+            if (row_ok) {
+              // a hidden key whose score is not finite (see kFlagHiddenNonfinite)
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(sv[c]);
-            } else {
-              if (row_ok) {
-                // a hidden key whose score is not finite (see kFlagHiddenNonfinite)
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  hidden_nonfinite |= !((v32 >> c) & 1u) && (sv[c] & 0x7f800000u) == 0x7f800000u;
-              }
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                x[c] = ((v32 >> c) & 1u) ? __uint_as_float(sv[c]) * (raw_scores ? 1.f : p.scale_log2)
-                                         : -INFINITY;
+              for (int c = 0; c < 64; ++c)
+                hidden_nonfinite |= !((v64 >> c) & 1ull) &&
+                                    (__float_as_uint(x[c]) & 0x7f800000u) == 0x7f800000u;
             }
-            float t4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int c = 4; c < 32; ++c) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
-            // (a row past the unit's is not written, and must not move anything)
-            if (row_ok) mth = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+            for (int c = 0; c < 64; ++c)
+              x[c] = ((v64 >> c) & 1ull) ? x[c] * (raw_scores ? 1.f : p.scale_log2) : -INFINITY;
           }
-          mx[half * kRows + r] = mth;
-          if (!named_sync_and(kRowBar, kSoftmax, wok)) {
-            if (issuer) fail();
-            ok = false;
-            break;
+          float t4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int c = 4; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], x[c]);
+          // (a row past the unit's is not written, and must not move anything)
+          const float mt =
+              row_ok ? fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc : -INFINITY;
+          // the reference of the tile before, and on to the tile after
+          float before = -INFINITY;
+          if (i > 0) {
+            if (!wait(B_REF + 4 * (bs ^ 1) + q4, (t - 1) >> 1)) fail();
+            before = ref_s[(bs ^ 1) * kRows + r];
           }
-          const float mt = fmaxf(mx[r], mx[kRows + r]);
-          float alpha = 1.f;
-          if (mt > m_ref + kRescaleLog2) {
-            alpha = ex2_approx(m_ref - mt);   // 0 when nothing was seen before
-            l *= alpha;
-            m_ref = mt;
+          float now = before, alpha = 1.f;
+          if (mt > before + kRescaleLog2) {
+            now = mt;
+            alpha = ex2_approx(before - mt);   // 0 when nothing was seen before
           }
-          const float mr = m_ref == -INFINITY ? 0.f : m_ref;
-          uint32_t pk[16];
+          ref_s[bs * kRows + r] = now;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_REF + 4 * bs + q4));
+          if (now != m_ref) {
+            l *= ex2_approx(m_ref - now);   // (NaN stays)
+            m_ref = now;
+          }
+          const float mr = now == -INFINITY ? 0.f : now;
+          // the copy two tiles back has read the staging buffer
+          if (t >= 2 && !wait(B_STGFREE + bs, (t >> 1) - 1)) fail();
+          uint8_t* stg = gb + kOffStage + uint32_t(bs) * kPBufBytes;
           float lt = 0.f;
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            pk[c] = pack_bf16(ex2_approx(fmaf(x[2 * c], sc, -mr)),
-                              ex2_approx(fmaf(x[2 * c + 1], sc, -mr)), lt);
-          l += lt;
-          // the copy two tiles back has read the staging buffer (should the wait
-          // give up, the next barrier ends the run for everyone)
-          if (T >= 2 && !wait(B_STGFREE + bs, (T >> 1) - 1)) fail();
-          uint8_t* stg = gb + kOffStage + uint32_t(bs) * kPBufBytes;
+          for (int j = 0; j < 8; ++j) {
+            uint32_t pk[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(stg + r * 128 + (((4 * half + j) ^ (r & 7)) * 16)) =
-                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-          if (half == 0) {
-            reinterpret_cast<float*>(stg + kPAlpha)[r] = alpha;
-            const uint32_t moved = __ballot_sync(0xffffffffu, alpha != 1.f);
-            if (lane == 0) reinterpret_cast<uint32_t*>(stg + kPFlags)[q4] = moved ? 1u : 0u;
+            for (int c = 0; c < 4; ++c)
+              pk[c] = pack_bf16(ex2_approx(fmaf(x[8 * j + 2 * c], sc, -mr)),
+                                ex2_approx(fmaf(x[8 * j + 2 * c + 1], sc, -mr)), lt);
+            *reinterpret_cast<uint4*>(stg + r * 128 + ((j ^ (r & 7)) * 16)) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
+          l += lt;
+          reinterpret_cast<float*>(stg + kPAlpha)[r] = alpha;
+          const uint32_t moved = __ballot_sync(0xffffffffu, alpha != 1.f);
+          if (lane == 0) reinterpret_cast<uint32_t*>(stg + kPFlags)[q4] = moved ? 1u : 0u;
           fence_proxy_async_cta();   // staging writes, read by the bulk copy
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_STGFULL + bs));
         }
-        if (!ok) break;
-        // row sums: the two warpgroups' partial sums share the reference
-        sum_s[half * kRows + r] = l;
-        named_sync(kRowBar, kSoftmax);
-        if (half == 0) {
-          const float lt = sum_s[r] + sum_s[kRows + r];
-          const float lse = lt == 0.f ? -INFINITY : (m_ref + log2f(lt)) * kLn2;
+        T += n;
+        f += n;
+        // row sums: the two warpgroups' parts, to the unit's last reference
+        sum_s[wg * kRows + r] = l;
+        sum_s[(2 + wg) * kRows + r] = m_ref;
+        if (!named_sync_and(kRowBar, kSoftmax, ok)) {
+          if (tid == 128) fail();
+          break;
+        }
+        if (wg == 0) {
+          const float l1 = sum_s[kRows + r], m1 = sum_s[3 * kRows + r];
+          const float m = fmaxf(m_ref, m1);
+          float lt = 0.f;
+          if (m_ref != -INFINITY || l != 0.f) lt += l * ex2_approx(m_ref - m);
+          if (m1 != -INFINITY || l1 != 0.f) lt += l1 * ex2_approx(m1 - m);
+          const float lse = lt == 0.f ? -INFINITY : (m + log2f(lt)) * kLn2;
           if (row_ok) {
             if (direct) p.lse[grow + r] = lse;
             else p.part_lse[slot * kUnitRows + hh * kRows + r] = lse;
@@ -672,20 +717,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_cta();
         tc_fence_after();
         const uint64_t ad = smem_desc(pbase, 16, 1024, kSwizzle128B);
+        if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < kDv / 256; ++q) {
-          const uint64_t bd = smem_desc(sb + kOffV + uint32_t(s) * kVTileBytes + uint32_t(2 * q) * kVBlock,
-                                        kVBlock, 1024, kSwizzle128B);
+          for (int q = 0; q < kDv / 256; ++q) {
+            const uint64_t bd = smem_desc(sb + kOffV + uint32_t(s) * kVTileBytes + uint32_t(2 * q) * kVBlock,
+                                          kVBlock, 1024, kSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma2_ss_warp(tmem + uint32_t(256 * q), ad + uint64_t((uint32_t(k) * 32u) >> 4),
-                         bd + uint64_t((uint32_t(k) * 2048u) >> 4), idesc, (!first || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kTile / 16; ++k)
+              mma2_ss(tmem + uint32_t(256 * q), ad + uint64_t((uint32_t(k) * 32u) >> 4),
+                      bd + uint64_t((uint32_t(k) * 2048u) >> 4), idesc, (!first || k > 0) ? 1u : 0u);
+          }
+          mma2_commit_mc(bar(B_VEMPTY + s), kPvMask);
+          // re-armed before its release can reach the QK CTA
+          if (T + kPBufs < steps) mbar_arrive_expect_tx(bar(B_PFULL + pb), kPPayload);
+          mma2_commit_mc(bar(B_PFREE + pb), kQkMask);
         }
-        mma2_commit_mc_warp(bar(B_VEMPTY + s), kPvMask);
-        // re-armed before its release can reach the QK CTA
-        if (lane == 0 && T + kPBufs < steps) mbar_arrive_expect_tx(bar(B_PFULL + pb), kPPayload);
         __syncwarp();
-        mma2_commit_mc_warp(bar(B_PFREE + pb), kQkMask);
         if (--n == 0) {   // the unit's last product here: its rows may be written out
           mma2_commit_mc_warp(bar(B_OFULL), kPvMask);
           command(kCmdUnit);
