@@ -276,21 +276,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_o = idesc_bf16(128, uint32_t(n16), 1, 0);
       const uint32_t v0 = sb + kOffK + uint32_t(s & 1) * kTileBytes;
       const uint64_t bd = smem_desc(sb + kOffP, 16, 1024, kSwizzle128B);
+      if (elect_one()) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint64_t ad = smem_desc(v0 + uint32_t(2 * m) * kSlot, kSlot, 1024, kSwizzle128B);
+        for (int m = 0; m < 4; ++m) {
+          const uint64_t ad = smem_desc(v0 + uint32_t(2 * m) * kSlot, kSlot, 1024, kSwizzle128B);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ss_warp(tmem + kTmemO + uint32_t(64 * m), ad + uint64_t((uint32_t(k) * 2048u) >> 4),
-                      bd + uint64_t((uint32_t(k) * 32u) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
-        // blocks 0-2, 3-5 and 6-8 are done with after value blocks 0-3, 4-5, 6-7
-        if (m > 0) mma_commit_warp(bar(B_KEMPTY + (s & 1) * kGroups + m - 1));
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ss(tmem + kTmemO + uint32_t(64 * m), ad + uint64_t((uint32_t(k) * 2048u) >> 4),
+                   bd + uint64_t((uint32_t(k) * 32u) >> 4), idesc_o, (!first || k > 0) ? 1u : 0u);
+          // blocks 0-2, 3-5 and 6-8 are done with after value blocks 0-3, 4-5, 6-7
+          if (m > 0) mma_commit(bar(B_KEMPTY + (s & 1) * kGroups + m - 1));
+        }
+        mma_commit(bar(B_PFREE));
+        if (last) mma_commit(bar(B_OFULL));
       }
-      mma_commit_warp(bar(B_PFREE));
-      if (last) {
-        mma_commit_warp(bar(B_OFULL));
-        ++piece;
-      }
+      __syncwarp();
+      if (last) ++piece;
       return true;
     };
     // the tile whose second product is still to be issued
@@ -319,24 +320,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
 #pragma unroll
-      for (int c = 0; c < kBlocks; ++c) {
-        if (c % 3 == 0) {
-          ok = ok && __all_sync(0xffffffffu, wait(full + c / 3, uint32_t(s >> 1)));
-          if (!ok) break;
-          fence_proxy_async_cta();   // the producers' copies, seen by the tensor core
-          tc_fence_after();
-        }
-        const uint64_t ad = smem_desc(sb + kOffQ + uint32_t(c) * kSlot, 16, 1024, kSwizzle128B);
-        const uint64_t bd = smem_desc(sb + kOffK + uint32_t(s & 1) * kTileBytes + uint32_t(c) * kSlot,
-                                      16, 1024, kSwizzle128B);
+      for (int g = 0; g < kGroups; ++g) {
+        ok = ok && __all_sync(0xffffffffu, wait(full + g, uint32_t(s >> 1)));
+        if (!ok) break;
+        fence_proxy_async_cta();   // the producers' copies, seen by the tensor core
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss_warp(tmem + kTmemS + uint32_t(64 * (s & 1)), ad + uint64_t(2 * kk),
-                      bd + uint64_t(2 * kk), idesc_s, (c | kk) != 0 ? 1u : 0u);
+          for (int c = 3 * g; c < 3 * g + 3; ++c) {
+            const uint64_t ad = smem_desc(sb + kOffQ + uint32_t(c) * kSlot, 16, 1024, kSwizzle128B);
+            const uint64_t bd = smem_desc(
+                sb + kOffK + uint32_t(s & 1) * kTileBytes + uint32_t(c) * kSlot, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss(tmem + kTmemS + uint32_t(64 * (s & 1)), ad + uint64_t(2 * kk),
+                     bd + uint64_t(2 * kk), idesc_s, (c | kk) != 0 ? 1u : 0u);
+          }
+          if (g + 1 == kGroups) {
+            mma_commit(bar(B_SFULL + (s & 1)));
+            if (last) mma_commit(bar(B_QEMPTY));
+          }
+        }
+        __syncwarp();
       }
       if (!ok) break;
-      mma_commit_warp(bar(B_SFULL + (s & 1)));
-      if (last) mma_commit_warp(bar(B_QEMPTY));
       if (pending && !second(s - 1, pend_n, pend_first, pend_last)) {
         ok = false;
         break;
