@@ -383,20 +383,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t ad = smem_desc(sb + C::kOffK + uint32_t(c) * kKSlot, 16, 1024, kSwizzle128B);
           const uint64_t bd =
               smem_desc(sb + C::kOffQ + uint32_t(qs) * C::kQSlot, 16, 1024, kSwizzle128B);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t acc = (c | kk) != 0 ? 1u : 0u;
-            if constexpr (kPair) mma2_ss_warp(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc, acc);
-            else mma_ss_warp(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc, acc);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t acc = (c | kk) != 0 ? 1u : 0u;
+              if constexpr (kPair) mma2_ss(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc, acc);
+              else mma_ss(d, ad + uint64_t(2 * kk), bd + uint64_t(2 * kk), idesc, acc);
+            }
+            if (last_q) {
+              if constexpr (kPair) mma2_commit_mc(bar(C::B_QEMPTY + qs), kBoth);
+              else mma_commit(bar(C::B_QEMPTY + qs));
+            }
+            if (last_k && c == 3 * g + 2) {
+              if constexpr (kPair) mma2_commit_mc(bar(C::B_KEMPTY + g), kBoth);
+              else mma_commit(bar(C::B_KEMPTY + g));
+            }
           }
-          if (last_q) {
-            if constexpr (kPair) mma2_commit_mc_warp(bar(C::B_QEMPTY + qs), kBoth);
-            else mma_commit_warp(bar(C::B_QEMPTY + qs));
-          }
-          if (last_k && c == 3 * g + 2) {
-            if constexpr (kPair) mma2_commit_mc_warp(bar(C::B_KEMPTY + g), kBoth);
-            else mma_commit_warp(bar(C::B_KEMPTY + g));
-          }
+          __syncwarp();
         }
         if (!ok) {
           if (lane == 0) fail();
