@@ -34,7 +34,7 @@
 //    cycles, where the tensor cores need 32.  Either change alone gained 0 to 4%,
 //    both 15%.
 //
-// A request of 512 tokens, 64 heads, with 16k keys in front: 778 us, 78% of the
+// A request of 512 tokens, 64 heads, with 16k keys in front: 780 us, 78% of the
 // cuBLAS rate; per tile about 1590 cycles, of which the QK SMs' tensor cores work
 // 1152.
 //
@@ -86,7 +86,7 @@ constexpr float kRescaleLog2 = 8.f;
 
 // What a unit costs besides its tiles, in tiles: queries into tensor memory, the
 // pipeline's fill, rows out of it.
-constexpr int kUnitCost = 5;
+constexpr int kUnitCost = 6;
 using Run = ChunkRun<kUnitRows, kUnitCost>;
 
 // Barriers: one layout in all four CTAs, QK and PV sides side by side.
