@@ -27,8 +27,11 @@
 // times as long).  In place, an output may lie where another warp still reads:
 // the kept entries then wait in shared memory until the cluster has read all of
 // a window of the list -- the whole list when what stays of it fits.
-// Bound by latency: barriers and dependent reads for a short list, the reads'
-// round trips for long ones.
+// Bound by latency: barriers and dependent reads for a short list (4096 entries:
+// 11 us, of which three digits take a third), and for long ones by how many
+// reads 27 warps of an SM keep on their way: 64 lists of 20k to 200k entries,
+// 76 us, a sixth of the memory's rate counted once; the compaction is a third of
+// it, the passes of the first two digits and the count a sixth each.
 #include <math.h>
 #include <string.h>
 
@@ -45,8 +48,9 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kWarps = kEvictThreads / 32;
 constexpr int kBits1 = 12, kBits2 = 10, kBits3 = 10;   // digits, from the top
-constexpr int kCtaBudget = 2;
-constexpr int kPer = 8;                                // entries of a thread and round
+constexpr int kCtaBudget = 2;   // CTAs per SM that a launch may fill (see va_kv_evict)
+constexpr int kPer = 8;                                // entries of a thread and step
+constexpr int kBatch = 16;                             // of a thread at once in the histograms
 constexpr int kList = 4096;                            // collected candidates per CTA
 constexpr int kHeld = 10240;                           // kept entries that a CTA can hold back
 
@@ -160,6 +164,7 @@ __device__ void find_digit(EvictSmem& sm, const uint32_t* hist, int ctas, uint32
 #pragma unroll
   for (int k = 0; k < kN; ++k) bin[k] = 0;
   const uint32_t at = smem_u32(hist + t * kN);
+#pragma unroll 4
   for (int c = 0; c < ctas; ++c) {
     const uint32_t a = sm100::mapa(at, uint32_t(c));
     if constexpr (kN % 4 == 0) {
@@ -253,23 +258,34 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
   if (nfreed && m > 0) {
     const float* w = p.weights + base;
     want = uint32_t(m);
-#pragma unroll 16
-    for (int i = c0 + tid; i < c1; i += kEvictThreads)
-      atomicAdd(&sm.hist1[weight_key(w[i]) >> (kBits2 + kBits3)], 1u);
+    // all of this CTA's candidates, kBatch loads of a thread on their way at once,
+    // the last ones included
+    auto each = [&](auto&& use) {
+      for (int i0 = c0 + tid; i0 < c1; i0 += kBatch * kEvictThreads) {
+        float x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = i0 + k * kEvictThreads;
+          x[k] = i < c1 ? w[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * kEvictThreads < c1) use(weight_key(x[k]));
+      }
+    };
+    each([&](uint32_t k) { atomicAdd(&sm.hist1[k >> (kBits2 + kBits3)], 1u); });
     sm100::cluster_sync();
     find_digit<1 << kBits1>(sm, sm.hist1, ctas, want);
     const uint32_t d1 = sm.digit;
     want -= sm.above;
     __syncthreads();
-#pragma unroll 16
-    for (int i = c0 + tid; i < c1; i += kEvictThreads) {
-      const uint32_t k = weight_key(w[i]);
+    each([&](uint32_t k) {
       if ((k >> (kBits2 + kBits3)) == d1) {
         atomicAdd(&sm.hist2[(k >> kBits3) & ((1u << kBits2) - 1u)], 1u);
         const uint32_t at = atomicAdd(&sm.nlist, 1u);
         if (at < kList) sm.list[at] = k & ((1u << (kBits2 + kBits3)) - 1u);
       }
-    }
+    });
     sm100::cluster_sync();
     find_digit<1 << kBits2>(sm, sm.hist2, ctas, want);
     const uint32_t d2 = sm.digit;
@@ -282,11 +298,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
         if ((sm.list[i] >> kBits3) == d2) atomicAdd(&sm.hist3[sm.list[i] & kLow], 1u);
     } else {   // more matched the first digit than the list holds
       const uint32_t d12 = d1 << kBits2 | d2;
-#pragma unroll 16
-      for (int i = c0 + tid; i < c1; i += kEvictThreads) {
-        const uint32_t k = weight_key(w[i]);
+      each([&](uint32_t k) {
         if ((k >> kBits3) == d12) atomicAdd(&sm.hist3[k & kLow], 1u);
-      }
+      });
     }
     sm100::cluster_sync();
     find_digit<1 << kBits3>(sm, sm.hist3, ctas, want);
@@ -375,6 +389,28 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
         const int i = i0 + 32 * k + lane;
         s[k] = i < q1 ? slot_in[i] : 0;
         v[k] = i < q1 ? w_in[i] : 0.f;
+      }
+      // The usual step: candidates all of them, none equal to the threshold, no
+      // output held back.
+      bool other = i0 < lo || i0 + kStep > (hi < q1 ? hi : q1) || p.hold || (fr && !fits);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) other |= fmaxf(v[k], -INFINITY) == T;
+      if (!__any_sync(0xffffffffu, other)) {
+        const uint32_t e0 = eq_kept(eq);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const bool a = v[k] > T;
+          const uint32_t ba = __ballot_sync(0xffffffffu, a);
+          const uint32_t at = stay + e0 + uint32_t(__popc(ba & below));
+          stay += uint32_t(__popc(ba));
+          if (a) {
+            slot_o[at] = s[k];
+            w_o[at] = v[k];
+          } else if (fr) {
+            fr[i0 + 32 * k + lane - int(at)] = s[k];
+          }
+        }
+        continue;
       }
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
@@ -503,8 +539,9 @@ VA_API int va_kv_evict(const int32_t* slot_idx, const int32_t* kv_indptr,
   // A length or head that is rewritten while other requests' CTAs still read
   // it for their place in the free list is left to a second kernel.
   p.finish = free_slots && (prefix_len_out == prefix_len || free_head_out == free_head);
-  // As many CTAs per request as the batch leaves room for, and no more than its
-  // average list has rounds for.
+  // As many CTAs per request as the batch leaves room for at once, and no more
+  // than its average list has steps for (64 lists of 20k to 200k entries: four
+  // CTAs each 82 us; two 96; eight, in two waves, 155).
   int ctas = 1;
   while (ctas < 8 && int64_t(2 * ctas) * B <= kCtaBudget * di.num_sms &&
          num_entries / B > int64_t(ctas) * kPer * kEvictThreads)
