@@ -470,7 +470,7 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *                  num_entries, flags) bytes, 256-byte aligned; first 4 bytes:
  *                  the status word, rewritten by every call.  It includes room
  *                  for the listed rows (1152 bytes per entry) when the average
- *                  request brings 1024 query rows (tokens x heads) or more: the
+ *                  request brings 640 query rows (tokens x heads) or more: the
  *                  call then first packs them side by side.
  *   out            bf16 [total_q, H, 512], 16-byte aligned; lse float
  *                  [total_q, H] (natural log).  A token none of whose keys has

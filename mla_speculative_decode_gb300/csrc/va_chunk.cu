@@ -11,10 +11,10 @@
 //
 // Two paths: the tensor cores -- a kernel for few rows per request
 // (va_decode_tc.cu), one for many (va_prefill_tc.cu), and between them that of the
-// verify calls in its chunk mode (va_tc.cu) -- followed by chunk_finish_kernel, which merges the splits; and one
-// warp per row on CUDA cores (VA_PATH_FMA), an independent implementation that
-// the finish kernel also uses for the rare rows that the products may have
-// spoilt (see kFlagHiddenNonfinite).
+// verify calls in its chunk mode (va_tc.cu) -- followed by chunk_finish_kernel,
+// which merges the splits; and one warp per row on CUDA cores (VA_PATH_FMA), an
+// independent implementation that the finish kernel also uses for the rare rows
+// that the products may have spoilt (see kFlagHiddenNonfinite).
 #include <string.h>
 
 #include "va_chunk.cuh"
@@ -91,109 +91,109 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
   }
   const bool hidden = __syncthreads_or((bits & kFlagHiddenNonfinite) != 0u);
   for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
-  // which of 256 units need work: listed in the same order by every CTA
-  ChunkUnit unit;
-  unit.ns = 1;
-  uint32_t f = 0u;
-  if (u0 + tid < total_units) {
-    unit = p.units[u0 + tid];
-    if (hidden)
-      for (int s = 0; s < unit.ns; ++s)
-        for (int c = 0; c < p.ctas; ++c)
-          f |= p.cta_flags[size_t(unit.item + s * unit.istride) * p.ctas + c];
-    if (f & kFlagHiddenNonfinite) unit.b = ~unit.b;
-  }
-  const bool need = unit.ns > 1 || (f & kFlagHiddenNonfinite);
-  const uint32_t ballot = __ballot_sync(0xffffffffu, need);
-  if (lane == 0) warp_count[warp] = __popc(ballot);
-  __syncthreads();
-  int at = __popc(ballot & ((1u << lane) - 1u)), count = 0;
-#pragma unroll
-  for (int k = 0; k < kFinishWarps; ++k) {
-    at += k < warp ? warp_count[k] : 0;
-    count += warp_count[k];
-  }
-  if (need) list[at] = unit;
-  __syncthreads();
-  for (int id = int(blockIdx.x) * kRowsPerCta + (kW == 1 ? warp : 0); id < count * U;
-       id += int(gridDim.x) * kRowsPerCta) {
-    const ChunkUnit& x = list[id / U];
-    const int r = id % U;
-    if (r >= x.rows) continue;
-    if (x.b < 0) {   // a hidden key may have spoilt the unit's rows
-      if (kW == 1 || warp == 0) {
-        bool bad = false;
-        chunk_row(p, chunk_req(p, ~x.b), (x.i0 + r) / p.H, (x.i0 + r) % p.H, lane, &bad);
-      }
-      continue;
+    // which of 256 units need work: listed in the same order by every CTA
+    ChunkUnit unit;
+    unit.ns = 1;
+    uint32_t f = 0u;
+    if (u0 + tid < total_units) {
+      unit = p.units[u0 + tid];
+      if (hidden)
+        for (int s = 0; s < unit.ns; ++s)
+          for (int c = 0; c < p.ctas; ++c)
+            f |= p.cta_flags[size_t(unit.item + s * unit.istride) * p.ctas + c];
+      if (f & kFlagHiddenNonfinite) unit.b = ~unit.b;
     }
-    const int ns = x.ns < kMaxNs ? x.ns : kMaxNs;
-    auto slot = [&](int s) -> size_t {
-      return size_t(s == 0 ? x.pslot : x.pslot1 + (s - 1) * x.pstride) * U + r;
-    };
-    float m = -INFINITY;
-    for (int s = lane; s < ns; s += 32) {
-      const float ls = p.part_lse[slot(s)];
-      w[s] = ls;
-      m = fmaxf(m, ls);
+    const bool need = unit.ns > 1 || (f & kFlagHiddenNonfinite);
+    const uint32_t ballot = __ballot_sync(0xffffffffu, need);
+    if (lane == 0) warp_count[warp] = __popc(ballot);
+    __syncthreads();
+    int at = __popc(ballot & ((1u << lane) - 1u)), count = 0;
+#pragma unroll
+    for (int k = 0; k < kFinishWarps; ++k) {
+      at += k < warp ? warp_count[k] : 0;
+      count += warp_count[k];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float z = 0.f;
-    for (int s = lane; s < ns; s += 32)
-      if (w[s] != -INFINITY) z += expf(w[s] - m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    const float L = z == 0.f ? -INFINITY : m + logf(z);
-    for (int s = lane; s < ns; s += 32) w[s] = w[s] == -INFINITY ? 0.f : expf(w[s] - L);
-    __syncwarp();
-    if (lane == 0 && (kW == 1 || warp == 0)) p.lse[x.row0 + r] = L;
-    // columns 4 * lane + 128 q .. + 3
-    float4 acc[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = kW == 1 ? 0 : warp; s < ns; s += kW) {
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(s) * kDv) + lane;
-      const float ws = w[s];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float4 v = src[32 * q];
-        acc[q].x = fmaf(ws, v.x, acc[q].x);
-        acc[q].y = fmaf(ws, v.y, acc[q].y);
-        acc[q].z = fmaf(ws, v.z, acc[q].z);
-        acc[q].w = fmaf(ws, v.w, acc[q].w);
-      }
-    }
-    __syncwarp();   // w is read
-    uint2* out = reinterpret_cast<uint2*>(p.out + size_t(x.row0 + r) * kDv);
-    auto pack = [](float4 v) -> uint2 {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-      return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    };
-    if constexpr (kW == 1) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) out[32 * q + lane] = pack(acc[q]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) sums[warp][32 * q + lane] = acc[q];
-      __syncthreads();
-      if (tid < kDv / 4) {
-        float4 t = sums[0][tid];
-#pragma unroll
-        for (int k = 1; k < kW; ++k) {
-          const float4 v = sums[k][tid];
-          t.x += v.x;
-          t.y += v.y;
-          t.z += v.z;
-          t.w += v.w;
+    if (need) list[at] = unit;
+    __syncthreads();
+    for (int id = int(blockIdx.x) * kRowsPerCta + (kW == 1 ? warp : 0); id < count * U;
+         id += int(gridDim.x) * kRowsPerCta) {
+      const ChunkUnit& x = list[id / U];
+      const int r = id % U;
+      if (r >= x.rows) continue;
+      if (x.b < 0) {   // a hidden key may have spoilt the unit's rows
+        if (kW == 1 || warp == 0) {
+          bool bad = false;
+          chunk_row(p, chunk_req(p, ~x.b), (x.i0 + r) / p.H, (x.i0 + r) % p.H, lane, &bad);
         }
-        out[tid] = pack(t);
+        continue;
       }
-      __syncthreads();
+      const int ns = x.ns < kMaxNs ? x.ns : kMaxNs;
+      auto slot = [&](int s) -> size_t {
+        return size_t(s == 0 ? x.pslot : x.pslot1 + (s - 1) * x.pstride) * U + r;
+      };
+      float m = -INFINITY;
+      for (int s = lane; s < ns; s += 32) {
+        const float ls = p.part_lse[slot(s)];
+        w[s] = ls;
+        m = fmaxf(m, ls);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float z = 0.f;
+      for (int s = lane; s < ns; s += 32)
+        if (w[s] != -INFINITY) z += expf(w[s] - m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      const float L = z == 0.f ? -INFINITY : m + logf(z);
+      for (int s = lane; s < ns; s += 32) w[s] = w[s] == -INFINITY ? 0.f : expf(w[s] - L);
+      __syncwarp();
+      if (lane == 0 && (kW == 1 || warp == 0)) p.lse[x.row0 + r] = L;
+      // columns 4 * lane + 128 q .. + 3
+      float4 acc[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int s = kW == 1 ? 0 : warp; s < ns; s += kW) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + slot(s) * kDv) + lane;
+        const float ws = w[s];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 v = src[32 * q];
+          acc[q].x = fmaf(ws, v.x, acc[q].x);
+          acc[q].y = fmaf(ws, v.y, acc[q].y);
+          acc[q].z = fmaf(ws, v.z, acc[q].z);
+          acc[q].w = fmaf(ws, v.w, acc[q].w);
+        }
+      }
+      __syncwarp();   // w is read
+      uint2* out = reinterpret_cast<uint2*>(p.out + size_t(x.row0 + r) * kDv);
+      auto pack = [](float4 v) -> uint2 {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      };
+      if constexpr (kW == 1) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) out[32 * q + lane] = pack(acc[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sums[warp][32 * q + lane] = acc[q];
+        __syncthreads();
+        if (tid < kDv / 4) {
+          float4 t = sums[0][tid];
+#pragma unroll
+          for (int k = 1; k < kW; ++k) {
+            const float4 v = sums[k][tid];
+            t.x += v.x;
+            t.y += v.y;
+            t.z += v.z;
+            t.w += v.w;
+          }
+          out[tid] = pack(t);
+        }
+        __syncthreads();
+      }
     }
-  }
-  __syncthreads();   // the list is read
+    __syncthreads();   // the list is read
   }
   // the status word: every CTA's bits, and requests whose bounds were clamped
   if (blockIdx.x == 0) {
@@ -214,12 +214,14 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
 // Clusters of the tensor-core kernel that a GB300's 152 SMs hold at most; the
 // workspace is sized for them, so that sizing it takes no device call.
 constexpr int kMaxSms = 152, kMaxPairs = 76, kMaxQuads = 38;
-// The prefill kernel (va_prefill_tc.cu) from this many query rows per request, on
-// the average, on: paged rows are packed side by side for it (0.5 ns a key), which
-// pays when they are read by about three units of 256 rows instead of gathered by
-// them (a tile costs 0.95 us with boxes, 1.45 us gathered).  Enormous lists, whose
-// copy would, are left to the split kernel.
-constexpr int kPrefillRows = 1024;
+// Paged rows are packed side by side for the prefill kernel (va_prefill_tc.cu),
+// which pays from this many query rows per request on, on the average: then about
+// three units read the packed rows instead of gathering them.  64 heads, split
+// kernel against prefill kernel: 32 requests of 8k keys, 512 rows 342 and 331 us,
+// 768 rows 514 and 428, 2048 rows 1292 and 883; 4 requests of 16k keys, 117 and 124,
+// 150 and 144, 323 and 261.  Enormous lists, whose copy would not, are left to the
+// split kernel.
+constexpr int kPrefillRows = 640;
 constexpr int64_t kPackEntriesMax = int64_t(1) << 21;
 
 struct ChunkPlan {
@@ -233,9 +235,13 @@ struct ChunkPlan {
   size_t off_units, off_flags, off_lse, off_o, off_pack_flags, off_valid, off_tails, off_pack, total;
 };
 
-// The decode kernel when the average request has at most 64 rows, the prefill
-// kernel when it has at least kPrefillRows; between them the split kernel, with
-// two-SM products when it has more than 128.
+// By the average request's rows.  Up to 64, one unit of the decode kernel (64 rows
+// each in 32 requests of 8k paged keys: 89 us, the split kernel 143; with 128 rows,
+// two units, 161 and 146).  Up to 128, the split kernel with a pair of SMs per
+// unit.  Above that products of two SMs (128 rows: one-SM products 146 us, two-SM
+// 191; 192 rows: 234 and 183): the prefill kernel where keys lie side by side
+// (192 rows: split 162 us, prefill 131; 4 requests of 16k keys, 82 and 55) or can be
+// packed (see kPrefillRows), else the split kernel.
 ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) {
   ChunkPlan c;
   memset(&c, 0, sizeof c);
@@ -251,7 +257,9 @@ ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) 
   // three quarters of them at least, see launch)
   const int waves = (c.units_bound + c.max_clusters * 3 / 4 - 1) / (c.max_clusters * 3 / 4);
   c.max_waves = waves > kSplitWaves ? waves : kSplitWaves;
-  c.prefill = c.pair && rows >= kPrefillRows * int64_t(busy) && num_entries <= kPackEntriesMax;
+  const bool paged = num_entries > 0;
+  c.prefill = c.pair && (!paged || (rows >= kPrefillRows * int64_t(busy) &&
+                                    num_entries <= kPackEntriesMax));
   // the decode and prefill kernels: an item and two slots per CTA or cluster
   const bool even = c.decode || c.prefill;
   const size_t items = even ? size_t(c.max_clusters) : size_t(c.max_waves) * c.max_clusters;
@@ -477,8 +485,8 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
 
 VA_API size_t va_chunk_workspace_bytes(int B, int total_q, int H, int64_t num_entries,
                                        int flags) {
-  if (num_entries < 0 || num_entries > 0x7fffffff || B < 1 || B > 65535 || total_q < 0 || H < 1 || flags < VA_PATH_AUTO ||
-      flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX)
+  if (num_entries < 0 || num_entries > 0x7fffffff || B < 1 || B > 65535 || total_q < 0 || H < 1 ||
+      flags < VA_PATH_AUTO || flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX)
     return 0;
   if (total_q == 0 || flags == VA_PATH_FMA) return va::kHeaderBytes;
   return va::chunk_plan(B, total_q, H, num_entries, flags).total;

@@ -250,7 +250,7 @@ def test_refusals(va):
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5), (33, 70)])
 def test_many_rows_per_request_read_packed_lists(va, window, sinks):
-    """1024 query rows and more per request: the call packs the listed rows
+    """640 query rows and more per request: the call packs the listed rows
     first (invisible ones not at all, ones without a row as zeros that count for
     nothing)."""
     c = _chunk.make([400, 0, 130], [40, 33, 1], 64, seed=40 + window, stride=584, list_gap=3,
