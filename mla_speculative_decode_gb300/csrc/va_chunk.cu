@@ -90,7 +90,10 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
       for (int i = tid; i < p.pack_blocks; i += kFinishThreads) bits |= p.pack_flags[i] & ~kPackMissing;
   }
   const bool hidden = __syncthreads_or((bits & kFlagHiddenNonfinite) != 0u);
-  for (int u0 = 0; u0 < total_units; u0 += kFinishThreads) {
+  // (a CTA that gave up a wait has not written the entries of the units that it
+  // did not reach: then nothing is merged, and the status word says so)
+  const bool gave_up = __syncthreads_or((bits & VA_STATUS_TIMEOUT) != 0u);
+  for (int u0 = 0; !gave_up && u0 < total_units; u0 += kFinishThreads) {
     // which of 256 units need work: listed in the same order by every CTA
     ChunkUnit unit;
     unit.ns = 1;

@@ -74,7 +74,11 @@ constexpr uint32_t kPBytes = kRows * 128;
 constexpr uint32_t kPAlpha = kPBytes, kPFlags = kPAlpha + 4 * kRows, kPPayload = kPFlags + 16;
 constexpr uint32_t kPBufBytes = 17 * 1024;
 constexpr int kPBufs = 3;
-constexpr int kFinRing = 4;            // row sums of units on their way to the PV CTA
+// Row sums of units on their way to the PV CTA.  When a tile has been staged, the
+// product of the tile kPBufs + 2 before it is done (two staging buffers, kPBufs at
+// the PV CTA), and the sums of the unit before that one's have been read: with
+// units of one tile those of kPBufs + 2 more may wait, besides the new ones.
+constexpr int kFinRing = kPBufs + 3;
 constexpr int kSoftmax = 256;          // warps 4-11
 constexpr uint32_t kRowBar = 1;        // their named barrier
 constexpr uint32_t kCmdDone = 0xFFFFFFFFu, kCmdUnit = 0x80000000u;
@@ -123,7 +127,7 @@ constexpr uint32_t kOffRun = 544;              // RunPlace
 constexpr uint32_t kOffPeerAny = 640;          // PV, even rank: uint32 [kPBufs]
 constexpr uint32_t kOffRef = 1024;             // QK: float [2][128] reference maxima, by tile parity
 constexpr uint32_t kOffSum = 2048;             // QK: float [2][2][128] partial sums, their references
-constexpr uint32_t kOffFin = 2048;             // PV: float [kFinRing][128] 1 / row sum
+constexpr uint32_t kOffFin = 1024;             // PV: float [kFinRing][128] 1 / row sum
 constexpr uint32_t kOffK = 4096;               // QK: ring
 constexpr uint32_t kOffStage = kOffK + kRing * kSlotBytes;   // QK: P staging [2]
 constexpr uint32_t kOffP = 4096;               // PV: P buffers
@@ -134,6 +138,7 @@ constexpr uint32_t kEndQK = kOffStage + 2 * kPBufBytes;
 constexpr uint32_t kEndPV = kOffOut + 8 * 32 * kOutRow;
 constexpr uint32_t kSmemBytes = (kEndQK > kEndPV ? kEndQK : kEndPV) + 1024;
 static_assert(8 * kNumBars <= int(kOffTmemSlot), "barrier area");
+static_assert(kOffFin + kFinRing * kRows * 4 <= kOffP, "row sums");
 static_assert(kOffStage % 1024 == 0 && kOffV % 1024 == 0 && kSmemBytes <= 232448, "layout");
 
 struct RunPlace {
