@@ -293,9 +293,9 @@ struct ChunkMode {
 
 // Raw pool row of key j of the split as stored in the slot list (contiguous
 // pools: the row itself; segmented lists: the draft list past the prefix), or
-// -1 when no row of the unit sees key j or the list ends before it.  The value is only range-checked
-// when it is used, a tile later, so the load's latency overlaps the current
-// tile's copies instead of stalling the warp.
+// -1 when no row of the unit sees key j or the list ends before it.  The value
+// is only range-checked when it is used, a tile later, so the load's latency
+// overlaps the current tile's copies instead of stalling the warp.
 template <class Mode>
 __device__ __forceinline__ int fetch_row(const typename Mode::P& p, const typename Mode::Req& ri,
                                          const typename Mode::Range& sr, int j) {
@@ -873,40 +873,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = window_first(p.window, pos);
         first_last = window_first(p.window, pos_last);
       } else {
-       named_sync(kSoftmaxBar, kSoftmax);   // parents staged
-       if (row_ok) {
-        const int node = lr / p.H;
-        if (p.tree_parent) {
-          nbits = 1ull << node;
-          int q = par[node];
-          if (q < -1 || q >= node) {
-            atomicOr(cta_flags, VA_STATUS_BAD_PARENT);
-          } else {
-            while (q >= 0) {
-              nbits |= 1ull << q;
-              const int up = par[q];
-              if (up < -1 || up >= q) break;
-              q = up;
-            }
-          }
-        } else if (p.dense_mask) {
-          const int64_t first = p.kv_indptr[0];
-          const int64_t e0 = int64_t(p.T) * ((ri.base - first) + int64_t(b) * p.T) +
-                             int64_t(node) * (ri.P + p.T) + ri.P;
-          bool bad = false;
-          for (int k = 0; k < p.T; ++k) {
-            const int64_t e = e0 + k;
-            if (e >= 0 && e < p.dense_mask_len) {
-              if (p.dense_mask[e]) nbits |= 1ull << k;
+        named_sync(kSoftmaxBar, kSoftmax);   // parents staged
+        if (row_ok) {
+          const int node = lr / p.H;
+          if (p.tree_parent) {
+            nbits = 1ull << node;
+            int q = par[node];
+            if (q < -1 || q >= node) {
+              atomicOr(cta_flags, VA_STATUS_BAD_PARENT);
             } else {
-              bad = true;
+              while (q >= 0) {
+                nbits |= 1ull << q;
+                const int up = par[q];
+                if (up < -1 || up >= q) break;
+                q = up;
+              }
             }
+          } else if (p.dense_mask) {
+            const int64_t first = p.kv_indptr[0];
+            const int64_t e0 = int64_t(p.T) * ((ri.base - first) + int64_t(b) * p.T) +
+                               int64_t(node) * (ri.P + p.T) + ri.P;
+            bool bad = false;
+            for (int k = 0; k < p.T; ++k) {
+              const int64_t e = e0 + k;
+              if (e >= 0 && e < p.dense_mask_len) {
+                if (p.dense_mask[e]) nbits |= 1ull << k;
+              } else {
+                bad = true;
+              }
+            }
+            if (bad) atomicOr(cta_flags, VA_STATUS_BAD_MASK);
+          } else {
+            nbits = p.bits[size_t(b) * p.T + node];
           }
-          if (bad) atomicOr(cta_flags, VA_STATUS_BAD_MASK);
-        } else {
-          nbits = p.bits[size_t(b) * p.T + node];
         }
-       }
       }
       float* mx = reinterpret_cast<float*>(gb + C::kOffMx);
       const uint32_t pv_p = mapa(sb + C::kOffP, other);
@@ -1370,35 +1370,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!f32) {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t v[32];
-          tmem_ld32(tl + 32u * uint32_t(c), v);
-          tmem_wait_ld();
-          uint32_t pk[16];
+          for (int c = 0; c < 8; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tl + 32u * uint32_t(c), v);
+            tmem_wait_ld();
+            uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * e]) * inv,
-                                                           __uint_as_float(v[2 * e + 1]) * inv);
-            pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int e = 0; e < 16; ++e) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * e]) * inv,
+                                                             __uint_as_float(v[2 * e + 1]) * inv);
+              pk[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(rowp + 64 * c + 16 * j) =
+                  make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(rowp + 64 * c + 16 * j) =
-                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-        }
-        fence_proxy_async_cta();   // staged half row, read by this thread's bulk copy
-        if (tid == 128) VA_TRACE_CTA(5, 0);
-        // each thread sends its own half row as soon as it is staged, and
-        // waits only until the copy has read it (the writes complete before
-        // the grid does)
-        __nv_bfloat16* dst;
-        if constexpr (kChunk)
-          dst = p.out + (size_t(ri.q0) * p.H + lr) * kDv + 256 * half;
-        else
-          dst = p.part_o + (size_t(split) * rows_total + size_t(b) * R + lr) * kDv + 256 * half;
-        if (row_ok) bulk_store_global(dst, smem_u32(rowp), 512u);
-        bulk_commit();
-        bulk_wait_read<0>();
+          fence_proxy_async_cta();   // staged half row, read by this thread's bulk copy
+          if (tid == 128) VA_TRACE_CTA(5, 0);
+          // each thread sends its own half row as soon as it is staged, and
+          // waits only until the copy has read it (the writes complete before
+          // the grid does)
+          __nv_bfloat16* dst;
+          if constexpr (kChunk)
+            dst = p.out + (size_t(ri.q0) * p.H + lr) * kDv + 256 * half;
+          else
+            dst = p.part_o + (size_t(split) * rows_total + size_t(b) * R + lr) * kDv + 256 * half;
+          if (row_ok) bulk_store_global(dst, smem_u32(rowp), 512u);
+          bulk_commit();
+          bulk_wait_read<0>();
         }
         if (lane == 0 && warp == 4) VA_TRACE_CTA(5, 1);
       } else if (ok && !fin) {
