@@ -27,10 +27,12 @@
  *  - Step-varying data (prefix lengths, slot tables, tree parents) is read on
  *    the device, so one captured graph replays across decode steps.
  *  - Stream order holds as for any launch.  The first kernel of the attention
- *    calls and of the placement calls (va_kv_append_contiguous,
- *    va_kv_compact_accepted) is a programmatic dependent of the stream's
- *    previous kernel: its CTAs may become resident while that kernel
- *    finishes, but read no input until it has completed (griddepcontrol.wait).
+ *    calls (verify and, on the tensor-core paths, chunk), of va_kv_weights_paged
+ *    (tensor-core paths), of va_kv_evict and of the placement calls
+ *    (va_kv_append_contiguous, va_kv_compact_accepted) is a programmatic
+ *    dependent of the stream's previous kernel: its CTAs may become resident
+ *    while that kernel finishes, but read no input until it has completed
+ *    (griddepcontrol.wait).
  *    Their last kernel lets the stream's next kernel do the same once it has
  *    itself passed that point,
  *    so a caller's next kernel launched as a programmatic dependent must wait
@@ -471,7 +473,8 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *                  the status word, rewritten by every call.  It includes room
  *                  for the listed rows (1152 bytes per entry) when the average
  *                  request brings 640 query rows (tokens x heads) or more: the
- *                  call then first packs them side by side.
+ *                  call then first packs them side by side.  Reused across
+ *                  calls; calls that overlap on the device must not share one.
  *   out            bf16 [total_q, H, 512], 16-byte aligned; lse float
  *                  [total_q, H] (natural log).  A token none of whose keys has
  *                  a valid pool row gets out 0 and lse -inf.
@@ -511,9 +514,11 @@ int va_chunk_attn_contiguous(const void *q, const void *kv_pool, int64_t num_slo
  *                  otherwise.
  *   weights_out    float [num_entries] device.  Written for the entries of
  *                  every request's P_b + n_b keys; other entries are left.
- *   num_entries    entries of slot_idx, weights_in and weights_out.
+ *   num_entries    entries of slot_idx, weights_in and weights_out; at most
+ *                  2^31 - 1025.
  *   workspace      >= va_kv_weights_workspace_bytes(...) bytes, 256-byte
- *                  aligned; first 4 bytes: the status word.
+ *                  aligned; first 4 bytes: the status word.  As above, not to
+ *                  be shared by calls that overlap on the device.
  * The requests' lists must not overlap.  Sums are taken in a fixed order: the
  * result is deterministic.  Other arguments as for va_chunk_attn_paged.
  */

@@ -24,6 +24,14 @@
 // unit) form one row of steps, and every SM takes an equal run of it, whatever
 // the lengths.  A unit inside one run goes straight to out and lse; of a unit cut
 // by run ends each piece leaves an fp32 partial for the merge (va_chunk.cu).
+//
+// Measured: 32 requests of one token, 64 heads, 1k to 32k paged keys (701 MB): 177 us,
+// 4.0 TB/s, where a kernel that only gathers such rows reaches 5.6.  A tile takes
+// about 5200 cycles: its copies 3700 if nothing disturbs them, and with two tiles of
+// shared memory a tile's products, softmax and release (2800) overlap the next one's
+// copies only in part.  (Slower: copies without the producers' barrier 182 to 208,
+// the next rows brought into L2 first 210, more copying warps 191 to 211.)  One
+// thread issues a group's products; elected one by one they took it to 192.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>

@@ -157,9 +157,12 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
   p.wout = weights_out;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (flags != VA_PATH_FMA) {
-    // two-SM products when the average request has more than 128 rows
+    // Two-SM products when the average request has more than one row tile of the
+    // one-SM kernel (32 requests of 8k keys: 64 rows 72 us with one SM and 73 with
+    // two, 128 rows 116 and 77, 256 rows 205 and 74; 4 of 16k keys: 29 and 28, 41
+    // and 31, 64 and 30).
     const int busy = B < total_q ? B : total_q;
-    const bool pair = flags != VA_PATH_TC_1SM && int64_t(total_q) * H > 128 * int64_t(busy);
+    const bool pair = flags != VA_PATH_TC_1SM && int64_t(total_q) * H > 64 * int64_t(busy);
     const WeightsLayout L = weights_layout(num_entries);
     uint8_t* w = static_cast<uint8_t*>(workspace);
     WeightTcParams t;
