@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kRowThreads) chunk_fma_kernel(const ChunkParam
   for (int b = 0; b < p.B; ++b) {
     const ChunkReq r = chunk_req(p, b);
     if (r.bad) bits |= VA_STATUS_BAD_INDPTR;
+    if (chunk_ends(p, b)) break;
     const int64_t rows = int64_t(r.n) * p.H;
     // the warp whose turn it is among all rows of the batch
     const int64_t g0 = int64_t(r.q0) * p.H;

@@ -87,6 +87,22 @@ __device__ inline ChunkReq chunk_req(const ChunkParams& p, int b) {
   return r;
 }
 
+// Whether request b's query bounds decrease, which ends the batch before it: only
+// bounds that never do are sure to name no row twice, and no more rows than q has.
+// (b past the batch: false.)
+__device__ inline bool chunk_ends(const ChunkParams& p, int b) {
+  return b < p.B && p.q_indptr[b + 1] < p.q_indptr[b];
+}
+
+// Requests before the batch's end.  A whole warp takes part.
+__device__ inline int chunk_requests(const ChunkParams& p, int lane) {
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const uint32_t ends = __ballot_sync(0xffffffffu, chunk_ends(p, b0 + lane));
+    if (ends) return b0 + __ffs(int(ends)) - 1;
+  }
+  return p.B;
+}
+
 // Pool row of key j (0 <= j < P + n), or -1 when it has none.
 __device__ inline int64_t chunk_key_row(const ChunkParams& p, const ChunkReq& r, int j) {
   if (j >= r.nlist) return -1;
@@ -266,9 +282,10 @@ __device__ inline void chunk_work(const ChunkParams& p, const ChunkSched& s, int
 __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s, int item,
                                        int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
+  const int B = chunk_requests(p, lane);
   int u0 = 0, t0 = 0;   // requests 0 .. 31 stay in registers
   int64_t work = 0;
-  for (int b = lane; b < p.B; b += 32) {
+  for (int b = lane; b < B; b += 32) {
     int u, t;
     chunk_work(p, s, b, &u, &t);
     if (b < 32) { u0 = u; t0 = t; }
@@ -277,7 +294,7 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(kAll, work, o);
   int all_units = 0;
-  for (int b = lane; b < p.B; b += 32) {
+  for (int b = lane; b < B; b += 32) {
     int u = u0, t = t0;
     if (b >= 32) chunk_work(p, s, b, &u, &t);
     all_units += u;
@@ -296,7 +313,7 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
     if (k * (c + kFixedTiles) >= best) continue;   // could not be better even if it fitted
     for (int n = INT32_MAX; c < 0x3fffffff; c += c / 8 + 1) {
       n = 0;
-      for (int b = lane; b < p.B; b += 32) {
+      for (int b = lane; b < B; b += 32) {
         int u = u0, t = t0;
         if (b >= 32) chunk_work(p, s, b, &u, &t);
         n += u * int((t + c - 1) / c);
@@ -315,12 +332,12 @@ __device__ inline ChunkItem chunk_item(const ChunkParams& p, const ChunkSched& s
   it.live = false;
   it.b = it.unit = it.split = it.units = it.ns = it.unit0 = it.item0 = it.pslot0 = 0;
   int items = 0, slots = 0, units = 0;   // of the requests before this round
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
+  for (int b0 = 0; b0 < B; b0 += 32) {
     const int b = b0 + lane;
     int u = u0, t = t0;
     if (b0 > 0) {
       u = t = 0;
-      if (b < p.B) chunk_work(p, s, b, &u, &t);
+      if (b < B) chunk_work(p, s, b, &u, &t);
     }
     const int ns = (t + chunk - 1) / chunk;
     const int n_items = u * ns, n_slots = ns > 1 ? n_items : 0;
@@ -460,10 +477,13 @@ __device__ int find_run(ChunkRun<kRows, kCost>& w, int c, int grid, int lane) {
   int all_units = 0, n0 = 0;
   for (int b0 = 0; b0 < w.p.B; b0 += 32) {
     int n;
-    const int64_t s = count_steps(w, b0, lane, &n);
+    int64_t s = count_steps(w, b0, lane, &n);
+    const uint32_t ends = __ballot_sync(kAll, chunk_ends(w.p, b0 + lane));
+    if (ends && lane >= __ffs(int(ends)) - 1) s = n = 0;
     if (b0 == 0) { s0 = s; n0 = n; }
     total += s;
     all_units += n;
+    if (ends) break;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {

@@ -156,6 +156,23 @@ def test_bad_bounds_are_clamped_and_flagged(va, path):
     assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
 
 
+@pytest.mark.parametrize("layout", ["paged", "contiguous"])
+@pytest.mark.parametrize("B,T,H,flags", [(40, 6, 8, 0), (40, 1, 1, 0), (5, 10, 64, 0), (5, 50, 64, 0),
+                                         (70, 50, 64, 0), (9, 33, 16, 1), (9, 33, 16, 3)])
+def test_query_bounds_that_decrease_end_the_batch(va, B, T, H, flags, layout):
+    """q_indptr 0, T, 0, T, ...: many requests claim the same rows, more in all than q
+    has.  The first has them; the others bring none."""
+    c = _chunk.make([30] * B, [T] + [0] * (B - 1), H, seed=15, layout=layout)
+    call = _chunk.call(va, c, flags=flags, prepare=True)
+    first = [x.clone() for x in call()]
+    assert va.read_status(call.workspace) == 0
+    c.q_indptr[2::2] = 0
+    call = _chunk.call(va, c, flags=flags, prepare=True)
+    out, lse = call()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
+
+
 @pytest.mark.parametrize("path", list(PATHS.values()), ids=list(PATHS))
 @pytest.mark.parametrize("sm_scale", [0.0, -0.05, 1.0])
 def test_scales(va, sm_scale, path):
