@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kRowThreads) chunk_fma_kernel(const ChunkParam
 // rows of three prompts, all of them final.)
 constexpr int kFinishThreads = 256;
 constexpr int kFinishWarps = kFinishThreads / 32;
-constexpr int kMaxNs = 512;   // splits of a unit: at most the launch's target + 1
+constexpr int kMaxNs = 544;   // splits of a unit: at most all items of a launch (see below)
 
 template <int kW>
 __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const ChunkTcParams p) {
@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kFinishThreads) chunk_finish_kernel(const Chun
 // Clusters of the tensor-core kernel that a GB300's 152 SMs hold at most; the
 // workspace is sized for them, so that sizing it takes no device call.
 constexpr int kMaxSms = 152, kMaxPairs = 76, kMaxQuads = 38;
+static_assert(kMaxNs >= kMaxSms && kMaxNs >= kSplitWaves * kMaxPairs, "splits of a unit");
 // Paged rows are packed side by side for the prefill kernel (va_prefill_tc.cu),
 // which pays from this many query rows per request on, on the average: then about
 // three units read the packed rows instead of gathering them.  64 heads, split

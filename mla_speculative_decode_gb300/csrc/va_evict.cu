@@ -541,7 +541,7 @@ VA_API int va_kv_evict(const int32_t* slot_idx, const int32_t* kv_indptr,
   p.finish = free_slots && (prefix_len_out == prefix_len || free_head_out == free_head);
   // As many CTAs per request as the batch leaves room for at once, and no more
   // than its average list has steps for (64 lists of 20k to 200k entries: four
-  // CTAs each 82 us; two 96; eight, in two waves, 155).
+  // CTAs each 76 us; two 94; eight, in two waves, 140).
   int ctas = 1;
   while (ctas < 8 && int64_t(2 * ctas) * B <= kCtaBudget * di.num_sms &&
          num_entries / B > int64_t(ctas) * kPer * kEvictThreads)
