@@ -156,6 +156,41 @@ def test_bad_bounds_are_clamped_and_flagged(va, path):
     assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
 
 
+@pytest.mark.parametrize("B,P,T,H", [(700, 0, 2, 128), (500, 61, 3, 128), (400, 10, 17, 16)])
+@pytest.mark.parametrize("layout", ["paged", "contiguous"])
+def test_many_units_of_one_or_two_tiles(va, B, P, T, H, layout):
+    """Short requests by the hundred: row sums of many units are on their way at once."""
+    c = _chunk.make([P] * B, [T] * B, H, seed=17, layout=layout)
+    call = _chunk.call(va, c, prepare=True)
+    first = [x.clone() for x in call()]
+    fma_out, fma_lse = _chunk.call(va, c, flags=1)     # the CUDA-core path, on every row
+    assert float((first[1] - fma_lse).abs().max()) < 1e-4
+    d = (first[0].float() - fma_out.float()).abs()
+    assert float((d - 2 * 2.0 ** -8 * fma_out.float().abs()).max()) < 2e-2
+    for _ in range(5):
+        out, lse = call()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert va.read_status(call.workspace) == 0
+
+
+@pytest.mark.parametrize("T,H,flags", [(1, 8, 0), (2, 64, 0), (40, 8, 0), (40, 8, 3), (40, 8, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3)])
+def test_contiguous_rows_that_leave_the_pool(va, T, H, flags, window, sinks):
+    """Starts before the pool, near its end and far outside: keys without a row are
+    skipped and reported."""
+    c = _chunk.make([70, 200, 130, 30], [T] * 4, H, seed=16, layout="contiguous", unused_nan=False)
+    rows = c.pool.shape[0]
+    starts = [-33, rows - 150, 1 << 40, -(1 << 62)]
+    c.kv_start = torch.tensor(starts, dtype=torch.int64)
+    for b, at in enumerate(starts):
+        r = np.arange(c.P[b] + T, dtype=np.int64) + at
+        c.key_rows[b] = np.where((r >= 0) & (r < rows), r, -1)
+    call = _chunk.call(va, c, flags=flags, window=window, sinks=sinks, prepare=True)
+    out, lse = call()
+    _chunk.check(c, out, lse, window=window, sinks=sinks)
+    assert va.read_status(call.workspace) == va.STATUS_BAD_SLOT
+
+
 @pytest.mark.parametrize("layout", ["paged", "contiguous"])
 @pytest.mark.parametrize("B,T,H,flags", [(40, 6, 8, 0), (40, 1, 1, 0), (5, 10, 64, 0), (5, 50, 64, 0),
                                          (70, 50, 64, 0), (9, 33, 16, 1), (9, 33, 16, 3)])
