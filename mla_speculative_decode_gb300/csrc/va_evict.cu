@@ -390,9 +390,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
         s[k] = i < q1 ? slot_in[i] : 0;
         v[k] = i < q1 ? w_in[i] : 0.f;
       }
-      // The usual step: candidates all of them, none equal to the threshold, no
-      // output held back.
-      bool other = i0 < lo || i0 + kStep > (hi < q1 ? hi : q1) || p.hold || (fr && !fits);
+      // The usual step: candidates all of them, none equal to the threshold.
+      bool other = i0 < lo || i0 + kStep > (hi < q1 ? hi : q1) || (fr && !fits);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) other |= fmaxf(v[k], -INFINITY) == T;
       if (!__any_sync(0xffffffffu, other)) {
@@ -403,7 +402,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
           const uint32_t ba = __ballot_sync(0xffffffffu, a);
           const uint32_t at = stay + e0 + uint32_t(__popc(ba & below));
           stay += uint32_t(__popc(ba));
-          if (a) {
+          if (a && p.hold) {
+            held[at - out0] = make_uint2(uint32_t(s[k]), __float_as_uint(v[k]));
+          } else if (a) {
             slot_o[at] = s[k];
             w_o[at] = v[k];
           } else if (fr) {
