@@ -31,7 +31,7 @@ struct ChunkParams {
   const int64_t* kv_start;     // contiguous: [B] (NULL when paged)
   const int32_t* prefix_len;   // [B]
   const int32_t* q_indptr;     // [B+1]
-  int64_t num_entries;         // entries of slot_idx (weights call), else 2^31 - 1
+  int64_t num_entries;         // entries of slot_idx (contiguous: 0)
   int B, total_q, H;
   int window, sinks;           // window 0: every earlier key is visible
   float scale_log2;            // sm_scale * log2(e)
@@ -241,7 +241,7 @@ __device__ inline ChunkTiles chunk_tiles(const ChunkParams& p, const ChunkReq& r
 }
 
 struct ChunkSched {
-  int unit_rows;   // 128, or 256 with two-SM products
+  int unit_rows;   // 64 (decode kernel), 128, or 256 with two-SM products
   int clusters;    // clusters resident at once
   int max_waves;   // waves of clusters that the grid holds
 };
