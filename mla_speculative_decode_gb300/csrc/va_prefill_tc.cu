@@ -430,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int N = w.r.nlist < w.r.P + w.r.n ? w.r.nlist : w.r.P + w.r.n;
         const bool direct = w.k == 0 && w.piece() == w.t.ntiles;
         const size_t slot = size_t(2 * cluster + (w.g > w.begin(cluster) ? 1 : 0));
+        bad_slot |= k1 > N;   // the list ends before the unit's last token's own key
         if (w.b != last_b) {
           last_b = w.b;
           bool all = true;
@@ -490,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the piece's first).
         int in_a = 0, in_b = 0, in_c = 0;
         if (all_valid) {
-          const int seen = (pos_a + 1) / kTile;      // tiles of the list that all rows reach
+          // tiles of the list that all rows reach (a list may end before their own keys)
+          const int seen = (pos_a + 1 < N ? pos_a + 1 : N) / kTile;
           const int whole = p.sinks / kTile < seen ? p.sinks / kTile : seen;
           in_a = (tiles.nst < whole ? tiles.nst : whole) - tiles.t0;
           // list tile x >= wt is the unit's tile x - wt + nst
