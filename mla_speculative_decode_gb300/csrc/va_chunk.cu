@@ -343,21 +343,29 @@ __global__ void __launch_bounds__(kPackThreads) chunk_pack_kernel(const ChunkTcP
   const int64_t e = int64_t(blockIdx.x) * kPackThreads + tid, e0 = e - lane;
   int64_t row = -2;
   bool bad = false;
-  if (e < p.num_entries) {
+  const int requests = chunk_requests(p, lane);
+  const bool sorted = chunk_lists_sorted(p, lane);
+  // what request b makes of the entry
+  auto look = [&](int b) {
+    const ChunkReq r = chunk_req(p, b);
+    const int64_t j = e - r.base;
+    const int first = window_first(p.window, r.P);
+    if (r.n > 0 && j >= 0 && j < r.P + r.n && j < r.nlist &&
+        (j >= (first & ~63) || j < (int64_t(p.sinks) + 63) / 64 * 64)) {
+      row = chunk_key_row(p, r, int(j));
+      bad |= row < 0 && (j >= first || j < p.sinks);
+    }
+  };
+  if (e < p.num_entries && sorted) {
     int lo = 0, hi = p.B;   // the last list that begins at or before e
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (p.kv_indptr[mid] <= e) lo = mid;
       else hi = mid;
     }
-    const ChunkReq r = chunk_req(p, lo);
-    const int64_t j = e - r.base;
-    const int first = window_first(p.window, r.P);
-    if (r.n > 0 && j >= 0 && j < r.P + r.n && j < r.nlist &&
-        (j >= (first & ~63) || j < (int64_t(p.sinks) + 63) / 64 * 64)) {
-      row = chunk_key_row(p, r, int(j));
-      bad = row < 0 && (j >= first || j < p.sinks);
-    }
+    if (lo < requests) look(lo);
+  } else if (e < p.num_entries) {   // bounds in error: any request's list may hold it
+    for (int b = 0; b < requests; ++b) look(b);
   }
   const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
   if (lane == 0) const_cast<uint32_t*>(p.valid)[e0 >> 5] = have;

@@ -103,6 +103,14 @@ __device__ inline int chunk_requests(const ChunkParams& p, int lane) {
   return p.B;
 }
 
+// Whether the bounds of the requests' lists never decrease: then the list that an
+// entry lies in is the last one that begins at or before it.  A whole warp takes part.
+__device__ inline bool chunk_lists_sorted(const ChunkParams& p, int lane) {
+  bool falls = false;
+  for (int b = lane; b < p.B; b += 32) falls |= p.kv_indptr[b + 1] < p.kv_indptr[b];
+  return !__any_sync(0xffffffffu, falls);
+}
+
 // Pool row of key j (0 <= j < P + n), or -1 when it has none.
 __device__ inline int64_t chunk_key_row(const ChunkParams& p, const ChunkReq& r, int j) {
   if (j >= r.nlist) return -1;

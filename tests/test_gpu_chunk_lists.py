@@ -1,5 +1,6 @@
 """Chunk attention over lists that are not what the header asks for: shorter than
-the new tokens.  Flagged, and the same rows on every path (needs an sm_103 GPU)."""
+the new tokens, or with bounds that decrease.  Flagged, and the same rows on every
+path (needs an sm_103 GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -48,3 +49,25 @@ def test_a_list_shorter_than_the_new_tokens(va, P, n, H, m, window, sinks, path)
     out, lse = call()
     _chunk.check(c, out, lse, window=window, sinks=sinks)
     assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR | va.STATUS_BAD_SLOT
+
+
+@pytest.mark.parametrize("path", list(PATHS.values()), ids=list(PATHS))
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 2), (100, 0), (64, 130)])
+@pytest.mark.parametrize("ind", [[0, 600, 200, 800], [300, 900, 0, 600], [600, 1200, 0, 600]])
+def test_list_bounds_that_decrease(va, ind, window, sinks, path):
+    """The request whose bounds decrease has an empty list; those behind it have
+    theirs, also where two requests' lists share entries.  What the workspace held
+    before shows nowhere."""
+    n, H, L = 20, 64, 600
+    c = _chunk.make([L - n, 0, L - n], [n, n, n], H, seed=420, unused_nan=False)
+    rng = np.random.default_rng(421)
+    slots = rng.permutation(c.pool.shape[0])[:1200].astype(np.int32)
+    c.slot_idx = torch.from_numpy(slots)
+    c.kv_indptr = torch.tensor(ind, dtype=torch.int32)
+    c.key_rows = [slots[ind[0]:ind[1]].astype(np.int64), np.full(n, -1),
+                  slots[ind[2]:ind[3]].astype(np.int64)]
+    ws = torch.full((va.load().va_chunk_workspace_bytes(3, 3 * n, H, 1200, path),), 0x41,
+                    dtype=torch.uint8, device="cuda")
+    out, lse = _chunk.call(va, c, flags=path, window=window, sinks=sinks, workspace=ws)
+    _chunk.check(c, out, lse, window=window, sinks=sinks)
+    assert va.read_status(ws) == va.STATUS_BAD_INDPTR | va.STATUS_BAD_SLOT
