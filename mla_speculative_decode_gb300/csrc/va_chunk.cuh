@@ -52,12 +52,15 @@ struct ChunkReq {
   bool bad;      // bounds were clamped (VA_STATUS_BAD_INDPTR)
 };
 
-__device__ inline ChunkReq chunk_req(const ChunkParams& p, int b) {
+// (`ended`: the request lies behind the batch's end, see chunk_ends, and brings no
+// tokens)
+__device__ inline ChunkReq chunk_req(const ChunkParams& p, int b, bool ended = false) {
   ChunkReq r;
   const int a0 = p.q_indptr[b], a1 = p.q_indptr[b + 1];
   int q0 = a0 < 0 ? 0 : (a0 > p.total_q ? p.total_q : a0);
   int q1 = a1 < q0 ? q0 : (a1 > p.total_q ? p.total_q : a1);
   r.bad = q0 != a0 || q1 != a1;
+  if (ended) q1 = q0;
   r.q0 = q0;
   r.n = q1 - q0;
   int P = p.prefix_len[b];

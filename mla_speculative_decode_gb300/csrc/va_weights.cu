@@ -34,8 +34,9 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fma_kernel(const Weigh
   const ChunkParams& c = p.c;
   uint32_t bits = 0u;
   int64_t turn = 0;
+  const int requests = chunk_requests(c, lane);
   for (int b = 0; b < c.B; ++b) {
-    const ChunkReq r = chunk_req(c, b);
+    const ChunkReq r = chunk_req(c, b, b >= requests);
     if (r.bad) bits |= VA_STATUS_BAD_INDPTR;
     const int N = r.nlist < r.P + r.n ? r.nlist : r.P + r.n;
     for (int64_t k = (warp - turn % warps + warps) % warps; k < N; k += warps) {

@@ -194,11 +194,18 @@ struct Walk {
 __device__ void find_run(Walk& w, int c, int C, int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
   int64_t total = 0, s0 = 0;   // s0: steps of request `lane`, kept for B <= 32
-  for (int b = lane; b < w.p.B; b += 32) {
-    w.load(b);
-    const int64_t s = w.steps();
-    if (b < 32) s0 = s;
+  for (int b0 = 0; b0 < w.p.B; b0 += 32) {
+    int64_t s = 0;
+    if (b0 + lane < w.p.B) {
+      w.load(b0 + lane);
+      s = w.steps();
+    }
+    // (no run goes past the steps counted here, so none reaches the batch's end)
+    const uint32_t ends = __ballot_sync(kAll, chunk_ends(w.p, b0 + lane));
+    if (ends && lane >= __ffs(int(ends)) - 1) s = 0;
+    if (b0 == 0) s0 = s;
     total += s;
+    if (ends) break;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
@@ -624,6 +631,7 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
   if (tid == 0) s_bits = 0u;
   // the entry's request: the last list that begins at or before it (the bounds
   // are inputs of the call, so they are read before the wait)
+  const int requests = chunk_requests(c, tid & 31);
   const int64_t e = int64_t(blockIdx.x) * 256 + tid;
   ChunkReq r;
   r.n = r.P = r.nlist = 0;
@@ -635,7 +643,7 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
       if (c.kv_indptr[mid] <= e) lo = mid;
       else hi = mid;
     }
-    r = chunk_req(c, lo);
+    r = chunk_req(c, lo, lo >= requests);
   }
   griddep_wait();                // the sums are complete
   griddep_launch_dependents();   // the next kernel may start its set-up
