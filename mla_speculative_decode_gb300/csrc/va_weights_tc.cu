@@ -629,14 +629,16 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
   const int tid = threadIdx.x;
   uint32_t bits = 0u;
   if (tid == 0) s_bits = 0u;
-  // the entry's request: the last list that begins at or before it (the bounds
-  // are inputs of the call, so they are read before the wait)
+  // the entry's request: the last list that begins at or before it, or, where the
+  // bounds are in error, any whose keys it is among (the bounds are inputs of the
+  // call, so they are read before the wait)
   const int requests = chunk_requests(c, tid & 31);
+  const bool sorted = chunk_lists_sorted(c, tid & 31);
   const int64_t e = int64_t(blockIdx.x) * 256 + tid;
   ChunkReq r;
   r.n = r.P = r.nlist = 0;
   r.base = 0;
-  if (e < c.num_entries) {
+  if (e < c.num_entries && sorted) {
     int lo = 0, hi = c.B;   // indptr[lo] <= e (or lo = 0), indptr[hi] > e (or hi = B)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -644,6 +646,15 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
       else hi = mid;
     }
     r = chunk_req(c, lo, lo >= requests);
+  } else if (e < c.num_entries) {
+    for (int b = 0; b < c.B; ++b) {
+      const ChunkReq x = chunk_req(c, b, b >= requests);
+      const int64_t j = e - x.base;
+      if (j >= 0 && j < x.nlist && j < x.P + x.n) {
+        r = x;
+        break;
+      }
+    }
   }
   griddep_wait();                // the sums are complete
   griddep_launch_dependents();   // the next kernel may start its set-up

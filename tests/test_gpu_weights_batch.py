@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import synth
 from tests import _chunk
 
@@ -43,4 +44,40 @@ def test_query_bounds_that_decrease_end_the_batch(va, B, T, H, end, path):
     # (the sums of a key may be cut into runs at other places: their order)
     assert bool((whole[:e] != w[:e]).any())
     assert torch.allclose(got[:e], whole[:e], rtol=T * H * 2.0 ** -23, atol=1e-30)
+    assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
+
+
+@pytest.mark.parametrize("path", list(PATHS.values()), ids=list(PATHS))
+@pytest.mark.parametrize("ind", [[50, 100, 20, 40], [700, 1300, 0, 600], [300, 301, 100, 290]])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (9, 2)])
+def test_list_bounds_that_decrease(va, ind, window, sinks, path):
+    """The request whose bounds decrease has an empty list; the one behind it has its
+    own, although it lies before the first one's."""
+    n, H = 7, 8
+    L = [ind[1] - ind[0], 0, ind[3] - ind[2]]
+    P = [max(0, L[0] - n), 0, L[2] - n]
+    c = _chunk.make(P, [min(n, L[0]), 2, n], H, seed=430)
+    slots = c.slot_idx.numpy()
+    two = slots[c.kv_indptr[2]:c.kv_indptr[2] + L[2]]
+    lists = np.full(1400, -5, dtype=np.int32)
+    lists[ind[0]:ind[1]] = slots[:L[0]]
+    lists[ind[2]:ind[3]] = two
+    c.slot_idx = torch.from_numpy(lists)
+    c.key_rows[1] = np.full(2, -1)
+    c.kv_indptr = torch.tensor(ind, dtype=torch.int32)
+    _, lse, _, spread = _chunk.reference(c, window=window, sinks=sinks)
+    lse = lse.astype(np.float32)
+    w = np.random.default_rng(431).random(1400).astype(np.float32)
+    call = va.prepare_kv_weights(*args(c), torch.from_numpy(lse).cuda(),
+                                 torch.from_numpy(w).cuda(), sm_scale=synth.SM_SCALE,
+                                 window=window, sinks=sinks, flags=path)
+    got = call().cpu().numpy()
+    ref = oracle.chunk_weights(synth.as_u16(c.q), synth.as_u16(c.pool), c.key_rows, c.P,
+                               c.q_indptr.numpy(), lse, synth.SM_SCALE, window, sinks)
+    want = w.astype(np.float64)
+    for b in (0, 2):
+        want[ind[b]:ind[b] + L[b]] += ref[b]
+    rel = _chunk.score_error(spread) + 2.0 ** -22 * np.abs(lse[np.isfinite(lse)]).max() \
+        + (n * H + 2) * 2.0 ** -24
+    assert np.all(np.abs(got - want) <= rel * (want - w) + 2.0 ** -23 * want)
     assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
