@@ -12,6 +12,7 @@ and ``kv_evict`` (with ``prepare_`` forms) for the calls around them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -559,6 +560,18 @@ def tree_build(cand_tokens: torch.Tensor, cand_logp: torch.Tensor, T: int,
     return par, tok, depth, (loc if free_slots is not None else None)
 
 
+def _on_stream(stream, device: int):
+    """The context in which torch's own work goes to the call's stream (the current
+    one when none is given)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle \
+            else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 class BoundCall:
     """A chunk, weight or eviction call whose arguments were checked and
     marshalled once.
@@ -566,11 +579,13 @@ class BoundCall:
     Calling it launches again on the same buffers, whose contents may change
     between calls, on the stream it was prepared for, or, when none was given,
     on the current stream of the buffers' device at the time of the call.  The
-    host work per call is one C call.  It keeps the tensors it refers to alive;
-    `result` is what it returns.
+    host work per call is one C call (and `fill`, which puts values into outputs
+    that the kernels leave in part, on the same stream before them).  It keeps the
+    tensors it refers to alive; `result` is what it returns.
     """
 
-    def __init__(self, name: str, args: tuple, result, keep: tuple, device: int, stream):
+    def __init__(self, name: str, args: tuple, result, keep: tuple, device: int, stream,
+                 fill=None):
         self._fn = getattr(load(), name)
         self._name = name
         self._args = args
@@ -578,6 +593,8 @@ class BoundCall:
         self._keep = keep
         self._device = device
         self._stream = None if stream is None else _stream(stream)
+        self._on = _on_stream(stream, device)
+        self._fill = fill
 
     @property
     def workspace(self) -> Optional[torch.Tensor]:
@@ -588,6 +605,9 @@ class BoundCall:
         st = self._stream
         if st is None:
             st = torch.cuda.current_stream(self._device).cuda_stream
+        if self._fill is not None:
+            with self._on:
+                self._fill()
         if torch.cuda.current_device() == self._device:
             rc = self._fn(*self._args, st)
         else:   # kernels launch on the buffers' device, whichever is current
@@ -738,10 +758,16 @@ def prepare_kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.T
     if tuple(lse.shape) != (total_q, H):
         raise ValueError(f"lse must be [{total_q}, {H}], got {tuple(lse.shape)}")
     n = slot_idx.numel()
+    fill = None
     if weights_out is None:
-        # entries that no request's keys cover keep their totals (or zero)
-        weights_out = torch.zeros(n, dtype=torch.float32, device=q.device) \
-            if weights_in is None else weights_in.clone()
+        # entries that no request's keys cover hold weights_in's totals (or zero)
+        out = weights_out = torch.empty(n, dtype=torch.float32, device=q.device)
+
+        def fill():
+            if weights_in is None:
+                out.zero_()
+            else:
+                out.copy_(weights_in)
     for t, name in ((weights_in, "weights_in"), (weights_out, "weights_out")):
         if t is not None:
             _dev(t, name, torch.float32)
@@ -758,7 +784,7 @@ def prepare_kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.T
             workspace.numel(), _ptr(weights_out))
     return BoundCall("va_kv_weights_paged", args, weights_out,
                      (workspace, q, kv_pool, slot_idx, kv_indptr, prefix_len, q_indptr, lse,
-                      weights_in, weights_out), q.device.index, stream)
+                      weights_in, weights_out), q.device.index, stream, fill)
 
 
 def kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
@@ -770,8 +796,9 @@ def kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
     """Attention weight that each listed key received from the rows of a
     chunk_attn_paged call (same arguments, and the lse it returned), added to
     weights_in (fp32, one entry per entry of slot_idx; None: zeros).  Returns
-    weights_out, which may be given, weights_in itself included (in place).  See
-    va_kv_weights_paged in verify_attn.h."""
+    weights_out, which may be given, weights_in itself included (in place); of a given
+    one, entries that no request's keys cover are left, else they hold weights_in's.
+    See va_kv_weights_paged in verify_attn.h."""
     return prepare_kv_weights(q, kv_pool, slot_idx, kv_indptr, prefix_len, q_indptr, lse,
                               weights_in, sm_scale=sm_scale, window=window, sinks=sinks,
                               flags=flags, workspace=workspace, weights_out=weights_out,

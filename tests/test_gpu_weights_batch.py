@@ -1,4 +1,5 @@
-"""Weight totals of batches that end early (needs an sm_103 GPU)."""
+"""Weight totals of batches that end early, of entries that no request's keys cover, and
+on other streams (needs an sm_103 GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -81,3 +82,49 @@ def test_list_bounds_that_decrease(va, ind, window, sinks, path):
         + (n * H + 2) * 2.0 ** -24
     assert np.all(np.abs(got - want) <= rel * (want - w) + 2.0 ** -23 * want)
     assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
+
+
+@pytest.mark.parametrize("path", list(PATHS.values()), ids=list(PATHS))
+def test_a_prepared_call_gives_uncovered_entries_the_totals_of_its_time(va, path):
+    """Entries behind a request's keys: weights_in as it is when the call runs (zero
+    without one), not as it was when the call was prepared."""
+    c = _chunk.make([30, 5], [3, 2], 8, seed=410, list_gap=4)
+    lse = _chunk.call(va, c)[1]
+    w = torch.rand(c.slot_idx.numel(), generator=torch.Generator().manual_seed(2)).cuda()
+    call = va.prepare_kv_weights(*args(c), lse, w, sm_scale=synth.SM_SCALE, flags=path)
+    call()
+    w += 1
+    got = call()
+    behind = np.concatenate([np.arange(int(c.kv_indptr[b]) + c.P[b] + c.n[b],
+                                       int(c.kv_indptr[b + 1])) for b in range(2)])
+    assert behind.size == 8
+    assert torch.equal(got[behind], w[behind])
+    fresh = va.prepare_kv_weights(*args(c), lse, None, sm_scale=synth.SM_SCALE, flags=path)
+    fresh().fill_(7.0)
+    assert bool((fresh()[behind] == 0).all())
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("start", [False, True])
+def test_totals_without_weights_out_on_another_stream(va, start, handle):
+    """All of the call's work is on the stream it was given: what is still queued on the
+    current stream does not come between."""
+    c = _chunk.make([30, 5], [3, 2], 8, seed=411, list_gap=4)
+    lse = _chunk.call(va, c)[1]
+    w = torch.rand(c.slot_idx.numel(), generator=torch.Generator().manual_seed(3)).cuda()
+    w = w if start else None
+    want = va.kv_weights(*args(c), lse, w, sm_scale=synth.SM_SCALE)
+    a = args(c)
+    side = torch.cuda.Stream()
+    first = torch.empty(c.slot_idx.numel(), dtype=torch.float32, pin_memory=True)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)          # the current stream is busy for 0.1 s
+    got = va.kv_weights(*a, lse, w, sm_scale=synth.SM_SCALE,
+                        stream=side.cuda_stream if handle else side)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()
+    with torch.cuda.stream(side):
+        first.copy_(got, non_blocking=True)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(first, want.cpu()) and torch.equal(got, want)
