@@ -581,11 +581,15 @@ class BoundCall:
     on the current stream of the buffers' device at the time of the call.  The
     host work per call is one C call (and `fill`, which puts values into outputs
     that the kernels leave in part, on the same stream before them).  It keeps the
-    tensors it refers to alive; `result` is what it returns.
+    tensors it refers to alive; `result` is what it returns.  Memory that was taken
+    for the call (`own`: workspace and outputs that were not given) belongs to the
+    stream it was prepared for, or prepared on, and is held for any other stream that
+    a call runs on, so the object may go while its kernels are still queued.  (A graph
+    that captured a call needs the object for as long as it is replayed.)
     """
 
     def __init__(self, name: str, args: tuple, result, keep: tuple, device: int, stream,
-                 fill=None):
+                 own: tuple = (), fill=None):
         self._fn = getattr(load(), name)
         self._name = name
         self._args = args
@@ -595,6 +599,12 @@ class BoundCall:
         self._stream = None if stream is None else _stream(stream)
         self._on = _on_stream(stream, device)
         self._fill = fill
+        self._own = own
+        here = torch.cuda.current_stream(device)
+        self._home = here.cuda_stream
+        if stream is not None and not torch.cuda.is_current_stream_capturing():
+            for t in own:          # the results may be used and dropped here
+                t.record_stream(here)
 
     @property
     def workspace(self) -> Optional[torch.Tensor]:
@@ -605,6 +615,9 @@ class BoundCall:
         st = self._stream
         if st is None:
             st = torch.cuda.current_stream(self._device).cuda_stream
+            if st != self._home and not torch.cuda.is_current_stream_capturing():
+                for t in self._own:
+                    t.record_stream(torch.cuda.current_stream(self._device))
         if self._fill is not None:
             with self._on:
                 self._fill()
@@ -669,9 +682,13 @@ def _prepare_chunk(name, q, kv_pool, keys, dims, prefix_len, q_indptr, sm_scale,
     B, total_q, H = dims
     init(q.device.index)
     n = keys[0].numel() if len(keys) == 2 else 0     # entries of a paged call's lists
-    workspace = _workspace(workspace, load().va_chunk_workspace_bytes(B, total_q, H, n, flags),
-                           q.device, "va_chunk_workspace_bytes")
-    out, lse = _outputs(total_q, H, q.device, out, lse)
+    given = (workspace, out, lse)
+    with _on_stream(stream, q.device.index):
+        workspace = _workspace(workspace,
+                               load().va_chunk_workspace_bytes(B, total_q, H, n, flags), q.device,
+                               "va_chunk_workspace_bytes")
+        out, lse = _outputs(total_q, H, q.device, out, lse)
+    own = tuple(t for t, g in zip((workspace, out, lse), given) if g is None)
     _same_device(q.device, out=out, lse=lse)
     args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), *(_ptr(k) for k in keys),
             _ptr(prefix_len), _ptr(q_indptr), *([n] if len(keys) == 2 else []), B, total_q, H,
@@ -679,7 +696,7 @@ def _prepare_chunk(name, q, kv_pool, keys, dims, prefix_len, q_indptr, sm_scale,
             workspace.numel(), _ptr(out), _ptr(lse))
     return BoundCall(name, args, (out, lse),
                      (workspace, q, kv_pool, keys, prefix_len, q_indptr, out, lse),
-                     q.device.index, stream)
+                     q.device.index, stream, own)
 
 
 def prepare_chunk_paged(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
@@ -758,10 +775,12 @@ def prepare_kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.T
     if tuple(lse.shape) != (total_q, H):
         raise ValueError(f"lse must be [{total_q}, {H}], got {tuple(lse.shape)}")
     n = slot_idx.numel()
-    fill = None
+    fill, own = None, ()
     if weights_out is None:
         # entries that no request's keys cover hold weights_in's totals (or zero)
-        out = weights_out = torch.empty(n, dtype=torch.float32, device=q.device)
+        with _on_stream(stream, q.device.index):
+            out = weights_out = torch.empty(n, dtype=torch.float32, device=q.device)
+        own += (out,)
 
         def fill():
             if weights_in is None:
@@ -775,16 +794,19 @@ def prepare_kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.T
                 raise ValueError(f"{name} must hold one entry per entry of slot_idx ({n})")
     _same_device(q.device, weights_in=weights_in, weights_out=weights_out)
     init(q.device.index)
-    workspace = _workspace(workspace,
-                           load().va_kv_weights_workspace_bytes(B, total_q, H, n, flags),
-                           q.device, "va_kv_weights_workspace_bytes")
+    taken = workspace is None
+    with _on_stream(stream, q.device.index):
+        workspace = _workspace(workspace,
+                               load().va_kv_weights_workspace_bytes(B, total_q, H, n, flags),
+                               q.device, "va_kv_weights_workspace_bytes")
+    own += (workspace,) if taken else ()
     args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), _ptr(slot_idx),
             _ptr(kv_indptr), _ptr(prefix_len), _ptr(q_indptr), _ptr(lse), _ptr(weights_in), n, B,
             total_q, H, float(sm_scale), int(window), int(sinks), int(flags), _ptr(workspace),
             workspace.numel(), _ptr(weights_out))
     return BoundCall("va_kv_weights_paged", args, weights_out,
                      (workspace, q, kv_pool, slot_idx, kv_indptr, prefix_len, q_indptr, lse,
-                      weights_in, weights_out), q.device.index, stream, fill)
+                      weights_in, weights_out), q.device.index, stream, own, fill)
 
 
 def kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor,
