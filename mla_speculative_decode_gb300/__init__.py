@@ -166,6 +166,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream, device: int):
+    """The context in which torch's own work goes to the call's stream (the current
+    one when none is given)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle \
+            else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _lend(stream, *tensors) -> None:
+    """Results taken on a given stream may also be used and dropped on the current one."""
+    if stream is not None and not torch.cuda.is_current_stream_capturing():
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def alloc_workspace(B: int, T: int, H: int, nsplit: int = 0, flags: int = PATH_AUTO,
                     device=None) -> Tuple[torch.Tensor, int]:
     """A workspace tensor for these sizes and the nsplit it was sized for."""
@@ -185,14 +204,17 @@ def _dims(q: torch.Tensor, B: int) -> Tuple[int, int]:
     return q.shape[0] // B, q.shape[1]
 
 
-def _outputs(rows: int, H: int, device, out, lse):
-    """Allocates out / lse when not given; a given one must have the step's
-    exact shape (the kernels write [rows, H, 512] and [rows, H] through a bare
-    pointer, so an undersized buffer would be written past its end)."""
-    if out is None:
-        out = torch.empty(rows, H, D_V, dtype=torch.bfloat16, device=device)
-    if lse is None:
-        lse = torch.empty(rows, H, dtype=torch.float32, device=device)
+def _outputs(rows: int, H: int, device, out, lse, stream=None):
+    """Allocates out / lse, on the call's stream, when not given; a given one must
+    have the step's exact shape (the kernels write [rows, H, 512] and [rows, H]
+    through a bare pointer, so an undersized buffer would be written past its end)."""
+    given = (out, lse)
+    with _on_stream(stream, device.index):
+        if out is None:
+            out = torch.empty(rows, H, D_V, dtype=torch.bfloat16, device=device)
+        if lse is None:
+            lse = torch.empty(rows, H, dtype=torch.float32, device=device)
+    _lend(stream, *(t for t, g in zip((out, lse), given) if g is None))
     _dev(out, "out", torch.bfloat16)
     _dev(lse, "lse", torch.float32)
     if tuple(out.shape) != (rows, H, D_V):
@@ -259,8 +281,9 @@ def prepare_paged(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.Tensor
     B = prefix_len.shape[0]
     T, H = _dims(q, B)
     if workspace is None:
-        workspace, nsplit = alloc_workspace(B, T, H, nsplit, flags, q.device)
-    out, lse = _outputs(q.shape[0], H, q.device, out, lse)
+        with _on_stream(stream, q.device.index):
+            workspace, nsplit = alloc_workspace(B, T, H, nsplit, flags, q.device)
+    out, lse = _outputs(q.shape[0], H, q.device, out, lse, stream)
     par, bits = _tree_args(tree_parent, tree_bits, B, T)
     args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), _ptr(slot_idx),
             _ptr(kv_indptr), _ptr(prefix_len), par, bits, B, T, H, float(sm_scale), nsplit, flags,
@@ -307,8 +330,9 @@ def verify_attn_contiguous(q: torch.Tensor, kv_pool: torch.Tensor, kv_start: tor
     B = prefix_len.shape[0]
     T, H = _dims(q, B)
     if workspace is None:
-        workspace, nsplit = alloc_workspace(B, T, H, nsplit, flags, q.device)
-    out, lse = _outputs(q.shape[0], H, q.device, out, lse)
+        with _on_stream(stream, q.device.index):
+            workspace, nsplit = alloc_workspace(B, T, H, nsplit, flags, q.device)
+    out, lse = _outputs(q.shape[0], H, q.device, out, lse, stream)
     par, bits = _tree_args(tree_parent, tree_bits, B, T)
     rc = load().verify_attn_contiguous(
         _ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), _ptr(kv_start),
@@ -356,8 +380,9 @@ def verify_attn_segmented(q: torch.Tensor, kv_pool: torch.Tensor, kv_indices: to
         if tuple(draft_kv.shape) != (B * T, D_QK):
             raise ValueError("draft_kv must be [B*T, 576]")
     if workspace is None:
-        workspace, nsplit = alloc_workspace(B, T, H, nsplit, flags, q.device)
-    out, lse = _outputs(q.shape[0], H, q.device, out, lse)
+        with _on_stream(stream, q.device.index):
+            workspace, nsplit = alloc_workspace(B, T, H, nsplit, flags, q.device)
+    out, lse = _outputs(q.shape[0], H, q.device, out, lse, stream)
     par, bits = _tree_args(tree_parent, tree_bits, B, T)
     rc = load().verify_attn_segmented(
         _ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), _ptr(kv_indices),
@@ -483,13 +508,17 @@ def tree_accept(root_logits: torch.Tensor, logits: torch.Tensor, draft_tokens: t
         n = load().va_tree_accept_workspace_bytes(B, T, V)
         if n == 0:
             raise VaError("va_tree_accept_workspace_bytes", -2)
-        workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
+        with _on_stream(stream, logits.device.index):
+            workspace = torch.empty(n, dtype=torch.uint8, device=logits.device)
+        _lend(stream, workspace)
     dev = logits.device
     if outputs is None:
-        outputs = (torch.empty(B, dtype=torch.int32, device=dev),
-                   torch.empty(B, T, dtype=torch.int32, device=dev),
-                   torch.empty(B, T, dtype=torch.int32, device=dev),
-                   torch.empty(B, dtype=torch.int32, device=dev))
+        with _on_stream(stream, dev.index):
+            outputs = (torch.empty(B, dtype=torch.int32, device=dev),
+                       torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B, dtype=torch.int32, device=dev))
+        _lend(stream, *outputs)
     alen, nodes, slots, bonus = outputs
     for t, name in zip(outputs, ("accept_len", "accept_nodes", "accept_slots", "bonus_token")):
         _dev(t, name, torch.int32)
@@ -535,11 +564,13 @@ def tree_build(cand_tokens: torch.Tensor, cand_logp: torch.Tensor, T: int,
         if free_head.numel() != 1:
             raise ValueError("free_head must hold one int32")
     if outputs is None:
-        outputs = (torch.empty(B, T, dtype=torch.int32, device=dev),
-                   torch.empty(B, T, dtype=torch.int32, device=dev),
-                   torch.empty(B, T, dtype=torch.int32, device=dev),
-                   torch.empty(B * T, dtype=torch.int32, device=dev)
-                   if free_slots is not None else None)
+        with _on_stream(stream, dev.index):
+            outputs = (torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B * T, dtype=torch.int32, device=dev)
+                       if free_slots is not None else None)
+        _lend(stream, *(t for t in outputs if t is not None))
     par, tok, depth, loc = outputs
     for t, n, size in ((par, "tree_parent", B * T), (tok, "draft_tokens", B * T),
                        (depth, "node_depth", B * T), (loc, "out_cache_loc", B * T)):
@@ -558,18 +589,6 @@ def tree_build(cand_tokens: torch.Tensor, cand_logp: torch.Tensor, T: int,
                               _stream(stream))
     _check("va_tree_build", rc)
     return par, tok, depth, (loc if free_slots is not None else None)
-
-
-def _on_stream(stream, device: int):
-    """The context in which torch's own work goes to the call's stream (the current
-    one when none is given)."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle \
-            else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
 
 
 class BoundCall:
@@ -600,11 +619,7 @@ class BoundCall:
         self._on = _on_stream(stream, device)
         self._fill = fill
         self._own = own
-        here = torch.cuda.current_stream(device)
-        self._home = here.cuda_stream
-        if stream is not None and not torch.cuda.is_current_stream_capturing():
-            for t in own:          # the results may be used and dropped here
-                t.record_stream(here)
+        self._home = torch.cuda.current_stream(device).cuda_stream
 
     @property
     def workspace(self) -> Optional[torch.Tensor]:
@@ -687,7 +702,7 @@ def _prepare_chunk(name, q, kv_pool, keys, dims, prefix_len, q_indptr, sm_scale,
         workspace = _workspace(workspace,
                                load().va_chunk_workspace_bytes(B, total_q, H, n, flags), q.device,
                                "va_chunk_workspace_bytes")
-        out, lse = _outputs(total_q, H, q.device, out, lse)
+    out, lse = _outputs(total_q, H, q.device, out, lse, stream)
     own = tuple(t for t, g in zip((workspace, out, lse), given) if g is None)
     _same_device(q.device, out=out, lse=lse)
     args = (_ptr(q), _ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), *(_ptr(k) for k in keys),
@@ -780,6 +795,7 @@ def prepare_kv_weights(q: torch.Tensor, kv_pool: torch.Tensor, slot_idx: torch.T
         # entries that no request's keys cover hold weights_in's totals (or zero)
         with _on_stream(stream, q.device.index):
             out = weights_out = torch.empty(n, dtype=torch.float32, device=q.device)
+        _lend(stream, out)
         own += (out,)
 
         def fill():

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import synth
-from tests import _chunk
+from tests import _chunk, _gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,53 @@ def test_results_used_and_dropped_on_the_current_stream(va):
     assert not torch.cuda.current_stream().query()
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
+
+
+@pytest.mark.parametrize("what", ["paged", "contiguous", "segmented", "accept", "build"])
+def test_verify_and_tree_calls_on_a_given_stream(va, what, monkeypatch):
+    """One call each on a stream that is busy: neither workspace nor results may be had
+    by the current stream while the call is still queued."""
+    s = synth.Spec("st", B=2, H=8, T=16, prefix=[900, 70], num_slots=1 << 12, seed=501,
+                   layout="contiguous" if what == "contiguous" else "scattered")
+    d = _gpu.to_device(synth.make(s))
+    side = torch.cuda.Stream()
+    places = []
+    alloc = va.alloc_workspace
+
+    def spy(*a, **k):
+        ws, ns = alloc(*a, **k)
+        places.append((ws.data_ptr(), ws.numel()))
+        return ws, ns
+
+    monkeypatch.setattr(va, "alloc_workspace", spy)
+    kw = dict(sm_scale=s.sm_scale, stream=side)
+    g = torch.Generator().manual_seed(502)
+    pre = torch.cat([d["slot_idx"][int(d["kv_indptr"][b]):][:p] for b, p in enumerate(s.prefix)])
+    loc = torch.cat([d["slot_idx"][int(d["kv_indptr"][b]) + p:][:s.T]
+                     for b, p in enumerate(s.prefix)])
+    ind = torch.tensor([0, 900, 970], dtype=torch.int32, device="cuda")
+    root, lg = torch.randn(2, 999, generator=g).cuda(), torch.randn(2, 16, 999, generator=g).cuda()
+    tok = torch.randint(0, 999, (2, 16), generator=g, dtype=torch.int32).cuda()
+    ctok = torch.randint(0, 999, (2, 4, 4), generator=g, dtype=torch.int32).cuda()
+    clp = torch.log_softmax(torch.randn(2, 4, 4, generator=g), -1).cuda()
+    a = (d["prefix_len"], d["parents"])
+    run = {"paged": lambda: va.verify_attn_paged(d["q"], d["kv_pool"], d["slot_idx"],
+                                                 d["kv_indptr"], *a, **kw),
+           "contiguous": lambda: va.verify_attn_contiguous(d["q"], d["kv_pool"], d["kv_start"], *a,
+                                                           **kw),
+           "segmented": lambda: va.verify_attn_segmented(d["q"], d["kv_pool"], pre, ind, loc,
+                                                         tree_parent=d["parents"], **kw),
+           "accept": lambda: va.tree_accept(root, lg, tok, d["parents"], stream=side),
+           "build": lambda: va.tree_build(ctok, clp, 8, stream=side)}[what]
+    run()
+    torch.cuda.synchronize()
+    places.clear()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)       # 0.2 s
+    got = run()
+    places += [(t.data_ptr(), t.numel() * t.element_size()) for t in got if t is not None]
+    del got
+    new = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in places]
+    assert not any(overlaps(places, t) for t in new)
+    assert not side.query()
+    side.synchronize()
