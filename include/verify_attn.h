@@ -523,7 +523,8 @@ int va_chunk_attn_contiguous(const void *q, const void *kv_pool, int64_t num_slo
  * The requests' lists must not overlap.  Sums are taken in a fixed order: the
  * result is deterministic.  Other arguments as for va_chunk_attn_paged; where
  * q_indptr decreases the batch ends here too, and the requests behind it add
- * nothing to their keys' totals.
+ * nothing to their keys' totals.  When the status word holds VA_STATUS_TIMEOUT
+ * no key's total has grown.
  */
 size_t va_kv_weights_workspace_bytes(int B, int total_q, int H, int64_t num_entries, int flags);
 int va_kv_weights_paged(const void *q, const void *kv_pool, int64_t num_slots,

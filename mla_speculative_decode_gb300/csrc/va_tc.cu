@@ -82,9 +82,14 @@ extern "C" __attribute__((visibility("default"))) int va_trace_set(void* buf) {
 // VA_STATUS_TIMEOUT, every role leaves through its abort path, and the next
 // call on the stream is correct.  NULL (the default) = no gate.
 __device__ const int32_t* g_va_test_gate = nullptr;
+namespace va {
+cudaError_t set_weights_gate(const int32_t* flag);   // va_weights_tc.cu
+}
 extern "C" __attribute__((visibility("default"))) int va_test_set_gate(const int32_t* flag) {
-  return cudaMemcpyToSymbol(g_va_test_gate, &flag, sizeof(flag)) == cudaSuccess ? VA_OK
-                                                                               : VA_ERR_CUDA;
+  return cudaMemcpyToSymbol(g_va_test_gate, &flag, sizeof(flag)) == cudaSuccess &&
+                 va::set_weights_gate(flag) == cudaSuccess
+             ? VA_OK
+             : VA_ERR_CUDA;
 }
 #endif
 

@@ -41,9 +41,20 @@
 #include "va_sm100.cuh"
 #include "va_weights.cuh"
 
+#ifdef VA_TEST_HOOKS
+// Test build only: the gate of va_tc.cu, for the producer warps of this kernel.
+__device__ const int32_t* g_va_weights_gate = nullptr;
+#endif
+
 namespace va {
 
 extern PFN_cuTensorMapEncodeTiled_v12000 g_encode;   // va_tc.cu, resolved by va_init
+
+#ifdef VA_TEST_HOOKS
+cudaError_t set_weights_gate(const int32_t* flag) {
+  return cudaMemcpyToSymbol(g_va_weights_gate, &flag, sizeof(flag));
+}
+#endif
 
 namespace {
 
@@ -304,8 +315,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* srow = reinterpret_cast<int*>(gb + C::kOffSrow);
     const int pw = ptid >> 5;
     bool ok = true;
+#ifdef VA_TEST_HOOKS
+    {
+      bool open = true;
+      if (ptid == 0 && g_va_weights_gate) {
+        const long long t0 = clock64();
+        while (open && *reinterpret_cast<const volatile int32_t*>(g_va_weights_gate) == 0) {
+          open = clock64() - t0 <= kWaitCycles;
+          __nanosleep(2000);
+        }
+      }
+      ok = named_sync_and(kProducerBar, kProducers, open);
+    }
+#endif
     int visit = 0, kt = -1, b = -1;
-    for (; w.left > 0; w.next()) {
+    for (; ok && w.left > 0; w.next()) {
       if (w.kt == kt && w.b == b) continue;   // another row tile of the same keys
       kt = w.kt;
       b = w.b;
@@ -659,7 +683,10 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
   griddep_wait();                // the sums are complete
   griddep_launch_dependents();   // the next kernel may start its set-up
   for (int i = tid; i < p.clusters; i += 256) heads[i] = p.cont_entry[i];
-  __syncthreads();
+  for (int i = tid; i < p.clusters * (p.tile_keys / kKeys); i += 256) bits |= p.cta_flags[i];
+  // (a CTA that gave up a wait has not written the shares of its last tiles: then
+  // every key keeps its total, and the status word says so)
+  const bool gave_up = __syncthreads_or((bits & VA_STATUS_TIMEOUT) != 0u);
   const int64_t j64 = e - r.base;
   const int N = r.nlist < r.P + r.n ? r.nlist : r.P + r.n;
   if (e < c.num_entries && j64 >= 0 && j64 < N) {
@@ -671,7 +698,7 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
     if (c.window > 0 && j >= c.sinks && int64_t(j) + c.window - 1 - r.P < last)
       last = int64_t(j) + c.window - 1 - r.P;
     float v = 0.f;
-    if (first <= last) {
+    if (first <= last && !gave_up) {
       if (chunk_key_row(c, r, j) < 0) {
         bits |= VA_STATUS_BAD_SLOT;
       } else {
@@ -684,12 +711,9 @@ __global__ void __launch_bounds__(256) weights_finish_kernel(const WeightTcParam
     }
     p.wout[e] = (p.win ? p.win[e] : 0.f) + v;
   }
-  if (blockIdx.x == 0) {
-    const int ctas = p.clusters * (p.tile_keys / kKeys);
-    for (int i = tid; i < ctas; i += 256) bits |= p.cta_flags[i];
+  if (blockIdx.x == 0)
     for (int b = tid; b < c.B; b += 256)
       if (chunk_req(c, b).bad) bits |= VA_STATUS_BAD_INDPTR;
-  }
   if (bits) atomicOr(&s_bits, bits);
   __syncthreads();
   if (tid == 0 && s_bits) atomicOr(c.status, s_bits);
