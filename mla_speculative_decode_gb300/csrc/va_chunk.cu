@@ -460,6 +460,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   ChunkTcParams t;
   memset(&t, 0, sizeof t);
   static_cast<ChunkParams&>(t) = p;
+  t.scale_log2 = tc_scale_log2(sm_scale);
   const int resident = c.decode ? di.num_sms : c.pair ? di.quads : di.pairs;
   t.sched.unit_rows = c.unit_rows;
   t.sched.clusters = resident < c.max_clusters ? resident : c.max_clusters;
@@ -490,6 +491,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
     e = launch_chunk_tc(t, t.sched.max_waves * t.sched.clusters, c.pair, st);
   }
   if (e != cudaSuccess) return VA_ERR_LAUNCH;
+  t.scale_log2 = p.scale_log2;   // (rows that it computes again are CUDA-core rows)
   return launch_finish(t, c.units_bound, di.num_sms, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }
 

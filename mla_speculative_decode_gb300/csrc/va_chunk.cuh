@@ -608,6 +608,20 @@ cudaError_t launch_decode_tc(const ChunkTcParams& p, int ctas, cudaStream_t st);
 cudaError_t launch_prefill_tc(const ChunkTcParams& p, int clusters, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkTcParams& p, int grid_items, bool pair, cudaStream_t st);
 
+// The scale, for base-2 exponents, of scores from the tensor cores.  They accumulate a
+// score in 36 steps that round towards zero.  What that takes off depends on how the
+// partial sums run: 4.5e-7 s on the average for keys and queries without structure,
+// 1.4e-7 s where the last columns make up the score, 1.1e-6 s where the first ones do
+// or all do evenly, up to 1.5e-6 s where half of them cancel the others.  The scale
+// makes up the average, in the attention and in the weight kernels alike: a weight
+// exp(s - lse) from an attention call's own lse then keeps no trace of what was lost
+// (totals of rows with scores up to 33: 2e-7 high; with the scale made up in the
+// weights alone 1.25e-5), and lse agrees better with an exact one (there 2e-6 off instead
+// of 1.4e-5).  The CUDA-core path rounds to nearest and takes the scale as it is.
+inline float tc_scale_log2(float sm_scale) {
+  return float(double(sm_scale) * 1.4426950408889634 * (1.0 + 4.5e-7));
+}
+
 // Checks shared by the chunk calls (va_chunk.cu).
 int chunk_check(const ChunkParams& p, bool paged, float sm_scale, int flags, const void* ws);
 

@@ -169,11 +169,7 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
     WeightTcParams t;
     memset(&t, 0, sizeof t);
     t.c = c;
-    // The tensor cores accumulate a score in 36 steps that round towards zero.
-    // A partial sum that grows evenly to s loses about 4.5e-7 s in all (measured
-    // for |s| from 16 to 64; 1.2e-6 of a total that large scores make up), so
-    // the scale makes that up: the totals' error fell to what rounding leaves.
-    t.c.scale_log2 = float(double(sm_scale) * 1.4426950408889634 * (1.0 + 4.5e-7));
+    t.c.scale_log2 = tc_scale_log2(sm_scale);
     t.win = weights_in;
     t.wout = weights_out;
     const int clusters = pair ? di.pairs : di.num_sms;
