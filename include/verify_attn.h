@@ -466,8 +466,8 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *   num_slots <= 0x7fffff00.
  *   window, sinks  >= 0; host values, the same for every request.
  *   flags          VA_PATH_*.
- *   num_entries    entries of slot_idx (lists that leave them are clamped; 0
- *                  for the contiguous form's workspace).
+ *   num_entries    entries of slot_idx, at most 2^31 - 1025 (lists that leave them
+ *                  are clamped; 0 for the contiguous form's workspace).
  *   workspace      device, >= va_chunk_workspace_bytes(B, total_q, H,
  *                  num_entries, flags) bytes, 256-byte aligned; first 4 bytes:
  *                  the status word, rewritten by every call.  It includes room
@@ -552,9 +552,9 @@ int va_kv_weights_paged(const void *q, const void *kv_pool, int64_t num_slots,
  *   slot_idx_out, prefix_len_out, weights_out, free_head_out  may each be the
  *                  matching input itself (in place), but must not overlap it
  *                  otherwise.  The requests' lists must not overlap.
- *   num_entries    entries of slot_idx, weights and their outputs; a list that
- *                  leaves them, or is shorter than prefix_len, is clamped and
- *                  sets VA_STATUS_BAD_INDPTR.
+ *   num_entries    entries of slot_idx, weights and their outputs, at most
+ *                  2^31 - 2^25 - 1; a list that leaves them, or is shorter than
+ *                  prefix_len, is clamped and sets VA_STATUS_BAD_INDPTR.
  *   status         uint32 device word or NULL; bits are OR-ed in (the caller
  *                  clears it).
  */

@@ -436,7 +436,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
   if (rc != VA_OK) return rc;
   if (p.total_q > 0 && !p.out) return VA_ERR_NULL;
   if (!aligned(p.out, 16)) return VA_ERR_ALIGN;
-  if (p.num_entries < 0 || p.num_entries > 0x7fffffff) return VA_ERR_SHAPE;
+  if (p.num_entries < 0 || p.num_entries > kKeysMax) return VA_ERR_SHAPE;
   if (p.num_slots > 0x7fffff00) return VA_ERR_SHAPE;   // rows are named by 32-bit coordinates
   if (ws_bytes < va_chunk_workspace_bytes(p.B, p.total_q, p.H, p.num_entries, flags))
     return VA_ERR_WORKSPACE;
@@ -500,7 +500,7 @@ int chunk_common(ChunkParams& p, bool paged, float sm_scale, int flags, void* ws
 
 VA_API size_t va_chunk_workspace_bytes(int B, int total_q, int H, int64_t num_entries,
                                        int flags) {
-  if (num_entries < 0 || num_entries > 0x7fffffff || B < 1 || B > 65535 || total_q < 0 || H < 1 ||
+  if (num_entries < 0 || num_entries > va::kKeysMax || B < 1 || B > 65535 || total_q < 0 || H < 1 ||
       flags < VA_PATH_AUTO || flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX)
     return 0;
   if (total_q == 0 || flags == VA_PATH_FMA) return va::kHeaderBytes;

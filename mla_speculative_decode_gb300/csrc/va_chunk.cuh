@@ -18,6 +18,10 @@ namespace va {
 constexpr int kFixedTiles = 10;
 constexpr int kSplitWaves = 7;
 
+// List positions are 32-bit: a request's keys, and the entries of all lists, stay below
+// 2^31 with some key tiles to spare.
+constexpr int kKeysMax = 0x7fffffff - 1024;
+
 // Arguments of a chunk call (va_chunk_attn_*, va_kv_weights_paged), by value.
 // Request b's new tokens are query tokens q_indptr[b] .. q_indptr[b+1] - 1; its
 // keys are P = prefix_len[b] prefix rows followed by the new tokens' own rows.
@@ -68,7 +72,7 @@ __device__ inline ChunkReq chunk_req(const ChunkParams& p, int b, bool ended = f
   if (p.kv_start) {
     // a prefix longer than the pool cannot be there
     if (P > p.num_slots) { P = int(p.num_slots); r.bad = true; }
-    if (P > 0x7fffffff - r.n) { P = 0x7fffffff - r.n; r.bad = true; }
+    if (P > kKeysMax - r.n) { P = kKeysMax - r.n; r.bad = true; }
     r.base = p.kv_start[b];
     r.nlist = P + r.n;
   } else {

@@ -52,6 +52,9 @@ constexpr int kCtaBudget = 2;   // CTAs per SM that a launch may fill (see va_kv
 constexpr int kPer = 8;                                // entries of a thread and step
 constexpr int kBatch = 16;                             // of a thread at once in the histograms
 constexpr int kList = 4096;                            // collected candidates per CTA
+// Entries at most: positions are 32-bit, and threads step past a list's end by up to
+// two batches, warps by a piece of it (1/128 of a list, of 2^31 entries 2^24).
+constexpr int64_t kEntriesMax = 0x7fffffff - (1 << 25);
 constexpr int kHeld = 10240;                           // kept entries that a CTA can hold back
 
 struct EvictParams {
@@ -506,7 +509,7 @@ VA_API int va_kv_evict(const int32_t* slot_idx, const int32_t* kv_indptr,
       !weights_out)
     return VA_ERR_NULL;
   if (free_slots && (!free_head || !free_head_out)) return VA_ERR_NULL;
-  if (B < 1 || B > 65535 || num_entries < 0 || num_entries > 0x7fffffff || budget < 0 ||
+  if (B < 1 || B > 65535 || num_entries < 0 || num_entries > kEntriesMax || budget < 0 ||
       sinks < 0 || recent < 0 || int64_t(sinks) + recent > budget ||
       (free_slots && free_capacity < 0))
     return VA_ERR_SHAPE;

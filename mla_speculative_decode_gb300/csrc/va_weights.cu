@@ -84,9 +84,6 @@ __global__ void __launch_bounds__(kWeightThreads) weights_fma_kernel(const Weigh
   if (lane == 0 && bits) atomicOr(c.status, bits);
 }
 
-// List positions stay below 2^31 with a key tile's worth to spare.
-constexpr int64_t kEntriesMax = 0x7fffffff - 1024;
-
 struct WeightsLayout {
   size_t flags, entry, cont, sums, total;
 };
@@ -110,7 +107,7 @@ VA_API size_t va_kv_weights_workspace_bytes(int B, int total_q, int H, int64_t n
                                             int flags) {
   if (B < 1 || B > 65535 || total_q < 0 || H < 1 || flags < VA_PATH_AUTO ||
       flags > VA_PATH_TC_1SM || int64_t(total_q) * H > VA_CHUNK_ROWS_MAX || num_entries < 0 ||
-      num_entries > va::kEntriesMax)
+      num_entries > va::kKeysMax)
     return 0;
   if (flags == VA_PATH_FMA) return va::kHeaderBytes;
   return va::weights_layout(num_entries).total;
@@ -145,7 +142,7 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
   const int rc = chunk_check(c, true, sm_scale, flags, workspace);
   if (rc != VA_OK) return rc;
   if (!weights_out) return VA_ERR_NULL;
-  if (num_entries < 0 || num_entries > kEntriesMax) return VA_ERR_SHAPE;
+  if (num_entries < 0 || num_entries > kKeysMax) return VA_ERR_SHAPE;
   if (!aligned4(weights_in) || !aligned4(weights_out)) return VA_ERR_ALIGN;
   if (workspace_bytes < va_kv_weights_workspace_bytes(B, total_q, H, num_entries, flags))
     return VA_ERR_WORKSPACE;

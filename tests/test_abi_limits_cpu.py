@@ -1,0 +1,31 @@
+"""The largest lists that the chunk, weight and eviction calls take: the kernels count list
+positions in 32 bits and step past a list's end by up to a tile (or a block's step), so
+longer ones are refused before any device work."""
+import pytest
+
+import mla_speculative_decode_gb300 as va
+from tests.test_abi_chunk_cpu import CHUNK, EVICT, WEIGHTS
+
+LISTS = 2 ** 31 - 1025             # chunk and weight calls
+EVICTED = 2 ** 31 - 2 ** 25 - 1    # eviction
+
+
+@pytest.fixture(scope="module")
+def lib():
+    va.build()
+    return va.load()
+
+
+@pytest.mark.parametrize("n,good", [(LISTS, True), (LISTS + 1, False), (2 ** 31 - 1, False)])
+def test_lists_of_attention_and_weights(lib, n, good):
+    want = (-5, -7) if good else (-2,)
+    for flags in range(4):
+        assert lib.va_chunk_attn_paged(*(CHUNK | dict(n=n, flags=flags)).values()) in want
+        assert lib.va_kv_weights_paged(*(WEIGHTS | dict(n=n, flags=flags)).values()) in want
+        assert (lib.va_chunk_workspace_bytes(2, 5, 8, n, flags) > 0) == good
+        assert (lib.va_kv_weights_workspace_bytes(2, 5, 8, n, flags) > 0) == good
+
+
+@pytest.mark.parametrize("n,good", [(EVICTED, True), (EVICTED + 1, False), (2 ** 31 - 1, False)])
+def test_lists_of_eviction(lib, n, good):
+    assert lib.va_kv_evict(*(EVICT | dict(n=n)).values()) in ((-5, -7) if good else (-2,))
