@@ -73,7 +73,10 @@ __device__ inline ChunkReq chunk_req(const ChunkParams& p, int b, bool ended = f
     // a prefix longer than the pool cannot be there
     if (P > p.num_slots) { P = int(p.num_slots); r.bad = true; }
     if (P > kKeysMax - r.n) { P = kKeysMax - r.n; r.bad = true; }
-    r.base = p.kv_start[b];
+    // (a start behind the pool, or so far before it that no key reaches it, names no
+    // row: clamped, so that no sum with a list position overflows)
+    const int64_t at = p.kv_start[b], before = -(int64_t(1) << 31);
+    r.base = at > p.num_slots ? p.num_slots : at < before ? before : at;
     r.nlist = P + r.n;
   } else {
     int64_t i0 = p.kv_indptr[b], i1 = p.kv_indptr[b + 1];

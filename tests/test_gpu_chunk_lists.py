@@ -1,6 +1,6 @@
-"""Chunk attention over lists that are not what the header asks for: shorter than
-the new tokens, or with bounds that decrease.  Flagged, and the same rows on every
-path (needs an sm_103 GPU)."""
+"""Chunk attention over lists that are not what the header asks for: shorter than the new
+tokens, with bounds that decrease, or outside the pool.  Flagged, and the same rows on
+every path (needs an sm_103 GPU)."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +71,18 @@ def test_list_bounds_that_decrease(va, ind, window, sinks, path):
     out, lse = _chunk.call(va, c, flags=path, window=window, sinks=sinks, workspace=ws)
     _chunk.check(c, out, lse, window=window, sinks=sinks)
     assert va.read_status(ws) == va.STATUS_BAD_INDPTR | va.STATUS_BAD_SLOT
+
+
+@pytest.mark.parametrize("H,flags", [(8, 0), (16, 0), (64, 0), (64, 1), (64, 3), (200, 0)])
+def test_contiguous_starts_at_the_ends_of_64_bits(va, H, flags):
+    """Rows that cannot be, however far outside the pool they start: no key has one."""
+    c = _chunk.make([70, 200, 130, 90], [7] * 4, H, seed=440, layout="contiguous",
+                    unused_nan=False)
+    c.kv_start = torch.tensor([2 ** 63 - 1, -2 ** 63, 2 ** 63 - 100, int(c.kv_start[3])],
+                              dtype=torch.int64)
+    for b in range(3):
+        c.key_rows[b] = np.full(c.P[b] + 7, -1)
+    call = _chunk.call(va, c, flags=flags, prepare=True)
+    out, lse = call()
+    _chunk.check(c, out, lse)
+    assert va.read_status(call.workspace) == va.STATUS_BAD_SLOT
