@@ -154,7 +154,8 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
   p.win = weights_in;
   p.wout = weights_out;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (flags != VA_PATH_FMA) {
+  // (no rows at all: there is no map of them to launch the tensor-core kernel with)
+  if (flags != VA_PATH_FMA && total_q > 0) {
     // Two-SM products when the average request has more than one row tile of the
     // one-SM kernel (32 requests of 8k keys: 64 rows 72 us with one SM and 73 with
     // two, 128 rows 116 and 77, 256 rows 205 and 74; 4 of 16k keys: 29 and 28, 41

@@ -128,3 +128,23 @@ def test_totals_without_weights_out_on_another_stream(va, start, handle):
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(first, want.cpu()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("path", list(PATHS.values()), ids=list(PATHS))
+def test_no_tokens_at_all_in_many_requests(va, path):
+    """A call without query rows copies the totals of every request's keys, reports bad
+    bounds, and touches nothing else."""
+    c = _chunk.make([10, 0, 700, 3] * 20, [0] * 80, 4, seed=412, list_gap=2)
+    w = torch.rand(c.slot_idx.numel(), generator=torch.Generator().manual_seed(5)).cuda()
+    c.prefix_len[7] = -1
+    call = va.prepare_kv_weights(*args(c), torch.empty(0, 4, device="cuda"), w,
+                                 weights_out=torch.full_like(w, -2.0), sm_scale=synth.SM_SCALE,
+                                 flags=path)
+    got = call().cpu()
+    want = torch.full_like(got, -2.0)
+    for b in range(80):
+        e = int(c.kv_indptr[b])
+        n = max(int(c.prefix_len[b]), 0)
+        want[e:e + n] = w[e:e + n].cpu()
+    assert torch.equal(got, want)
+    assert va.read_status(call.workspace) == va.STATUS_BAD_INDPTR
