@@ -467,7 +467,9 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *   window, sinks  >= 0; host values, the same for every request.
  *   flags          VA_PATH_*.
  *   num_entries    entries of slot_idx, at most 2^31 - 1025 (lists that leave them
- *                  are clamped; 0 for the contiguous form's workspace).
+ *                  are clamped; 0 for the contiguous form's workspace).  With 0
+ *                  entries, here and in the calls below, the arrays that hold
+ *                  them may be NULL.
  *   workspace      device, >= va_chunk_workspace_bytes(B, total_q, H,
  *                  num_entries, flags) bytes, 256-byte aligned; first 4 bytes:
  *                  the status word, rewritten by every call.  It includes room

@@ -416,7 +416,8 @@ cudaError_t launch_finish(const ChunkTcParams& p, int units_bound, int num_sms, 
 int chunk_check(const ChunkParams& p, bool paged, float sm_scale, int flags, const void* ws) {
   if (!p.kv || !p.prefix_len || !p.q_indptr || !ws) return VA_ERR_NULL;
   if (p.total_q > 0 && (!p.q || !p.lse)) return VA_ERR_NULL;
-  if (paged ? (!p.slot_idx || !p.kv_indptr) : !p.kv_start) return VA_ERR_NULL;
+  // (an empty list has no address)
+  if (paged ? ((!p.slot_idx && p.num_entries != 0) || !p.kv_indptr) : !p.kv_start) return VA_ERR_NULL;
   if (p.B < 1 || p.B > 65535 || p.H < 1 || p.total_q < 0) return VA_ERR_SHAPE;
   if (int64_t(p.total_q) * p.H > VA_CHUNK_ROWS_MAX) return VA_ERR_SHAPE;
   if (p.num_slots < 1 || p.kv_stride < VA_D_QK || p.window < 0 || p.sinks < 0) return VA_ERR_SHAPE;

@@ -505,8 +505,9 @@ VA_API int va_kv_evict(const int32_t* slot_idx, const int32_t* kv_indptr,
                        int32_t* prefix_len_out, float* weights_out, int32_t* free_head_out,
                        uint32_t* status, va_stream_t stream) {
   using namespace va;
-  if (!slot_idx || !kv_indptr || !prefix_len || !weights || !slot_idx_out || !prefix_len_out ||
-      !weights_out)
+  if (!kv_indptr || !prefix_len || !prefix_len_out) return VA_ERR_NULL;
+  // (empty lists have no address)
+  if (num_entries != 0 && (!slot_idx || !weights || !slot_idx_out || !weights_out))
     return VA_ERR_NULL;
   if (free_slots && (!free_head || !free_head_out)) return VA_ERR_NULL;
   if (B < 1 || B > 65535 || num_entries < 0 || num_entries > kEntriesMax || budget < 0 ||

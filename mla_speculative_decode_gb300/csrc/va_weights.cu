@@ -141,7 +141,7 @@ VA_API int va_kv_weights_paged(const void* q, const void* kv_pool, int64_t num_s
   c.lse = const_cast<float*>(lse);
   const int rc = chunk_check(c, true, sm_scale, flags, workspace);
   if (rc != VA_OK) return rc;
-  if (!weights_out) return VA_ERR_NULL;
+  if (!weights_out && num_entries != 0) return VA_ERR_NULL;
   if (num_entries < 0 || num_entries > kKeysMax) return VA_ERR_SHAPE;
   if (!aligned4(weights_in) || !aligned4(weights_out)) return VA_ERR_ALIGN;
   if (workspace_bytes < va_kv_weights_workspace_bytes(B, total_q, H, num_entries, flags))

@@ -29,3 +29,15 @@ def test_lists_of_attention_and_weights(lib, n, good):
 @pytest.mark.parametrize("n,good", [(EVICTED, True), (EVICTED + 1, False), (2 ** 31 - 1, False)])
 def test_lists_of_eviction(lib, n, good):
     assert lib.va_kv_evict(*(EVICT | dict(n=n)).values()) in ((-5, -7) if good else (-2,))
+
+
+def test_an_empty_list_may_be_null(lib):
+    """num_entries 0: there is nothing to point to (an empty tensor's address is NULL)."""
+    none = dict(n=0, slot=None)
+    assert lib.va_chunk_attn_paged(*(CHUNK | none).values()) in (-5, -7)
+    assert lib.va_chunk_attn_paged(*(CHUNK | none | dict(indptr=None)).values()) == -1
+    assert lib.va_kv_weights_paged(*(WEIGHTS | none | dict(wout=None)).values()) in (-5, -7)
+    assert lib.va_kv_weights_paged(*(WEIGHTS | none | dict(ws=None)).values()) == -1
+    none |= dict(w=None, so=None, wo=None)
+    assert lib.va_kv_evict(*(EVICT | none).values()) in (-5, -7)
+    assert lib.va_kv_evict(*(EVICT | none | dict(po=None)).values()) == -1
