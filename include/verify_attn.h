@@ -482,11 +482,12 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *                  a valid pool row gets out 0 and lse -inf.
  * Device-data errors: bounds outside the arrays, or a list shorter than
  * P_b + n_b, are clamped (the prefix gives way) and set
- * VA_STATUS_BAD_INDPTR, and where q_indptr decreases the batch ends (that
- * request and those behind it bring no rows); a slot outside the pool is
- * skipped and sets VA_STATUS_BAD_SLOT when a token would have seen it.  What
- * keys hold that a token does not see (later tokens, keys outside the window),
- * NaN and infinities included, does not change that token's result.
+ * VA_STATUS_BAD_INDPTR (a request whose kv_indptr decreases has an empty list, and
+ * tokens past the end of their request's list have no row), and where q_indptr
+ * decreases the batch ends (that request and those behind it bring no rows); a key
+ * without a row in the pool is skipped and sets VA_STATUS_BAD_SLOT when a token would
+ * have seen it.  What keys hold that a token does not see (later tokens, keys outside
+ * the window), NaN and infinities included, does not change that token's result.
  */
 #define VA_CHUNK_ROWS_MAX (1 << 24)
 size_t va_chunk_workspace_bytes(int B, int total_q, int H, int64_t num_entries, int flags);

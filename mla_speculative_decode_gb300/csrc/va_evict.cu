@@ -28,10 +28,11 @@
 // the kept entries then wait in shared memory until the cluster has read all of
 // a window of the list -- the whole list when what stays of it fits.
 // Bound by latency: barriers and dependent reads for a short list (4096 entries:
-// 11 us, of which three digits take a third), and for long ones by how many
-// reads 27 warps of an SM keep on their way: 64 lists of 20k to 200k entries,
-// 76 us, a sixth of the memory's rate counted once; the compaction is a third of
-// it, the passes of the first two digits and the count a sixth each.
+// 11.7 us, of which three digits take a third).  Of long ones (64 lists of 20k to 200k
+// entries, 76 us, a sixth of the memory's rate counted once) the compaction takes a
+// third, the passes of the first two digits and the count a sixth each; every list has
+// the same number of CTAs, so those of the longest, 49.7k entries each, have twice an
+// equal share of all entries, and the launch lasts as long as they do.
 #include <math.h>
 #include <string.h>
 

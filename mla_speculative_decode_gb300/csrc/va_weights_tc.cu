@@ -30,10 +30,11 @@
 // fixed order.
 //
 // Measured: 8 requests of one token, 64 heads, 1k to 65k paged keys (282 MB):
-// 67 us, the kernel 58 of them at 4.9 TB/s (a bare gather of such rows: 5.6).  256
-// tokens, 64 heads, 16k keys in front: 231 us, 69% of the cuBLAS rate; the tensor
-// pipe is active 57% of a launch, the rest are the waits between steps and the
-// exponentials of a tile's last columns.
+// 68 us, the kernel 58 of them at 4.9 TB/s (a bare gather of such rows: 5.6).  256
+// tokens, 64 heads, 16k keys in front: 229 us, 70% of the cuBLAS rate; the tensor
+// pipe is active 57% of a launch.  What the rest is has not been taken apart: the
+// waits between steps, the exponentials of a tile's last columns, and the query rows,
+// which at the pipe's full rate would take 9.7 TB/s from L2.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <string.h>
