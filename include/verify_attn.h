@@ -465,7 +465,8 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *   1 <= B <= 65535, 1 <= H, 0 <= total_q, total_q * H <= VA_CHUNK_ROWS_MAX,
  *   num_slots <= 0x7fffff00.
  *   window, sinks  >= 0; host values, the same for every request.
- *   flags          VA_PATH_*.
+ *   flags          VA_PATH_*.  (VA_PATH_TC_1SM takes one kernel whatever the sizes;
+ *                  its time grows with the square of B.)
  *   num_entries    entries of slot_idx, at most 2^31 - 1025 (lists that leave them
  *                  are clamped; 0 for the contiguous form's workspace).  With 0
  *                  entries, here and in the calls below, the arrays that hold
@@ -474,8 +475,9 @@ int verify_attn_paged_noalloc(const void *q, const void *kv_pool, int64_t num_sl
  *                  num_entries, flags) bytes, 256-byte aligned; first 4 bytes:
  *                  the status word, rewritten by every call.  It includes room
  *                  for the listed rows (1152 bytes per entry) when the average
- *                  request brings 640 query rows (tokens x heads) or more: the
- *                  call then first packs them side by side.  Reused across
+ *                  request brings 640 query rows (tokens x heads) or more, or
+ *                  more than 128 in a batch of more than 96 requests: the call
+ *                  then first packs them side by side.  Reused across
  *                  calls; calls that overlap on the device must not share one.
  *   out            bf16 [total_q, H, 512], 16-byte aligned; lse float
  *                  [total_q, H] (natural log).  A token none of whose keys has

@@ -229,6 +229,17 @@ static_assert(kMaxNs >= kMaxSms && kMaxNs >= kSplitWaves * kMaxPairs, "splits of
 constexpr int kPrefillRows = 640;
 constexpr int64_t kPackEntriesMax = int64_t(1) << 21;
 
+// Requests up to which the split kernel is taken.  Each of its clusters looks through
+// all requests for its piece, so a launch's time grows with their square; the decode and
+// prefill kernels look once per SM.  64 heads' worth of rows, split kernel against the
+// other: 128 rows of 8k keys, 64 requests 280 and 299 us, 128 702 and 568, 256 1371 and
+// 1106; 256 rows of 4k keys against the prefill kernel, 245 and 250, 667 and 444, 939 and
+// 830; 1024 requests of 1k keys 2164 and 668, 4159 and 959.  (65535 requests of 200
+// rows took 14 s.)  Lists too long to be packed go to the decode kernel, which reads the
+// keys once per 64 rows, from more requests on only (256 rows: 512 requests of 4.5k keys
+// 2542 and 3029 us, 1024 of 2.2k 5155 and 3639, 4096 of 600 69.8 and 7.8 ms).
+constexpr int kSplitRequests = 96, kSplitRequestsLong = 768;
+
 struct ChunkPlan {
   bool decode;       // va_decode_tc.cu
   bool prefill;      // va_prefill_tc.cu
@@ -246,14 +257,22 @@ struct ChunkPlan {
 // unit.  Above that products of two SMs (128 rows: one-SM products 146 us, two-SM
 // 191; 192 rows: 234 and 183): the prefill kernel where keys lie side by side
 // (192 rows: split 162 us, prefill 131; 4 requests of 16k keys, 82 and 55) or can be
-// packed (see kPrefillRows), else the split kernel.
+// packed (see kPrefillRows), else the split kernel.  Batches of many requests: see
+// kSplitRequests.
 ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) {
   ChunkPlan c;
   memset(&c, 0, sizeof c);
   const int64_t rows = int64_t(total_q) * H;
   const int busy = B < total_q ? B : total_q;   // requests with tokens, at most
-  c.decode = flags != VA_PATH_TC_1SM && rows <= 64 * int64_t(busy);
+  const bool paged = num_entries > 0, many = B > kSplitRequests;
+  c.decode = flags != VA_PATH_TC_1SM && rows <= (many ? 128 : 64) * int64_t(busy);
   c.pair = flags != VA_PATH_TC_1SM && rows > 128 * int64_t(busy);
+  c.prefill = c.pair && (!paged || ((many || rows >= kPrefillRows * int64_t(busy)) &&
+                                    num_entries <= kPackEntriesMax));
+  if (c.pair && !c.prefill && B > kSplitRequestsLong) {
+    c.decode = true;
+    c.pair = false;
+  }
   c.unit_rows = c.decode ? 64 : c.pair ? 256 : 128;
   c.ctas = c.decode ? 1 : c.pair ? 4 : 2;
   c.max_clusters = c.decode ? kMaxSms : c.pair ? kMaxQuads : kMaxPairs;
@@ -262,9 +281,6 @@ ChunkPlan chunk_plan(int B, int total_q, int H, int64_t num_entries, int flags) 
   // three quarters of them at least, see launch)
   const int waves = (c.units_bound + c.max_clusters * 3 / 4 - 1) / (c.max_clusters * 3 / 4);
   c.max_waves = waves > kSplitWaves ? waves : kSplitWaves;
-  const bool paged = num_entries > 0;
-  c.prefill = c.pair && (!paged || (rows >= kPrefillRows * int64_t(busy) &&
-                                    num_entries <= kPackEntriesMax));
   // the decode and prefill kernels: an item and two slots per CTA or cluster
   const bool even = c.decode || c.prefill;
   const size_t items = even ? size_t(c.max_clusters) : size_t(c.max_waves) * c.max_clusters;

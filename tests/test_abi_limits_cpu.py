@@ -41,3 +41,14 @@ def test_an_empty_list_may_be_null(lib):
     none |= dict(w=None, so=None, wo=None)
     assert lib.va_kv_evict(*(EVICT | none).values()) in (-5, -7)
     assert lib.va_kv_evict(*(EVICT | none | dict(po=None)).values()) == -1
+
+
+def test_batches_of_many_requests_pack_their_lists(lib):
+    """More than 128 rows per request, more than 96 requests: room for the listed rows."""
+    f = lib.va_chunk_workspace_bytes
+    n = 20000
+    for B, packs in ((96, False), (97, True), (4096, True)):
+        assert (f(B, 3 * B, 64, n, 0) - f(B, 3 * B, 64, 1, 0) >= (n - 1) * 1152) == packs
+        assert f(B, 2 * B, 64, n, 0) == f(B, 2 * B, 64, 1, 0)         # 128 rows: no packing
+        assert f(B, 3 * B, 64, n, 3) == f(B, 3 * B, 64, 1, 3)
+    assert f(4096, 3 * 4096, 64, 1 << 22, 0) == f(4096, 3 * 4096, 64, 1 << 23, 0)
