@@ -49,7 +49,7 @@ namespace {
 constexpr int kEvictThreads = 512;
 constexpr int kWarps = kEvictThreads / 32;
 constexpr int kBits1 = 12, kBits2 = 10, kBits3 = 10;   // digits, from the top
-constexpr int kCtaBudget = 2;   // CTAs per SM that a launch may fill (see va_kv_evict)
+constexpr int kCtaBudget = 2;   // CTAs that an SM's registers and shared memory hold
 constexpr int kPer = 8;                                // entries of a thread and step
 constexpr int kBatch = 16;                             // of a thread at once in the histograms
 constexpr int kList = 4096;                            // collected candidates per CTA

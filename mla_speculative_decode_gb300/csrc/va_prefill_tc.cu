@@ -89,8 +89,8 @@ constexpr long long kDrainCycles = 2000000ll;     // after an abort: boxes in fl
 constexpr float kRescaleLog2 = 8.f;
 
 // What a unit costs besides its tiles, in tiles: queries into tensor memory, the
-// pipeline's fill, rows out of it.  (Three prompts of 517 to 2047 tokens: 4 494 us, 5
-// 461, 6 451, 7 458, 9 472.)
+// pipeline's fill, rows out of it: about 8000 cycles, and a tile takes 1590.  (Three
+// prompts of 517 to 2047 tokens: 4 494 us, 5 461, 6 451, 7 458, 9 472.)
 constexpr int kUnitCost = 6;
 using Run = ChunkRun<kUnitRows, kUnitCost>;
 
