@@ -28,11 +28,11 @@
  *    the device, so one captured graph replays across decode steps.
  *  - Stream order holds as for any launch.  The first kernel of the attention
  *    calls (verify and, on the tensor-core paths, chunk), of va_kv_weights_paged
- *    (tensor-core paths), of va_kv_evict and of the placement calls
- *    (va_kv_append_contiguous, va_kv_compact_accepted) is a programmatic
- *    dependent of the stream's previous kernel: its CTAs may become resident
- *    while that kernel finishes, but read no input until it has completed
- *    (griddepcontrol.wait).
+ *    (tensor-core paths), of va_kv_evict, of the placement calls
+ *    (va_kv_append_contiguous, va_kv_compact_accepted), of va_rope, of
+ *    va_kv_append_paged and of the sampling calls is a programmatic dependent of
+ *    the stream's previous kernel: its CTAs may become resident while that kernel
+ *    finishes, but read no input until it has completed (griddepcontrol.wait).
  *    Their last kernel lets the stream's next kernel do the same once it has
  *    itself passed that point,
  *    so a caller's next kernel launched as a programmatic dependent must wait
@@ -568,6 +568,98 @@ int va_kv_evict(const int32_t *slot_idx, const int32_t *kv_indptr, const int32_t
                 int recent, int32_t *free_slots, int64_t free_capacity, const int32_t *free_head,
                 int32_t *slot_idx_out, int32_t *prefix_len_out, float *weights_out,
                 int32_t *free_head_out, uint32_t *status, va_stream_t stream);
+
+/*
+ * Rotary positions of heads, before the attention calls.  For every token t, head h and
+ * pair i < rot_dim / 2 of the columns [rot_offset, rot_offset + rot_dim) of a head,
+ * with c = cos(positions[t] * inv_freq[i]), s = sin(...), the pair (a, b) becomes
+ *   a' = amplitude * (a c - b s),    b' = amplitude * (a s + b c).
+ * Pair i is columns i and i + rot_dim / 2 (half layout), or 2i and 2i + 1
+ * (VA_ROPE_INTERLEAVED).  VA_ROPE_INVERSE rotates backwards (s = -sin): with the same
+ * amplitude that is the gradient with respect to x of a forward call.
+ * The other columns are copied.
+ *   x, out         [tokens, heads, width] of the type dtype (VA_F32, VA_BF16, VA_F16) at the
+ *                  given strides in elements (0 <= stride <= 2^40; columns lie next to
+ *                  each other).  out may be x itself (same strides: only the rotated
+ *                  columns are then touched), but must not overlap it otherwise; its
+ *                  rows must not overlap each other.  Aligned to the type; 16-byte alignment
+ *                  throughout (and width, rot_offset, rot_dim multiples of 8) is faster.
+ *   positions      int32 [tokens] device; may be negative.
+ *   inv_freq       HOST array, rot_dim / 2 frequencies in radians per position (finite,
+ *                  |f| < 2^40), read during the call (a captured call keeps them).
+ *                  Angles are exact to 2^-60 of a turn at every position.
+ *   0 <= tokens < 2^31 (0: x, out and positions may be NULL), 1 <= heads <= 65535,
+ *   1 <= width <= 2^20, rot_dim even, 2 <= rot_dim <= VA_ROPE_DIM_MAX.
+ * Computed in 32 bits, rounded once to the type of out.  One launch (two or more past 2^30
+ * groups of 16 bytes).
+ */
+#define VA_F32  0
+#define VA_BF16 1
+#define VA_F16  2
+#define VA_ROPE_DIM_MAX     256
+#define VA_ROPE_INTERLEAVED 1   /* flags */
+#define VA_ROPE_INVERSE     2
+int va_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+            int64_t out_token_stride, int64_t out_head_stride, int dtype,
+            const int32_t *positions, int64_t tokens, int heads, int width, int rot_offset,
+            int rot_dim, const double *inv_freq, float amplitude, int flags, va_stream_t stream);
+
+/*
+ * Frequencies for va_rope and va_kv_append_paged, in radians per position, into the host
+ * array inv_freq [rot_dim / 2].  Pure host arithmetic.  f_i = base^(-2i / rot_dim), and by
+ * `scaling`, to reach `factor` (>= 1) times the length a model was trained for:
+ *   VA_ROPE_PLAIN   f_i;
+ *   VA_ROPE_LINEAR  f_i / factor;
+ *   VA_ROPE_NTK     with base * factor^(rot_dim / (rot_dim - 2)) for base (rot_dim > 2);
+ *   VA_ROPE_YARN    (YaRN, Peng et al. 2023) f_i for the pairs that turn beta_fast times or
+ *                   more over original_len, f_i / factor for those that turn beta_slow times
+ *                   or less, and between the two a mix, linear in the pair's number:
+ *                   f_i (1 - r) + f_i / factor * r, r = clamp((i - lo) / (hi - lo), 0, 1),
+ *                   lo = max(floor(n(beta_fast)), 0), hi = min(ceil(n(beta_slow)), rot_dim - 1),
+ *                   n(b) = rot_dim ln(original_len / (2 pi b)) / (2 ln base).
+ *                   (The amplitude that goes with it is the caller's: often
+ *                   0.1 ln(factor) + 1.)
+ * beta_slow <= beta_fast, both > 0; the last three are used by VA_ROPE_YARN only.  base > 1.
+ */
+#define VA_ROPE_PLAIN  0
+#define VA_ROPE_LINEAR 1
+#define VA_ROPE_NTK    2
+#define VA_ROPE_YARN   3
+int va_rope_inv_freq(int rot_dim, double base, int scaling, double factor, int64_t original_len,
+                     double beta_fast, double beta_slow, double *inv_freq);
+
+/*
+ * The new tokens' rows of the latent cache, and the queries that go with them.  Row t of
+ * kv_new, 512 latent columns x and 64 rotary ones, becomes pool row slots[t] (bf16):
+ *   latent   x_j * norm_weight_j / sqrt(mean(x^2) + eps), or x_j where norm_weight is NULL;
+ *   rotary   rotated to positions[t] as by va_rope (rot_dim 64).
+ * With heads > 0 the same launch rotates the queries' rotary columns: q_out[t, h, 0:64] =
+ * q_pe[t, h, 0:64] rotated to positions[t] (q_out is usually columns 512 to 575 of the
+ * queries that the attention calls take).
+ *   kv_pool        bf16 [num_slots, kv_row_stride], as for the attention calls, num_slots < 2^31;
+ *                  columns from 576 on are left.
+ *   kv_new         [tokens, 576] of the type dtype, rows new_row_stride elements apart,
+ *                  16-byte aligned (rows too).
+ *   norm_weight    [512] of the type dtype, 16-byte aligned, or NULL; eps >= 0.
+ *   slots          int32 [tokens] device, distinct where they lie inside the pool (of two
+ *                  rows for one slot, parts of either may stay).  A row whose slot lies
+ *                  outside the pool (-1 for padding, say) is not written and sets
+ *                  VA_STATUS_BAD_SLOT; its query is rotated all the same.
+ *   positions, inv_freq [32], amplitude  as for va_rope.
+ *   flags          0 or VA_ROPE_INTERLEAVED, for rows and queries.
+ *   q_pe, q_out    bf16 [tokens, heads, 64], strides and alignment as for va_rope's x and out;
+ *                  q_out may be q_pe itself.  Ignored when heads is 0.
+ *   status         uint32 device word or NULL; bits are OR-ed in (the caller clears it).
+ *   0 <= tokens < 2^31, 0 <= heads <= 65535.
+ */
+int va_kv_append_paged(void *kv_pool, int64_t num_slots, int64_t kv_row_stride,
+                       const void *kv_new, int64_t new_row_stride, int dtype,
+                       const void *norm_weight, float eps, const int32_t *slots,
+                       const int32_t *positions, int64_t tokens, const double *inv_freq,
+                       float amplitude, int flags, const void *q_pe, int64_t q_pe_token_stride,
+                       int64_t q_pe_head_stride, void *q_out, int64_t q_out_token_stride,
+                       int64_t q_out_head_stride, int heads, uint32_t *status,
+                       va_stream_t stream);
 
 /*
  * Benchmark helper: while both handles are non-NULL, every verify call on this

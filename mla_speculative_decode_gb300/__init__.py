@@ -8,14 +8,15 @@ library has not been built, :func:`load` raises.
 Names follow the C ABI: ``verify_attn_paged``, ``verify_attn_contiguous``,
 ``verify_attn_defrag``, ``workspace_bytes``, ``auto_nsplit``, ``init``,
 ``read_status``; ``chunk_attn_paged``, ``chunk_attn_contiguous``, ``kv_weights``
-and ``kv_evict`` (with ``prepare_`` forms) for the calls around them.
+and ``kv_evict`` (with ``prepare_`` forms) for the calls around them; ``rope`` and
+``kv_append`` for what comes before attention (``prepare_`` forms, too).
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import List, Optional, Tuple
 
 import torch
 
@@ -35,6 +36,10 @@ STATUS_TIMEOUT = 0x8
 STATUS_BAD_DST = 0x10
 STATUS_BAD_MASK = 0x20
 PATH_AUTO, PATH_FMA, PATH_TC, PATH_TC_1SM = 0, 1, 2, 3
+ROPE_DIM_MAX = 256
+ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 LIB_PATH = _build_mod.LIB
 
@@ -64,6 +69,7 @@ def load() -> ctypes.CDLL:
                            "mla_speculative_decode_gb300.build() first")
     lib = ctypes.CDLL(LIB_PATH)
     P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    f64 = ctypes.c_double
     lib.va_version.argtypes = []
     lib.va_version.restype = i32
     lib.va_init.argtypes = [i32]
@@ -108,6 +114,14 @@ def load() -> ctypes.CDLL:
     lib.va_kv_weights_paged.restype = i32
     lib.va_kv_evict.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, P, i64, P, P, P, P, P, P, P]
     lib.va_kv_evict.restype = i32
+    lib.va_rope.argtypes = [P, i64, i64, P, i64, i64, i32, P, i64, i32, i32, i32, i32, P, f32, i32,
+                            P]
+    lib.va_rope.restype = i32
+    lib.va_rope_inv_freq.argtypes = [i32, f64, i32, f64, i64, f64, f64, P]
+    lib.va_rope_inv_freq.restype = i32
+    lib.va_kv_append_paged.argtypes = [P, i64, i64, P, i64, i32, P, f32, P, P, i64, P, f32, i32, P,
+                                       i64, i64, P, i64, i64, i32, P, P]
+    lib.va_kv_append_paged.restype = i32
     lib.verify_attn_paged_noalloc.argtypes = [P, P, i64, i64, P, P, P, P, P, i32, i32, i32, f32,
                                               i32, i32, P, P, P]
     lib.verify_attn_paged_noalloc.restype = i32
@@ -914,6 +928,164 @@ def kv_evict(slot_idx: torch.Tensor, kv_indptr: torch.Tensor, prefix_len: torch.
     return prepare_kv_evict(slot_idx, kv_indptr, prefix_len, weights, budget=budget, sinks=sinks,
                             recent=recent, free_slots=free_slots, free_head=free_head,
                             outputs=outputs, status=status, stream=stream)()
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
+                  factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
+                  beta_slow: float = 1.0) -> List[float]:
+    """Frequencies of the rot_dim / 2 pairs, radians per position: what rope and kv_append
+    take.  scaling: "none", "linear", "ntk" or "yarn" (see va_rope_inv_freq in
+    verify_attn.h).  Host arithmetic only."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    got = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    _check("va_rope_inv_freq",
+           load().va_rope_inv_freq(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                   int(original_len), float(beta_fast), float(beta_slow),
+                                   ctypes.addressof(got)))
+    return list(got)
+
+
+def _frequencies(inv_freq):
+    """inv_freq as a host array of doubles."""
+    if isinstance(inv_freq, torch.Tensor):
+        if inv_freq.is_cuda:
+            raise ValueError("inv_freq must be host values: a sequence or a CPU tensor")
+        inv_freq = inv_freq.double().tolist()
+    values = [float(v) for v in inv_freq]
+    return (ctypes.c_double * len(values))(*values)
+
+
+def _heads_arg(t: torch.Tensor, name: str, dtype=None) -> None:
+    """[tokens, heads, width] at any strides with columns next to each other."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, heads, width] with adjacent columns")
+
+
+def _token_values(t: torch.Tensor, name: str, tokens: int) -> None:
+    _dev(t, name, torch.int32)
+    if t.numel() != tokens:
+        raise ValueError(f"{name} must hold one entry per token ({tokens})")
+
+
+def prepare_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq, *, rot_offset: int = 0,
+                 interleaved: bool = False, inverse: bool = False, amplitude: float = 1.0,
+                 out: Optional[torch.Tensor] = None, stream=None) -> BoundCall:
+    """rope's checks and marshalling, done once."""
+    _heads_arg(x, "x")
+    tokens, heads, width = x.shape
+    _token_values(positions, "positions", tokens)
+    freq = _frequencies(inv_freq)
+    own = ()
+    if out is None:
+        with _on_stream(stream, x.device.index):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _lend(stream, out)
+        own = (out,)
+    _heads_arg(out, "out", x.dtype)
+    if out.shape != x.shape:
+        raise ValueError(f"out must be {tuple(x.shape)}, got {tuple(out.shape)}")
+    _same_device(x.device, positions=positions, out=out)
+    init(x.device.index)
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
+    args = (_ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0), out.stride(1),
+            DTYPES[x.dtype], _ptr(positions), tokens, heads, width, int(rot_offset), 2 * len(freq),
+            ctypes.addressof(freq), float(amplitude), flags)
+    return BoundCall("va_rope", args, out, (None, x, positions, out, freq), x.device.index, stream,
+                     own)
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq, *, rot_offset: int = 0,
+         interleaved: bool = False, inverse: bool = False, amplitude: float = 1.0,
+         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rotary positions: columns [rot_offset, rot_offset + 2 len(inv_freq)) of every head of
+    x [tokens, heads, width] (fp32, bf16 or fp16, any strides) rotated to positions (int32
+    [tokens]); the other columns are copied.  Returns out, which may be given, x itself
+    included (in place).
+
+    inv_freq: host frequencies (rope_inv_freq, or a model's own).  Pairs are columns i and
+    i + rot_dim / 2, or 2i and 2i + 1 with interleaved.  inverse rotates backwards, which is
+    the gradient with respect to x.  See va_rope in verify_attn.h."""
+    return prepare_rope(x, positions, inv_freq, rot_offset=rot_offset, interleaved=interleaved,
+                        inverse=inverse, amplitude=amplitude, out=out, stream=stream)()
+
+
+def prepare_kv_append(kv_pool: torch.Tensor, kv_new: torch.Tensor, slots: torch.Tensor,
+                      positions: torch.Tensor, inv_freq, *,
+                      norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      interleaved: bool = False, amplitude: float = 1.0,
+                      q_pe: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> BoundCall:
+    """kv_append's checks and marshalling, done once."""
+    _pool_arg(kv_pool)
+    if not kv_new.is_cuda:
+        raise ValueError("kv_new must be a CUDA tensor")
+    if kv_new.dtype not in DTYPES:
+        raise TypeError(f"kv_new must be float32, bfloat16 or float16, got {kv_new.dtype}")
+    if kv_new.dim() != 2 or kv_new.shape[1] != D_QK or kv_new.stride(1) != 1:
+        raise ValueError(f"kv_new must be [tokens, {D_QK}] with adjacent columns")
+    tokens = kv_new.shape[0]
+    _token_values(slots, "slots", tokens)
+    _token_values(positions, "positions", tokens)
+    freq = _frequencies(inv_freq)
+    if len(freq) != (D_QK - D_V) // 2:
+        raise ValueError(f"inv_freq must hold {(D_QK - D_V) // 2} frequencies, got {len(freq)}")
+    if norm_weight is not None:
+        _dev(norm_weight, "norm_weight", kv_new.dtype)
+        if norm_weight.numel() != D_V:
+            raise ValueError(f"norm_weight must hold {D_V} entries")
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    own, heads, q_args = (), 0, (None, 0, 0, None, 0, 0)
+    if q_pe is not None:
+        _heads_arg(q_pe, "q_pe", torch.bfloat16)
+        heads = q_pe.shape[1]
+        if tuple(q_pe.shape) != (tokens, heads, D_QK - D_V):
+            raise ValueError(f"q_pe must be [{tokens}, heads, {D_QK - D_V}], got {tuple(q_pe.shape)}")
+        if q_out is None:
+            with _on_stream(stream, q_pe.device.index):
+                q_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
+            _lend(stream, q_out)
+            own = (q_out,)
+        _heads_arg(q_out, "q_out", torch.bfloat16)
+        if q_out.shape != q_pe.shape:
+            raise ValueError(f"q_out must be {tuple(q_pe.shape)}, got {tuple(q_out.shape)}")
+        q_args = (_ptr(q_pe), q_pe.stride(0), q_pe.stride(1), _ptr(q_out), q_out.stride(0),
+                  q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out needs q_pe")
+    dev = kv_pool.device
+    _same_device(dev, kv_new=kv_new, slots=slots, positions=positions, norm_weight=norm_weight,
+                 status=status, q_pe=q_pe, q_out=q_out)
+    init(dev.index)
+    args = (_ptr(kv_pool), kv_pool.shape[0], kv_pool.stride(0), _ptr(kv_new), kv_new.stride(0),
+            DTYPES[kv_new.dtype], _ptr(norm_weight), float(eps), _ptr(slots), _ptr(positions),
+            tokens, ctypes.addressof(freq), float(amplitude),
+            ROPE_INTERLEAVED if interleaved else 0, *q_args, heads, _ptr(status))
+    return BoundCall("va_kv_append_paged", args, (kv_pool, q_out),
+                     (None, kv_pool, kv_new, slots, positions, norm_weight, q_pe, q_out, status,
+                      freq), dev.index, stream, own)
+
+
+def kv_append(kv_pool: torch.Tensor, kv_new: torch.Tensor, slots: torch.Tensor,
+              positions: torch.Tensor, inv_freq, *, norm_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, interleaved: bool = False, amplitude: float = 1.0,
+              q_pe: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None):
+    """The new tokens' rows of the latent cache: kv_new [tokens, 576] (fp32, bf16 or fp16;
+    512 latent columns, RMS-normalised with norm_weight unless that is None, and 64 rotary
+    ones, rotated to positions) into pool rows slots (int32 [tokens]; rows whose slot lies
+    outside the pool are skipped).  With q_pe (bf16 [tokens, heads, 64]) the same launch
+    rotates the queries' rotary columns into q_out, usually q[..., 512:] of the queries that
+    the attention calls take.  Returns (kv_pool, q_out).  See va_kv_append_paged in
+    verify_attn.h."""
+    return prepare_kv_append(kv_pool, kv_new, slots, positions, inv_freq, norm_weight=norm_weight,
+                             eps=eps, interleaved=interleaved, amplitude=amplitude, q_pe=q_pe,
+                             q_out=q_out, status=status, stream=stream)()
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

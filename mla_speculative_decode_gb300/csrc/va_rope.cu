@@ -1,0 +1,648 @@
+// va_rope.cu -- what prepares new tokens for the attention calls: rotary positions of
+// heads (queries, keys), and the new tokens' rows of the latent cache.
+//
+// A pair (a, b) of columns at position p and frequency f becomes
+//   a' = amp (a cos(p f) - b sin(p f)),   b' = amp (a sin(p f) + b cos(p f)).
+// The angle is kept in turns, as a 64-bit fraction of one: the frequency is held as
+// f / 2 pi * 2^64 (modulo one turn), a position's angle is the low 64 bits of its product
+// with that, exact for every 32-bit position, and only what is left after the nearest
+// quarter turn, at most an eighth of a turn, is rounded to 32 bits.  (p f in 32 bits would
+// be off by 0.06 radians at position 1e6.)
+//
+// Both kernels are bound by memory for prompts and by launch latency for single tokens.
+#include <cuda_fp16.h>
+#include <math.h>
+#include <string.h>
+
+#include "va_common.cuh"
+
+#ifndef VA_API
+#define VA_API extern "C" __attribute__((visibility("default")))
+#endif
+
+namespace va {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kUnit = 8;                       // columns of an item: four pairs, or eight to copy
+constexpr int kPairsMax = VA_ROPE_DIM_MAX / 2;
+constexpr int kRowRot = kDqk - kDv;            // rotary columns of a latent row: 64
+constexpr int64_t kItemsMax = int64_t(1) << 30;   // of one launch
+
+struct Freq {
+  uint64_t turn[kPairsMax];   // turns per position, in units of 2^-64 turn
+};
+
+// Division of 31-bit numbers by a fixed divisor: n / d = (n * mul) >> (31 + shift).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  f.shift = 0;
+  while ((uint64_t(1) << f.shift) < d) ++f.shift;
+  // ceil(2^(31 + shift) / d) < 2^32 and exact for n < 2^31
+  f.mul = uint32_t(((uint64_t(1) << (31 + f.shift)) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
+  return uint32_t((uint64_t(n) * f.mul) >> (31 + f.shift));
+}
+
+struct HeadParams {
+  const void* x;
+  void* out;
+  int64_t x_token, x_head, out_token, out_head;   // strides in elements
+  const int32_t* positions;
+  FastDiv per_row;     // items of a head's row
+  FastDiv heads;
+  uint32_t items;
+  int rot_offset, pairs;
+  int before;          // copied items in front of the rotated ones
+  float cos_amp, sin_amp;   // amplitude, with the sign of the direction
+};
+
+// (cos, sin) of a position's angle, an angle of `turn` per position.
+__device__ __forceinline__ float2 cos_sin(uint64_t turn, int32_t position) {
+  const uint64_t a = turn * uint64_t(int64_t(position));
+  const uint64_t quarter = (a + (uint64_t(1) << 61)) >> 62;
+  const int64_t rest = int64_t(a - (quarter << 62));   // of a turn, in [-1/8, 1/8)
+  float s, c;
+  sincospif(float(int32_t(rest >> 30)) * 0x1p-33f, &s, &c);   // (2^-34 turn is 2^-33 pi)
+  const bool swap = quarter & 1;
+  const float x = swap ? s : c, y = swap ? c : s;
+  // 0: (c, s)   1: (-s, c)   2: (-c, -s)   3: (s, -c)
+  return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter >= 2 ? -y : y);
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// kN consecutive elements as one access of kN * sizeof(T) bytes (16 at most).
+template <typename T, int kN>
+struct alignas(sizeof(T) * kN) Vec {
+  T v[kN];
+};
+
+// An item: kN pairs of a row, or 2 kN columns that are copied, as two pieces of kN
+// elements (next to each other unless the layout splits pairs by halves).  With kN = 1
+// nothing is known of alignment, and a copied item is one column.
+template <typename T, bool kInterleaved, int kN>
+struct Item {
+  Vec<T, kN> a, b;
+  __device__ __forceinline__ void load(const T* p0, const T* p1) {
+    if constexpr (kInterleaved && kN > 1 && sizeof(T) * 2 * kN <= 16) {
+      const Vec<T, 2 * kN> w = *reinterpret_cast<const Vec<T, 2 * kN>*>(p0);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) { a.v[i] = w.v[i]; b.v[i] = w.v[kN + i]; }
+    } else {
+      a = *reinterpret_cast<const Vec<T, kN>*>(p0);
+      b = *reinterpret_cast<const Vec<T, kN>*>(p1);
+    }
+  }
+  __device__ __forceinline__ void store(T* p0, T* p1) const {
+    if constexpr (kInterleaved && kN > 1 && sizeof(T) * 2 * kN <= 16) {
+      Vec<T, 2 * kN> w;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) { w.v[i] = a.v[i]; w.v[kN + i] = b.v[i]; }
+      *reinterpret_cast<Vec<T, 2 * kN>*>(p0) = w;
+    } else {
+      *reinterpret_cast<Vec<T, kN>*>(p0) = a;
+      *reinterpret_cast<Vec<T, kN>*>(p1) = b;
+    }
+  }
+  __device__ __forceinline__ void rotate(const float2 (&cs)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      // pair i: (a_i, b_i) in the half layout, (2i, 2i + 1) of the 2 kN columns interleaved
+      T& lo = !kInterleaved ? a.v[i] : (2 * i < kN ? a.v[(2 * i) % kN] : b.v[(2 * i) % kN]);
+      T& hi = !kInterleaved ? b.v[i]
+                            : (2 * i + 1 < kN ? a.v[(2 * i + 1) % kN] : b.v[(2 * i + 1) % kN]);
+      const float x = to_f32(lo), y = to_f32(hi);
+      lo = from_f32<T>(x * cs[i].x - y * cs[i].y);
+      hi = from_f32<T>(x * cs[i].y + y * cs[i].x);
+    }
+  }
+};
+
+// Items base + lane, base + 32 + lane, ...: a warp takes 32 kK of them, so that its rows
+// are neighbours and mostly share a token, whose angles a thread then computes once.
+template <typename T, bool kInterleaved, int kN, int kK>
+__device__ __forceinline__ void rotate_heads(const HeadParams& p, const Freq& f, uint32_t block) {
+  const uint32_t warp = block * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t base = warp * (32 * kK) + (threadIdx.x & 31);
+  Item<T, kInterleaved, kN> it[kK];
+  T *o0[kK], *o1[kK];
+  int32_t pos[kK];
+  int first[kK];   // first pair of an item, -1: copied
+#pragma unroll
+  for (int k = 0; k < kK; ++k) {
+    const uint32_t g = base + 32 * k;
+    first[k] = -2;
+    pos[k] = 0;
+    if (g < p.items) {
+      const uint32_t row = div_by(g, p.per_row), i = g - row * p.per_row.d;
+      const uint32_t token = div_by(row, p.heads), head = row - token * p.heads.d;
+      const int r = int(i) - p.before;          // among the rotated items
+      const bool rot = r >= 0 && r * kN < p.pairs;
+      int c0, c1;   // columns of the two pieces
+      if (rot) {
+        c0 = p.rot_offset + (kInterleaved ? 2 * kN : kN) * r;
+        c1 = c0 + (kInterleaved ? kN : p.pairs);
+      } else if (kN > 1) {
+        c0 = int(i) * 2 * kN;
+        c1 = c0 + kN;
+      } else {
+        c0 = c1 = r < 0 ? int(i) : int(i) + p.pairs;
+      }
+      first[k] = rot ? r * kN : -1;
+      const T* x = static_cast<const T*>(p.x) + int64_t(token) * p.x_token + int64_t(head) * p.x_head;
+      T* o = static_cast<T*>(p.out) + int64_t(token) * p.out_token + int64_t(head) * p.out_head;
+      it[k].load(x + c0, x + c1);
+      o0[k] = o + c0;
+      o1[k] = o + c1;
+      if (rot) pos[k] = p.positions[token];
+    }
+  }
+  float2 cs[kN];
+  int have = -1, have_pos = 0;
+#pragma unroll
+  for (int k = 0; k < kK; ++k) {
+    if (first[k] < -1) continue;
+    if (first[k] >= 0) {
+      if (first[k] != have || pos[k] != have_pos) {
+        have = first[k];
+        have_pos = pos[k];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const float2 v = cos_sin(f.turn[have + i], have_pos);
+          cs[i] = make_float2(v.x * p.cos_amp, v.y * p.sin_amp);
+        }
+      }
+      it[k].rotate(cs);
+    }
+    it[k].store(o0[k], o1[k]);
+  }
+}
+
+template <typename T, bool kInterleaved, int kN, int kK>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ HeadParams p,
+                                                            const __grid_constant__ Freq f) {
+  griddep_wait();                // the stream's previous kernel has completed
+  griddep_launch_dependents();   // the next kernel may start its set-up
+  rotate_heads<T, kInterleaved, kN, kK>(p, f, blockIdx.x);
+}
+
+struct RowParams {
+  __nv_bfloat16* pool;
+  int64_t num_slots, stride;
+  const void* rows;
+  int64_t row_stride;
+  const void* weight;   // [512] or NULL
+  float eps;
+  const int32_t* slots;
+  const int32_t* positions;
+  int64_t tokens;
+  float cos_amp, sin_amp;
+  uint32_t* status;
+  uint32_t blocks;      // of the launch, in front of those of the queries
+};
+
+// A warp per row: 16 latent columns and one pair of rotary ones per lane.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void write_row(const RowParams& p, const Freq& f) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = int64_t(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  if (r >= p.tokens) return;
+  constexpr int kPer = 16 / sizeof(T);   // elements of a 16-byte access
+  constexpr int kVecs = 16 / kPer;       // accesses of a lane's 16 columns
+  const int64_t slot = p.slots[r];
+  const int32_t pos = p.positions[r];
+  const T* row = static_cast<const T*>(p.rows) + r * p.row_stride;
+  // lane l holds the kPer columns from (l + 32 j) kPer on
+  Vec<T, kPer> v[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+    v[j] = reinterpret_cast<const Vec<T, kPer>*>(row)[lane + 32 * j];
+  const int c0 = kDv + (kInterleaved ? 2 * lane : lane), c1 = c0 + (kInterleaved ? 1 : kRowRot / 2);
+  float a, b;
+  if constexpr (kInterleaved) {
+    const Vec<T, 2> w = *reinterpret_cast<const Vec<T, 2>*>(row + c0);
+    a = to_f32(w.v[0]);
+    b = to_f32(w.v[1]);
+  } else {
+    a = to_f32(row[c0]);
+    b = to_f32(row[c1]);
+  }
+  if (slot < 0 || slot >= p.num_slots) {
+    if (lane == 0 && p.status) atomicOr(p.status, VA_STATUS_BAD_SLOT);
+    return;
+  }
+  Vec<T, kPer> g[kVecs];
+  if (p.weight) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      g[j] = reinterpret_cast<const Vec<T, kPer>*>(p.weight)[lane + 32 * j];
+  }
+  float scale = 1.f;
+  if (p.weight) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float x = to_f32(v[j].v[i]);
+        ss += x * x;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    scale = rsqrtf(ss * (1.f / kDv) + p.eps);
+  }
+  __nv_bfloat16* out = p.pool + slot * p.stride;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    Vec<__nv_bfloat16, kPer> w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      float x = to_f32(v[j].v[i]);
+      if (p.weight) x = x * scale * to_f32(g[j].v[i]);
+      w.v[i] = __float2bfloat16_rn(x);
+    }
+    reinterpret_cast<Vec<__nv_bfloat16, kPer>*>(out)[lane + 32 * j] = w;
+  }
+  const float2 cs = cos_sin(f.turn[lane], pos);
+  const float c = cs.x * p.cos_amp, s = cs.y * p.sin_amp;
+  const __nv_bfloat16 y0 = __float2bfloat16_rn(a * c - b * s);
+  const __nv_bfloat16 y1 = __float2bfloat16_rn(a * s + b * c);
+  if constexpr (kInterleaved) {
+    Vec<__nv_bfloat16, 2> w;
+    w.v[0] = y0;
+    w.v[1] = y1;
+    *reinterpret_cast<Vec<__nv_bfloat16, 2>*>(out + c0) = w;
+  } else {
+    out[c0] = y0;
+    out[c1] = y1;
+  }
+}
+
+// The rows' blocks, then those of the queries (bf16, 64 rotary columns).
+template <typename T, bool kInterleaved, int kN, int kK>
+__global__ void __launch_bounds__(kRopeThreads) append_rows_kernel(const __grid_constant__ RowParams r,
+                                                                   const __grid_constant__ HeadParams p,
+                                                                   const __grid_constant__ Freq f) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (blockIdx.x < r.blocks)
+    write_row<T, kInterleaved>(r, f);
+  else
+    rotate_heads<__nv_bfloat16, kInterleaved, kN, kK>(p, f, blockIdx.x - r.blocks);
+}
+
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// inv_freq (radians per position) as a fraction of a turn.  1 / 2 pi in two parts, so that
+// the fraction is good to its last bits.
+bool set_freq(const double* inv_freq, int pairs, Freq* f) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  for (int i = 0; i < pairs; ++i) {
+    const double x = inv_freq[i];
+    if (!(fabs(x) < 0x1p40)) return false;
+    const double hi = x * kHi, lo = fma(x, kHi, -hi) + x * kLo;
+    f->turn[i] = uint64_t((hi - floor(hi)) * 0x1p64) + uint64_t(int64_t(lo * 0x1p64));
+  }
+  return true;
+}
+
+template <typename... A, typename... B>
+int launch(void (*kernel)(A...), uint32_t blocks, va_stream_t stream, const B&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(blocks, 1u, 1u);
+  cfg.blockDim = dim3(kRopeThreads, 1u, 1u);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
+}
+
+// Whether rows of `width` elements at these strides keep apart.
+bool rows_apart(int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride,
+                int64_t width) {
+  if (tokens == 1) return heads == 1 || head_stride >= width;
+  if (heads == 1) return token_stride >= width;
+  const bool inner = head_stride <= token_stride;   // heads within tokens
+  const int64_t s0 = inner ? head_stride : token_stride, n0 = inner ? heads : tokens;
+  const int64_t s1 = inner ? token_stride : head_stride;
+  return s0 >= width && s1 >= (n0 - 1) * s0 + width;
+}
+
+struct HeadArgs {
+  const void* x;
+  int64_t x_token, x_head;
+  void* out;
+  int64_t out_token, out_head;
+  size_t elem;
+  int64_t tokens, heads;
+  int width, rot_offset, rot_dim;
+};
+
+constexpr int64_t kStrideMax = int64_t(1) << 40;
+
+int check_heads(const HeadArgs& h) {
+  if (h.x_token < 0 || h.x_head < 0 || h.out_token < 0 || h.out_head < 0 ||
+      h.x_token > kStrideMax || h.x_head > kStrideMax || h.out_token > kStrideMax ||
+      h.out_head > kStrideMax)
+    return VA_ERR_SHAPE;
+  if (!rows_apart(h.tokens, h.out_token, h.heads, h.out_head, h.width)) return VA_ERR_SHAPE;
+  if (!aligned_to(h.x, h.elem) || !aligned_to(h.out, h.elem)) return VA_ERR_ALIGN;
+  return VA_OK;
+}
+
+// 16-byte accesses (8 and 8 in the half layout) where every item allows them.
+bool vectors(const HeadArgs& h) {
+  const size_t unit = h.elem * kUnit < 16 ? h.elem * kUnit : 16;
+  if (h.width % kUnit || h.rot_offset % kUnit || h.rot_dim % kUnit) return false;
+  if (!aligned_to(h.x, unit) || !aligned_to(h.out, unit)) return false;
+  const int64_t e = int64_t(h.elem), u = int64_t(unit);
+  return (h.tokens == 1 || (h.x_token * e % u == 0 && h.out_token * e % u == 0)) &&
+         (h.heads == 1 || (h.x_head * e % u == 0 && h.out_head * e % u == 0));
+}
+
+// Launch parameters for all tokens, in items of `unit` pairs; in place only the rotated
+// columns are touched.
+HeadParams head_params(const HeadArgs& h, int unit, const int32_t* positions, float amplitude,
+                       bool inverse) {
+  HeadParams p;
+  memset(&p, 0, sizeof p);
+  p.x = h.x;
+  p.out = h.out;
+  p.x_token = h.x_token;
+  p.x_head = h.x_head;
+  p.out_token = h.out_token;
+  p.out_head = h.out_head;
+  p.positions = positions;
+  p.heads = fast_div(uint32_t(h.heads));
+  p.pairs = h.rot_dim / 2;
+  int width = h.width, off = h.rot_offset;
+  const bool in_place = h.x == h.out && (h.tokens == 1 || h.x_token == h.out_token) &&
+                        (h.heads == 1 || h.x_head == h.out_head);
+  if (in_place) {   // rows begin at the rotated columns
+    p.x = static_cast<const uint8_t*>(h.x) + size_t(off) * h.elem;
+    p.out = static_cast<uint8_t*>(h.out) + size_t(off) * h.elem;
+    width = h.rot_dim;
+    off = 0;
+  }
+  p.rot_offset = off;
+  p.before = unit > 1 ? off / (2 * unit) : off;
+  p.per_row = fast_div(uint32_t(unit > 1 ? width / (2 * unit) : width - p.pairs));
+  p.cos_amp = amplitude;
+  p.sin_amp = inverse ? -amplitude : amplitude;
+  return p;
+}
+
+template <int kK>
+uint32_t blocks_of(uint32_t items) {
+  return (items + kRopeThreads * kK - 1) / (kRopeThreads * kK);
+}
+
+// A thread takes four items (their loads are all on the way at once) when there are
+// enough of them to fill the SMs, one when there are not.
+constexpr uint32_t kManyItems = 1u << 20;
+
+template <typename T, bool kInterleaved, int kN>
+int launch_rope(const HeadParams& p, const Freq& f, va_stream_t stream) {
+  if (p.items < kManyItems)
+    return launch(rope_kernel<T, kInterleaved, kN, 1>, blocks_of<1>(p.items), stream, p, f);
+  return launch(rope_kernel<T, kInterleaved, kN, 4>, blocks_of<4>(p.items), stream, p, f);
+}
+
+template <typename T>
+int launch_rope(const HeadParams& p, const Freq& f, bool interleaved, bool vec, va_stream_t stream) {
+  if (vec)
+    return interleaved ? launch_rope<T, true, kUnit / 2>(p, f, stream)
+                       : launch_rope<T, false, kUnit / 2>(p, f, stream);
+  return interleaved ? launch_rope<T, true, 1>(p, f, stream) : launch_rope<T, false, 1>(p, f, stream);
+}
+
+// All tokens' heads, in launches of kItemsMax items at most.
+int run_heads(const HeadArgs& h, int dtype, const int32_t* positions, const Freq& f,
+              float amplitude, int flags, va_stream_t stream) {
+  const bool interleaved = flags & VA_ROPE_INTERLEAVED, vec = vectors(h);
+  const HeadParams p = head_params(h, vec ? kUnit / 2 : 1, positions, amplitude,
+                                   flags & VA_ROPE_INVERSE);
+  const int64_t per_token = int64_t(p.per_row.d) * h.heads;
+  const int64_t step = kItemsMax / per_token;
+  for (int64_t t = 0; t < h.tokens; t += step) {
+    HeadParams q = p;
+    q.x = static_cast<const uint8_t*>(p.x) + t * h.x_token * int64_t(h.elem);
+    q.out = static_cast<uint8_t*>(p.out) + t * h.out_token * int64_t(h.elem);
+    q.positions = positions + t;
+    q.items = uint32_t((h.tokens - t < step ? h.tokens - t : step) * per_token);
+    int rc;
+    if (dtype == VA_F32)
+      rc = launch_rope<float>(q, f, interleaved, vec, stream);
+    else if (dtype == VA_BF16)
+      rc = launch_rope<__nv_bfloat16>(q, f, interleaved, vec, stream);
+    else
+      rc = launch_rope<__half>(q, f, interleaved, vec, stream);
+    if (rc != VA_OK) return rc;
+  }
+  return VA_OK;
+}
+
+template <typename T, bool kInterleaved>
+int launch_append(const RowParams& r, const HeadParams& p, const Freq& f, va_stream_t stream) {
+  if (p.items < kManyItems)
+    return launch(append_rows_kernel<T, kInterleaved, kUnit / 2, 1>, r.blocks + blocks_of<1>(p.items),
+                  stream, r, p, f);
+  return launch(append_rows_kernel<T, kInterleaved, kUnit / 2, 4>, r.blocks + blocks_of<4>(p.items),
+                stream, r, p, f);
+}
+
+template <typename T>
+int launch_append(const RowParams& r, const HeadParams& p, const Freq& f, bool interleaved,
+                  va_stream_t stream) {
+  return interleaved ? launch_append<T, true>(r, p, f, stream)
+                     : launch_append<T, false>(r, p, f, stream);
+}
+
+}  // namespace
+}  // namespace va
+
+VA_API int va_rope_inv_freq(int rot_dim, double base, int scaling, double factor,
+                            int64_t original_len, double beta_fast, double beta_slow,
+                            double* inv_freq) {
+  using namespace va;
+  if (!inv_freq) return VA_ERR_NULL;
+  if (rot_dim < 2 || rot_dim > VA_ROPE_DIM_MAX || rot_dim % 2 || !(base > 1.0) || isinf(base) ||
+      scaling < VA_ROPE_PLAIN || scaling > VA_ROPE_YARN)
+    return VA_ERR_SHAPE;
+  if (scaling != VA_ROPE_PLAIN && (!(factor >= 1.0) || isinf(factor))) return VA_ERR_SHAPE;
+  if (scaling == VA_ROPE_NTK && rot_dim == 2) return VA_ERR_SHAPE;
+  if (scaling == VA_ROPE_YARN &&
+      (original_len < 1 || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) || isinf(beta_fast)))
+    return VA_ERR_SHAPE;
+  const int pairs = rot_dim / 2;
+  const double pi = 3.14159265358979323846;
+  if (scaling == VA_ROPE_NTK) base *= pow(factor, double(rot_dim) / (rot_dim - 2));
+  // the pair that turns `n` times over the original length
+  auto pair_of = [&](double n) {
+    return rot_dim * log(double(original_len) / (2.0 * pi * n)) / (2.0 * log(base));
+  };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == VA_ROPE_YARN) {
+    lo = fmax(floor(pair_of(beta_fast)), 0.0);
+    hi = fmin(ceil(pair_of(beta_slow)), double(rot_dim - 1));
+  }
+  for (int i = 0; i < pairs; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == VA_ROPE_LINEAR) f /= factor;
+    if (scaling == VA_ROPE_YARN) {
+      const double ramp = fmin(1.0, fmax(0.0, (i - lo) / fmax(hi - lo, 0.001)));
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    inv_freq[i] = f;
+  }
+  return VA_OK;
+}
+
+VA_API int va_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* out,
+                   int64_t out_token_stride, int64_t out_head_stride, int dtype,
+                   const int32_t* positions, int64_t tokens, int heads, int width, int rot_offset,
+                   int rot_dim, const double* inv_freq, float amplitude, int flags,
+                   va_stream_t stream) {
+  using namespace va;
+  if (!inv_freq || (tokens != 0 && (!x || !out || !positions))) return VA_ERR_NULL;
+  if (tokens < 0 || tokens > 0x7fffffff || heads < 1 || heads > 65535 || width < 1 ||
+      width > (1 << 20) || rot_dim < 2 || rot_dim % 2 || rot_dim > VA_ROPE_DIM_MAX ||
+      rot_offset < 0 || rot_dim > width || rot_offset > width - rot_dim || dtype < VA_F32 ||
+      dtype > VA_F16 || flags < 0 || flags > (VA_ROPE_INTERLEAVED | VA_ROPE_INVERSE) ||
+      !isfinite(amplitude))
+    return VA_ERR_SHAPE;
+  HeadArgs h;
+  h.x = x;
+  h.x_token = x_token_stride;
+  h.x_head = x_head_stride;
+  h.out = out;
+  h.out_token = out_token_stride;
+  h.out_head = out_head_stride;
+  h.elem = dtype == VA_F32 ? 4 : 2;
+  h.tokens = tokens;
+  h.heads = heads;
+  h.width = width;
+  h.rot_offset = rot_offset;
+  h.rot_dim = rot_dim;
+  Freq f;
+  memset(&f, 0, sizeof f);
+  if (!set_freq(inv_freq, rot_dim / 2, &f)) return VA_ERR_SHAPE;
+  if (tokens) {
+    const int rc = check_heads(h);
+    if (rc != VA_OK) return rc;
+    if (!aligned_to(positions, 4)) return VA_ERR_ALIGN;
+  }
+  DeviceInfo di;
+  const int rc = device_info(&di);
+  if (rc != VA_OK || tokens == 0) return rc;
+  return run_heads(h, dtype, positions, f, amplitude, flags, stream);
+}
+
+VA_API int va_kv_append_paged(void* kv_pool, int64_t num_slots, int64_t kv_row_stride,
+                              const void* kv_new, int64_t new_row_stride, int dtype,
+                              const void* norm_weight, float eps, const int32_t* slots,
+                              const int32_t* positions, int64_t tokens, const double* inv_freq,
+                              float amplitude, int flags, const void* q_pe, int64_t q_pe_token_stride,
+                              int64_t q_pe_head_stride, void* q_out, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride, int heads, uint32_t* status,
+                              va_stream_t stream) {
+  using namespace va;
+  if (!kv_pool || !inv_freq || (tokens != 0 && (!kv_new || !slots || !positions)))
+    return VA_ERR_NULL;
+  if (heads > 0 && tokens != 0 && (!q_pe || !q_out)) return VA_ERR_NULL;
+  const size_t elem = dtype == VA_F32 ? 4 : 2;
+  if (tokens < 0 || tokens > 0x7fffffff || num_slots < 1 || num_slots > 0x7fffffff ||
+      kv_row_stride < VA_D_QK || kv_row_stride > kStrideMax || new_row_stride < 0 ||
+      new_row_stride > kStrideMax || dtype < VA_F32 || dtype > VA_F16 || heads < 0 ||
+      heads > 65535 || flags < 0 || flags > VA_ROPE_INTERLEAVED || !isfinite(amplitude) ||
+      !(eps >= 0.f) || !isfinite(eps))
+    return VA_ERR_SHAPE;
+  Freq f;
+  memset(&f, 0, sizeof f);
+  if (!set_freq(inv_freq, kRowRot / 2, &f)) return VA_ERR_SHAPE;
+  if (kv_row_stride % 8 != 0 || (tokens > 1 && new_row_stride * int64_t(elem) % 16 != 0))
+    return VA_ERR_ALIGN;
+  if (!aligned_to(kv_pool, 16) || !aligned_to(kv_new, 16) || !aligned_to(norm_weight, 16) ||
+      !aligned_to(slots, 4) || !aligned_to(positions, 4) || !aligned_to(status, 4))
+    return VA_ERR_ALIGN;
+  HeadArgs h;
+  memset(&h, 0, sizeof h);
+  if (heads > 0 && tokens != 0) {
+    h.x = q_pe;
+    h.x_token = q_pe_token_stride;
+    h.x_head = q_pe_head_stride;
+    h.out = q_out;
+    h.out_token = q_out_token_stride;
+    h.out_head = q_out_head_stride;
+    h.elem = 2;
+    h.tokens = tokens;
+    h.heads = heads;
+    h.width = kRowRot;
+    h.rot_offset = 0;
+    h.rot_dim = kRowRot;
+    const int rc = check_heads(h);
+    if (rc != VA_OK) return rc;
+  }
+  DeviceInfo di;
+  int rc = device_info(&di);
+  if (rc != VA_OK || tokens == 0) return rc;
+  RowParams r;
+  memset(&r, 0, sizeof r);
+  r.pool = static_cast<__nv_bfloat16*>(kv_pool);
+  r.num_slots = num_slots;
+  r.stride = kv_row_stride;
+  r.rows = kv_new;
+  r.row_stride = new_row_stride;
+  r.weight = norm_weight;
+  r.eps = eps;
+  r.slots = slots;
+  r.positions = positions;
+  r.tokens = tokens;
+  r.cos_amp = r.sin_amp = amplitude;
+  r.status = status;
+  r.blocks = uint32_t((tokens + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
+  HeadParams p;
+  memset(&p, 0, sizeof p);
+  p.per_row = p.heads = fast_div(1);
+  // the queries in the same launch, unless they lie askew or are too many for one
+  const bool apart = heads > 0 && (!vectors(h) || tokens * heads > kItemsMax * kUnit / kRowRot);
+  if (heads > 0 && !apart) {
+    p = head_params(h, kUnit / 2, positions, amplitude, false);
+    p.items = uint32_t(tokens * heads * p.per_row.d);
+  }
+  const bool interleaved = flags & VA_ROPE_INTERLEAVED;
+  if (dtype == VA_F32)
+    rc = launch_append<float>(r, p, f, interleaved, stream);
+  else if (dtype == VA_BF16)
+    rc = launch_append<__nv_bfloat16>(r, p, f, interleaved, stream);
+  else
+    rc = launch_append<__half>(r, p, f, interleaved, stream);
+  if (rc != VA_OK || !apart) return rc;
+  return run_heads(h, VA_BF16, positions, f, amplitude, flags, stream);
+}

@@ -58,6 +58,10 @@ Functions and the passages they follow (page titles and sections):
                    of ragged chunks with a window and sinks, the attention
                    weight each key receives, eviction by that weight), in plain
                    numpy; no page gives them.
+  rope, latent_rows
+                -- the definitions in include/verify_attn.h (rotary positions, the
+                   new tokens' rows of the latent cache), in plain numpy; no page
+                   gives them.
 """
 from __future__ import annotations
 
@@ -566,3 +570,32 @@ def evict(slots, weights, budget: int, sinks: int, recent: int):
     kept = [j for j in range(L) if j in stay]
     return np.array(kept, dtype=np.int64), \
         np.array([j for j in range(L) if j not in stay], dtype=np.int64)
+
+
+def rope(x, positions, inv_freq, rot_offset: int = 0, interleaved: bool = False,
+         inverse: bool = False, amplitude: float = 1.0):
+    """x [tokens, heads, width] with the pairs of columns [rot_offset, rot_offset +
+    2 len(inv_freq)) turned by positions * inv_freq and scaled by amplitude."""
+    y = np.array(x, dtype=np.float64)
+    pairs = len(inv_freq)
+    for i, f in enumerate(inv_freq):
+        ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + pairs)
+        a, b = y[..., rot_offset + ia].copy(), y[..., rot_offset + ib].copy()
+        # positions are whole and f has 53 bits: the product loses 2^-53 of itself
+        ang = np.asarray(positions, dtype=np.float64)[:, None] * float(f)
+        c, s = amplitude * np.cos(ang), amplitude * np.sin(ang) * (-1.0 if inverse else 1.0)
+        y[..., rot_offset + ia] = a * c - b * s
+        y[..., rot_offset + ib] = a * s + b * c
+    return y
+
+
+def latent_rows(kv_new, positions, inv_freq, norm_weight=None, eps: float = 1e-6,
+                interleaved: bool = False, amplitude: float = 1.0):
+    """The cache rows of new tokens, [tokens, 576], before they are rounded to bf16."""
+    kv = np.array(kv_new, dtype=np.float64)
+    if norm_weight is not None:
+        rms = np.sqrt((kv[:, :D_V] ** 2).mean(axis=1, keepdims=True) + eps)
+        kv[:, :D_V] = kv[:, :D_V] / rms * np.asarray(norm_weight, dtype=np.float64)
+    kv[:, D_V:] = rope(kv[:, None, D_V:], positions, inv_freq, 0, interleaved,
+                       False, amplitude)[:, 0]
+    return kv
