@@ -82,6 +82,7 @@ typedef struct CUstream_st *va_stream_t;
 #define VA_STATUS_BAD_DST     0x10u /* defrag destination outside the pool           */
 #define VA_STATUS_BAD_MASK    0x20u /* a dense mask row past custom_mask_len; the
                                        node's missing draft columns read as 0      */
+#define VA_STATUS_EMPTY_ROW   0x40u /* a row of logits without a value above -inf    */
 
 /* Fixed widths of the MLA latent row. */
 #define VA_D_QK 576   /* key / query width: 512 latent + 64 rotary */
@@ -660,6 +661,67 @@ int va_kv_append_paged(void *kv_pool, int64_t num_slots, int64_t kv_row_stride,
                        int64_t q_pe_head_stride, void *q_out, int64_t q_out_token_stride,
                        int64_t q_out_head_stride, int heads, uint32_t *status,
                        va_stream_t stream);
+
+/*
+ * One token per row of logits l_i, i < V.  With m = max l, T = temperature and
+ * w_i = exp((l_i - m) / T):
+ *   top-k   of the row the k largest logits stay (k <= 0 or >= V: all);
+ *   top-p   of those, largest first, the shortest run that holds top_p of their mass
+ *           sum w (top_p >= 1: all; top_p <= 0: the first alone);
+ *   min-p   and of those the ones with w_i >= min_p (min_p <= 0: all; >= 1: the largest).
+ * Equal logits rank by index, the lower first.  The token is the first kept one, in index
+ * order, at which the kept mass so far exceeds uniform * (kept mass); logprob is
+ * ln(w / kept mass) of it.  T <= 0 (or NaN) is greedy: the lowest index among the
+ * largest, logprob 0.  NaN counts as -inf; rows may hold -inf (masked tokens) and +inf
+ * (they share the mass).  A row without a value above -inf gets token 0, logprob -inf, and
+ * sets VA_STATUS_EMPTY_ROW.
+ *   logits       [rows, V] of the type dtype (VA_F32, VA_BF16, VA_F16), rows row_stride
+ *                elements apart (0 <= row_stride <= 2^40), aligned to the type.
+ *   temperature  float [rows] device, or NULL (1).   top_k  int32 [rows] or NULL (all).
+ *   top_p, min_p float [rows] device, or NULL (all).  NaN: all.
+ *   uniform      float [rows] device, in [0, 1) (NaN and below 0 count as 0; at 1 or above
+ *                the last kept token with a mass).  Independent random numbers are the
+ *                caller's.
+ *   tokens       int32 [rows];  logprob  float [rows] or NULL.
+ *   status       uint32 device word or NULL; bits are OR-ed in (the caller clears it).
+ *   0 <= rows <= 2^23, 1 <= V <= VA_SAMPLE_V_MAX.
+ * Masses are summed as whole numbers of 2^-43 (a weight below half of that has none), so
+ * the result does not depend on the order of sums: the same call gives the same token.
+ * One launch; each logit is read from memory once (rows of more than 300k 32-bit logits:
+ * several times).
+ */
+#define VA_SAMPLE_V_MAX (1 << 20)
+int va_sample(const void *logits, int64_t row_stride, int dtype, int64_t rows, int64_t V,
+              const float *temperature, const int32_t *top_k, const float *top_p,
+              const float *min_p, const float *uniform, int32_t *tokens, float *logprob,
+              uint32_t *status, va_stream_t stream);
+
+/*
+ * Tree acceptance by sampling: va_tree_accept's walk, in which the target's token at the
+ * prefix and at each node is not the most likely one but drawn, as by va_sample, from that
+ * position's logits with the request's settings and the position's own uniform.  A path is
+ * followed as long as a child carries the token drawn at its parent, and the token drawn
+ * at the path's end is the bonus: whatever the drafter proposes, the tokens emitted are
+ * distributed as if they had been sampled from the target one by one.
+ *   root_logits  [B, V], logits [B, T, V], both of the type dtype, aligned to it.
+ *   temperature, top_k, top_p, min_p  [B] device, or NULL, as for va_sample.
+ *   uniform      float [B, T + 1] device: the prefix's, then the nodes'.
+ *   logprob      float [B, T + 1] or NULL: va_sample's, of the token drawn at the prefix and
+ *                at each node.
+ *   workspace    device, >= va_tree_accept_sampled_workspace_bytes(B, T) bytes, 256-byte
+ *                aligned; first 4 bytes: the status word, rewritten by every call
+ *                (VA_STATUS_BAD_PARENT, VA_STATUS_EMPTY_ROW).  Calls that overlap on the
+ *                device must not share one.
+ * Other arguments, and the outputs, as for va_tree_accept; 1 <= V <= VA_SAMPLE_V_MAX.
+ */
+size_t va_tree_accept_sampled_workspace_bytes(int B, int T);
+int va_tree_accept_sampled(const void *root_logits, const void *logits, int dtype, int64_t V,
+                           const int32_t *draft_tokens, const int32_t *tree_parent,
+                           const int32_t *draft_slots, int B, int T, const float *temperature,
+                           const int32_t *top_k, const float *top_p, const float *min_p,
+                           const float *uniform, void *workspace, size_t workspace_bytes,
+                           int32_t *accept_len, int32_t *accept_nodes, int32_t *accept_slots,
+                           int32_t *bonus_token, float *logprob, va_stream_t stream);
 
 /*
  * Benchmark helper: while both handles are non-NULL, every verify call on this

@@ -9,7 +9,8 @@ Names follow the C ABI: ``verify_attn_paged``, ``verify_attn_contiguous``,
 ``verify_attn_defrag``, ``workspace_bytes``, ``auto_nsplit``, ``init``,
 ``read_status``; ``chunk_attn_paged``, ``chunk_attn_contiguous``, ``kv_weights``
 and ``kv_evict`` (with ``prepare_`` forms) for the calls around them; ``rope`` and
-``kv_append`` for what comes before attention (``prepare_`` forms, too).
+``kv_append`` for what comes before attention, ``sample`` and
+``tree_accept_sampled`` for what comes after it (``prepare_`` forms, too).
 """
 from __future__ import annotations
 
@@ -35,8 +36,10 @@ STATUS_BAD_INDPTR = 0x4
 STATUS_TIMEOUT = 0x8
 STATUS_BAD_DST = 0x10
 STATUS_BAD_MASK = 0x20
+STATUS_EMPTY_ROW = 0x40
 PATH_AUTO, PATH_FMA, PATH_TC, PATH_TC_1SM = 0, 1, 2, 3
 ROPE_DIM_MAX = 256
+SAMPLE_V_MAX = 1 << 20
 ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -122,6 +125,13 @@ def load() -> ctypes.CDLL:
     lib.va_kv_append_paged.argtypes = [P, i64, i64, P, i64, i32, P, f32, P, P, i64, P, f32, i32, P,
                                        i64, i64, P, i64, i64, i32, P, P]
     lib.va_kv_append_paged.restype = i32
+    lib.va_sample.argtypes = [P, i64, i32, i64, i64, P, P, P, P, P, P, P, P, P]
+    lib.va_sample.restype = i32
+    lib.va_tree_accept_sampled_workspace_bytes.argtypes = [i32, i32]
+    lib.va_tree_accept_sampled_workspace_bytes.restype = sz
+    lib.va_tree_accept_sampled.argtypes = [P, P, i32, i64, P, P, P, i32, i32, P, P, P, P, P, P, sz,
+                                           P, P, P, P, P, P]
+    lib.va_tree_accept_sampled.restype = i32
     lib.verify_attn_paged_noalloc.argtypes = [P, P, i64, i64, P, P, P, P, P, i32, i32, i32, f32,
                                               i32, i32, P, P, P]
     lib.verify_attn_paged_noalloc.restype = i32
@@ -1086,6 +1096,166 @@ def kv_append(kv_pool: torch.Tensor, kv_new: torch.Tensor, slots: torch.Tensor,
     return prepare_kv_append(kv_pool, kv_new, slots, positions, inv_freq, norm_weight=norm_weight,
                              eps=eps, interleaved=interleaved, amplitude=amplitude, q_pe=q_pe,
                              q_out=q_out, status=status, stream=stream)()
+
+
+def _logits_arg(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+
+
+def _settings(n: int, temperature, top_k, top_p, min_p):
+    """Pointers of the sampling settings, one entry per row (or request)."""
+    for t, name, dt in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
+                        (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        if t is not None:
+            _dev(t, name, dt)
+            if t.numel() != n:
+                raise ValueError(f"{name} must hold {n} entries")
+    return _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p)
+
+
+def prepare_sample(logits: torch.Tensor, uniform: torch.Tensor, *,
+                   temperature: Optional[torch.Tensor] = None,
+                   top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                   min_p: Optional[torch.Tensor] = None, tokens: Optional[torch.Tensor] = None,
+                   logprob: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                   stream=None) -> BoundCall:
+    """sample's checks and marshalling, done once."""
+    _logits_arg(logits, "logits")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, V] with adjacent columns")
+    rows, V = logits.shape
+    dev = logits.device
+    settings = _settings(rows, temperature, top_k, top_p, min_p)
+    given = (tokens, logprob)
+    with _on_stream(stream, dev.index):
+        if tokens is None:
+            tokens = torch.empty(rows, dtype=torch.int32, device=dev)
+        if logprob is None:
+            logprob = torch.empty(rows, dtype=torch.float32, device=dev)
+    own = tuple(t for t, g in zip((tokens, logprob), given) if g is None)
+    _lend(stream, *own)
+    for t, name, dt in ((uniform, "uniform", torch.float32), (tokens, "tokens", torch.int32),
+                        (logprob, "logprob", torch.float32)):
+        _dev(t, name, dt)
+        if t.numel() != rows:
+            raise ValueError(f"{name} must hold one entry per row ({rows})")
+    if status is not None:
+        _dev(status, "status", torch.int32)
+    _same_device(dev, uniform=uniform, temperature=temperature, top_k=top_k, top_p=top_p,
+                 min_p=min_p, tokens=tokens, logprob=logprob, status=status)
+    init(dev.index)
+    args = (_ptr(logits), logits.stride(0), DTYPES[logits.dtype], rows, V, *settings, _ptr(uniform),
+            _ptr(tokens), _ptr(logprob), _ptr(status))
+    return BoundCall("va_sample", args, (tokens, logprob),
+                     (None, logits, uniform, temperature, top_k, top_p, min_p, tokens, logprob,
+                      status), dev.index, stream, own)
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, *,
+           temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+           top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+           tokens: Optional[torch.Tensor] = None, logprob: Optional[torch.Tensor] = None,
+           status: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """One token per row of logits [rows, V] (fp32, bf16 or fp16), drawn by the given random
+    numbers uniform (fp32 [rows], in [0, 1)).
+
+    temperature (fp32), top_k (int32), top_p and min_p (fp32), each [rows] or None: the
+    row's k largest logits, of those the shortest run that holds top_p of their mass, of
+    those the ones at least min_p times as likely as the likeliest; temperature 0 takes the
+    largest logit.  Returns (tokens int32 [rows], logprob fp32 [rows], the logarithm of
+    the token's share of the kept mass).  See va_sample in verify_attn.h."""
+    return prepare_sample(logits, uniform, temperature=temperature, top_k=top_k, top_p=top_p,
+                          min_p=min_p, tokens=tokens, logprob=logprob, status=status,
+                          stream=stream)()
+
+
+def prepare_tree_accept_sampled(root_logits: torch.Tensor, logits: torch.Tensor,
+                                draft_tokens: torch.Tensor, tree_parent: torch.Tensor,
+                                uniform: torch.Tensor, *,
+                                temperature: Optional[torch.Tensor] = None,
+                                top_k: Optional[torch.Tensor] = None,
+                                top_p: Optional[torch.Tensor] = None,
+                                min_p: Optional[torch.Tensor] = None,
+                                draft_slots: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None, outputs=None,
+                                stream=None) -> BoundCall:
+    """tree_accept_sampled's checks and marshalling, done once."""
+    _logits_arg(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, T, V]")
+    _dev(logits, "logits", logits.dtype)
+    B, T, V = logits.shape
+    _dev(root_logits, "root_logits", logits.dtype)
+    if tuple(root_logits.shape) != (B, V):
+        raise ValueError(f"root_logits must be [{B}, {V}], got {tuple(root_logits.shape)}")
+    dev = logits.device
+    _dev(uniform, "uniform", torch.float32)
+    if uniform.numel() != B * (T + 1):
+        raise ValueError(f"uniform must hold B * (T + 1) = {B * (T + 1)} entries")
+    settings = _settings(B, temperature, top_k, top_p, min_p)
+    taken_ws, taken_out = workspace is None, outputs is None
+    with _on_stream(stream, dev.index):
+        workspace = _workspace(workspace, load().va_tree_accept_sampled_workspace_bytes(B, T), dev,
+                               "va_tree_accept_sampled_workspace_bytes")
+        if outputs is None:
+            outputs = (torch.empty(B, dtype=torch.int32, device=dev),
+                       torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B, T, dtype=torch.int32, device=dev),
+                       torch.empty(B, dtype=torch.int32, device=dev),
+                       torch.empty(B, T + 1, dtype=torch.float32, device=dev))
+    own = ((workspace,) if taken_ws else ()) + (tuple(outputs) if taken_out else ())
+    _lend(stream, *own)
+    alen, nodes, slots, bonus, logprob = outputs
+    for t, name, dt, size in ((draft_tokens, "draft_tokens", torch.int32, B * T),
+                              (tree_parent, "tree_parent", torch.int32, B * T),
+                              (draft_slots, "draft_slots", torch.int32, B * T),
+                              (alen, "accept_len", torch.int32, B),
+                              (nodes, "accept_nodes", torch.int32, B * T),
+                              (slots, "accept_slots", torch.int32, B * T),
+                              (bonus, "bonus_token", torch.int32, B),
+                              (logprob, "logprob", torch.float32, B * (T + 1))):
+        if t is not None:
+            _dev(t, name, dt)
+            if t.numel() != size:
+                raise ValueError(f"{name} must hold {size} entries")
+    _same_device(dev, root_logits=root_logits, draft_tokens=draft_tokens, tree_parent=tree_parent,
+                 uniform=uniform, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p,
+                 draft_slots=draft_slots, accept_len=alen, accept_nodes=nodes, accept_slots=slots,
+                 bonus_token=bonus, logprob=logprob)
+    init(dev.index)
+    args = (_ptr(root_logits), _ptr(logits), DTYPES[logits.dtype], V, _ptr(draft_tokens),
+            _ptr(tree_parent), _ptr(draft_slots), B, T, *settings, _ptr(uniform), _ptr(workspace),
+            workspace.numel(), _ptr(alen), _ptr(nodes), _ptr(slots), _ptr(bonus), _ptr(logprob))
+    return BoundCall("va_tree_accept_sampled", args, tuple(outputs),
+                     (workspace, root_logits, logits, draft_tokens, tree_parent, uniform,
+                      temperature, top_k, top_p, min_p, draft_slots, outputs), dev.index, stream,
+                     own)
+
+
+def tree_accept_sampled(root_logits: torch.Tensor, logits: torch.Tensor,
+                        draft_tokens: torch.Tensor, tree_parent: torch.Tensor,
+                        uniform: torch.Tensor, *, temperature: Optional[torch.Tensor] = None,
+                        top_k: Optional[torch.Tensor] = None,
+                        top_p: Optional[torch.Tensor] = None,
+                        min_p: Optional[torch.Tensor] = None,
+                        draft_slots: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, outputs=None, stream=None):
+    """Tree acceptance by sampling: tree_accept's walk along tokens that are drawn, as by
+    sample, at the prefix and at every node.
+
+    root_logits [B, V] and logits [B, T, V] (fp32, bf16 or fp16), draft_tokens, tree_parent
+    and draft_slots (or None) int32 [B, T], uniform fp32 [B, T + 1] (the prefix's, then the
+    nodes'); the settings [B] or None.  Returns (accept_len int32 [B], accept_nodes int32
+    [B, T], accept_slots int32 [B, T], bonus_token int32 [B], logprob fp32 [B, T + 1]);
+    `outputs` = those tensors to write into instead of new ones (accept_slots and logprob
+    may be None there).  See va_tree_accept_sampled in verify_attn.h."""
+    return prepare_tree_accept_sampled(root_logits, logits, draft_tokens, tree_parent, uniform,
+                                       temperature=temperature, top_k=top_k, top_p=top_p,
+                                       min_p=min_p, draft_slots=draft_slots, workspace=workspace,
+                                       outputs=outputs, stream=stream)()
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -22,6 +22,7 @@
 // does not depend on the chunking.
 #include <string.h>
 
+#include "va_accept.cuh"
 #include "va_common.cuh"
 
 #ifndef VA_API
@@ -35,24 +36,6 @@ constexpr int kArgThreads = 256;
 constexpr int kWalkWarps = 8;
 constexpr int kTargetCtas = 1024;   // argmax CTAs aimed for (several per SM)
 constexpr int64_t kMinChunk = 4096; // logits per CTA at least
-
-struct AcceptParams {
-  const float* root_logits;   // [B, V]
-  const float* logits;        // [B, T, V]
-  int64_t V;
-  const int32_t* tokens;      // [B, T]
-  const int32_t* parent;      // [B, T]
-  const int32_t* slots;       // [B, T] or NULL
-  int B, T, chunks;
-  int64_t chunk_len;
-  float* part_val;            // [B*(T+1)][chunks]
-  int32_t* part_idx;          // [B*(T+1)][chunks]
-  uint32_t* status;
-  int32_t* accept_len;        // [B]
-  int32_t* accept_nodes;      // [B, T]
-  int32_t* accept_slots;      // [B, T] or NULL
-  int32_t* bonus;             // [B]
-};
 
 // (v, i) ranks above (bv, bi): a larger value, or the same value at a lower
 // index.  NaN compares false both ways, so it never ranks above anything.
@@ -134,6 +117,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32) accept_walk_kernel(AcceptPara
   const int T = a.T;
   // lane l merges the chunks of rows l, l + 32, ...: the loads of every row
   // are independent, so they are all in flight together
+  bool empty = false;
   for (int k = lane; k <= T; k += 32) {
     const size_t r = size_t(b) * (T + 1) + k;
     float bv = -INFINITY;
@@ -147,6 +131,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32) accept_walk_kernel(AcceptPara
       }
     }
     tok[warp][k] = bi < a.V ? bi : 0;   // a row of NaN only: token 0
+    empty |= bv == -INFINITY;
   }
   __syncwarp();
   // Node c = lane + 32h (h = 0, 1; T <= 64) in registers of lane c % 32: its
@@ -173,6 +158,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32) accept_walk_kernel(AcceptPara
     }
   }
   bad = __any_sync(0xffffffffu, bad);
+  empty = __any_sync(0xffffffffu, empty && a.flag_empty);
   // Each accepted node is a child of the previous one, so has a larger index:
   // at most T steps, each one vote of the lanes (the lowest-numbered child of
   // `cur` whose draft token is the target's token `t`).
@@ -199,6 +185,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32) accept_walk_kernel(AcceptPara
     a.accept_len[b] = n;
     a.bonus[b] = t;
     if (bad) atomicOr(a.status, VA_STATUS_BAD_PARENT);
+    if (empty) atomicOr(a.status, VA_STATUS_EMPTY_ROW);
   }
 }
 
@@ -226,6 +213,23 @@ AcceptLayout accept_layout(int B, int T, int64_t V) {
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
+
+// The walk kernel may be scheduled while the kernel before it runs; it waits
+// (griddepcontrol.wait) before reading its tokens.
+cudaError_t launch_accept_walk(const AcceptParams& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(unsigned((a.B + kWalkWarps - 1) / kWalkWarps), 1u, 1u);
+  cfg.blockDim = dim3(kWalkWarps * 32, 1u, 1u);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, accept_walk_kernel, a);
+}
+
 }  // namespace va
 
 VA_API size_t va_tree_accept_workspace_bytes(int B, int T, int64_t V) {
@@ -274,18 +278,5 @@ VA_API int va_tree_accept(const float* root_logits, const float* logits, int64_t
   argmax_partial_kernel<<<dim3(unsigned(B * (T + 1)), unsigned(L.chunks), 1u), kArgThreads, 0,
                           st>>>(a);
   if (cudaGetLastError() != cudaSuccess) return VA_ERR_LAUNCH;
-  // the walk kernel may be scheduled while the argmax CTAs run; it waits
-  // (griddepcontrol.wait) before reading their partials
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(unsigned((B + kWalkWarps - 1) / kWalkWarps), 1u, 1u);
-  cfg.blockDim = dim3(kWalkWarps * 32, 1u, 1u);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, accept_walk_kernel, a) != cudaSuccess) return VA_ERR_LAUNCH;
-  return VA_OK;
+  return launch_accept_walk(a, st) == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }

@@ -17,6 +17,7 @@ cudaError_t init_partial_fma();
 cudaError_t init_partial_tc(int* max_pairs, int* max_quads);
 cudaError_t init_weights_tc();
 cudaError_t init_evict();
+cudaError_t init_sample();
 cudaError_t init_decode_tc();
 cudaError_t init_prefill_tc();
 bool tc_supported(int B, int T, int H);
@@ -231,6 +232,7 @@ VA_API int va_init(int device) {
   cudaError_t e2 = va::init_partial_tc(&pairs, &quads);
   cudaError_t e3 = va::init_weights_tc();
   if (e3 == cudaSuccess) e3 = va::init_evict();
+  if (e3 == cudaSuccess) e3 = va::init_sample();
   if (e3 == cudaSuccess) e3 = va::init_decode_tc();
   if (e3 == cudaSuccess) e3 = va::init_prefill_tc();
   // the no-allocation scratch array: placed now, with the device current; a

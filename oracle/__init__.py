@@ -58,10 +58,10 @@ Functions and the passages they follow (page titles and sections):
                    of ragged chunks with a window and sinks, the attention
                    weight each key receives, eviction by that weight), in plain
                    numpy; no page gives them.
-  rope, latent_rows
+  rope, latent_rows, draw
                 -- the definitions in include/verify_attn.h (rotary positions, the
-                   new tokens' rows of the latent cache), in plain numpy; no page
-                   gives them.
+                   new tokens' rows of the latent cache, tokens drawn from rows
+                   of logits), in plain numpy; no page gives them.
 """
 from __future__ import annotations
 
@@ -599,3 +599,48 @@ def latent_rows(kv_new, positions, inv_freq, norm_weight=None, eps: float = 1e-6
     kv[:, D_V:] = rope(kv[:, None, D_V:], positions, inv_freq, 0, interleaved,
                        False, amplitude)[:, 0]
     return kv
+
+
+def draw(row, uniform, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One token of a row of logits: (token, logprob, margin).
+
+    margin says how far the outcome is from another one: the least relative distance of a
+    mass that was compared from what it was compared with (a border of top-p, or the drawn
+    mass and the ends of the token's stretch), as a share of the kept mass."""
+    l = np.array(row, dtype=np.float64)
+    l[np.isnan(l)] = -np.inf
+    V = len(l)
+    m = l.max()
+    if m == -np.inf:
+        return 0, -np.inf, 1.0
+    if not temperature > 0:
+        return int(np.argmax(l)), 0.0, 1.0
+    with np.errstate(invalid="ignore"):
+        w = np.where(l == m, 1.0, np.exp((l - m) / float(temperature)))
+    w[np.isneginf(l)] = 0.0
+    order = np.argsort(-l, kind="stable")          # equal ones by index
+    if 0 < top_k < V:
+        order = order[:int(top_k)]
+    margin = 1.0
+    if top_p < 1:
+        mass = np.cumsum(w[order])
+        want = max(float(top_p), 0.0) * mass[-1]
+        n = min(int(np.searchsorted(mass, want, side="left")) + 1, len(order))
+        if n > 1:
+            margin = min(margin, abs(mass[n - 2] - want) / mass[-1])
+        if n < len(order):
+            margin = min(margin, abs(mass[n - 1] - want) / mass[-1])
+        order = order[:n]
+    if min_p > 0:
+        order = order[w[order] >= min(float(min_p), 1.0)]
+    kept = np.sort(order)
+    cum = np.cumsum(w[kept])
+    u = float(uniform)
+    u = u if u > 0 else 0.0
+    x = u * cum[-1]
+    last = int(np.flatnonzero(w[kept] > 0)[-1])
+    at = min(int(np.searchsorted(cum, x, side="right")), last)
+    margin = min(margin, abs(cum[at] - x) / cum[-1] if u < 1 else 1.0)
+    if at and cum[at - 1] > 0:
+        margin = min(margin, abs(x - cum[at - 1]) / cum[-1])
+    return int(kept[at]), float(np.log(w[kept[at]] / cum[-1])), float(margin)

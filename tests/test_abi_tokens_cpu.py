@@ -1,4 +1,4 @@
-"""Argument checks of the entry points around attention (rotary positions, cache rows):
+"""Argument checks of the entry points around attention (rotary positions, cache rows, sampling):
 every refusal comes before any device work, so all of them show on a machine without a
 GPU; and the frequencies, which are host arithmetic."""
 import ctypes
@@ -120,3 +120,57 @@ def test_frequencies():
         va.rope_inv_freq(64, scaling="other")
     with pytest.raises(va.VaError):
         va.rope_inv_freq(63)
+
+
+A256 = 0x20000
+SAMPLE = dict(logits=A16, stride=1000, dtype=0, rows=3, V=1000, t=A16, k=A16, p=A16, m=A16, u=A16,
+              tok=A16, lp=A16, status=None, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(logits=None), -1), (dict(u=None), -1), (dict(tok=None), -1),
+    (dict(rows=-1), -2), (dict(rows=(1 << 23) + 1), -2), (dict(V=0), -2),
+    (dict(V=(1 << 20) + 1), -2), (dict(dtype=3), -2), (dict(dtype=-1), -2), (dict(stride=-1), -2),
+    (dict(stride=(1 << 40) + 1), -2),
+    (dict(logits=A16 + 2), -3), (dict(dtype=1, logits=A16 + 1), -3), (dict(t=A16 + 2), -3),
+    (dict(k=A16 + 2), -3), (dict(p=A16 + 2), -3), (dict(m=A16 + 2), -3), (dict(u=A16 + 2), -3),
+    (dict(tok=A16 + 2), -3), (dict(lp=A16 + 2), -3), (dict(status=A16 + 2), -3),
+])
+def test_sample_errors(lib, over, code):
+    assert lib.va_sample(*(SAMPLE | over).values()) == code
+
+
+@pytest.mark.parametrize("over", [
+    dict(), dict(t=None, k=None, p=None, m=None, lp=None), dict(dtype=1, logits=A16 + 2),
+    dict(stride=0), dict(V=1 << 20, rows=1 << 23), dict(rows=0, logits=None, u=None, tok=None)])
+def test_good_sample_calls_end_at_the_device_check(lib, over):
+    assert lib.va_sample(*(SAMPLE | over).values()) in (-5, -7)
+
+
+TREE = dict(root=A16, logits=A16, dtype=0, V=1000, tok=A16, par=A16, slots=A16, B=2, T=8, t=A16,
+            k=A16, p=A16, m=A16, u=A16, ws=A256, n=1 << 20, alen=A16, nodes=A16, aslots=A16,
+            bonus=A16, lp=A16, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(root=None), -1), (dict(logits=None), -1), (dict(tok=None), -1), (dict(par=None), -1),
+    (dict(u=None), -1), (dict(ws=None), -1), (dict(alen=None), -1), (dict(nodes=None), -1),
+    (dict(bonus=None), -1), (dict(B=0), -2), (dict(B=65536), -2), (dict(T=0), -2), (dict(T=65), -2),
+    (dict(V=0), -2), (dict(V=(1 << 20) + 1), -2), (dict(dtype=3), -2),
+    (dict(root=A16 + 2), -3), (dict(ws=A256 + 16), -3), (dict(aslots=A16 + 2), -3),
+    (dict(slots=A16 + 1), -3), (dict(lp=A16 + 2), -3), (dict(u=A16 + 2), -3), (dict(k=A16 + 1), -3),
+    (dict(n=300), -4),
+])
+def test_sampled_acceptance_errors(lib, over, code):
+    assert lib.va_tree_accept_sampled(*(TREE | over).values()) == code
+
+
+def test_good_sampled_acceptance_calls_end_at_the_device_check(lib):
+    for over in (dict(), dict(t=None, k=None, p=None, m=None), dict(slots=None, aslots=None, lp=None),
+                 dict(dtype=2, root=A16 + 2), dict(V=1 << 20)):
+        assert lib.va_tree_accept_sampled(*(TREE | over).values()) in (-5, -7)
+    f = lib.va_tree_accept_sampled_workspace_bytes
+    assert f(0, 1) == f(1, 0) == f(65536, 1) == f(1, 65) == 0
+    assert f(1, 1) == 256 * 3 and f(65535, 64) >= 256 + 8 * 65535 * 65
+    assert lib.va_tree_accept_sampled(*(TREE | dict(n=f(2, 8))).values()) in (-5, -7)
+    assert lib.va_tree_accept_sampled(*(TREE | dict(n=f(2, 8) - 1)).values()) == -4
