@@ -11,15 +11,24 @@
 // sums do not depend on their order.  w_i itself has 32-bit accuracy: the exponent's factor
 // log2(e) / T comes in two parts, so that its rounding does not tilt the distribution.
 //
-// One cluster of CTAs per row.  Each CTA reads its part of the row once, into shared
-// memory, and takes the maximum; then, by row:
-//   - with top-k or top-p, a histogram of counts and masses over -log2 w in steps of 1/64
-//     octave, added over the cluster; the step in which the border lies; the values in that
-//     step, gathered by every CTA, cut again by 512, and the few left taken largest first.
-//     (Where too many values share a step, the border is found digit by digit of the
-//     ordered values instead.)
-//   - the kept mass of each warp's piece of the row, and, in the CTA where the drawn mass
-//     falls, the token.
+// One cluster of CTAs per row, a warp per piece of it.
+//   1. Each warp reads its piece (copies into a ring in shared memory, four steps ahead), with
+//      a running maximum and sum per lane.  The cluster exchanges the maximum; the pieces'
+//      masses are then known, and a row without top-k and top-p is done but for 4.  Later
+//      steps read the row again, from L2.
+//   2. The lanes' maxima are values of the row: where k of them lie above a value, so do the k
+//      largest, and where they hold top_p of the mass, so does what lies above.  A histogram
+//      of them, over the cluster, gives that bound.
+//      Where the bound would leave too much (rows whose mass lies in thousands of tokens, or a
+//      k of thousands) a histogram of all values over -log2 w in steps of 1/32 octave, of
+//      counts or of masses rounded to some 18 bits, finds the step of the border.
+//   3. The values above the bound (of a border's step, those in it, with the exact mass above)
+//      go to the first CTA's list.
+//   4. The first CTA, alone: the border among the listed values, the kept ones' masses added to
+//      their pieces, the piece in which the drawn mass falls, and in it the token.
+// Where the list does not hold what it should (thousands of equal values, a border that
+// rounding put into the next step), and for rows with a maximum beyond 1e30, the first CTA
+// goes through the whole row again, digit by digit of the ordered values.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -38,15 +47,23 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasMax = 8;               // of a cluster
-constexpr int kBins = 2048;               // of the histogram: 32 octaves
-constexpr int kPer = kBins / kThreads;    // bins of a thread
-constexpr int kSub = 512;                 // parts of a bin
-constexpr int kList = 2048;               // values of one bin, of a whole row
-constexpr int kRounds = 8;                // values taken out of a part of a bin
-constexpr float kBinsPerOctave = 64.f;
+constexpr int kPieces = kCtasMax * kWarps;
+constexpr int kStep = 2;                  // vectors of a lane's step
+constexpr int kAhead = 4;                 // steps on their way
+constexpr int kCoarse = 128;              // bins of the lanes' maxima: 64 octaves
+constexpr int kCoarsePer = kCoarse / 32;  // of a lane
+constexpr float kCoarsePerOctave = 2.f;
+constexpr int kBins = 2048;               // bins of all values: 64 octaves
+constexpr int kPer = kBins / kThreads;    // of a thread
+constexpr float kBinsPerOctave = 32.f;
+constexpr int kOctaveBits = 5;
+constexpr int kRest = 256;                // bins whose masses are held exactly: 8 octaves
+constexpr int kList = 4096;               // listed values of a row, in equal shares per CTA
+constexpr float kListAim = 3000.f;        // values that a list is expected to hold at most
 constexpr int kUnit = 43;                 // masses count 2^-43
 constexpr float kNothing = -46.f;         // a height whose mass is 0
-static_assert(kSub == kThreads, "a part of a bin per thread");
+constexpr float kLowest = -3.402823466e38f;
+constexpr float kPlain = 1e30f;           // maxima of this size and above take the slow way
 
 struct SampleParams {
   const void* root;      // rows of the prefix (trees), or NULL
@@ -64,41 +81,66 @@ struct SampleParams {
   uint32_t* status;      // or NULL
   bool clear_status;
   int ctas;              // of a row
-  bool staged;           // the row's parts fit shared memory
 };
 
 struct alignas(16) SampleSmem {
-  uint32_t cnt[kBins];   // values of a bin
-  uint32_t lo[kBins];    // their masses, in 2^-(23 + octave): low 12 bits summed,
-  uint32_t hi[kBins];    // and the rest
-  float list[kList];     // this CTA's values of the border's bin
-  float merged[kList];   // the row's
-  uint32_t nlist;
-  float min_above;       // min-p keeps what is above
-  // what the cluster's CTAs tell each other
+  union {
+    uint32_t hist[kBins];                // all values: counts or masses,
+    uint4 x_lanes[kCtasMax][kCoarse / 2];   // before that what the cluster's CTAs wrote of their `lanes`
+  };
+  uint32_t rest[kRest];                  // what the histogram's masses of the first octaves round off
+  uint4 lanes[kCoarse / 2];              // the lanes' maxima: counts, masses in 2^-19, two bins each
+  // the first CTA's, written by all of the cluster
+  float list_value[kList];               // listed values,
+  uint32_t list_index[kList];            // their places in the row,
+  uint32_t list_count[kCtasMax];         // and how many each CTA listed
+  uint4 piece[kPieces];                  // kept mass, mass above the border's step
+  uint32_t first[kCtasMax];              // lowest index of the maximum
+  // every CTA's, written by all of the cluster
   float x_max[kCtasMax];
-  uint32_t x_total[kCtasMax][2];
-  uint32_t x_mass[kCtasMax][2];
-  uint32_t x_eq[kCtasMax];
-  uint32_t x_first[kCtasMax];
+  uint2 x_total[kCtasMax];               // mass
   // within the CTA
+  uint32_t nlist, last, pick;
+  float pick_value;
+  uint64_t drawn, total;
+  float min_above;                       // min-p keeps what is above
+  double min_gap;                        // T ln(min_p)
   float w_max[kWarps];
-  uint64_t w_mass[kWarps];
   uint32_t w_eq[kWarps];
   uint64_t s_mass[kWarps];
   uint32_t s_cnt[kWarps];
-  // results of a search
+  uint32_t piece_ties[kPieces];
   uint32_t f_bin, f_cnt, f_in;
   uint64_t f_mass;
+};
+// Where the first CTA searches, over the rings: counts of parts, and their
+// masses (44 bits) in four pieces of 11 bits, whose sums over a row of 2^20 fit 32.
+constexpr int kParts = 1024;
+constexpr int kPer2 = kParts / kThreads;
+struct SearchSmem {
+  uint32_t cnt[kParts];
+  uint32_t mass[4][kParts];
+  float value[kList];      // the listed values, side by side,
+  uint32_t index[kList];   // and their places in the row
+  __device__ __forceinline__ void clear() {
+#pragma unroll 1
+    for (int i = int(threadIdx.x); i < kParts * 5 / 4; i += kThreads)
+      reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void add(int part, uint32_t n, uint64_t w) {
+    atomicAdd(cnt + part, n);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      atomicAdd(mass[k] + part, uint32_t(w >> (11 * k)) & (k < 3 ? 0x7ffu : 0xffffffffu));
+  }
+  __device__ __forceinline__ uint64_t sum(int part) const {
+    return uint64_t(mass[0][part]) + (uint64_t(mass[1][part]) << 11) +
+           (uint64_t(mass[2][part]) << 22) + (uint64_t(mass[3][part]) << 33);
+  }
 };
 
 // ------------------------------------------------------------- small pieces
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -106,6 +148,15 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
 template <typename T>
@@ -133,6 +184,9 @@ __device__ __forceinline__ void unpack<__half>(const uint4& r, float (&x)[8]) {
     x[2 * i + 1] = __half2float(__ushort_as_half(uint16_t(w[i] >> 16)));
   }
 }
+__device__ __forceinline__ float value_of(float v) { return v; }
+__device__ __forceinline__ float value_of(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float value_of(__half v) { return __half2float(v); }
 template <typename T>
 __device__ __forceinline__ T minus_inf();
 template <>
@@ -143,6 +197,13 @@ __device__ __forceinline__ __nv_bfloat16 minus_inf<__nv_bfloat16>() {
 }
 template <>
 __device__ __forceinline__ __half minus_inf<__half>() { return __ushort_as_half(0xfc00u); }
+
+template <typename T>
+__device__ __forceinline__ uint32_t minus_inf_bits() { return 0; }
+template <>
+__device__ __forceinline__ uint32_t minus_inf_bits<__nv_bfloat16>() { return 0xff80u; }
+template <>
+__device__ __forceinline__ uint32_t minus_inf_bits<__half>() { return 0xfc00u; }
 
 // A value as an unsigned integer of the opposite order (the largest first), and back.
 __device__ __forceinline__ uint32_t down_key(float v) {
@@ -163,10 +224,18 @@ struct Scale {
     const float x = l == m ? 0.f : l - m, h = x * c_hi;
     return h > kNothing ? sm100::ex2_approx(fmaf(x, c_lo, h)) : 0.f;
   }
-  __device__ __forceinline__ int bin(float h) const {
-    return int(fminf(h * -kBinsPerOctave, float(kBins - 1)));
+  // the same from a finite value on, without a look at what is equal or infinite
+  // (c_lo > 0: -inf has no weight)
+  __device__ __forceinline__ float plain(float l, float from) const {
+    const float x = l - from;
+    return sm100::ex2_approx(fmaf(x, c_lo, x * c_hi));
   }
 };
+// A height's bin among kBins, the nearest multiple of 1/32 octave (by the rounding of a sum
+// with 2^23), and a bin's octave.
+__device__ __forceinline__ uint32_t bin_of(float h) {
+  return min(__float_as_uint(fmaf(h, -kBinsPerOctave, 8388608.f)) - 0x4b000000u, uint32_t(kBins - 1));
+}
 
 // A weight, or a sum of a few, in units of 2^-43.
 __device__ __forceinline__ uint64_t mass_of(float e) {
@@ -176,20 +245,11 @@ __device__ __forceinline__ uint64_t mass_of(float e) {
   if (up >= 0) return f << up;
   return up < -32 ? 0 : (f + (uint64_t(1) << (-up - 1))) >> -up;
 }
-// The same in units of 2^-(23 + octave), for a weight of that octave (or less).
+// A weight in units of 2^-(22 + octave): 2^22 or a little more for one of that octave.
 __device__ __forceinline__ uint32_t octave_mass(float e, int octave) {
   const uint32_t b = __float_as_uint(e);
   const float v = b < 0x00800000u ? 0.f : __uint_as_float(b + (uint32_t(octave) << 23));
-  return __float_as_uint(fminf(v, 1.f) + 1.f) - 0x3f800000u;
-}
-__device__ __forceinline__ uint64_t from_octave(uint64_t mass, int octave) {
-  const int down = octave - (kUnit - 23);
-  return down <= 0 ? mass << -down : mass >> down;
-}
-// ... and back, rounded up (a part of a sum stays a part of it).
-__device__ __forceinline__ uint64_t to_octave(uint64_t mass, int octave) {
-  const int up = octave - (kUnit - 23);
-  return up >= 0 ? mass << up : (mass + (uint64_t(1) << -up) - 1) >> -up;
+  return __float_as_uint(fminf(v, 1.9f) + 2.f) - 0x40000000u;
 }
 
 // The least whole number not below p * mass, 0 < p < 1.
@@ -199,147 +259,208 @@ __device__ __forceinline__ uint64_t part_of(float p, uint64_t mass) {
   return ((hi << 1) | (lo >> 63)) + ((lo << 1) != 0 ? 1 : 0);
 }
 
+// How many of `of` equal weights w reach `mass` (0 < mass <= of * w).
+__device__ __forceinline__ uint32_t ties_of(uint64_t mass, uint64_t w, uint32_t of) {
+  uint32_t n = 0;   // (by bits: a division of 64 bits is a long piece of code)
+#pragma unroll 1
+  for (uint32_t b = 1u << (31 - __clz(of)); b; b >>= 1)
+    if ((n + b) * w < mass) n += b;
+  return n + 1;
+}
+
+__device__ __forceinline__ float largest_below(double t) {
+  const float f = __double2float_rd(t);
+  return double(f) == t ? nextafterf(f, -INFINITY) : f;
+}
+
 // What is kept of a row: values above `above`, and the first `ties` equal to it.
 struct Cut {
   float above;
   uint32_t ties;
 };
 
-// This CTA's part of a row, vectors of 16 bytes [v0, v1) counted from the 16-byte boundary
-// at or before the row's first element.
+// Vectors of 16 bytes [v0, v1) of a row, counted from the 16-byte boundary at or before its
+// first element.
 template <typename T>
 struct Part {
   static constexpr int kE = 16 / int(sizeof(T));
   const T* row;       // element 0
-  const uint4* mem;   // vector v0, in shared memory (NULL: not staged)
   int64_t V;
   int skew;           // elements between the boundary and the row
   int v0, v1;
-  __device__ __forceinline__ uint4 from_global(int v) const {
-    const int64_t i0 = int64_t(v) * kE - skew;
-    if (i0 >= 0 && i0 + kE <= V) return *reinterpret_cast<const uint4*>(row + i0);
+  __device__ static __forceinline__ uint4 nothing() {   // a vector of -inf
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : (minus_inf_bits<T>() * 0x10001u);
+    return make_uint4(w, w, w, w);
+  }
+  __device__ __forceinline__ bool whole(int v) const {   // no element of v outside the row
+    return v * kE >= skew && int64_t(v) * kE + kE - skew <= V;
+  }
+  __device__ __forceinline__ const T* at(int v) const { return row + (int64_t(v) * kE - skew); }
+  __device__ __forceinline__ uint4 raw(int v) const {
+    if (whole(v)) return *reinterpret_cast<const uint4*>(at(v));
     union { T e[kE]; uint4 q; } u;
 #pragma unroll
-    for (int j = 0; j < kE; ++j) u.e[j] = i0 + j >= 0 && i0 + j < V ? row[i0 + j] : minus_inf<T>();
+    for (int j = 0; j < kE; ++j) {
+      const int64_t i = int64_t(v) * kE - skew + j;
+      u.e[j] = i >= 0 && i < V ? row[i] : minus_inf<T>();
+    }
     return u.q;
   }
   // NaN counts as -inf
   __device__ __forceinline__ void load(int v, float (&x)[kE]) const {
-    unpack<T>(mem ? mem[v - v0] : from_global(v), x);
+    unpack<T>(raw(v), x);
 #pragma unroll
     for (int j = 0; j < kE; ++j) x[j] = fmaxf(x[j], -INFINITY);
   }
+  __device__ __forceinline__ uint32_t index(int v, int j) const {
+    return uint32_t(v * kE + j - skew);
+  }
   // a warp's piece, in index order
+  __device__ __forceinline__ int piece_len() const { return (v1 - v0 + kWarps - 1) / kWarps; }
   __device__ __forceinline__ void piece(int warp, int* p0, int* p1) const {
-    const int n = (v1 - v0 + kWarps - 1) / kWarps;
+    const int n = piece_len();
     *p0 = v0 + warp * n < v1 ? v0 + warp * n : v1;
     *p1 = *p0 + n < v1 ? *p0 + n : v1;
   }
-  template <typename F>
-  __device__ __forceinline__ void each(F&& use) const {
-    for (int v = v0 + int(threadIdx.x); v < v1; v += kThreads) {
-      float x[kE];
-      load(v, x);
+};
+
+// A warp's way through its piece [p0, p1): use(v, q) gets kStep vectors of a lane, v, v + 32, ...;
+// those past the piece's end hold -inf.  `ring`: this lane's 16 bytes of the warp's ring,
+// whose vectors are 512 bytes apart.  A lane reads only what it copied itself.  started() runs
+// once the first copies are on their way.
+template <typename T, typename F, typename S>
+__device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1, F&& use,
+                                       S&& started) {
+  const int lane = int(threadIdx.x) & 31, steps = (p1 - p0 + 32 * kStep - 1) / (32 * kStep);
+  auto copy = [&](int t, int slot) {
 #pragma unroll
-      for (int j = 0; j < kE; ++j) use(x[j]);
+    for (int k = 0; k < kStep; ++k) {
+      const int v = p0 + lane + 32 * (kStep * t + k);
+      if (v < p1 && part.whole(v)) sm100::cp_async16(ring + 512u * uint32_t(kStep * slot + k), part.at(v), 16u);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int t = 0; t < kAhead; ++t) copy(t, t);
+  started();
+#pragma unroll 1
+  for (int t = 0, slot = 0; t < steps; ++t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const int v = p0 + lane + 32 * kStep * t;
+    uint4 q[kStep];
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      q[k] = sm100::ld_shared_v4(ring + 512u * uint32_t(kStep * slot + k));
+      if (v + 32 * k >= p1) q[k] = Part<T>::nothing();
+      else if (!part.whole(v + 32 * k)) q[k] = part.raw(v + 32 * k);
+    }
+    use(v, q);
+    copy(t + kAhead, slot);   // (past the end: an empty group)
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
   }
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1, F&& use) {
+  stream(part, ring, p0, p1, use, [] {});
+}
+
+// The functions below are called from several places and kept out of line, and their loops
+// rolled: most of this kernel runs once per row, where fetching instructions costs more than
+// executing them (everything inline and unrolled, the search took 2.5 times as long).
+
+__device__ __noinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct Sums {
+  uint64_t mass;
+  uint32_t cnt;
 };
 
 // Exclusive sums over the block of a count and a mass, in thread order.
-__device__ __forceinline__ void block_scan(SampleSmem& sm, uint32_t& cnt, uint64_t& mass) {
+__device__ __noinline__ Sums block_scan(SampleSmem& sm, uint32_t cnt, uint64_t mass) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t c0 = cnt;
-  const uint64_t m0 = mass;
-#pragma unroll
+  uint32_t c = cnt;
+  uint64_t m = mass;
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t c = __shfl_up_sync(0xffffffffu, cnt, o);
-    const uint64_t m = __shfl_up_sync(0xffffffffu, mass, o);
-    if (lane >= o) { cnt += c; mass += m; }
+    const uint32_t c1 = __shfl_up_sync(0xffffffffu, c, o);
+    const uint64_t m1 = __shfl_up_sync(0xffffffffu, m, o);
+    if (lane >= o) { c += c1; m += m1; }
   }
   if (lane == 31) {
-    sm.s_cnt[warp] = cnt;
-    sm.s_mass[warp] = mass;
+    sm.s_cnt[warp] = c;
+    sm.s_mass[warp] = m;
   }
   __syncthreads();
-  cnt -= c0;
-  mass -= m0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) { cnt += sm.s_cnt[w]; mass += sm.s_mass[w]; }
+  const bool before = lane < warp;   // (kWarps <= 32)
+  c += __reduce_add_sync(0xffffffffu, before ? sm.s_cnt[lane] : 0u) - cnt;
+  m += warp_sum(before ? sm.s_mass[lane] : 0) - mass;
   __syncthreads();
+  return {m, c};
 }
 
-__device__ __forceinline__ float block_max(SampleSmem& sm, float v) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (lane == 0) sm.w_max[warp] = v;
+__device__ __noinline__ uint64_t block_sum(SampleSmem& sm, uint64_t v) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) sm.s_mass[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = sm.w_max[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) v = fmaxf(v, sm.w_max[w]);
+  v = warp_sum((threadIdx.x & 31) < kWarps ? sm.s_mass[threadIdx.x & 31] : 0);
   __syncthreads();
   return v;
 }
 
-// ------------------------------------------------------------ border search
-
-// The histogram's bins of this thread, added over the cluster; masses in 2^-43.
-struct Bins {
-  uint32_t cnt[kPer];
-  uint64_t mass[kPer];
-};
-
-__device__ __forceinline__ void gather_bins(SampleSmem& sm, int ctas, Bins& b) {
-  const int t = int(threadIdx.x) * kPer;
-  uint64_t low[kPer], high[kPer];
+__device__ __noinline__ float block_max(SampleSmem& sm, float v) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) { b.cnt[k] = 0; low[k] = high[k] = 0; }
-  static_assert(kPer == 4, "a 16-byte read per array");
-  for (int c = 0; c < ctas; ++c) {
-    const uint4 n = ld_cluster_v4(sm100::mapa(smem_u32(sm.cnt + t), uint32_t(c)));
-    const uint4 l = ld_cluster_v4(sm100::mapa(smem_u32(sm.lo + t), uint32_t(c)));
-    const uint4 h = ld_cluster_v4(sm100::mapa(smem_u32(sm.hi + t), uint32_t(c)));
-    b.cnt[0] += n.x; b.cnt[1] += n.y; b.cnt[2] += n.z; b.cnt[3] += n.w;
-    low[0] += l.x; low[1] += l.y; low[2] += l.z; low[3] += l.w;
-    high[0] += h.x; high[1] += h.y; high[2] += h.z; high[3] += h.w;
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (k) break;
+    if (lane == 0) sm.w_max[warp] = v;
+    __syncthreads();
+    v = lane < kWarps ? sm.w_max[lane] : -INFINITY;
   }
-#pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    b.mass[k] = from_octave(low[k] + (high[k] << 12), (t + k) >> 6);
+  __syncthreads();
+  return v;
 }
 
 struct Found {
-  int bin;         // kBins: none
+  int bin;         // (past the last: none)
   uint32_t cnt;    // above it
   uint64_t mass;
   uint32_t in;     // values in it
 };
 
-// The first bin at which the count, or the mass, from the top reaches `want` (>= 1).
-__device__ __forceinline__ Found find_bin(SampleSmem& sm, const Bins& b, bool by_mass, uint64_t want) {
-  if (threadIdx.x == 0) sm.f_bin = kBins;
-  uint32_t cnt = 0;
-  uint64_t mass = 0;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) { cnt += b.cnt[k]; mass += b.mass[k]; }
-  const uint32_t c1 = cnt;
-  const uint64_t m1 = mass;
-  block_scan(sm, cnt, mass);
-  const uint64_t before = by_mass ? mass : cnt, mine = by_mass ? m1 : c1;
-  if (before < want && want <= before + mine) {
-    bool found = false;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (!found && (by_mass ? mass + b.mass[k] : uint64_t(cnt + b.cnt[k])) >= want) {
-        found = true;
-        sm.f_bin = uint32_t(int(threadIdx.x) * kPer + k);
-        sm.f_cnt = cnt;
-        sm.f_mass = mass;
-        sm.f_in = b.cnt[k];
+// Where the count, or the mass, from the top reaches `want` (>= 1): this thread has kPer bins in
+// a row, whose counts and masses get(k) gives; `none` if it is not reached.
+template <int kN, typename F>
+__device__ __forceinline__ Found find_bin(SampleSmem& sm, bool by_mass, uint64_t want, F&& get) {
+  if (threadIdx.x == 0) sm.f_bin = kN * kThreads;
+  Sums mine = {0, 0};
+#pragma unroll 1
+  for (int k = 0; k < kN; ++k) {
+    const Sums b = get(k);
+    mine.cnt += b.cnt;
+    mine.mass += b.mass;
+  }
+  Sums at = block_scan(sm, mine.cnt, mine.mass);
+  const uint64_t before = by_mass ? at.mass : at.cnt, here = by_mass ? mine.mass : mine.cnt;
+  if (before < want && want <= before + here) {
+#pragma unroll 1
+    for (int k = 0; k < kN; ++k) {
+      const Sums b = get(k);
+      if ((by_mass ? at.mass + b.mass : uint64_t(at.cnt + b.cnt)) >= want) {
+        sm.f_bin = uint32_t(int(threadIdx.x) * kN + k);
+        sm.f_cnt = at.cnt;
+        sm.f_mass = at.mass;
+        sm.f_in = b.cnt;
+        break;
       }
-      if (!found) { cnt += b.cnt[k]; mass += b.mass[k]; }
+      at.cnt += b.cnt;
+      at.mass += b.mass;
     }
   }
   __syncthreads();
@@ -347,165 +468,165 @@ __device__ __forceinline__ Found find_bin(SampleSmem& sm, const Bins& b, bool by
   __syncthreads();
   return f;
 }
-
-// The row's values of one bin (weights from `least` on) in every CTA's `merged`, and their counts and masses over
-// kSub parts of the bin in cnt, lo and hi.  The cluster has met since the histogram was read.
-template <typename T>
-__device__ __forceinline__ int gather_list(SampleSmem& sm, const Part<T>& part, const Scale& s, int ctas,
-                                           int bin, float least) {
-  const int tid = int(threadIdx.x);
-  part.each([&](float l) {
-    const float h = s.height(l);
-    if (s.bin(h) == bin && s.weight(l) >= least) {
-      const uint32_t at = atomicAdd(&sm.nlist, 1u);
-      if (at < kList) sm.list[at] = l;
-    }
+__device__ __noinline__ Found find_part(SampleSmem& sm, const SearchSmem& ss, bool by_mass,
+                                        uint64_t want) {
+  return find_bin<kPer2>(sm, by_mass, want, [&](int k) {
+    const int i = int(threadIdx.x) * kPer2 + k;
+    return Sums{ss.sum(i), ss.cnt[i]};
   });
-  sm100::cluster_sync();
-  sm.cnt[tid] = sm.lo[tid] = sm.hi[tid] = 0;
-  __syncthreads();
-  int n = 0;
-  const int octave = bin >> 6;
-  for (int c = 0; c < ctas; ++c) {
-    const int nc = min(int(ld_cluster(sm100::mapa(smem_u32(&sm.nlist), uint32_t(c)))), kList);
-    const uint32_t from = sm100::mapa(smem_u32(sm.list), uint32_t(c));
-    for (int i = tid; i < nc && n + i < kList; i += kThreads) {
-      const float l = __uint_as_float(ld_cluster(from + 4u * uint32_t(i)));
-      sm.merged[n + i] = l;
-      const float h = s.height(l);
-      const int sub = int(h * (-kBinsPerOctave * kSub)) & (kSub - 1);
-      const uint32_t w = octave_mass(s.weight(l), octave);
-      atomicAdd(&sm.cnt[sub], 1u);
-      atomicAdd(&sm.lo[sub], w & 0xfffu);
-      atomicAdd(&sm.hi[sub], w >> 12);
-    }
-    n += nc;
-  }
-  __syncthreads();
-  return min(n, kList);
 }
 
-// The border among the values of one bin (gather_list has run): `want` of their count, or of
-// their mass (in the octave's unit), from the top.  False if the values in the border's part
-// are too many different ones.  *mass: what of the bin is kept, in the octave's unit.
-__device__ __forceinline__ bool border_in_list(SampleSmem& sm, const Scale& s, int n, int bin, bool by_mass,
-                                               uint64_t want, Cut* cut, uint64_t* mass_out) {
-  const int tid = int(threadIdx.x), octave = bin >> 6;
-  if (tid == 0) sm.f_bin = kSub;
-  uint32_t cnt = sm.cnt[tid];
-  uint64_t mass = uint64_t(sm.lo[tid]) + (uint64_t(sm.hi[tid]) << 12);
-  const uint32_t c1 = cnt;
-  const uint64_t m1 = mass;
-  block_scan(sm, cnt, mass);
-  const uint64_t before = by_mass ? mass : cnt, mine = by_mass ? m1 : c1;
-  if (before < want && want <= before + mine) {
-    sm.f_bin = uint32_t(tid);
-    sm.f_cnt = cnt;
-    sm.f_mass = mass;
-  }
-  __syncthreads();
-  const int sub = int(sm.f_bin);
-  if (sub == kSub) return false;
-  uint64_t left = want - (by_mass ? sm.f_mass : uint64_t(sm.f_cnt));
-  mass = sm.f_mass;
-  constexpr int kMine = kList / kThreads;
-  float v[kMine];
-#pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    const int i = tid + k * kThreads;
-    v[k] = i < n ? sm.merged[i] : -INFINITY;
-    if (i < n && (int(s.height(v[k]) * (-kBinsPerOctave * kSub)) & (kSub - 1)) != sub)
-      v[k] = -INFINITY;
-  }
-  for (int round = 0; round < kRounds; ++round) {
-    float top = v[0];
-#pragma unroll
-    for (int k = 1; k < kMine; ++k) top = fmaxf(top, v[k]);
-    top = block_max(sm, top);
-    if (top == -INFINITY) return false;   // (-inf itself is the last bin's)
-    uint32_t eq = 0;
-#pragma unroll
-    for (int k = 0; k < kMine; ++k) {
-      const uint32_t n_eq = __popc(__ballot_sync(0xffffffffu, v[k] == top));
-      eq += n_eq;
-      if (v[k] == top) v[k] = -INFINITY;
-    }
-    if ((tid & 31) == 0) sm.w_eq[tid >> 5] = eq;
-    __syncthreads();
-    eq = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) eq += sm.w_eq[w];
-    __syncthreads();
-    const uint32_t w = octave_mass(s.weight(top), octave);
-    const uint64_t all = by_mass ? uint64_t(eq) * w : uint64_t(eq);
-    if (left <= all) {
-      const uint64_t ties = by_mass ? (left + w - 1) / w : left;
-      cut->above = top;
-      cut->ties = uint32_t(ties);
-      *mass_out = mass + ties * w;
-      return true;
-    }
-    left -= all;
-    mass += uint64_t(eq) * w;
-  }
-  return false;
+__device__ __forceinline__ void tighten(Cut& cut, const Cut& other) {
+  if (other.above > cut.above || (other.above == cut.above && other.ties < cut.ties)) cut = other;
 }
 
-// The border over the whole row, digit by digit (11, 11, 10 bits) of the ordered values:
-// for rows with thousands of values in one bin.  *mass: what is kept, in 2^-43.
-template <typename T>
-__device__ void border_by_digits(SampleSmem& sm, const Part<T>& part, const Scale& s, int ctas,
-                                 bool by_mass, uint64_t want, Cut* cut, uint64_t* mass_out) {
-  const int tid = int(threadIdx.x);
-  unsigned long long* sums = reinterpret_cast<unsigned long long*>(sm.lo);   // lo and hi
-  uint32_t prefix = 0;
-  uint64_t left = want, mass = 0;
-  Bins b;
+// The border among the n listed values (ss.value): `want` of their count, or of their mass,
+// from the top.  They are cut into parts by height (scale parts an octave, from `base` on),
+// the border's part again, until so few are left in it that one warp compares each with
+// each.  False if the list does not reach that far, or too many different values lie too
+// close (equal ones may be any number).  *kept: mass down to the cut.  The cut is tightened.
+__device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, const Scale s, int n,
+                                            float base, float scale, bool by_mass, uint64_t want,
+                                            Cut* cut, uint64_t* kept) {
+  const int tid = int(threadIdx.x), lane = tid & 31;
+  const float* from = ss.value;
+  uint64_t left = want, sum = 0;
+#pragma unroll 1
   for (int level = 0; level < 3; ++level) {
-    const int shift = level == 0 ? 21 : (level == 1 ? 10 : 0);
-    const uint32_t mask = level < 2 ? 2047u : 1023u;
-    const int above = level == 0 ? 32 : (level == 1 ? 21 : 10);
-    sm100::cluster_sync();   // the histogram has been read
-    for (int i = tid; i < kBins; i += kThreads) { sm.cnt[i] = 0; sums[i] = 0; }
+    auto part_of_list = [&](float l) {
+      return int(fminf(fmaxf((-s.height(l) - base) * scale, 0.f), float(kParts - 1)));
+    };
+    ss.clear();
+    if (tid == 0) sm.nlist = 0;
     __syncthreads();
-    part.each([&](float l) {
-      const uint32_t key = down_key(l);
-      if (s.height(l) > kNothing && (above == 32 || (key >> above) == prefix)) {
-        const uint32_t d = (key >> shift) & mask;
-        atomicAdd(&sm.cnt[d], 1u);
-        const uint64_t w = mass_of(s.weight(l));
-        if (w) atomicAdd(&sums[d], (unsigned long long)w);
-      }
-    });
-    sm100::cluster_sync();
-    const int t = tid * kPer;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) { b.cnt[k] = 0; b.mass[k] = 0; }
-    for (int c = 0; c < ctas; ++c) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        b.cnt[k] += ld_cluster(sm100::mapa(smem_u32(sm.cnt + t + k), uint32_t(c)));
-        const uint32_t a = sm100::mapa(smem_u32(sums + t + k), uint32_t(c));
-        b.mass[k] += uint64_t(ld_cluster(a)) | (uint64_t(ld_cluster(a + 4)) << 32);
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) ss.add(part_of_list(from[i]), 1u, mass_of(s.weight(from[i])));
+    __syncthreads();
+    const Found f = find_part(sm, ss, by_mass, left);
+    if (f.bin == kParts) return false;
+    left -= by_mass ? f.mass : uint64_t(f.cnt);
+    sum += f.mass;
+    float* to = level & 1 ? sm.list_value : reinterpret_cast<float*>(sm.list_index);
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      const float l = from[i];
+      if (part_of_list(l) == f.bin) to[atomicAdd(&sm.nlist, 1u)] = l;
+    }
+    n = int(f.in);
+    from = to;
+    __syncthreads();
+    if (n <= 32) break;
+    base += float(f.bin) / scale;
+    scale *= float(kParts);
+  }
+  uint32_t within = 0;   // equal ones, where there are many
+  if (n > 32) {
+    float most = -INFINITY, least = INFINITY;
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      most = fmaxf(most, from[i]);
+      least = fminf(least, from[i]);
+    }
+    most = block_max(sm, most);
+    if (block_max(sm, -least) != -most) return false;
+    within = uint32_t(n);
+    n = 1;
+  }
+  // every warp finds the same: values above this lane's, and equal to it
+  const float mine = lane < n ? from[lane] : -INFINITY;
+  const uint64_t w = mass_of(s.weight(mine));
+  uint64_t over = 0;
+  uint32_t eq = 0, over_n = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const float other = from[j];
+    eq += other == mine ? 1u : 0u;
+    over_n += other > mine ? 1u : 0u;
+    over += other > mine ? mass_of(s.weight(other)) : 0;
+  }
+  eq = within ? within : eq;
+  const uint64_t before = by_mass ? over : over_n, all = by_mass ? eq * w : uint64_t(eq);
+  const uint32_t who = __ballot_sync(0xffffffffu, lane < n && before < left && left <= before + all);
+  if (who == 0) return false;
+  // (a mass of a few whole units: 32 bits of quotient are enough, see ties_of)
+  const uint32_t ties = by_mass ? ties_of(left - before, w, eq) : uint32_t(left - before);
+  const int lead = __ffs(who) - 1;
+  const Cut found = {__shfl_sync(0xffffffffu, mine, lead), __shfl_sync(0xffffffffu, ties, lead)};
+  tighten(*cut, found);
+  *kept = sum + __shfl_sync(0xffffffffu, over + ties * w, lead);
+  __syncthreads();
+  return true;
+}
+
+// The border over a whole row, by one CTA: by height, then, of the border's part, digit by
+// digit (10, 10, 10 and 2 bits) of the ordered values.  *kept: mass down to the cut.
+template <typename T>
+__device__ __noinline__ void border_of_row(SampleSmem& sm, SearchSmem& ss, const Part<T> part,
+                                           const Scale s, bool by_mass, uint64_t want, Cut* cut,
+                                           uint64_t* kept) {
+  constexpr float kScale = float(kParts) / -kNothing;
+  const int lane = int(threadIdx.x) & 31;
+  uint32_t prefix = 0;
+  int step = 0;
+  uint64_t left = want, sum = 0;
+  static_assert(kParts == 1024, "digits of ten bits");
+  for (int level = 0; level < 5; ++level) {
+    const int above = 42 - 10 * level;                       // bits of the key that are known
+    const int shift = above > 10 ? above - 10 : 0;
+    __syncthreads();   // the last level's parts have been read
+    ss.clear();
+    __syncthreads();
+    for (int v0 = part.v0; v0 < part.v1; v0 += kThreads) {   // (whole warps)
+      const int v = v0 + int(threadIdx.x);
+      float x[Part<T>::kE];
+      if (v < part.v1) part.load(v, x);
+#pragma unroll 1
+      for (int j = 0; j < Part<T>::kE; ++j) {
+        const float l = v < part.v1 ? x[j] : -INFINITY, h = s.height(l);
+        const int by_height = int(fminf(h * -kScale, float(kParts - 1)));
+        const uint32_t key = down_key(l);
+        int at = -1;
+        if (h > kNothing) {
+          if (level == 0) at = by_height;
+          else if (by_height == step && (level == 1 || key >> above == prefix))
+            at = int((key >> shift) & ((1u << (min(above, 32) - shift)) - 1u));
+        }
+        // rows of equal values: one lane adds for a warp that has a single place
+        const uint32_t has = __ballot_sync(0xffffffffu, at >= 0);
+        if (has == 0) continue;
+        const int lead = __ffs(has) - 1, place = __shfl_sync(0xffffffffu, at, lead);
+        const uint32_t same = __ballot_sync(0xffffffffu, at == place);
+        if (same == has) {
+          const uint64_t w = warp_sum(at >= 0 ? mass_of(s.weight(l)) : 0);
+          if (lane == lead) ss.add(place, uint32_t(__popc(has)), w);
+        } else if (at >= 0) {
+          ss.add(at, 1u, mass_of(s.weight(l)));
+        }
       }
     }
-    const Found f = find_bin(sm, b, by_mass, left);
-    if (f.bin == kBins) {   // (a rounding of the total: all of it is kept)
-      cut->above = -INFINITY;
-      cut->ties = 0;
+    __syncthreads();
+    const Found f = find_part(sm, ss, by_mass, left);
+    if (f.bin == kParts) {   // fewer than that have a mass: all of them stay
+      uint64_t all = 0;
+      for (int k = 0; k < kPer2; ++k) all += ss.sum(int(threadIdx.x) * kPer2 + k);
+      *kept = sum + block_sum(sm, all);
       return;
     }
-    prefix = (prefix << (level == 0 ? 0 : (level == 1 ? 11 : 10))) | uint32_t(f.bin);
+    if (level == 0) step = f.bin;
+    else prefix = (prefix << (level == 1 ? 0 : above - shift)) | uint32_t(f.bin);
     left -= by_mass ? f.mass : uint64_t(f.cnt);
-    mass += f.mass;
+    sum += f.mass;
   }
-  cut->above = down_value(prefix);
-  const uint64_t w = mass_of(s.weight(cut->above));
-  cut->ties = by_mass ? uint32_t((left + (w ? w : 1) - 1) / (w ? w : 1)) : uint32_t(left);
-  *mass_out = mass + cut->ties * w;
+  Cut found = {down_value(prefix), 0u};
+  const uint64_t w = mass_of(s.weight(found.above));
+  found.ties = by_mass ? ties_of(left, w, 1u << 20) : uint32_t(left);
+  tighten(*cut, found);
+  *kept = sum + found.ties * w;
 }
 
 // ------------------------------------------------------------------ kernel
+
+enum Mode { kAll, kTopK, kTopP };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
@@ -516,19 +637,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int ctas = p.ctas, rank = int(sm100::cluster_ctarank());
   const int r = int(blockIdx.x) / ctas, g = r / p.group, at = r - g * p.group;
   sm100::cluster_arrive_relaxed();   // (every CTA of the cluster runs before any writes to it)
-  for (int i = tid; i < kBins; i += kThreads) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
-  if (tid == 0) sm.nlist = 0;
+  if (tid < kCoarse / 2) sm.lanes[tid] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) sm.nlist = sm.last = 0;
   griddep_wait();                // the stream's previous kernel has completed
   griddep_launch_dependents();   // the next kernel may start its set-up
   if (p.clear_status && blockIdx.x == 0 && tid == 0) *p.status = 0u;
 
-  const float temp = p.temperature ? p.temperature[g] : 1.f;
-  const int top_k = p.top_k ? p.top_k[g] : 0;
-  const float top_p = p.top_p ? p.top_p[g] : 1.f;
-  const float min_p = p.min_p ? p.min_p[g] : 0.f;
-  const bool greedy = !(temp > 0.f);
-  const bool use_k = !greedy && top_k > 0 && top_k < p.V;
-  const bool use_p = !greedy && top_p < 1.f;
   Part<T> part;
   part.row = p.group == 1 ? static_cast<const T*>(p.logits) + int64_t(r) * p.stride
              : at == 0    ? static_cast<const T*>(p.root) + int64_t(g) * p.V
@@ -539,330 +653,608 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int nv = int((p.V + part.skew + kE - 1) / kE), per = (nv + ctas - 1) / ctas;
   part.v0 = rank * per < nv ? rank * per : nv;
   part.v1 = part.v0 + per < nv ? part.v0 + per : nv;
-  part.mem = nullptr;
 
-  // ---- the row's part into shared memory, and its maximum
-  float top = -INFINITY;
-  {
-    uint4* stage = reinterpret_cast<uint4*>(smem_raw + sizeof(SampleSmem));
-    constexpr int kBatch = 4;
-    for (int v = part.v0 + tid; v < part.v1; v += kBatch * kThreads) {
-      uint4 q[kBatch];
+  // ---- the warp's piece: a running maximum and sum per lane
+  int p0, p1;
+  part.piece(warp, &p0, &p1);
+  const uint32_t ring = smem_u32(smem_raw + sizeof(SampleSmem)) +
+                        uint32_t(warp) * (512u * kStep * kAhead) + uint32_t(lane) * 16u;
+  float lane_max = kLowest, lane_sum = 0.f;
+  float temp, temp_in, top_p, min_p, u;
+  int top_k;
+  bool greedy;
+  Mode mode;
+  Scale s;
+  stream(part, ring, p0, p1, [&](int, const uint4 (&q)[kStep]) {
+    float x[kStep][kE], most = lane_max;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (v + k * kThreads < part.v1) q[k] = part.from_global(v + k * kThreads);
+    for (int k = 0; k < kStep; ++k) {
+      unpack<T>(q[k], x[k]);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (v + k * kThreads < part.v1) {
-          float x[kE];
-          unpack<T>(q[k], x);
-#pragma unroll
-          for (int j = 0; j < kE; ++j) top = fmaxf(top, x[j]);
-          if (p.staged) stage[v + k * kThreads - part.v0] = q[k];
-        }
+      for (int i = 0; i < kE; ++i) most = fmaxf(most, x[k][i]);
     }
-    if (p.staged) part.mem = stage;
-  }
-  top = block_max(sm, top);
+    if (!greedy) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        float e = 0.f;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) e += s.plain(x[k][i], most);
+        sum += e;
+      }
+      lane_sum = fmaf(lane_sum, s.plain(lane_max, most), sum);
+    }
+    lane_max = most;
+  }, [&] {
+    temp = p.temperature ? p.temperature[g] : 1.f;
+    top_k = p.top_k ? p.top_k[g] : 0;
+    top_p = p.top_p ? p.top_p[g] : 1.f;
+    min_p = p.min_p ? p.min_p[g] : 0.f;
+    u = p.uniform[r];
+    greedy = !(temp > 0.f);
+    mode = top_k > 0 && top_k < p.V ? kTopK : (top_p < 1.f ? kTopP : kAll);
+    temp_in = fminf(fmaxf(temp, 0x1p-100f), 3.4e38f);
+    // log2(e) / T in two parts
+    constexpr float kHi = 1.4426950216293335f, kLo = 1.925962989e-8f;
+    s.c_hi = __fdiv_rz(kHi, temp_in);
+    s.c_lo = fmaxf((fmaf(-s.c_hi, temp_in, kHi) + kLo) / temp_in, 1e-45f);
+  });
+  // (a row with NaN is left to the slow way, by a maximum out of range)
+  float top = block_max(sm, lane_sum == lane_sum ? lane_max : INFINITY);
   sm100::cluster_wait();
   if (tid < ctas) sm100::st_cluster_f32(sm100::mapa(smem_u32(&sm.x_max[rank]), uint32_t(tid)), top);
-  sm100::cluster_sync();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  // (64 bits are slow: one thread, while the cluster meets)
+  if (tid == 0 && min_p > 0.f) sm.min_gap = fmin(double(temp) * log(double(min_p)), 0.0);
+  sm100::cluster_wait();
   top = sm.x_max[0];
   for (int c = 1; c < ctas; ++c) top = fmaxf(top, sm.x_max[c]);
-
-  Scale s;
   s.m = top;
-  {   // log2(e) / T in two parts
-    constexpr float kHi = 1.4426950216293335f, kLo = 1.925962989e-8f;
-    const float t = fminf(fmaxf(temp, 0x1p-100f), 3.4e38f);
-    s.c_hi = kHi / t;
-    s.c_lo = (fmaf(-s.c_hi, t, kHi) + kLo) / t;
-  }
-  Cut cut = {-INFINITY, 0u};
+  bool slow = !(fabsf(top) < kPlain);   // (no more barriers of the cluster then)
+  if (slow && rank != 0) return;
 
-  if (top == -INFINITY) {   // nothing to draw from (the whole cluster leaves)
-    if (rank == 0 && tid == 0) {
-      p.tokens[r] = 0;
-      if (p.logprob) p.logprob[r] = -INFINITY;
-      if (p.status && !p.clear_status) atomicOr(p.status, VA_STATUS_EMPTY_ROW);
-    }
-    return;
-  }
   if (greedy) {   // the lowest index of the largest
+    if (slow) {
+      part.v0 = 0;
+      part.v1 = nv;
+      top = -INFINITY;
+      for (int v = tid; v < nv; v += kThreads) {
+        float x[kE];
+        part.load(v, x);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) top = fmaxf(top, x[i]);
+      }
+      top = block_max(sm, top);
+    }
     uint32_t first = 0xffffffffu;
     for (int v = part.v0 + tid; v < part.v1 && first == 0xffffffffu; v += kThreads) {
       float x[kE];
       part.load(v, x);
 #pragma unroll
       for (int j = kE - 1; j >= 0; --j)
-        if (x[j] == top) first = uint32_t(int64_t(v) * kE - part.skew + j);
+        if (x[j] == top && part.index(v, j) < uint32_t(p.V)) first = part.index(v, j);
     }
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) sm.w_eq[warp] = first;
     __syncthreads();
-    if (tid == 0) {
-      for (int w = 0; w < kWarps; ++w) first = min(first, sm.w_eq[w]);
-      sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.x_first[rank]), 0u), first);
+    for (int w = 0; w < kWarps; ++w) first = min(first, sm.w_eq[w]);
+    if (!slow) {
+      if (tid == 0) sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.first[rank]), 0u), first);
+      sm100::cluster_sync();
+      if (rank != 0) return;
+      for (int c = 0; c < ctas; ++c) first = min(first, sm.first[c]);
     }
-    sm100::cluster_sync();
-    if (rank == 0 && tid == 0) {
-      for (int c = 0; c < ctas; ++c) first = min(first, sm.x_first[c]);
-      p.tokens[r] = int32_t(first);
-      if (p.logprob) p.logprob[r] = 0.f;
+    if (tid == 0) {
+      const bool empty = top == -INFINITY;
+      p.tokens[r] = empty ? 0 : int32_t(first);
+      if (p.logprob) p.logprob[r] = empty ? -INFINITY : 0.f;
+      if (empty && p.status && !p.clear_status) atomicOr(p.status, VA_STATUS_EMPTY_ROW);
     }
     return;
   }
 
-  if (use_k || use_p) {
-    // ---- histogram of the heights.  Weights below (1 - top_p) / V cannot reach the
-    // border (all of them together weigh less than what top_p drops of a total >= 1).
-    const float dropped = use_p && !use_k ? (1.f - fmaxf(top_p, 0.f)) / float(p.V) * 0.999f : 0.f;
-    uint64_t total = 0;
-    for (int v = part.v0 + tid; v < part.v1; v += kThreads) {
-      float x[kE], sum = 0.f;
-      part.load(v, x);
-#pragma unroll
-      for (int j = 0; j < kE; ++j) {
-        const float h = s.height(x[j]);
-        if (!(h > kNothing)) continue;   // (top-k may count as many of these as it likes)
-        const int bin = s.bin(h);
-        if (use_p) {
-          const float e = s.weight(x[j]);
-          sum += e;
-          if (e >= dropped) {
-            const uint32_t w = octave_mass(e, bin >> 6);
-            atomicAdd(&sm.lo[bin], w & 0xfffu);
-            atomicAdd(&sm.hi[bin], w >> 12);
-            atomicAdd(&sm.cnt[bin], 1u);
-          }
-        } else {
-          atomicAdd(&sm.cnt[bin], 1u);
-        }
+  float min_above = -INFINITY;
+  if (min_p > 0.f && !slow) {   // the largest value below m + T ln(min_p)
+    if (tid == 0) sm.min_above = largest_below(double(top) + sm.min_gap);
+    __syncthreads();
+    min_above = sm.min_above;
+  }
+
+  const uint32_t share = uint32_t(kList / ctas);
+  int border = -1;        // kTopP: the bin of the border, if masses above it were added up
+  float depth = 0.f;      // octaves below the maximum that are listed
+  uint64_t row_mass = 0;
+  if (!slow) {
+    const float lane_top = s.plain(lane_max, top);
+    uint64_t kept = warp_sum(mass_of(lane_sum * lane_top)), over = 0;
+    float reach = 0.f;   // what lies that far below the maximum is listed
+    if (mode != kAll) {
+      // ---- a bound from the lanes' maxima
+      const float h = (lane_max - top) * s.c_hi;
+      if (h > kNothing) {
+        const int b = int(fminf(h * -kCoarsePerOctave, float(kCoarse - 1)));
+        uint32_t* bin = reinterpret_cast<uint32_t*>(sm.lanes) + 2 * b;
+        atomicAdd(bin, 1u);
+        atomicAdd(bin + 1, uint32_t(lane_top * 0x1p19f));
       }
-      total += mass_of(sum);
-    }
-    if (use_p && !use_k) {   // the row's mass
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      if (lane == 0) sm.w_mass[warp] = total;
+      if (lane == 0) sm.s_mass[warp] = kept;
       __syncthreads();
       if (tid < ctas) {
-        total = 0;
-        for (int w = 0; w < kWarps; ++w) total += sm.w_mass[w];
-        const uint32_t a = sm100::mapa(smem_u32(&sm.x_total[rank][0]), uint32_t(tid));
-        sm100::st_cluster_u32(a, uint32_t(total));
-        sm100::st_cluster_u32(a + 4, uint32_t(total >> 32));
+        uint64_t m = 0;
+        for (int w = 0; w < kWarps; ++w) m += sm.s_mass[w];
+        st_cluster_v2(sm100::mapa(smem_u32(&sm.x_total[rank]), uint32_t(tid)), uint32_t(m),
+                      uint32_t(m >> 32));
       }
-    }
-    sm100::cluster_sync();
-    Bins bins;
-    gather_bins(sm, ctas, bins);
-    int listed = -1, n = 0;   // bin whose values are in `merged`
-    uint64_t kept = 0;
-    bool done_p = !use_p;
-    if (use_k) {
-      const Found f = find_bin(sm, bins, false, uint64_t(top_k));
-      const int bin = f.bin;
-      uint64_t in_bin = 0;
-      bool ok = bin < kBins - 1 && f.in <= kList;
-      if (bin == kBins) {   // fewer than k have a mass: all of them stay
-        ok = true;
-        uint32_t n_all = 0;
-        kept = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) kept += bins.mass[k];
-        const uint64_t mine = kept;
-        block_scan(sm, n_all, kept);
-        kept += mine;   // (the last thread's is the total)
-        if (tid == kThreads - 1) sm.f_mass = kept;
-        __syncthreads();
-        kept = sm.f_mass;
-        __syncthreads();
-      } else if (ok) {
-        n = gather_list(sm, part, s, ctas, bin, dropped);
-        listed = bin;
-        ok = border_in_list(sm, s, n, bin, false, uint64_t(top_k) - f.cnt, &cut, &in_bin);
-        kept = f.mass + from_octave(in_bin, bin >> 6);
+      // (written to every CTA before the barrier: a read of another's memory takes 1500 cycles)
+      for (int i = tid; i < ctas * (kCoarse / 2); i += kThreads) {
+        const uint4 q = sm.lanes[i % (kCoarse / 2)];
+        sm100::st_cluster_v4(sm100::mapa(smem_u32(&sm.x_lanes[rank][i % (kCoarse / 2)]),
+                                         uint32_t(i / (kCoarse / 2))), q.x, q.y, q.z, q.w);
       }
-      if (!ok) {
-        listed = -1;
-        border_by_digits(sm, part, s, ctas, false, uint64_t(top_k), &cut, &kept);
-        if (use_p) {
-          Cut c2 = {-INFINITY, 0u};
-          uint64_t m2;
-          const uint64_t want_p = top_p > 0.f ? part_of(top_p, kept) : 1u;
-          border_by_digits(sm, part, s, ctas, true, want_p > 0 ? want_p : 1u, &c2, &m2);
-          if (c2.above > cut.above || (c2.above == cut.above && c2.ties < cut.ties)) cut = c2;
-          done_p = true;
-        }
-      }
-    } else {
-      kept = 0;
+      sm100::cluster_sync();
       for (int c = 0; c < ctas; ++c)
-        kept += uint64_t(sm.x_total[c][0]) | (uint64_t(sm.x_total[c][1]) << 32);
-    }
-    if (!done_p) {
-      uint64_t want = top_p > 0.f ? part_of(top_p, kept) : 1u;
-      want = want > 0 ? want : 1u;
-      const Found f = find_bin(sm, bins, true, want);
-      const int bin = f.bin;
-      if (bin < kBins) {   // (else, by a rounding of the total, all of it stays)
-        const uint64_t inside = to_octave(want - f.mass, bin >> 6);
-        Cut c2 = {-INFINITY, 0u};
-        uint64_t m2;
-        bool ok = bin < kBins - 1 && f.in <= kList;
-        if (ok) {
-          if (bin != listed) {
-            if (listed >= 0) {   // the first list has been read by the whole cluster
-              sm100::cluster_sync();
-              if (tid == 0) sm.nlist = 0;
-              __syncthreads();
-            }
-            n = gather_list(sm, part, s, ctas, bin, dropped);
+        row_mass += uint64_t(sm.x_total[c].x) | (uint64_t(sm.x_total[c].y) << 32);
+      if (warp == 0) {   // (one warp: no barriers)
+        uint32_t cnt[kCoarsePer], mass[kCoarsePer], c1 = 0, m1 = 0;
+#pragma unroll
+        for (int k = 0; k < kCoarsePer; ++k) cnt[k] = mass[k] = 0;
+#pragma unroll 1
+        for (int c = 0; c < ctas; ++c) {
+#pragma unroll
+          for (int k = 0; k < kCoarsePer; k += 2) {
+            const uint4 q = sm.x_lanes[c][(lane * kCoarsePer + k) / 2];
+            cnt[k] += q.x;
+            mass[k] += q.y;
+            cnt[k + 1] += q.z;
+            mass[k + 1] += q.w;
           }
-          ok = border_in_list(sm, s, n, bin, true, inside > 0 ? inside : 1u, &c2, &m2);
         }
-        if (!ok) border_by_digits(sm, part, s, ctas, true, want, &c2, &m2);
-        if (c2.above > cut.above || (c2.above == cut.above && c2.ties < cut.ties)) cut = c2;
+#pragma unroll
+        for (int k = 0; k < kCoarsePer; ++k) { c1 += cnt[k]; m1 += mass[k]; }
+        uint32_t c_at = c1, m_at = m1;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, c_at, o), y = __shfl_up_sync(0xffffffffu, m_at, o);
+          if (lane >= o) { c_at += x; m_at += y; }
+        }
+        c_at -= c1;
+        m_at -= m1;
+        // (weights round down here, and sums elsewhere by 2^-23: a little more is asked for)
+        uint32_t want = uint32_t(top_k);
+        if (mode == kTopP)
+          want = top_p > 0.f ? uint32_t(min((part_of(top_p, row_mass) >> (kUnit - 19)) * 65537 / 65536 + 2,
+                                            uint64_t(0xffffffffu)))
+                             : 1u;
+        if (lane == 0) sm.f_bin = kCoarse;
+        __syncwarp();
+        const uint32_t before = mode == kTopK ? c_at : m_at, mine = mode == kTopK ? c1 : m1;
+        if (before < want && want - before <= mine) {
+          uint32_t run = before;
+          bool found = false;
+#pragma unroll
+          for (int k = 0; k < kCoarsePer; ++k) {
+            run += mode == kTopK ? cnt[k] : mass[k];
+            if (!found) c_at += cnt[k];
+            if (!found && run >= want) {
+              found = true;
+              sm.f_bin = uint32_t(lane * kCoarsePer + k);
+            }
+          }
+          sm.f_cnt = c_at;   // down to the bound
+        }
       }
+      __syncthreads();
+      const int bound = int(sm.f_bin);
+      // (no bound: fewer than k values have a mass, of all lanes' maxima at least.)
+      // With a share f of the lanes' maxima above it, the bound has some -ln(1 - f) values
+      // above it for every lane.
+      const float lanes = float(ctas * kThreads);
+      const bool few = p.V <= share || (bound < kCoarse &&
+                                        -__logf(fmaxf(1.f - float(sm.f_cnt) / lanes, 1e-9f)) * lanes < kListAim);
+      __syncthreads();
+      if (few) {
+        depth = bound < kCoarse ? float(bound + 1) / kCoarsePerOctave : -kNothing;
+      } else {
+        // ---- the step of the border, from all values
+        for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0;
+        if (tid < kRest) sm.rest[tid] = 0;
+        __syncthreads();
+        const int shift = max(32 - __clz(per * kE) - 9, 1);   // a bin's sum fits 32 bits
+        // Weights below (1 - top_p) / V of the row's mass cannot reach the border: all of
+        // them together weigh less than what top_p drops.
+        const float dropped = (1.f - fmaxf(top_p, 0.f)) * (float(row_mass) * 0x1p-43f) / float(p.V) * 0.999f;
+        stream(part, ring, p0, p1, [&](int, const uint4 (&q)[kStep]) {
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            float x[kE];
+            unpack<T>(q[k], x);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+              const float d = x[i] - top, hh = d * s.c_hi;
+              const uint32_t bin = bin_of(hh);
+              if (mode == kTopK) {
+                if (hh > kNothing) atomicAdd(&sm.hist[bin], 1u);   // (of the others any may stay)
+              } else {
+                const float e = sm100::ex2_approx(fmaf(d, s.c_lo, hh));
+                if (e >= dropped) {
+                  const uint32_t w = octave_mass(e, int(bin >> kOctaveBits));
+                  if (bin < kRest) {   // (few, as a rule)
+                    atomicAdd(&sm.hist[bin], w >> shift);
+                    atomicAdd(&sm.rest[bin], w & ((1u << shift) - 1u));
+                  } else {
+                    atomicAdd(&sm.hist[bin], (w + (1u << (shift - 1))) >> shift);
+                  }
+                }
+              }
+            }
+          }
+        });
+        sm100::cluster_sync();
+        const int t = tid * kPer;
+        static_assert(kPer == 4, "a 16-byte read");
+        uint4 w[kCtasMax];
+#pragma unroll
+        for (int c = 0; c < kCtasMax; ++c)
+          if (c < ctas) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.hist + t), uint32_t(c)));
+        uint64_t sums[kPer] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < kCtasMax; ++c)
+          if (c < ctas) { sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w; }
+        uint64_t goal = uint64_t(top_k);
+        if (mode == kTopP) {   // in units of 2^-43
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) sums[k] <<= shift;
+          if (t < kRest) {
+#pragma unroll 1
+            for (int c = 0; c < ctas; ++c) {
+              const uint4 x = ld_cluster_v4(sm100::mapa(smem_u32(sm.rest + t), uint32_t(c)));
+              sums[0] += x.x; sums[1] += x.y; sums[2] += x.z; sums[3] += x.w;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int up = kUnit - 22 - ((t + k) >> kOctaveBits);
+            sums[k] = up >= 0 ? sums[k] << up : sums[k] >> -up;
+          }
+          goal = top_p > 0.f ? part_of(top_p, row_mass) : 1u;
+          goal = goal > 0 ? goal : 1u;
+        }
+        const int bin = find_bin<kPer>(sm, true, goal, [&](int k) {
+          return Sums{k < 2 ? (k ? sums[1] : sums[0]) : (k == 3 ? sums[3] : sums[2]), 0u};
+        }).bin;
+        if (mode == kTopP)
+          border = bin;
+        else   // (without a border fewer than k values have a mass: all of them are listed)
+          depth = bin < kBins ? (float(bin) + 0.5f) / kBinsPerOctave : -kNothing;
+      }
+      reach = depth * 1.00001f / s.c_hi;
     }
+
+    // ---- the list, or masses and list
+    const uint32_t to_value = sm100::mapa(smem_u32(sm.list_value + rank * share), 0u);
+    const uint32_t to_index = sm100::mapa(smem_u32(sm.list_index + rank * share), 0u);
+    auto list = [&](float x, uint32_t index) {
+      const uint32_t n = atomicAdd(&sm.nlist, 1u);
+      if (n < share) {
+        sm100::st_cluster_f32(to_value + 4u * n, x);
+        sm100::st_cluster_u32(to_index + 4u * n, index);
+      }
+    };
+    if (border >= 0) {
+      kept = 0;
+      stream(part, ring, p0, p1, [&](int v, const uint4 (&q)[kStep]) {
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          float x[kE], sum = 0.f, sum_kept = 0.f;
+          unpack<T>(q[k], x);
+#pragma unroll
+          for (int i = 0; i < kE; ++i) {
+            const float d = x[i] - top, hh = d * s.c_hi;
+            const uint32_t bin = bin_of(hh);
+            const float e = bin < uint32_t(border) ? sm100::ex2_approx(fmaf(d, s.c_lo, hh)) : 0.f;
+            sum += e;
+            sum_kept += x[i] > min_above ? e : 0.f;
+            if (bin == uint32_t(border) && hh > kNothing) list(x[i], part.index(v + 32 * k, i));
+          }
+          over += mass_of(sum);
+          kept += mass_of(sum_kept);
+        }
+      });
+      kept = warp_sum(kept);
+      over = warp_sum(over);
+    } else if (mode != kAll) {
+      kept = 0;
+      if (lane_max - top >= -reach)   // (a lane whose maximum is not listed has nothing to list)
+      stream(part, ring, p0, p1, [&](int v, const uint4 (&q)[kStep]) {
+        float x[kStep][kE], most = kLowest;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          unpack<T>(q[k], x[k]);
+#pragma unroll
+          for (int i = 0; i < kE; ++i) most = fmaxf(most, x[k][i]);
+        }
+        if (most - top >= -reach) {
+#pragma unroll
+          for (int k = 0; k < kStep; ++k)
+#pragma unroll
+            for (int i = 0; i < kE; ++i)
+              if (x[k][i] - top >= -reach && x[k][i] > -INFINITY) list(x[k][i], part.index(v + 32 * k, i));
+        }
+      });
+    } else if (min_p > 0.f) {
+      kept = 0;
+      if (lane_max > min_above)
+      stream(part, ring, p0, p1, [&](int, const uint4 (&q)[kStep]) {
+        float x[kStep][kE], most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          unpack<T>(q[k], x[k]);
+#pragma unroll
+          for (int i = 0; i < kE; ++i) most = fmaxf(most, x[k][i]);
+        }
+        if (most > min_above) {
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) sum += x[k][i] > min_above ? s.plain(x[k][i], top) : 0.f;
+            kept += mass_of(sum);
+          }
+        }
+      });
+      kept = warp_sum(kept);
+    }
+    if (lane == 0)
+      sm100::st_cluster_v4(sm100::mapa(smem_u32(&sm.piece[rank * kWarps + warp]), 0u), uint32_t(kept),
+                           uint32_t(kept >> 32), uint32_t(over), uint32_t(over >> 32));
+    __syncthreads();
+    if (tid == 0) sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.list_count[rank]), 0u), sm.nlist);
+    sm100::cluster_sync();   // (no CTA touches another's memory from here on)
+    if (rank != 0) return;
   }
-  if (min_p > 0.f) {   // the largest value below m + T ln(min_p)
-    if (tid == 0) {    // (64 bits are slow: one thread)
-      const double gap = double(temp) * log(double(min_p));
-      const double t = double(top) + fmin(gap, 0.0);
-      const float f = __double2float_rd(t);
-      sm.min_above = double(f) == t ? nextafterf(f, -INFINITY) : f;
+
+  // ---- the first CTA: what is kept of the list
+  SearchSmem& ss = *reinterpret_cast<SearchSmem*>(smem_raw + sizeof(SampleSmem));
+  Cut cut = {-INFINITY, 0u};
+  int n = 0;
+  if (!slow && mode != kAll) {
+    bool ok = true;
+    for (int c = 0; c < ctas; ++c) {   // the lists side by side
+      const int here = int(min(sm.list_count[c], share));
+      ok = ok && sm.list_count[c] <= share;
+#pragma unroll 1
+      for (int i = tid; i < here; i += kThreads) {
+        ss.value[n + i] = sm.list_value[c * share + i];
+        ss.index[n + i] = sm.list_index[c * share + i];
+      }
+      n += here;
     }
     __syncthreads();
-    const float f = sm.min_above;
-    if (f >= cut.above) cut = {f, 0u};
-  }
-
-  // ---- kept masses, piece by piece in index order
-  const uint64_t tie_mass = cut.ties ? mass_of(s.weight(cut.above)) : 0;
-  int p0, p1;
-  part.piece(warp, &p0, &p1);
-  uint64_t mass = 0;
-  uint32_t eq = 0;
-  for (int v = p0 + lane; v < p1; v += 32) {
-    float x[kE], sum = 0.f;
-    part.load(v, x);
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < kE; ++j) {
-      any |= x[j] > cut.above;
-      eq += x[j] == cut.above ? 1u : 0u;
+    uint64_t mass = row_mass;   // of which top-p takes its part
+    const float scale = float(kParts) / fmaxf(depth, 1e-3f);
+    if (ok && mode == kTopK)   // (fewer than k are listed where no others have a mass)
+      ok = border_in_list(sm, ss, s, n, 0.f, scale, false, uint64_t(min(top_k, n)), &cut, &mass);
+    if (ok && top_p < 1.f) {
+      uint64_t want = top_p > 0.f ? part_of(top_p, mass) : 1u, over = 0;
+      want = want > 0 ? want : 1u;
+      if (border >= 0) {
+        if (tid < ctas * kWarps) {
+          const uint4 q = sm.piece[tid];
+          over = uint64_t(q.z) | (uint64_t(q.w) << 32);
+        }
+        over = block_sum(sm, over);
+        ok = border < kBins && want > over;
+      }
+      ok = ok && border_in_list(sm, ss, s, n,
+                                border >= 0 ? (float(border) - 0.5f) / kBinsPerOctave : 0.f,
+                                border >= 0 ? kBinsPerOctave * kParts : scale, true, want - over, &cut,
+                                &mass);
     }
-    if (any) {
-#pragma unroll
-      for (int j = 0; j < kE; ++j) sum += x[j] > cut.above ? s.weight(x[j]) : 0.f;
-      mass += mass_of(sum);
-    }
+    slow = !ok;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mass += __shfl_xor_sync(0xffffffffu, mass, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  }
-  if (lane == 0) {
-    sm.w_mass[warp] = mass;
-    sm.w_eq[warp] = eq;
-  }
-  __syncthreads();
-  if (tid < ctas) {
-    uint64_t m = 0;
-    uint32_t e = 0;
-    for (int w = 0; w < kWarps; ++w) { m += sm.w_mass[w]; e += sm.w_eq[w]; }
-    const uint32_t a = sm100::mapa(smem_u32(&sm.x_mass[rank][0]), uint32_t(tid));
-    sm100::st_cluster_u32(a, uint32_t(m));
-    sm100::st_cluster_u32(a + 4, uint32_t(m >> 32));
-    sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.x_eq[rank]), uint32_t(tid)), e);
-  }
-  sm100::cluster_sync();   // (the last time that a CTA touches another's memory is before it)
-
-  // ---- where the drawn mass falls
-  auto tied = [&](uint32_t e) { return uint64_t(e < cut.ties ? e : cut.ties) * tie_mass; };
-  uint64_t all = 0, before = 0;
-  uint32_t all_eq = 0, eq_before = 0;
-  for (int c = 0; c < ctas; ++c) {
-    if (c == rank) { before = all; eq_before = all_eq; }
-    all += uint64_t(sm.x_mass[c][0]) | (uint64_t(sm.x_mass[c][1]) << 32);
-    all_eq += sm.x_eq[c];
-  }
-  const uint64_t total = all + tied(all_eq);
-  const float u = p.uniform[r];
-  const uint64_t u64 = u >= 1.f ? ~uint64_t(0) : (u > 0.f ? __float2ull_rz(u * 0x1p64f) : 0);
-  const uint64_t drawn = __umul64hi(u64, total);   // < total: the token is the first past it
-  for (int w = 0; w < warp; ++w) { before += sm.w_mass[w]; eq_before += sm.w_eq[w]; }
-  if (drawn < before + tied(eq_before) ||
-      drawn >= before + sm.w_mass[warp] + tied(eq_before + sm.w_eq[warp]))
-    return;
-  for (int vb = p0; vb < p1; vb += 32) {   // this warp's piece holds it
-    const int v = vb + lane;
-    float x[kE];
-    uint32_t my_eq = 0;
-    float sum = 0.f;
-    if (v < p1) {
+  int pieces = ctas * kWarps;
+  if (slow) {   // the whole row once more, by this CTA alone
+    part.v0 = 0;
+    part.v1 = nv;
+    part.piece(warp, &p0, &p1);
+    pieces = kWarps;
+    cut = {-INFINITY, 0u};
+    top = -INFINITY;
+    for (int v = tid; v < nv; v += kThreads) {
+      float x[kE];
       part.load(v, x);
 #pragma unroll
-      for (int j = 0; j < kE; ++j) {
-        sum += x[j] > cut.above ? s.weight(x[j]) : 0.f;
-        my_eq += x[j] == cut.above ? 1u : 0u;
-      }
+      for (int i = 0; i < kE; ++i) top = fmaxf(top, x[i]);
     }
-    const uint64_t mine = sum > 0.f ? mass_of(sum) : 0;
-    uint64_t m = mine;
-    uint32_t e = my_eq;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t m1 = __shfl_up_sync(0xffffffffu, m, o);
-      const uint32_t e1 = __shfl_up_sync(0xffffffffu, e, o);
-      if (lane >= o) { m += m1; e += e1; }
-    }
-    const uint64_t m_at = before + m - mine;
-    uint32_t e_at = eq_before + e - my_eq;
-    const bool here = drawn >= m_at + tied(e_at) && drawn < m_at + mine + tied(e_at + my_eq);
-    if (__any_sync(0xffffffffu, here)) {
-      if (here) {
-        int pick = 0;
-        bool found = false;
-        float run = 0.f;
-#pragma unroll
-        for (int j = 0; j < kE; ++j) {
-          const bool a = x[j] > cut.above, b = x[j] == cut.above && e_at < cut.ties;
-          if (a) run += s.weight(x[j]);
-          if (x[j] == cut.above) ++e_at;
-          if ((a || b) && !found) {
-            pick = j;   // (the last kept one, should a rounding leave none)
-            found = drawn < m_at + (run > 0.f ? mass_of(run) : 0) + tied(e_at);
-          }
-        }
-        float l = x[0];
-#pragma unroll
-        for (int j = 1; j < kE; ++j) l = pick == j ? x[j] : l;
-        p.tokens[r] = int32_t(int64_t(v) * kE - part.skew + pick);
-        if (p.logprob) {
-          // ln(w / total): near a total of 1 from what it exceeds 1 by
-          const uint64_t one = uint64_t(1) << kUnit;
-          const float ln = total < 2 * one && total >= one
-                               ? log1pf(float(total - one) * 0x1p-43f)
-                               : logf(float(total) * 0x1p-43f);
-          const float t = fminf(fmaxf(temp, 0x1p-100f), 3.4e38f);
-          p.logprob[r] = (l == top ? 0.f : (l - top) / t) - ln;
-        }
+    s.m = top = block_max(sm, top);
+    if (top == -INFINITY) {   // nothing to draw from
+      if (tid == 0) {
+        p.tokens[r] = 0;
+        if (p.logprob) p.logprob[r] = -INFINITY;
+        if (p.status && !p.clear_status) atomicOr(p.status, VA_STATUS_EMPTY_ROW);
       }
       return;
     }
-    before += __shfl_sync(0xffffffffu, m, 31);
-    eq_before += __shfl_sync(0xffffffffu, e, 31);
+    if (min_p > 0.f) min_above = largest_below(double(top) + sm.min_gap);
+    uint64_t mass = 0;
+    if (mode == kTopK) {
+      border_of_row(sm, ss, part, s, false, uint64_t(top_k), &cut, &mass);
+    } else if (top_p < 1.f) {
+      for (int v = tid; v < nv; v += kThreads) {
+        float x[kE];
+        part.load(v, x);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) mass += mass_of(s.weight(x[i]));
+      }
+      mass = block_sum(sm, mass);
+    }
+    if (top_p < 1.f) {
+      const uint64_t want = top_p > 0.f ? part_of(top_p, mass) : 1u;
+      border_of_row(sm, ss, part, s, true, want > 0 ? want : 1u, &cut, &mass);
+    }
+  }
+  if (min_p > 0.f && min_above >= cut.above) cut = {min_above, 0u};
+
+  // ---- masses and ties of the pieces
+  if (tid < kPieces) sm.piece_ties[tid] = 0;
+  __syncthreads();
+  if (slow) {
+    uint64_t mass = 0;
+    uint32_t ties = 0;
+    for (int v = p0 + lane; v < p1; v += 32) {
+      float x[kE], sum = 0.f;
+      part.load(v, x);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        sum += x[i] > cut.above ? s.weight(x[i]) : 0.f;
+        ties += x[i] == cut.above ? 1u : 0u;
+      }
+      mass += mass_of(sum);
+    }
+    mass = warp_sum(mass);
+    ties = __reduce_add_sync(0xffffffffu, ties);
+    if (lane == 0) {
+      sm.piece[warp] = make_uint4(uint32_t(mass), uint32_t(mass >> 32), 0u, 0u);
+      sm.piece_ties[warp] = ties;
+    }
+  } else if (mode != kAll) {
+#pragma unroll 1
+    for (int i = tid; i < n; i += kThreads) {
+      const float l = ss.value[i];
+      if (l >= cut.above) {
+        const int v = int((ss.index[i] + uint32_t(part.skew)) / uint32_t(kE)), c = v / per;
+        const int len = (min((c + 1) * per, nv) - c * per + kWarps - 1) / kWarps;
+        const int piece = c * kWarps + (v - c * per) / len;
+        if (l > cut.above)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&sm.piece[piece]),
+                    (unsigned long long)mass_of(s.weight(l)));
+        else
+          atomicAdd(&sm.piece_ties[piece], 1u);
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- the piece in which the drawn mass falls
+  const uint64_t tie_mass = cut.ties ? mass_of(s.weight(cut.above)) : 0;
+  auto tied = [&](uint32_t e) { return uint64_t(e < cut.ties ? e : cut.ties) * tie_mass; };
+  if (warp == 0) {   // (one warp: no barriers)
+    constexpr int kPiecesPer = kPieces / 32;
+    Sums one[kPiecesPer], sum = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kPiecesPer; ++k) {
+      const int i = lane * kPiecesPer + k;
+      const uint4 q = i < pieces ? sm.piece[i] : make_uint4(0, 0, 0, 0);
+      one[k] = {uint64_t(q.x) | (uint64_t(q.y) << 32), i < pieces ? sm.piece_ties[i] : 0u};
+      sum.mass += one[k].mass;
+      sum.cnt += one[k].cnt;
+    }
+    Sums to = sum;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t m = __shfl_up_sync(0xffffffffu, to.mass, o);
+      const uint32_t c = __shfl_up_sync(0xffffffffu, to.cnt, o);
+      if (lane >= o) { to.mass += m; to.cnt += c; }
+    }
+    const uint64_t total = __shfl_sync(0xffffffffu, to.mass + tied(to.cnt), 31);
+    const uint64_t u64 = u >= 1.f ? ~uint64_t(0) : (u > 0.f ? __float2ull_rz(u * 0x1p64f) : 0);
+    const uint64_t drawn = __umul64hi(u64, total);   // < total: the token is the first past it
+    uint64_t mass = to.mass - sum.mass;
+    uint32_t eq = to.cnt - sum.cnt;
+#pragma unroll
+    for (int k = 0; k < kPiecesPer; ++k) {
+      if (drawn >= mass + tied(eq) && drawn < mass + one[k].mass + tied(eq + one[k].cnt)) {
+        sm.f_bin = uint32_t(lane * kPiecesPer + k);   // one lane's
+        sm.f_cnt = eq;
+        sm.f_mass = mass;
+        sm.drawn = drawn;
+        sm.total = total;
+      }
+      mass += one[k].mass;
+      eq += one[k].cnt;
+    }
+  }
+  __syncthreads();
+  const uint64_t drawn = sm.drawn;
+  const int piece = int(sm.f_bin);
+  uint64_t m_at = sm.f_mass;
+  uint32_t e_at = sm.f_cnt;
+  if (!slow) {
+    part.v0 = min(piece / kWarps * per, nv);
+    part.v1 = min(part.v0 + per, nv);
+  }
+  part.piece(piece % kWarps, &p0, &p1);
+
+  // ---- the token in it: a run of vectors per thread, then the run's values one by one.  Sums
+  // of other groups of values may leave the drawn mass a rounding past the piece's end: it is
+  // then the piece's last kept token.
+  const int run = (p1 - p0 + kThreads - 1) / kThreads;
+  const int r0 = min(p0 + tid * run, p1), r1 = min(r0 + run, p1);
+  uint64_t m = 0;
+  uint32_t e = 0, last = 0;
+#pragma unroll 1
+  for (int v = r0; v < r1; ++v) {
+    float x[kE], sum = 0.f;
+    part.load(v, x);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      const float w = x[i] > cut.above ? s.weight(x[i]) : 0.f;
+      sum += w;
+      if (w > 0.f) last = part.index(v, i) + 1;
+      e += x[i] == cut.above && cut.ties > 0 ? 1u : 0u;
+    }
+    m += mass_of(sum);
+  }
+  const uint64_t my_mass = m;
+  const uint32_t my_eq = e;
+  const Sums run_at = block_scan(sm, e, m);
+  m = m_at + run_at.mass;
+  e = e_at + run_at.cnt;
+  const bool here = drawn >= m + tied(e) && drawn < m + my_mass + tied(e + my_eq);
+  if (here || (my_eq && e < cut.ties)) {
+    uint64_t m_run = m;
+    uint32_t e_run = e;
+    bool found = false;
+#pragma unroll 1
+    for (int v = r0; v < r1 && !found; ++v) {
+      float x[kE], sum = 0.f;
+      part.load(v, x);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const bool tie = x[i] == cut.above && cut.ties > 0;
+        sum += x[i] > cut.above ? s.weight(x[i]) : 0.f;
+        e_run += tie ? 1u : 0u;
+        if (tie && e_run <= cut.ties) last = max(last, part.index(v, i) + 1);
+        if (here && !found && drawn < m_run + mass_of(sum) + tied(e_run)) {
+          found = true;
+          sm.pick = part.index(v, i);
+          sm.pick_value = x[i];
+        }
+      }
+      m_run += mass_of(sum);
+    }
+  }
+  if (last) atomicMax(&sm.last, last);
+  const bool hit = __syncthreads_or(here);
+  if (tid == 0) {
+    const uint32_t token = hit ? sm.pick : (sm.last ? sm.last - 1 : uint32_t(max(p0 * kE - part.skew, 0)));
+    p.tokens[r] = int32_t(token);
+    if (p.logprob) {
+      // ln(w / total): near a total of 1 from what it exceeds 1 by
+      const uint64_t one = uint64_t(1) << kUnit, total = sm.total;
+      const float ln = total < 2 * one && total >= one ? log1pf(float(total - one) * 0x1p-43f)
+                                                       : logf(float(total) * 0x1p-43f);
+      const float l = hit ? sm.pick_value : value_of(part.row[token]);
+      p.logprob[r] = (l == top ? 0.f : (l - top) / temp_in) - ln;
+    }
   }
 }
 
 // -------------------------------------------------------------------- host
 
-constexpr size_t kStageMax = 190 * 1024 - sizeof(SampleSmem);   // staged bytes of a CTA at most
-constexpr size_t kStageTwo = 112 * 1024 - sizeof(SampleSmem);   // with two CTAs on an SM
+// The rings, which the search then takes.
+constexpr size_t kRings = size_t(kWarps) * 512 * kStep * kAhead;
+constexpr size_t kSmem = sizeof(SampleSmem) + (kRings > sizeof(SearchSmem) ? kRings : sizeof(SearchSmem));
 constexpr int64_t kRowsMax = int64_t(1) << 23;
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -870,14 +1262,10 @@ bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stream_t stream) {
   const size_t elem = dtype == VA_F32 ? 4 : 2;
   const int64_t vecs = (p.V * int64_t(elem) + 15) / 16 + 1;
-  auto bytes = [&](int ctas) { return size_t((vecs + ctas - 1) / ctas) * 16; };
-  // As many CTAs per row as leave two on an SM, and more while SMs are idle.
+  // As many CTAs per row as leave two on an SM.
   int ctas = 1;
-  while (ctas < kCtasMax &&
-         (bytes(ctas) > kStageTwo || (rows * ctas * 2 <= 2 * num_sms && bytes(ctas) > 4096)))
-    ctas *= 2;
+  while (ctas < kCtasMax && rows * ctas * 2 <= 2 * num_sms && vecs / ctas > kThreads / 2) ctas *= 2;
   p.ctas = ctas;
-  p.staged = bytes(ctas) <= kStageMax;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -889,7 +1277,7 @@ int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stre
   memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(unsigned(rows * ctas), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = sizeof(SampleSmem) + (p.staged ? bytes(ctas) : 0);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -918,7 +1306,7 @@ TreeLayout tree_layout(int B, int T) {
 }  // namespace
 
 cudaError_t init_sample() {
-  const int smem = int(sizeof(SampleSmem) + kStageMax);
+  const int smem = int(kSmem);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<float>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
