@@ -12,7 +12,7 @@
 // log2(e) / T comes in two parts, so that its rounding does not tilt the distribution.
 //
 // One cluster of CTAs per row, a warp per piece of it.
-//   1. Each warp reads its piece (copies into a ring in shared memory, four steps ahead), with
+//   1. Each warp reads its piece (copies into a ring in shared memory, three steps ahead), with
 //      a running maximum and sum per lane.  The cluster exchanges the maximum; the pieces'
 //      masses are then known, and a row without top-k and top-p is done but for 4.  Later
 //      steps read the row again, from L2.
@@ -20,10 +20,11 @@
 //      largest, and where they hold top_p of the mass, so does what lies above.  A histogram
 //      of them, over the cluster, gives that bound.
 //      Where the bound would leave too much (rows whose mass lies in thousands of tokens, or a
-//      k of thousands) a histogram of all values over -log2 w in steps of 1/32 octave, of
-//      counts or of masses rounded to some 18 bits, finds the step of the border.
-//   3. The values above the bound (of a border's step, those in it, with the exact mass above)
-//      go to the first CTA's list.
+//      k of thousands) a histogram of all values over -log2 w in steps of 1/32 octave finds
+//      the step of the border.  It counts values, which gives the mass of the many small ones
+//      to some 1e-4 of itself, and adds up the masses of the first 8 octaves exactly.
+//   3. The values above the bound (around such a border, those in
+//      its step or two, with the exact mass above) go to lists, which the first CTA gathers.
 //   4. The first CTA, alone: the border among the listed values, the kept ones' masses added to
 //      their pieces, the piece in which the drawn mass falls, and in it the token.
 // Where the list does not hold what it should (thousands of equal values, a border that
@@ -49,7 +50,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kCtasMax = 8;               // of a cluster
 constexpr int kPieces = kCtasMax * kWarps;
 constexpr int kStep = 2;                  // vectors of a lane's step
-constexpr int kAhead = 4;                 // steps on their way
+constexpr int kAhead = 3;                 // steps on their way
 constexpr int kCoarse = 128;              // bins of the lanes' maxima: 64 octaves
 constexpr int kCoarsePer = kCoarse / 32;  // of a lane
 constexpr float kCoarsePerOctave = 2.f;
@@ -57,9 +58,11 @@ constexpr int kBins = 2048;               // bins of all values: 64 octaves
 constexpr int kPer = kBins / kThreads;    // of a thread
 constexpr float kBinsPerOctave = 32.f;
 constexpr int kOctaveBits = 5;
-constexpr int kRest = 256;                // bins whose masses are held exactly: 8 octaves
-constexpr int kList = 4096;               // listed values of a row, in equal shares per CTA
+constexpr int kRest = 256;                // bins whose masses are added up: 8 octaves
+constexpr int kList = 4096;               // listed values of a row
+constexpr int kPart = 1024;               // of a part of the list
 constexpr float kListAim = 3000.f;        // values that a list is expected to hold at most
+constexpr int kSteps = 16;                // steps of a piece whose maxima are kept
 constexpr int kUnit = 43;                 // masses count 2^-43
 constexpr float kNothing = -46.f;         // a height whose mass is 0
 constexpr float kLowest = -3.402823466e38f;
@@ -85,15 +88,16 @@ struct SampleParams {
 
 struct alignas(16) SampleSmem {
   union {
-    uint32_t hist[kBins];                // all values: counts or masses,
+    uint32_t hist[kBins];                // all values: counts, of the first bins masses (top-p),
     uint4 x_lanes[kCtasMax][kCoarse / 2];   // before that what the cluster's CTAs wrote of their `lanes`
   };
-  uint32_t rest[kRest];                  // what the histogram's masses of the first octaves round off
+  uint32_t rest[kRest];                  // low parts of the first octaves' masses
   uint4 lanes[kCoarse / 2];              // the lanes' maxima: counts, masses in 2^-19, two bins each
+  float list_value[kList];               // this CTA's listed values (the first's: all of them, at
+  uint32_t list_index[kList];            // the end), and their places in the row
+  uint16_t step_max[kSteps][kThreads];   // a lane's steps' maxima, rounded up to bf16
   // the first CTA's, written by all of the cluster
-  float list_value[kList];               // listed values,
-  uint32_t list_index[kList];            // their places in the row,
-  uint32_t list_count[kCtasMax];         // and how many each CTA listed
+  uint32_t list_count[kCtasMax];         // values that each CTA listed
   uint4 piece[kPieces];                  // kept mass, mass above the border's step
   uint32_t first[kCtasMax];              // lowest index of the maximum
   // every CTA's, written by all of the cluster
@@ -120,8 +124,8 @@ constexpr int kPer2 = kParts / kThreads;
 struct SearchSmem {
   uint32_t cnt[kParts];
   uint32_t mass[4][kParts];
-  float value[kList];      // the listed values, side by side,
-  uint32_t index[kList];   // and their places in the row
+  float value[2][kPart];   // parts of the list
+  uint32_t index[kPart];
   __device__ __forceinline__ void clear() {
 #pragma unroll 1
     for (int i = int(threadIdx.x); i < kParts * 5 / 4; i += kThreads)
@@ -150,9 +154,9 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
@@ -268,6 +272,11 @@ __device__ __forceinline__ uint32_t ties_of(uint64_t mass, uint64_t w, uint32_t 
   return n + 1;
 }
 
+// The least bf16 value that is not below v.
+__device__ __forceinline__ uint16_t bf16_above(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return uint16_t((b + (b & 0x80000000u ? 0u : 0xffffu)) >> 16);
+}
 __device__ __forceinline__ float largest_below(double t) {
   const float f = __double2float_rd(t);
   return double(f) == t ? nextafterf(f, -INFINITY) : f;
@@ -324,7 +333,7 @@ struct Part {
   }
 };
 
-// A warp's way through its piece [p0, p1): use(v, q) gets kStep vectors of a lane, v, v + 32, ...;
+// A warp's way through its piece [p0, p1): use(t, v, q) gets kStep vectors of a lane's step t, v, v + 32, ...;
 // those past the piece's end hold -inf.  `ring`: this lane's 16 bytes of the warp's ring,
 // whose vectors are 512 bytes apart.  A lane reads only what it copied itself.  started() runs
 // once the first copies are on their way.
@@ -354,7 +363,7 @@ __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p
       if (v + 32 * k >= p1) q[k] = Part<T>::nothing();
       else if (!part.whole(v + 32 * k)) q[k] = part.raw(v + 32 * k);
     }
-    use(v, q);
+    use(t, v, q);
     copy(t + kAhead, slot);   // (past the end: an empty group)
     slot = slot + 1 == kAhead ? 0 : slot + 1;
   }
@@ -363,6 +372,38 @@ __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p
 template <typename T, typename F>
 __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1, F&& use) {
   stream(part, ring, p0, p1, use, [] {});
+}
+
+// The same for those steps only whose maximum `wanted` asks for, where the steps' maxima are kept.
+template <typename T, typename W, typename F>
+__device__ __forceinline__ void visit(const SampleSmem& sm, const Part<T>& part, uint32_t ring, int p0,
+                                      int p1, W&& wanted, F&& use) {
+  const int lane = int(threadIdx.x) & 31, steps = (p1 - p0 + 32 * kStep - 1) / (32 * kStep);
+  if (steps > kSteps) {
+    stream(part, ring, p0, p1, use);
+    return;
+  }
+  uint32_t hits = 0;
+#pragma unroll 4
+  for (int t = 0; t < steps; ++t)
+    hits |= wanted(__uint_as_float(uint32_t(sm.step_max[t][threadIdx.x]) << 16)) ? 1u << t : 0u;
+#pragma unroll 1
+  while (hits) {   // two steps at once, for their loads
+    uint4 q[2][kStep];
+    int at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = hits ? __ffs(hits) - 1 : -1;
+      hits &= hits - 1u;
+      at[h] = t < 0 ? p1 : p0 + lane + 32 * kStep * t;
+#pragma unroll
+      for (int k = 0; k < kStep; ++k)
+        q[h][k] = at[h] + 32 * k < p1 ? part.raw(at[h] + 32 * k) : Part<T>::nothing();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (at[h] < p1) use(0, at[h], q[h]);
+  }
 }
 
 // The functions below are called from several places and kept out of line, and their loops
@@ -480,7 +521,7 @@ __device__ __forceinline__ void tighten(Cut& cut, const Cut& other) {
   if (other.above > cut.above || (other.above == cut.above && other.ties < cut.ties)) cut = other;
 }
 
-// The border among the n listed values (ss.value): `want` of their count, or of their mass,
+// The border among the n listed values: `want` of their count, or of their mass,
 // from the top.  They are cut into parts by height (scale parts an octave, from `base` on),
 // the border's part again, until so few are left in it that one warp compares each with
 // each.  False if the list does not reach that far, or too many different values lie too
@@ -489,7 +530,7 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
                                             float base, float scale, bool by_mass, uint64_t want,
                                             Cut* cut, uint64_t* kept) {
   const int tid = int(threadIdx.x), lane = tid & 31;
-  const float* from = ss.value;
+  const float* from = sm.list_value;
   uint64_t left = want, sum = 0;
 #pragma unroll 1
   for (int level = 0; level < 3; ++level) {
@@ -506,7 +547,8 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
     if (f.bin == kParts) return false;
     left -= by_mass ? f.mass : uint64_t(f.cnt);
     sum += f.mass;
-    float* to = level & 1 ? sm.list_value : reinterpret_cast<float*>(sm.list_index);
+    if (f.in > kPart) return false;
+    float* to = ss.value[level & 1];
 #pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
       const float l = from[i];
@@ -556,6 +598,135 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
   *kept = sum + __shfl_sync(0xffffffffu, over + ties * w, lead);
   __syncthreads();
   return true;
+}
+
+// A token drawn: `w / total` of the kept mass, ln(w) = (l - m) / T.
+__device__ __noinline__ void write_token(const SampleParams& p, int r, uint32_t token, float below,
+                                         uint64_t total) {
+  p.tokens[r] = int32_t(token);
+  if (!p.logprob) return;
+  // near a total of 1 from what it exceeds 1 by
+  const uint64_t one = uint64_t(1) << kUnit;
+  p.logprob[r] = below - (total < 2 * one && total >= one ? log1pf(float(total - one) * 0x1p-43f)
+                                                          : logf(float(total) * 0x1p-43f));
+}
+
+__device__ __forceinline__ uint64_t drawn_mass(float u, uint64_t total) {   // < total
+  const uint64_t u64 = u >= 1.f ? ~uint64_t(0) : (u > 0.f ? __float2ull_rz(u * 0x1p64f) : 0);
+  return __umul64hi(u64, total);
+}
+
+// The whole search by one warp, where at most 32 values are listed: each is compared with
+// each, for its rank and the mass above it, and again for the kept mass before its index.
+__device__ __noinline__ void draw_of_few(const SampleParams& p, const SampleSmem& sm, const Scale s,
+                                         int r, int n, int top_k, float top_p, float min_above,
+                                         uint64_t row_mass, float u, float temp) {
+  const int lane = int(threadIdx.x) & 31;
+  const float l = lane < n ? sm.list_value[lane] : -INFINITY;
+  const uint32_t index = lane < n ? sm.list_index[lane] : 0xffffffffu;
+  const uint64_t w = lane < n ? mass_of(s.weight(l)) : 0;
+  uint32_t rank = 0;
+  uint64_t over = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const float other = __shfl_sync(0xffffffffu, l, j);
+    const uint32_t at = __shfl_sync(0xffffffffu, index, j);
+    const uint64_t w_other = __shfl_sync(0xffffffffu, w, j);
+    if (other > l || (other == l && at < index)) {
+      ++rank;
+      over += w_other;
+    }
+  }
+  bool keep = lane < n && rank < uint32_t(top_k);
+  if (top_p < 1.f) {
+    const uint64_t mass = row_mass ? row_mass : warp_sum(keep ? w : 0);
+    const uint64_t want = top_p > 0.f ? part_of(top_p, mass) : 1u;
+    keep = keep && (over < want || rank == 0);
+  }
+  keep = keep && l > min_above;
+  const uint64_t kept = keep ? w : 0, total = warp_sum(kept), drawn = drawn_mass(u, total);
+  uint64_t before = 0;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const uint32_t at = __shfl_sync(0xffffffffu, index, j);
+    const uint64_t w_other = __shfl_sync(0xffffffffu, kept, j);
+    if (at < index) before += w_other;
+  }
+  if (keep && before <= drawn && drawn < before + kept)   // one lane's
+    write_token(p, r, index, l == s.m ? 0.f : (l - s.m) / temp, total);
+}
+
+// The token among the n listed values, of which `cut` keeps some: the part of the row's
+// indices in which the drawn mass falls, and in it one by one.
+__device__ __noinline__ void draw_in_list(SampleSmem& sm, SearchSmem& ss, const SampleParams& p,
+                                          const Scale s, int r, int n, const Cut cut, float u,
+                                          float temp) {
+  const int tid = int(threadIdx.x);
+  const uint64_t tie_mass = cut.ties ? mass_of(s.weight(cut.above)) : 0;
+  auto tied = [&](uint32_t e) { return uint64_t(e < cut.ties ? e : cut.ties) * tie_mass; };
+  const int shift = max(0, 32 - __clz(uint32_t(p.V - 1) | 1u) - 10);   // 1024 parts at most
+  static_assert(kParts == 1024, "ten bits");
+  ss.clear();
+  if (tid == 0) sm.nlist = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < n; i += kThreads) {   // (cnt: ties)
+    const float l = sm.list_value[i];
+    const int part = int(sm.list_index[i] >> shift);
+    if (l >= cut.above) ss.add(part, l == cut.above ? 1u : 0u, l > cut.above ? mass_of(s.weight(l)) : 0);
+  }
+  __syncthreads();
+  Sums mine = {0, 0};
+#pragma unroll
+  for (int k = 0; k < kPer2; ++k) {
+    mine.mass += ss.sum(tid * kPer2 + k);
+    mine.cnt += ss.cnt[tid * kPer2 + k];
+  }
+  Sums at = block_scan(sm, mine.cnt, mine.mass);
+  if (tid == kThreads - 1) sm.total = at.mass + mine.mass + tied(at.cnt + mine.cnt);
+  __syncthreads();
+  const uint64_t total = sm.total, drawn = drawn_mass(u, total);
+#pragma unroll
+  for (int k = 0; k < kPer2; ++k) {
+    const uint64_t m = ss.sum(tid * kPer2 + k);
+    const uint32_t c = ss.cnt[tid * kPer2 + k];
+    if (drawn >= at.mass + tied(at.cnt) && drawn < at.mass + m + tied(at.cnt + c)) {   // one part
+      sm.f_bin = uint32_t(tid * kPer2 + k);
+      sm.f_mass = at.mass;
+      sm.f_cnt = at.cnt;
+    }
+    at.mass += m;
+    at.cnt += c;
+  }
+  __syncthreads();
+  const int part = int(sm.f_bin);
+#pragma unroll 1
+  for (int i = tid; i < n; i += kThreads)
+    if (int(sm.list_index[i] >> shift) == part && sm.list_value[i] >= cut.above) {
+      const uint32_t to = atomicAdd(&sm.nlist, 1u);   // (a part of 1024 indices at most)
+      ss.value[0][to] = sm.list_value[i];
+      ss.index[to] = sm.list_index[i];
+    }
+  __syncthreads();
+  n = int(sm.nlist);
+#pragma unroll 1
+  for (int i = tid; i < n; i += kThreads) {
+    const float l = ss.value[0][i];
+    const uint32_t index = ss.index[i];
+    uint64_t before = sm.f_mass;
+    uint32_t ties = sm.f_cnt;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j)
+      if (ss.index[j] < index) {
+        const float other = ss.value[0][j];
+        before += other > cut.above ? mass_of(s.weight(other)) : 0;
+        ties += other == cut.above ? 1u : 0u;
+      }
+    const bool tie = l == cut.above;
+    const uint64_t w = tie ? 0 : mass_of(s.weight(l));
+    if (drawn >= before + tied(ties) && drawn < before + w + tied(ties + (tie ? 1u : 0u)))
+      write_token(p, r, index, l == s.m ? 0.f : (l - s.m) / temp, total);
+  }
 }
 
 // The border over a whole row, by one CTA: by height, then, of the border's part, digit by
@@ -665,14 +836,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   bool greedy;
   Mode mode;
   Scale s;
-  stream(part, ring, p0, p1, [&](int, const uint4 (&q)[kStep]) {
-    float x[kStep][kE], most = lane_max;
+  stream(part, ring, p0, p1, [&](int t, int, const uint4 (&q)[kStep]) {
+    float x[kStep][kE], here = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
       unpack<T>(q[k], x[k]);
 #pragma unroll
-      for (int i = 0; i < kE; ++i) most = fmaxf(most, x[k][i]);
+      for (int i = 0; i < kE; ++i) here = fmaxf(here, x[k][i]);
     }
+    if (t < kSteps) sm.step_max[t][tid] = bf16_above(here);
+    const float most = fmaxf(lane_max, here);
     if (!greedy) {
       float sum = 0.f;
 #pragma unroll
@@ -760,8 +933,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     min_above = sm.min_above;
   }
 
-  const uint32_t share = uint32_t(kList / ctas);
-  int border = -1;        // kTopP: the bin of the border, if masses above it were added up
+  int border = -1, border_to = -1;   // kTopP: the bins that may hold the border, if masses are added up above
   float depth = 0.f;      // octaves below the maximum that are listed
   uint64_t row_mass = 0;
   if (!slow) {
@@ -849,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // With a share f of the lanes' maxima above it, the bound has some -ln(1 - f) values
       // above it for every lane.
       const float lanes = float(ctas * kThreads);
-      const bool few = p.V <= share || (bound < kCoarse &&
+      const bool few = p.V <= kList || (bound < kCoarse &&
                                         -__logf(fmaxf(1.f - float(sm.f_cnt) / lanes, 1e-9f)) * lanes < kListAim);
       __syncthreads();
       if (few) {
@@ -859,11 +1031,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0;
         if (tid < kRest) sm.rest[tid] = 0;
         __syncthreads();
-        const int shift = max(32 - __clz(per * kE) - 9, 1);   // a bin's sum fits 32 bits
-        // Weights below (1 - top_p) / V of the row's mass cannot reach the border: all of
-        // them together weigh less than what top_p drops.
-        const float dropped = (1.f - fmaxf(top_p, 0.f)) * (float(row_mass) * 0x1p-43f) / float(p.V) * 0.999f;
-        stream(part, ring, p0, p1, [&](int, const uint4 (&q)[kStep]) {
+        // (weights below (1 - top_p) / V of the row's mass cannot reach the border: all of them
+        // together weigh less than what top_p drops)
+        const float dropped = mode == kTopK ? 0.f : (1.f - fmaxf(top_p, 0.f)) * (float(row_mass) * 0x1p-43f) /
+                                                        float(p.V) * 0.99f;
+        const float lowest = mode == kTopK ? kNothing : fmaxf(__log2f(dropped), kNothing);
+        const uint32_t exact = mode == kTopK ? 0u : uint32_t(kRest);
+        stream(part, ring, p0, p1, [&](int, int, const uint4 (&q)[kStep]) {
 #pragma unroll
           for (int k = 0; k < kStep; ++k) {
             float x[kE];
@@ -872,20 +1046,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             for (int i = 0; i < kE; ++i) {
               const float d = x[i] - top, hh = d * s.c_hi;
               const uint32_t bin = bin_of(hh);
-              if (mode == kTopK) {
-                if (hh > kNothing) atomicAdd(&sm.hist[bin], 1u);   // (of the others any may stay)
-              } else {
-                const float e = sm100::ex2_approx(fmaf(d, s.c_lo, hh));
-                if (e >= dropped) {
-                  const uint32_t w = octave_mass(e, int(bin >> kOctaveBits));
-                  if (bin < kRest) {   // (few, as a rule)
-                    atomicAdd(&sm.hist[bin], w >> shift);
-                    atomicAdd(&sm.rest[bin], w & ((1u << shift) - 1u));
-                  } else {
-                    atomicAdd(&sm.hist[bin], (w + (1u << (shift - 1))) >> shift);
-                  }
-                }
+              uint32_t add = 1u;
+              if (bin < exact) {   // (few, as a rule)
+                const uint32_t w = octave_mass(sm100::ex2_approx(fmaf(d, s.c_lo, hh)), int(bin >> kOctaveBits));
+                atomicAdd(&sm.rest[bin], w & 0xfffu);
+                add = w >> 12;
               }
+              if (hh > lowest) atomicAdd(&sm.hist[bin], add);
             }
           }
         });
@@ -900,108 +1067,96 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
         for (int c = 0; c < kCtasMax; ++c)
           if (c < ctas) { sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w; }
-        uint64_t goal = uint64_t(top_k);
-        if (mode == kTopP) {   // in units of 2^-43
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) sums[k] <<= shift;
-          if (t < kRest) {
-#pragma unroll 1
-            for (int c = 0; c < ctas; ++c) {
-              const uint4 x = ld_cluster_v4(sm100::mapa(smem_u32(sm.rest + t), uint32_t(c)));
-              sums[0] += x.x; sums[1] += x.y; sums[2] += x.z; sums[3] += x.w;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int up = kUnit - 22 - ((t + k) >> kOctaveBits);
-            sums[k] = up >= 0 ? sums[k] << up : sums[k] >> -up;
-          }
-          goal = top_p > 0.f ? part_of(top_p, row_mass) : 1u;
-          goal = goal > 0 ? goal : 1u;
-        }
-        const int bin = find_bin<kPer>(sm, true, goal, [&](int k) {
+        auto sum_of = [&](int k) {
           return Sums{k < 2 ? (k ? sums[1] : sums[0]) : (k == 3 ? sums[3] : sums[2]), 0u};
-        }).bin;
-        if (mode == kTopP)
-          border = bin;
-        else   // (without a border fewer than k values have a mass: all of them are listed)
+        };
+        if (mode == kTopK) {   // (without a border fewer than k values have a mass: all are listed)
+          const int bin = find_bin<kPer>(sm, true, uint64_t(top_k), sum_of).bin;
           depth = bin < kBins ? (float(bin) + 0.5f) / kBinsPerOctave : -kNothing;
+        } else {
+          if (t < kRest) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) sums[k] <<= 12;
+#pragma unroll
+            for (int c = 0; c < kCtasMax; ++c)
+              if (c < ctas) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.rest + t), uint32_t(c)));
+#pragma unroll
+            for (int c = 0; c < kCtasMax; ++c)
+              if (c < ctas) { sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w; }
+          }
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            sums[k] = t < kRest ? sums[k] << (kUnit - 22 - ((t + k) >> kOctaveBits))
+                                : sums[k] * mass_of(exp2f(float(t + k) / -kBinsPerOctave));
+          // the border's bin, and others where 1/8192 of the mass, which the counts may be off
+          // by, may take it to
+          const uint64_t want = top_p > 0.f ? part_of(top_p, row_mass) : 1u;
+          const uint64_t slack = min(want >> 13, (row_mass - min(want, row_mass)) >> 1);
+          border = find_bin<kPer>(sm, true, want > slack ? want - slack : 1u, sum_of).bin;
+          border_to = find_bin<kPer>(sm, true, want + slack, sum_of).bin;
+        }
       }
       reach = depth * 1.00001f / s.c_hi;
     }
 
     // ---- the list, or masses and list
-    const uint32_t to_value = sm100::mapa(smem_u32(sm.list_value + rank * share), 0u);
-    const uint32_t to_index = sm100::mapa(smem_u32(sm.list_index + rank * share), 0u);
     auto list = [&](float x, uint32_t index) {
       const uint32_t n = atomicAdd(&sm.nlist, 1u);
-      if (n < share) {
-        sm100::st_cluster_f32(to_value + 4u * n, x);
-        sm100::st_cluster_u32(to_index + 4u * n, index);
+      if (n < kList) {
+        sm.list_value[n] = x;
+        sm.list_index[n] = index;
       }
     };
     if (border >= 0) {
+      const float upper = (float(border) - 0.5f) / -kBinsPerOctave;
+      const float lower = fmaxf((float(border_to) + 0.5f) / -kBinsPerOctave, kNothing);
       kept = 0;
-      stream(part, ring, p0, p1, [&](int v, const uint4 (&q)[kStep]) {
+      stream(part, ring, p0, p1, [&](int, int v, const uint4 (&q)[kStep]) {
+        float sum = 0.f, sum_kept = 0.f;
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
-          float x[kE], sum = 0.f, sum_kept = 0.f;
+          float x[kE];
           unpack<T>(q[k], x);
 #pragma unroll
           for (int i = 0; i < kE; ++i) {
             const float d = x[i] - top, hh = d * s.c_hi;
-            const uint32_t bin = bin_of(hh);
-            const float e = bin < uint32_t(border) ? sm100::ex2_approx(fmaf(d, s.c_lo, hh)) : 0.f;
+            const float e = hh > upper ? sm100::ex2_approx(fmaf(d, s.c_lo, hh)) : 0.f;
             sum += e;
-            sum_kept += x[i] > min_above ? e : 0.f;
-            if (bin == uint32_t(border) && hh > kNothing) list(x[i], part.index(v + 32 * k, i));
+            if (min_p > 0.f) sum_kept += x[i] > min_above ? e : 0.f;
+            if (hh <= upper && hh > lower) list(x[i], part.index(v + 32 * k, i));
           }
-          over += mass_of(sum);
-          kept += mass_of(sum_kept);
         }
+        over += mass_of(sum);
+        if (min_p > 0.f) kept += mass_of(sum_kept);
       });
-      kept = warp_sum(kept);
       over = warp_sum(over);
+      kept = min_p > 0.f ? warp_sum(kept) : over;
     } else if (mode != kAll) {
       kept = 0;
-      if (lane_max - top >= -reach)   // (a lane whose maximum is not listed has nothing to list)
-      stream(part, ring, p0, p1, [&](int v, const uint4 (&q)[kStep]) {
-        float x[kStep][kE], most = kLowest;
+      visit(sm, part, ring, p0, p1, [&](float most) { return most - top >= -reach; },
+            [&](int, int v, const uint4 (&q)[kStep]) {
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          unpack<T>(q[k], x[k]);
+              for (int k = 0; k < kStep; ++k) {
+                float x[kE];
+                unpack<T>(q[k], x);
 #pragma unroll
-          for (int i = 0; i < kE; ++i) most = fmaxf(most, x[k][i]);
-        }
-        if (most - top >= -reach) {
-#pragma unroll
-          for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < kE; ++i)
-              if (x[k][i] - top >= -reach && x[k][i] > -INFINITY) list(x[k][i], part.index(v + 32 * k, i));
-        }
-      });
+                for (int i = 0; i < kE; ++i)
+                  if (x[i] - top >= -reach && x[i] > -INFINITY) list(x[i], part.index(v + 32 * k, i));
+              }
+            });
     } else if (min_p > 0.f) {
       kept = 0;
-      if (lane_max > min_above)
-      stream(part, ring, p0, p1, [&](int, const uint4 (&q)[kStep]) {
-        float x[kStep][kE], most = -INFINITY;
+      visit(sm, part, ring, p0, p1, [&](float most) { return most > min_above; },
+            [&](int, int, const uint4 (&q)[kStep]) {
 #pragma unroll
-        for (int k = 0; k < kStep; ++k) {
-          unpack<T>(q[k], x[k]);
+              for (int k = 0; k < kStep; ++k) {
+                float x[kE], sum = 0.f;
+                unpack<T>(q[k], x);
 #pragma unroll
-          for (int i = 0; i < kE; ++i) most = fmaxf(most, x[k][i]);
-        }
-        if (most > min_above) {
-#pragma unroll
-          for (int k = 0; k < kStep; ++k) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < kE; ++i) sum += x[k][i] > min_above ? s.plain(x[k][i], top) : 0.f;
-            kept += mass_of(sum);
-          }
-        }
-      });
+                for (int i = 0; i < kE; ++i) sum += x[i] > min_above ? s.plain(x[i], top) : 0.f;
+                kept += mass_of(sum);
+              }
+            });
       kept = warp_sum(kept);
     }
     if (lane == 0)
@@ -1009,8 +1164,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                            uint32_t(kept >> 32), uint32_t(over), uint32_t(over >> 32));
     __syncthreads();
     if (tid == 0) sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.list_count[rank]), 0u), sm.nlist);
-    sm100::cluster_sync();   // (no CTA touches another's memory from here on)
-    if (rank != 0) return;
+    sm100::cluster_sync();
+    if (rank != 0) {   // (the first CTA may read this one's list)
+      if (mode != kAll) {
+        sm100::cluster_arrive_relaxed();
+        sm100::cluster_wait();
+      }
+      return;
+    }
   }
 
   // ---- the first CTA: what is kept of the list
@@ -1019,17 +1180,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   int n = 0;
   if (!slow && mode != kAll) {
     bool ok = true;
-    for (int c = 0; c < ctas; ++c) {   // the lists side by side
-      const int here = int(min(sm.list_count[c], share));
-      ok = ok && sm.list_count[c] <= share;
-#pragma unroll 1
-      for (int i = tid; i < here; i += kThreads) {
-        ss.value[n + i] = sm.list_value[c * share + i];
-        ss.index[n + i] = sm.list_index[c * share + i];
-      }
-      n += here;
+    for (int c = 0; c < ctas; ++c) {
+      ok = ok && sm.list_count[c] <= kList;
+      n += int(min(sm.list_count[c], uint32_t(kList)));
     }
+    ok = ok && n <= kList;
+    if (ok) {   // the lists side by side
+#pragma unroll 1
+      for (int i = int(sm.list_count[0]) + tid; i < n; i += kThreads) {
+        int c = 0, k = i;
+        for (; k >= int(sm.list_count[c]); ++c) k -= int(sm.list_count[c]);
+        sm.list_value[i] = __uint_as_float(ld_cluster(sm100::mapa(smem_u32(sm.list_value + k), uint32_t(c))));
+        sm.list_index[i] = ld_cluster(sm100::mapa(smem_u32(sm.list_index + k), uint32_t(c)));
+      }
+    }
+    sm100::cluster_arrive_relaxed();   // (no CTA touches another's memory from here on)
     __syncthreads();
+    if (ok && n <= 32 && border < 0) {
+      if (warp == 0)
+        draw_of_few(p, sm, s, r, n, mode == kTopK ? top_k : n, top_p, min_above,
+                    mode == kTopK ? 0 : row_mass, u, temp_in);
+      return;
+    }
     uint64_t mass = row_mass;   // of which top-p takes its part
     const float scale = float(kParts) / fmaxf(depth, 1e-3f);
     if (ok && mode == kTopK)   // (fewer than k are listed where no others have a mass)
@@ -1047,8 +1219,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       ok = ok && border_in_list(sm, ss, s, n,
                                 border >= 0 ? (float(border) - 0.5f) / kBinsPerOctave : 0.f,
-                                border >= 0 ? kBinsPerOctave * kParts : scale, true, want - over, &cut,
-                                &mass);
+                                border >= 0 ? kBinsPerOctave * kParts / float(border_to - border + 1) : scale,
+                                true, want - over, &cut, &mass);
+    }
+    if (ok && border < 0) {
+      if (min_p > 0.f && min_above >= cut.above) cut = {min_above, 0u};
+      draw_in_list(sm, ss, p, s, r, n, cut, u, temp_in);
+      return;
     }
     slow = !ok;
   }
@@ -1120,9 +1297,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   } else if (mode != kAll) {
 #pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
-      const float l = ss.value[i];
+      const float l = sm.list_value[i];
       if (l >= cut.above) {
-        const int v = int((ss.index[i] + uint32_t(part.skew)) / uint32_t(kE)), c = v / per;
+        const int v = int((sm.list_index[i] + uint32_t(part.skew)) / uint32_t(kE)), c = v / per;
         const int len = (min((c + 1) * per, nv) - c * per + kWarps - 1) / kWarps;
         const int piece = c * kWarps + (v - c * per) / len;
         if (l > cut.above)
@@ -1157,8 +1334,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (lane >= o) { to.mass += m; to.cnt += c; }
     }
     const uint64_t total = __shfl_sync(0xffffffffu, to.mass + tied(to.cnt), 31);
-    const uint64_t u64 = u >= 1.f ? ~uint64_t(0) : (u > 0.f ? __float2ull_rz(u * 0x1p64f) : 0);
-    const uint64_t drawn = __umul64hi(u64, total);   // < total: the token is the first past it
+    const uint64_t drawn = drawn_mass(u, total);   // the token is the first past it
     uint64_t mass = to.mass - sum.mass;
     uint32_t eq = to.cnt - sum.cnt;
 #pragma unroll
@@ -1188,19 +1364,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // ---- the token in it: a run of vectors per thread, then the run's values one by one.  Sums
   // of other groups of values may leave the drawn mass a rounding past the piece's end: it is
   // then the piece's last kept token.
+  constexpr int kRun = 2;   // vectors of a thread that stay in registers
   const int run = (p1 - p0 + kThreads - 1) / kThreads;
   const int r0 = min(p0 + tid * run, p1), r1 = min(r0 + run, p1);
+  uint4 q[kRun];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) q[k] = r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing();
   uint64_t m = 0;
   uint32_t e = 0, last = 0;
 #pragma unroll 1
-  for (int v = r0; v < r1; ++v) {
+  for (int k = 0; k < run; ++k) {
     float x[kE], sum = 0.f;
-    part.load(v, x);
+    unpack<T>(k < kRun ? (k ? q[1] : q[0]) : (r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing()), x);
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float w = x[i] > cut.above ? s.weight(x[i]) : 0.f;
       sum += w;
-      if (w > 0.f) last = part.index(v, i) + 1;
+      if (w > 0.f) last = part.index(r0 + k, i) + 1;
       e += x[i] == cut.above && cut.ties > 0 ? 1u : 0u;
     }
     m += mass_of(sum);
@@ -1216,18 +1396,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     uint32_t e_run = e;
     bool found = false;
 #pragma unroll 1
-    for (int v = r0; v < r1 && !found; ++v) {
+    for (int k = 0; k < run && !found; ++k) {
       float x[kE], sum = 0.f;
-      part.load(v, x);
+      unpack<T>(k < kRun ? (k ? q[1] : q[0]) : (r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing()), x);
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
         const bool tie = x[i] == cut.above && cut.ties > 0;
         sum += x[i] > cut.above ? s.weight(x[i]) : 0.f;
         e_run += tie ? 1u : 0u;
-        if (tie && e_run <= cut.ties) last = max(last, part.index(v, i) + 1);
+        if (tie && e_run <= cut.ties) last = max(last, part.index(r0 + k, i) + 1);
         if (here && !found && drawn < m_run + mass_of(sum) + tied(e_run)) {
           found = true;
-          sm.pick = part.index(v, i);
+          sm.pick = part.index(r0 + k, i);
           sm.pick_value = x[i];
         }
       }
@@ -1238,15 +1418,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const bool hit = __syncthreads_or(here);
   if (tid == 0) {
     const uint32_t token = hit ? sm.pick : (sm.last ? sm.last - 1 : uint32_t(max(p0 * kE - part.skew, 0)));
-    p.tokens[r] = int32_t(token);
-    if (p.logprob) {
-      // ln(w / total): near a total of 1 from what it exceeds 1 by
-      const uint64_t one = uint64_t(1) << kUnit, total = sm.total;
-      const float ln = total < 2 * one && total >= one ? log1pf(float(total - one) * 0x1p-43f)
-                                                       : logf(float(total) * 0x1p-43f);
-      const float l = hit ? sm.pick_value : value_of(part.row[token]);
-      p.logprob[r] = (l == top ? 0.f : (l - top) / temp_in) - ln;
-    }
+    const float l = hit ? sm.pick_value : value_of(part.row[token]);
+    write_token(p, r, token, l == top ? 0.f : (l - top) / temp_in, sm.total);
   }
 }
 
@@ -1255,6 +1428,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 // The rings, which the search then takes.
 constexpr size_t kRings = size_t(kWarps) * 512 * kStep * kAhead;
 constexpr size_t kSmem = sizeof(SampleSmem) + (kRings > sizeof(SearchSmem) ? kRings : sizeof(SearchSmem));
+constexpr size_t kSmemAlone = 120 * 1024;
 constexpr int64_t kRowsMax = int64_t(1) << 23;
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1263,8 +1437,12 @@ int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stre
   const size_t elem = dtype == VA_F32 ? 4 : 2;
   const int64_t vecs = (p.V * int64_t(elem) + 15) / 16 + 1;
   // As many CTAs per row as leave two on an SM.
+  // And more for long rows: 256 rows of 129280 32-bit logits take 142 us with one CTA each,
+  // 110 with two.
   int ctas = 1;
-  while (ctas < kCtasMax && rows * ctas * 2 <= 2 * num_sms && vecs / ctas > kThreads / 2) ctas *= 2;
+  while (ctas < kCtasMax && vecs / ctas > kThreads / 2 &&
+         (rows * ctas * 2 <= 2 * num_sms || vecs / ctas > 16384))
+    ctas *= 2;
   p.ctas = ctas;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1277,7 +1455,8 @@ int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stre
   memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(unsigned(rows * ctas), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  // (one CTA on an SM where there are enough of them: 17 rows in trees 35 us, two 38)
+  cfg.dynamicSmemBytes = rows * ctas <= num_sms ? kSmemAlone : kSmem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -1306,7 +1485,8 @@ TreeLayout tree_layout(int B, int T) {
 }  // namespace
 
 cudaError_t init_sample() {
-  const int smem = int(kSmem);
+  static_assert(kSmem <= 113 * 1024 && kSmemAlone >= kSmem, "two CTAs on an SM");
+  const int smem = int(kSmemAlone);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<float>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
