@@ -13,23 +13,30 @@
 //
 // One cluster of CTAs per row, a warp per piece of it.
 //   1. Each warp reads its piece (copies into a ring in shared memory, three steps ahead), with
-//      a running maximum and sum per lane.  The cluster exchanges the maximum; the pieces'
-//      masses are then known, and a row without top-k and top-p is done but for 4.  Later
-//      steps read the row again, from L2.
+//      a running maximum and sum per lane, and keeps the maximum of each lane's step of 32
+//      bytes.  The cluster exchanges the maximum; the pieces' masses are then known, and a
+//      row without top-k and top-p is done but for 4.
 //   2. The lanes' maxima are values of the row: where k of them lie above a value, so do the k
 //      largest, and where they hold top_p of the mass, so does what lies above.  A histogram
 //      of them, over the cluster, gives that bound.
 //      Where the bound would leave too much (rows whose mass lies in thousands of tokens, or a
 //      k of thousands) a histogram of all values over -log2 w in steps of 1/32 octave finds
 //      the step of the border.  It counts values, which gives the mass of the many small ones
-//      to some 1e-4 of itself, and adds up the masses of the first 8 octaves exactly.
-//   3. The values above the bound (around such a border, those in
-//      its step or two, with the exact mass above) go to lists, which the first CTA gathers.
-//   4. The first CTA, alone: the border among the listed values, the kept ones' masses added to
-//      their pieces, the piece in which the drawn mass falls, and in it the token.
-// Where the list does not hold what it should (thousands of equal values, a border that
-// rounding put into the next step), and for rows with a maximum beyond 1e30, the first CTA
-// goes through the whole row again, digit by digit of the ordered values.
+//      to some 1e-4 of the row's, and adds up the masses of the first 8 octaves.
+//   3. The values above the bound, from the steps whose maximum lies above it, go to lists, which
+//      the first CTA gathers.  (Around a border from the histogram: those of its step or
+//      two, with the exact mass of what lies above, in another pass over the row.)
+//   4. The first CTA, alone: the border among the listed values, and the token, among what is
+//      kept of them, or in the piece in which the drawn mass falls.
+// Where the list does not hold what it should (thousands of values that lie as close as
+// 1/32 octave), and for rows with NaN or a maximum beyond 1e30, the first CTA goes through the
+// whole row again, digit by digit of the ordered values.
+//
+// What bounds it: 256 rows of 129280 32-bit logits are read at the memory's rate in step 1 (20 us
+// of 39 without filters, one CTA per row); the rest, and all of a small batch, is latency, a
+// dozen exchanges over the block and three over the cluster.  Measured, with the clusters
+// that launch_sample chooses: 1 row of 32000 9.5 us; 64 rows of 129280 without filters 16,
+// with top-k 26, with top-p 49; 256 rows 44, 56 and 98, mixed 89.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -89,7 +96,7 @@ struct SampleParams {
 struct alignas(16) SampleSmem {
   union {
     uint32_t hist[kBins];                // all values: counts, of the first bins masses (top-p),
-    uint4 x_lanes[kCtasMax][kCoarse / 2];   // before that what the cluster's CTAs wrote of their `lanes`
+    uint4 x_lanes[kCtasMax][kCoarse / 2];   // before that the `lanes` of the cluster's CTAs
   };
   uint32_t rest[kRest];                  // low parts of the first octaves' masses
   uint4 lanes[kCoarse / 2];              // the lanes' maxima: counts, masses in 2^-19, two bins each
@@ -115,7 +122,7 @@ struct alignas(16) SampleSmem {
   uint32_t s_cnt[kWarps];
   uint32_t piece_ties[kPieces];
   uint32_t f_bin, f_cnt, f_in;
-  uint64_t f_mass;
+  uint64_t f_mass, f_here;
 };
 // Where the first CTA searches, over the rings: counts of parts, and their
 // masses (44 bits) in four pieces of 11 bits, whose sums over a row of 2^20 fit 32.
@@ -333,8 +340,8 @@ struct Part {
   }
 };
 
-// A warp's way through its piece [p0, p1): use(t, v, q) gets kStep vectors of a lane's step t, v, v + 32, ...;
-// those past the piece's end hold -inf.  `ring`: this lane's 16 bytes of the warp's ring,
+// A warp's way through its piece [p0, p1): use(t, v, q) gets the kStep vectors of a lane's step
+// t, v, v + 32, ...; those past the piece's end hold -inf.  `ring`: this lane's 16 bytes of the warp's ring,
 // whose vectors are 512 bytes apart.  A lane reads only what it copied itself.  started() runs
 // once the first copies are on their way.
 template <typename T, typename F, typename S>
@@ -374,7 +381,8 @@ __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p
   stream(part, ring, p0, p1, use, [] {});
 }
 
-// The same for those steps only whose maximum `wanted` asks for, where the steps' maxima are kept.
+// The same for those steps only whose maximum `wanted` asks for, where the steps' maxima are
+// kept (pieces of 16 steps at most).
 template <typename T, typename W, typename F>
 __device__ __forceinline__ void visit(const SampleSmem& sm, const Part<T>& part, uint32_t ring, int p0,
                                       int p1, W&& wanted, F&& use) {
@@ -472,11 +480,12 @@ struct Found {
   int bin;         // (past the last: none)
   uint32_t cnt;    // above it
   uint64_t mass;
-  uint32_t in;     // values in it
+  uint32_t in;     // values in it,
+  uint64_t here;   // and their mass
 };
 
-// Where the count, or the mass, from the top reaches `want` (>= 1): this thread has kPer bins in
-// a row, whose counts and masses get(k) gives; `none` if it is not reached.
+// Where the count, or the mass, from the top reaches `want` (>= 1): this thread has kN bins in a
+// row, whose counts and masses get(k) gives.
 template <int kN, typename F>
 __device__ __forceinline__ Found find_bin(SampleSmem& sm, bool by_mass, uint64_t want, F&& get) {
   if (threadIdx.x == 0) sm.f_bin = kN * kThreads;
@@ -498,6 +507,7 @@ __device__ __forceinline__ Found find_bin(SampleSmem& sm, bool by_mass, uint64_t
         sm.f_cnt = at.cnt;
         sm.f_mass = at.mass;
         sm.f_in = b.cnt;
+        sm.f_here = b.mass;
         break;
       }
       at.cnt += b.cnt;
@@ -505,7 +515,7 @@ __device__ __forceinline__ Found find_bin(SampleSmem& sm, bool by_mass, uint64_t
     }
   }
   __syncthreads();
-  const Found f = {int(sm.f_bin), sm.f_cnt, sm.f_mass, sm.f_in};
+  const Found f = {int(sm.f_bin), sm.f_cnt, sm.f_mass, sm.f_in, sm.f_here};
   __syncthreads();
   return f;
 }
@@ -524,14 +534,15 @@ __device__ __forceinline__ void tighten(Cut& cut, const Cut& other) {
 // The border among the n listed values: `want` of their count, or of their mass,
 // from the top.  They are cut into parts by height (scale parts an octave, from `base` on),
 // the border's part again, until so few are left in it that one warp compares each with
-// each.  False if the list does not reach that far, or too many different values lie too
-// close (equal ones may be any number).  *kept: mass down to the cut.  The cut is tightened.
+// each, or all are equal.  False if the list does not reach that far, or more than kPart
+// different values lie in a part.  *kept: mass down to the cut.  The cut is tightened.
 __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, const Scale s, int n,
                                             float base, float scale, bool by_mass, uint64_t want,
                                             Cut* cut, uint64_t* kept) {
   const int tid = int(threadIdx.x), lane = tid & 31;
   const float* from = sm.list_value;
   uint64_t left = want, sum = 0;
+  uint32_t within = 0;   // equal values, where there are many
 #pragma unroll 1
   for (int level = 0; level < 3; ++level) {
     auto part_of_list = [&](float l) {
@@ -547,32 +558,31 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
     if (f.bin == kParts) return false;
     left -= by_mass ? f.mass : uint64_t(f.cnt);
     sum += f.mass;
-    if (f.in > kPart) return false;
+    // the part's values, side by side, and whether they differ
     float* to = ss.value[level & 1];
+    float most = -INFINITY, least = INFINITY;
 #pragma unroll 1
     for (int i = tid; i < n; i += kThreads) {
       const float l = from[i];
-      if (part_of_list(l) == f.bin) to[atomicAdd(&sm.nlist, 1u)] = l;
+      if (part_of_list(l) != f.bin) continue;
+      const uint32_t at = atomicAdd(&sm.nlist, 1u);
+      if (at < kPart) to[at] = l;
+      most = fmaxf(most, l);
+      least = fminf(least, l);
     }
     n = int(f.in);
     from = to;
     __syncthreads();
     if (n <= 32) break;
+    most = block_max(sm, most);
+    if (block_max(sm, -least) == -most) {
+      within = uint32_t(n);
+      n = 1;
+      break;
+    }
+    if (n > kPart || level == 2) return false;
     base += float(f.bin) / scale;
     scale *= float(kParts);
-  }
-  uint32_t within = 0;   // equal ones, where there are many
-  if (n > 32) {
-    float most = -INFINITY, least = INFINITY;
-#pragma unroll 1
-    for (int i = tid; i < n; i += kThreads) {
-      most = fmaxf(most, from[i]);
-      least = fminf(least, from[i]);
-    }
-    most = block_max(sm, most);
-    if (block_max(sm, -least) != -most) return false;
-    within = uint32_t(n);
-    n = 1;
   }
   // every warp finds the same: values above this lane's, and equal to it
   const float mine = lane < n ? from[lane] : -INFINITY;
@@ -590,7 +600,6 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
   const uint64_t before = by_mass ? over : over_n, all = by_mass ? eq * w : uint64_t(eq);
   const uint32_t who = __ballot_sync(0xffffffffu, lane < n && before < left && left <= before + all);
   if (who == 0) return false;
-  // (a mass of a few whole units: 32 bits of quotient are enough, see ties_of)
   const uint32_t ties = by_mass ? ties_of(left - before, w, eq) : uint32_t(left - before);
   const int lead = __ffs(who) - 1;
   const Cut found = {__shfl_sync(0xffffffffu, mine, lead), __shfl_sync(0xffffffffu, ties, lead)};
@@ -933,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     min_above = sm.min_above;
   }
 
-  int border = -1, border_to = -1;   // kTopP: the bins that may hold the border, if masses are added up above
+  int border = -1, border_to = -1;   // kTopP: bins that may hold the border, from the histogram
   float depth = 0.f;      // octaves below the maximum that are listed
   uint64_t row_mass = 0;
   if (!slow) {
@@ -1035,7 +1044,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         // together weigh less than what top_p drops)
         const float dropped = mode == kTopK ? 0.f : (1.f - fmaxf(top_p, 0.f)) * (float(row_mass) * 0x1p-43f) /
                                                         float(p.V) * 0.99f;
-        const float lowest = mode == kTopK ? kNothing : fmaxf(__log2f(dropped), kNothing);
+        // (nor does it lie below the bound, if there was one)
+        const int bins = bound < kCoarse ? int(float(bound + 1) * (kBinsPerOctave / kCoarsePerOctave)) + 1 : kBins;
+        const float lowest = fmaxf(mode == kTopK ? kNothing : __log2f(dropped),
+                                   fmaxf(float(bins) / -kBinsPerOctave, kNothing));
         const uint32_t exact = mode == kTopK ? 0u : uint32_t(kRest);
         stream(part, ring, p0, p1, [&](int, int, const uint4 (&q)[kStep]) {
 #pragma unroll
@@ -1062,11 +1074,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         uint4 w[kCtasMax];
 #pragma unroll
         for (int c = 0; c < kCtasMax; ++c)
-          if (c < ctas) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.hist + t), uint32_t(c)));
+          if (c < ctas && t < bins) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.hist + t), uint32_t(c)));
         uint64_t sums[kPer] = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < kCtasMax; ++c)
-          if (c < ctas) { sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w; }
+          if (c < ctas && t < bins) {
+            sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w;
+          }
         auto sum_of = [&](int k) {
           return Sums{k < 2 ? (k ? sums[1] : sums[0]) : (k == 3 ? sums[3] : sums[2]), 0u};
         };
@@ -1092,8 +1106,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           // by, may take it to
           const uint64_t want = top_p > 0.f ? part_of(top_p, row_mass) : 1u;
           const uint64_t slack = min(want >> 13, (row_mass - min(want, row_mass)) >> 1);
-          border = find_bin<kPer>(sm, true, want > slack ? want - slack : 1u, sum_of).bin;
-          border_to = find_bin<kPer>(sm, true, want + slack, sum_of).bin;
+          const Found f = find_bin<kPer>(sm, true, want > slack ? want - slack : 1u, sum_of);
+          border = border_to = f.bin;
+          if (f.bin < kBins && f.mass + f.here < want + slack)
+            border_to = find_bin<kPer>(sm, true, want + slack, sum_of).bin;
         }
       }
       reach = depth * 1.00001f / s.c_hi;

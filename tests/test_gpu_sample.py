@@ -231,6 +231,53 @@ def test_many_equal_among_different(va):
         assert not got[p == 0].any() or "top_p" in kw
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("V,sigma", [(50000, 0.3), (129280, 1.0), (129281, 2.0), (262144, 1.5)])
+def test_borders_among_thousands_of_tokens(va, V, sigma, dtype):
+    """Rows whose mass lies in thousands of tokens: tokens for evenly spread uniforms follow the
+    shares, to BOUND of the mass (a border may lie off by that much, too: 2 BOUND and one
+    token at either end), and only kept tokens come."""
+    g = torch.Generator().manual_seed(V)
+    row = (sigma * torch.randn(V, generator=g)).to(dtype)
+    n = 400
+    for kw in (dict(top_p=0.5), dict(top_p=0.9), dict(top_p=0.99), dict(top_p=0.9, min_p=0.01),
+               dict(temperature=1.7, top_p=0.95), dict(top_k=3000), dict(top_k=3000, top_p=0.8),
+               dict(top_k=V // 3), dict(top_k=V // 3, top_p=0.6, min_p=0.002)):
+        p = shares(row, **kw)
+        got = stretches(va, row, n, **kw)
+        token = p[p > 0].max()
+        assert np.abs(np.cumsum(got) / n - np.cumsum(p)).max() <= 1 / n + 4 * BOUND + token, kw
+        stray = np.flatnonzero((p == 0) & (got > 0))
+        if "top_p" not in kw:
+            assert stray.size == 0, kw
+        elif stray.size:     # beyond the border by no more than BOUND of the mass
+            l = row.double().numpy() / kw.get("temperature", 1.0)
+            w = np.exp(l - l.max())
+            between = (l >= l[stray].min()) & (p == 0)
+            assert w[between].sum() <= 4 * BOUND * w.sum() + w[between].max(), kw
+
+
+@pytest.mark.parametrize("V", [3000, 6000, 20000])
+@pytest.mark.parametrize("levels", [2, 5])
+def test_few_different_logits(va, V, levels):
+    """Hundreds to thousands of ties at every border."""
+    n = 40
+    g = torch.Generator().manual_seed(V + levels)
+    row = torch.randint(0, levels, (n, V), generator=g).float() * 0.5
+    s = settings(n, 50)
+    s["temperature"] = [t or 1.0 for t in s["temperature"]]
+    check(va, row, np.random.default_rng(51).random(n).tolist(), sure=0.5, **s)
+
+
+def test_likely_tokens_at_one_end_of_the_row(va):
+    """Token ids sorted by frequency: all that is listed lies in the first part of the row."""
+    V, n = 60000, 24
+    row = model_logits(n, V, 52).sort(-1, descending=True)[0]
+    s = settings(n, 53)
+    check(va, row, np.random.default_rng(54).random(n).tolist(), **s)
+    check(va, row.flip(-1).contiguous(), np.random.default_rng(55).random(n).tolist(), **s)
+
+
 def test_masked_rows(va):
     V = 3000
     row = torch.full((8, V), -INF)
