@@ -61,7 +61,8 @@ struct HeadParams {
   uint32_t items;
   int rot_offset, pairs;
   int before;          // copied items in front of the rotated ones
-  uint32_t rows_ahead;   // rows of 32 items where these are whole rows and no more than a token has, or 0
+  // rows of 32 items where these are whole rows and no more than a token has, or 0
+  uint32_t rows_ahead;
   float cos_amp, sin_amp;   // amplitude, with the sign of the direction
 };
 
@@ -83,7 +84,9 @@ __device__ __forceinline__ float to_f32(T v);
 template <>
 __device__ __forceinline__ float to_f32<float>(float v) { return v; }
 template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
 template <>
 __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
 template <typename T>
@@ -91,7 +94,9 @@ __device__ __forceinline__ T from_f32(float v);
 template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
@@ -401,9 +406,9 @@ __device__ __forceinline__ void write_row(const RowParams& p, const Freq& f) {
 
 // The rows' blocks, then those of the queries (bf16, 64 rotary columns).
 template <typename T, bool kInterleaved, int kN, int kK>
-__global__ void __launch_bounds__(kRopeThreads) append_rows_kernel(const __grid_constant__ RowParams r,
-                                                                   const __grid_constant__ HeadParams p,
-                                                                   const __grid_constant__ Freq f) {
+__global__ void __launch_bounds__(kRopeThreads)
+    append_rows_kernel(const __grid_constant__ RowParams r, const __grid_constant__ HeadParams p,
+                       const __grid_constant__ Freq f) {
   griddep_wait();
   griddep_launch_dependents();
   if (blockIdx.x < r.blocks)
@@ -513,7 +518,8 @@ HeadParams head_params(const HeadArgs& h, int unit, const int32_t* positions, fl
   p.rot_offset = off;
   p.before = unit > 1 ? off / (2 * unit) : off;
   p.per_row = fast_div(uint32_t(unit > 1 ? width / (2 * unit) : width - p.pairs));
-  p.rows_ahead = 32 % p.per_row.d == 0 && 32 / p.per_row.d <= uint32_t(h.heads) ? 32 / p.per_row.d : 0;
+  const uint32_t ahead = 32 % p.per_row.d == 0 ? 32 / p.per_row.d : 0;
+  p.rows_ahead = ahead <= uint32_t(h.heads) ? ahead : 0;
   p.cos_amp = amplitude;
   p.sin_amp = inverse ? -amplitude : amplitude;
   return p;
@@ -536,11 +542,13 @@ int launch_rope(const HeadParams& p, const Freq& f, va_stream_t stream) {
 }
 
 template <typename T>
-int launch_rope(const HeadParams& p, const Freq& f, bool interleaved, bool vec, va_stream_t stream) {
+int launch_rope(const HeadParams& p, const Freq& f, bool interleaved, bool vec,
+                va_stream_t stream) {
   if (vec)
     return interleaved ? launch_rope<T, true, kUnit / 2>(p, f, stream)
                        : launch_rope<T, false, kUnit / 2>(p, f, stream);
-  return interleaved ? launch_rope<T, true, 1>(p, f, stream) : launch_rope<T, false, 1>(p, f, stream);
+  return interleaved ? launch_rope<T, true, 1>(p, f, stream)
+                     : launch_rope<T, false, 1>(p, f, stream);
 }
 
 // All tokens' heads, in launches of kItemsMax items at most.
@@ -572,7 +580,8 @@ int run_heads(const HeadArgs& h, int dtype, const int32_t* positions, const Freq
 template <typename T, bool kInterleaved>
 int launch_append(const RowParams& r, const HeadParams& p, const Freq& f, va_stream_t stream) {
   if (p.items < kManyItems)
-    return launch(append_rows_kernel<T, kInterleaved, kUnit / 2, 1>, r.blocks + blocks_of<1>(p.items),
+    return launch(append_rows_kernel<T, kInterleaved, kUnit / 2, 1>,
+                  r.blocks + blocks_of<1>(p.items),
                   stream, r, p, f);
   return launch(append_rows_kernel<T, kInterleaved, kUnit / 2, 4>, r.blocks + blocks_of<4>(p.items),
                 stream, r, p, f);
@@ -669,7 +678,8 @@ VA_API int va_kv_append_paged(void* kv_pool, int64_t num_slots, int64_t kv_row_s
                               const void* kv_new, int64_t new_row_stride, int dtype,
                               const void* norm_weight, float eps, const int32_t* slots,
                               const int32_t* positions, int64_t tokens, const double* inv_freq,
-                              float amplitude, int flags, const void* q_pe, int64_t q_pe_token_stride,
+                              float amplitude, int flags, const void* q_pe,
+                              int64_t q_pe_token_stride,
                               int64_t q_pe_head_stride, void* q_out, int64_t q_out_token_stride,
                               int64_t q_out_head_stride, int heads, uint32_t* status,
                               va_stream_t stream) {

@@ -99,7 +99,8 @@ struct alignas(16) SampleSmem {
     uint4 x_lanes[kCtasMax][kCoarse / 2];   // before that the `lanes` of the cluster's CTAs
   };
   uint32_t rest[kRest];                  // low parts of the first octaves' masses
-  uint4 lanes[kCoarse / 2];              // the lanes' maxima: counts, masses in 2^-19, two bins each
+  // the lanes' maxima: counts, masses in 2^-19, two bins each
+  uint4 lanes[kCoarse / 2];
   float list_value[kList];               // this CTA's listed values (the first's: all of them, at
   uint32_t list_index[kList];            // the end), and their places in the row
   uint16_t step_max[kSteps][kThreads];   // a lane's steps' maxima, rounded up to bf16
@@ -245,7 +246,8 @@ struct Scale {
 // A height's bin among kBins, the nearest multiple of 1/32 octave (by the rounding of a sum
 // with 2^23), and a bin's octave.
 __device__ __forceinline__ uint32_t bin_of(float h) {
-  return min(__float_as_uint(fmaf(h, -kBinsPerOctave, 8388608.f)) - 0x4b000000u, uint32_t(kBins - 1));
+  return min(__float_as_uint(fmaf(h, -kBinsPerOctave, 8388608.f)) - 0x4b000000u,
+             uint32_t(kBins - 1));
 }
 
 // A weight, or a sum of a few, in units of 2^-43.
@@ -341,9 +343,9 @@ struct Part {
 };
 
 // A warp's way through its piece [p0, p1): use(t, v, q) gets the kStep vectors of a lane's step
-// t, v, v + 32, ...; those past the piece's end hold -inf.  `ring`: this lane's 16 bytes of the warp's ring,
-// whose vectors are 512 bytes apart.  A lane reads only what it copied itself.  started() runs
-// once the first copies are on their way.
+// t, v, v + 32, ...; those past the piece's end hold -inf.  `ring`: this lane's 16 bytes of the
+// warp's ring, whose vectors are 512 bytes apart.  A lane reads only what it copied itself.
+// started() runs once the first copies are on their way.
 template <typename T, typename F, typename S>
 __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1, F&& use,
                                        S&& started) {
@@ -352,7 +354,8 @@ __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
       const int v = p0 + lane + 32 * (kStep * t + k);
-      if (v < p1 && part.whole(v)) sm100::cp_async16(ring + 512u * uint32_t(kStep * slot + k), part.at(v), 16u);
+      if (v < p1 && part.whole(v))
+        sm100::cp_async16(ring + 512u * uint32_t(kStep * slot + k), part.at(v), 16u);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -377,15 +380,16 @@ __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p
 }
 
 template <typename T, typename F>
-__device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1, F&& use) {
+__device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1,
+                                       F&& use) {
   stream(part, ring, p0, p1, use, [] {});
 }
 
 // The same for those steps only whose maximum `wanted` asks for, where the steps' maxima are
 // kept (pieces of 16 steps at most).
 template <typename T, typename W, typename F>
-__device__ __forceinline__ void visit(const SampleSmem& sm, const Part<T>& part, uint32_t ring, int p0,
-                                      int p1, W&& wanted, F&& use) {
+__device__ __forceinline__ void visit(const SampleSmem& sm, const Part<T>& part, uint32_t ring,
+                                      int p0, int p1, W&& wanted, F&& use) {
   const int lane = int(threadIdx.x) & 31, steps = (p1 - p0 + 32 * kStep - 1) / (32 * kStep);
   if (steps > kSteps) {
     stream(part, ring, p0, p1, use);
@@ -552,7 +556,8 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
     if (tid == 0) sm.nlist = 0;
     __syncthreads();
 #pragma unroll 1
-    for (int i = tid; i < n; i += kThreads) ss.add(part_of_list(from[i]), 1u, mass_of(s.weight(from[i])));
+    for (int i = tid; i < n; i += kThreads)
+      ss.add(part_of_list(from[i]), 1u, mass_of(s.weight(from[i])));
     __syncthreads();
     const Found f = find_part(sm, ss, by_mass, left);
     if (f.bin == kParts) return false;
@@ -598,7 +603,8 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
   }
   eq = within ? within : eq;
   const uint64_t before = by_mass ? over : over_n, all = by_mass ? eq * w : uint64_t(eq);
-  const uint32_t who = __ballot_sync(0xffffffffu, lane < n && before < left && left <= before + all);
+  const bool is = lane < n && before < left && left <= before + all;
+  const uint32_t who = __ballot_sync(0xffffffffu, is);
   if (who == 0) return false;
   const uint32_t ties = by_mass ? ties_of(left - before, w, eq) : uint32_t(left - before);
   const int lead = __ffs(who) - 1;
@@ -682,7 +688,8 @@ __device__ __noinline__ void draw_in_list(SampleSmem& sm, SearchSmem& ss, const 
   for (int i = tid; i < n; i += kThreads) {   // (cnt: ties)
     const float l = sm.list_value[i];
     const int part = int(sm.list_index[i] >> shift);
-    if (l >= cut.above) ss.add(part, l == cut.above ? 1u : 0u, l > cut.above ? mass_of(s.weight(l)) : 0);
+    if (l >= cut.above)
+      ss.add(part, l == cut.above ? 1u : 0u, l > cut.above ? mass_of(s.weight(l)) : 0);
   }
   __syncthreads();
   Sums mine = {0, 0};
@@ -809,7 +816,8 @@ __device__ __noinline__ void border_of_row(SampleSmem& sm, SearchSmem& ss, const
 enum Mode { kAll, kTopK, kTopP };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2)
+    sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SampleSmem& sm = *reinterpret_cast<SampleSmem*>(smem_raw);
   constexpr int kE = Part<T>::kE;
@@ -896,9 +904,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (slow && rank != 0) return;
 
   if (greedy) {   // the lowest index of the largest
+    uint32_t first = 0xffffffffu;
+    auto look = [&](int v, const uint4& q) {
+      float x[kE];
+      unpack<T>(q, x);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const uint32_t index = part.index(v, i);   // (past the row: elements outside it)
+        if (fmaxf(x[i], -INFINITY) == top && index < uint32_t(p.V)) first = min(first, index);
+      }
+    };
     if (slow) {
-      part.v0 = 0;
-      part.v1 = nv;
       top = -INFINITY;
       for (int v = tid; v < nv; v += kThreads) {
         float x[kE];
@@ -907,14 +923,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         for (int i = 0; i < kE; ++i) top = fmaxf(top, x[i]);
       }
       top = block_max(sm, top);
-    }
-    uint32_t first = 0xffffffffu;
-    for (int v = part.v0 + tid; v < part.v1 && first == 0xffffffffu; v += kThreads) {
-      float x[kE];
-      part.load(v, x);
+      for (int v = tid; v < nv; v += kThreads) look(v, part.raw(v));
+    } else {
+      visit(sm, part, ring, p0, p1, [&](float most) { return most >= top; },
+            [&](int, int v, const uint4 (&q)[kStep]) {
 #pragma unroll
-      for (int j = kE - 1; j >= 0; --j)
-        if (x[j] == top && part.index(v, j) < uint32_t(p.V)) first = part.index(v, j);
+              for (int k = 0; k < kStep; ++k) look(v + 32 * k, q[k]);
+            });
     }
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) sm.w_eq[warp] = first;
@@ -995,17 +1010,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         uint32_t c_at = c1, m_at = m1;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t x = __shfl_up_sync(0xffffffffu, c_at, o), y = __shfl_up_sync(0xffffffffu, m_at, o);
+          const uint32_t x = __shfl_up_sync(0xffffffffu, c_at, o);
+          const uint32_t y = __shfl_up_sync(0xffffffffu, m_at, o);
           if (lane >= o) { c_at += x; m_at += y; }
         }
         c_at -= c1;
         m_at -= m1;
         // (weights round down here, and sums elsewhere by 2^-23: a little more is asked for)
         uint32_t want = uint32_t(top_k);
-        if (mode == kTopP)
-          want = top_p > 0.f ? uint32_t(min((part_of(top_p, row_mass) >> (kUnit - 19)) * 65537 / 65536 + 2,
-                                            uint64_t(0xffffffffu)))
-                             : 1u;
+        if (mode == kTopP) {
+          const uint64_t part_p = top_p > 0.f ? part_of(top_p, row_mass) : 0;
+          want = uint32_t(min((part_p >> (kUnit - 19)) * 65537 / 65536 + 2, uint64_t(~0u)));
+        }
         if (lane == 0) sm.f_bin = kCoarse;
         __syncwarp();
         const uint32_t before = mode == kTopK ? c_at : m_at, mine = mode == kTopK ? c1 : m1;
@@ -1030,8 +1046,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       // With a share f of the lanes' maxima above it, the bound has some -ln(1 - f) values
       // above it for every lane.
       const float lanes = float(ctas * kThreads);
-      const bool few = p.V <= kList || (bound < kCoarse &&
-                                        -__logf(fmaxf(1.f - float(sm.f_cnt) / lanes, 1e-9f)) * lanes < kListAim);
+      const float below = fmaxf(1.f - float(sm.f_cnt) / lanes, 1e-9f);
+      const bool few = p.V <= kList || (bound < kCoarse && -__logf(below) * lanes < kListAim);
       __syncthreads();
       if (few) {
         depth = bound < kCoarse ? float(bound + 1) / kCoarsePerOctave : -kNothing;
@@ -1042,10 +1058,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         __syncthreads();
         // (weights below (1 - top_p) / V of the row's mass cannot reach the border: all of them
         // together weigh less than what top_p drops)
-        const float dropped = mode == kTopK ? 0.f : (1.f - fmaxf(top_p, 0.f)) * (float(row_mass) * 0x1p-43f) /
-                                                        float(p.V) * 0.99f;
+        const float share = (1.f - fmaxf(top_p, 0.f)) * 0.99f / float(p.V);
+        const float dropped = mode == kTopK ? 0.f : float(row_mass) * 0x1p-43f * share;
         // (nor does it lie below the bound, if there was one)
-        const int bins = bound < kCoarse ? int(float(bound + 1) * (kBinsPerOctave / kCoarsePerOctave)) + 1 : kBins;
+        constexpr int kFine = int(kBinsPerOctave / kCoarsePerOctave);
+        const int bins = bound < kCoarse ? (bound + 1) * kFine + 1 : kBins;
         const float lowest = fmaxf(mode == kTopK ? kNothing : __log2f(dropped),
                                    fmaxf(float(bins) / -kBinsPerOctave, kNothing));
         const uint32_t exact = mode == kTopK ? 0u : uint32_t(kRest);
@@ -1060,7 +1077,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
               const uint32_t bin = bin_of(hh);
               uint32_t add = 1u;
               if (bin < exact) {   // (few, as a rule)
-                const uint32_t w = octave_mass(sm100::ex2_approx(fmaf(d, s.c_lo, hh)), int(bin >> kOctaveBits));
+                const float e = sm100::ex2_approx(fmaf(d, s.c_lo, hh));
+                const uint32_t w = octave_mass(e, int(bin >> kOctaveBits));
                 atomicAdd(&sm.rest[bin], w & 0xfffu);
                 add = w >> 12;
               }
@@ -1074,7 +1092,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         uint4 w[kCtasMax];
 #pragma unroll
         for (int c = 0; c < kCtasMax; ++c)
-          if (c < ctas && t < bins) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.hist + t), uint32_t(c)));
+          if (c < ctas && t < bins)
+            w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.hist + t), uint32_t(c)));
         uint64_t sums[kPer] = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < kCtasMax; ++c)
@@ -1096,7 +1115,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
               if (c < ctas) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.rest + t), uint32_t(c)));
 #pragma unroll
             for (int c = 0; c < kCtasMax; ++c)
-              if (c < ctas) { sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w; }
+              if (c < ctas) {
+                sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w;
+              }
           }
 #pragma unroll
           for (int k = 0; k < kPer; ++k)
@@ -1157,7 +1178,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 unpack<T>(q[k], x);
 #pragma unroll
                 for (int i = 0; i < kE; ++i)
-                  if (x[i] - top >= -reach && x[i] > -INFINITY) list(x[i], part.index(v + 32 * k, i));
+                  if (x[i] - top >= -reach && x[i] > -INFINITY)
+                    list(x[i], part.index(v + 32 * k, i));
               }
             });
     } else if (min_p > 0.f) {
@@ -1175,9 +1197,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             });
       kept = warp_sum(kept);
     }
-    if (lane == 0)
-      sm100::st_cluster_v4(sm100::mapa(smem_u32(&sm.piece[rank * kWarps + warp]), 0u), uint32_t(kept),
-                           uint32_t(kept >> 32), uint32_t(over), uint32_t(over >> 32));
+    if (lane == 0) {
+      const uint32_t to = sm100::mapa(smem_u32(&sm.piece[rank * kWarps + warp]), 0u);
+      sm100::st_cluster_v4(to, uint32_t(kept), uint32_t(kept >> 32), uint32_t(over),
+                           uint32_t(over >> 32));
+    }
     __syncthreads();
     if (tid == 0) sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.list_count[rank]), 0u), sm.nlist);
     sm100::cluster_sync();
@@ -1206,8 +1230,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int i = int(sm.list_count[0]) + tid; i < n; i += kThreads) {
         int c = 0, k = i;
         for (; k >= int(sm.list_count[c]); ++c) k -= int(sm.list_count[c]);
-        sm.list_value[i] = __uint_as_float(ld_cluster(sm100::mapa(smem_u32(sm.list_value + k), uint32_t(c))));
-        sm.list_index[i] = ld_cluster(sm100::mapa(smem_u32(sm.list_index + k), uint32_t(c)));
+        const uint32_t value = sm100::mapa(smem_u32(sm.list_value + k), uint32_t(c));
+        const uint32_t index = sm100::mapa(smem_u32(sm.list_index + k), uint32_t(c));
+        sm.list_value[i] = __uint_as_float(ld_cluster(value));
+        sm.list_index[i] = ld_cluster(index);
       }
     }
     sm100::cluster_arrive_relaxed();   // (no CTA touches another's memory from here on)
@@ -1233,10 +1259,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         over = block_sum(sm, over);
         ok = border < kBins && want > over;
       }
-      ok = ok && border_in_list(sm, ss, s, n,
-                                border >= 0 ? (float(border) - 0.5f) / kBinsPerOctave : 0.f,
-                                border >= 0 ? kBinsPerOctave * kParts / float(border_to - border + 1) : scale,
-                                true, want - over, &cut, &mass);
+      float base = 0.f, parts = scale;   // of an octave
+      if (border >= 0) {
+        base = (float(border) - 0.5f) / kBinsPerOctave;
+        parts = kBinsPerOctave * kParts / float(border_to - border + 1);
+      }
+      ok = ok && border_in_list(sm, ss, s, n, base, parts, true, want - over, &cut, &mass);
     }
     if (ok && border < 0) {
       if (min_p > 0.f && min_above >= cut.above) cut = {min_above, 0u};
@@ -1386,12 +1414,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   uint4 q[kRun];
 #pragma unroll
   for (int k = 0; k < kRun; ++k) q[k] = r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing();
+  auto vector = [&](int k) {
+    if (k < kRun) return k ? q[1] : q[0];
+    return r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing();
+  };
   uint64_t m = 0;
   uint32_t e = 0, last = 0;
 #pragma unroll 1
   for (int k = 0; k < run; ++k) {
     float x[kE], sum = 0.f;
-    unpack<T>(k < kRun ? (k ? q[1] : q[0]) : (r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing()), x);
+    unpack<T>(vector(k), x);
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float w = x[i] > cut.above ? s.weight(x[i]) : 0.f;
@@ -1414,7 +1446,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll 1
     for (int k = 0; k < run && !found; ++k) {
       float x[kE], sum = 0.f;
-      unpack<T>(k < kRun ? (k ? q[1] : q[0]) : (r0 + k < r1 ? part.raw(r0 + k) : Part<T>::nothing()), x);
+      unpack<T>(vector(k), x);
 #pragma unroll
       for (int i = 0; i < kE; ++i) {
         const bool tie = x[i] == cut.above && cut.ties > 0;
@@ -1433,7 +1465,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (last) atomicMax(&sm.last, last);
   const bool hit = __syncthreads_or(here);
   if (tid == 0) {
-    const uint32_t token = hit ? sm.pick : (sm.last ? sm.last - 1 : uint32_t(max(p0 * kE - part.skew, 0)));
+    const uint32_t begin = uint32_t(max(p0 * kE - part.skew, 0));
+    const uint32_t token = hit ? sm.pick : (sm.last ? sm.last - 1 : begin);
     const float l = hit ? sm.pick_value : value_of(part.row[token]);
     write_token(p, r, token, l == top ? 0.f : (l - top) / temp_in, sm.total);
   }
@@ -1443,7 +1476,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 // The rings, which the search then takes.
 constexpr size_t kRings = size_t(kWarps) * 512 * kStep * kAhead;
-constexpr size_t kSmem = sizeof(SampleSmem) + (kRings > sizeof(SearchSmem) ? kRings : sizeof(SearchSmem));
+constexpr size_t kSmem =
+    sizeof(SampleSmem) + (kRings > sizeof(SearchSmem) ? kRings : sizeof(SearchSmem));
 constexpr size_t kSmemAlone = 120 * 1024;
 constexpr int64_t kRowsMax = int64_t(1) << 23;
 
@@ -1620,6 +1654,6 @@ VA_API int va_tree_accept_sampled(const void* root_logits, const void* logits, i
   a.accept_nodes = accept_nodes;
   a.accept_slots = accept_slots;
   a.bonus = bonus_token;
-  return launch_accept_walk(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? VA_OK
-                                                                                       : VA_ERR_LAUNCH;
+  const cudaError_t e = launch_accept_walk(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VA_OK : VA_ERR_LAUNCH;
 }
