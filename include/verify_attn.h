@@ -590,7 +590,8 @@ int va_kv_evict(const int32_t *slot_idx, const int32_t *kv_indptr, const int32_t
  *                  |f| < 2^40), read during the call (a captured call keeps them).
  *                  Angles are exact to 2^-60 of a turn at every position.
  *   0 <= tokens < 2^31 (0: x, out and positions may be NULL), 1 <= heads <= 65535,
- *   1 <= width <= 2^20, rot_dim even, 2 <= rot_dim <= VA_ROPE_DIM_MAX.
+ *   1 <= width <= 2^20, heads * width <= 2^30, rot_dim even, 2 <= rot_dim <= VA_ROPE_DIM_MAX;
+ *   no tensor spans more than 2^50 elements.
  * Computed in 32 bits, rounded once to the type of out.  One launch (two or more past 2^30
  * groups of 16 bytes).
  */
@@ -640,7 +641,7 @@ int va_rope_inv_freq(int rot_dim, double base, int scaling, double factor, int64
  *   kv_pool        bf16 [num_slots, kv_row_stride], as for the attention calls, num_slots < 2^31;
  *                  columns from 576 on are left.
  *   kv_new         [tokens, 576] of the type dtype, rows new_row_stride elements apart,
- *                  16-byte aligned (rows too).
+ *                  16-byte aligned (rows too); not part of the pool.
  *   norm_weight    [512] of the type dtype, 16-byte aligned, or NULL; eps >= 0.
  *   slots          int32 [tokens] device, distinct where they lie inside the pool (of two
  *                  rows for one slot, parts of either may stay).  A row whose slot lies
@@ -676,7 +677,8 @@ int va_kv_append_paged(void *kv_pool, int64_t num_slots, int64_t kv_row_stride,
  * (they share the mass).  A row without a value above -inf gets token 0, logprob -inf, and
  * sets VA_STATUS_EMPTY_ROW.
  *   logits       [rows, V] of the type dtype (VA_F32, VA_BF16, VA_F16), rows row_stride
- *                elements apart (0 <= row_stride <= 2^40), aligned to the type.
+ *                elements apart (0 <= row_stride <= 2^40, rows * row_stride <= 2^50), aligned
+ *                to the type.
  *   temperature  float [rows] device, or NULL (1).   top_k  int32 [rows] or NULL (all).
  *   top_p, min_p float [rows] device, or NULL (all).  NaN: all.
  *   uniform      float [rows] device, in [0, 1) (NaN and below 0 count as 0; at 1 or above
@@ -687,8 +689,8 @@ int va_kv_append_paged(void *kv_pool, int64_t num_slots, int64_t kv_row_stride,
  *   0 <= rows <= 2^23, 1 <= V <= VA_SAMPLE_V_MAX.
  * Masses are summed as whole numbers of 2^-43 (a weight below half of that has none), so
  * the result does not depend on the order of sums: the same call gives the same token.
- * One launch; each logit is read from memory once (rows of more than 300k 32-bit logits:
- * several times).
+ * One launch; each logit is read from memory once, and again, from L2 as a rule, where a
+ * border of top-k or top-p asks for it.  Settings and logits must not change during the call.
  */
 #define VA_SAMPLE_V_MAX (1 << 20)
 int va_sample(const void *logits, int64_t row_stride, int dtype, int64_t rows, int64_t V,

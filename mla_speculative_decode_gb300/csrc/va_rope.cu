@@ -469,12 +469,17 @@ struct HeadArgs {
 };
 
 constexpr int64_t kStrideMax = int64_t(1) << 40;
+constexpr int64_t kSpanMax = int64_t(1) << 50;   // elements from a tensor's first to its last
+
+bool stride_ok(int64_t n, int64_t stride) {
+  return stride >= 0 && stride <= kStrideMax && (stride == 0 || n - 1 <= kSpanMax / stride);
+}
 
 int check_heads(const HeadArgs& h) {
-  if (h.x_token < 0 || h.x_head < 0 || h.out_token < 0 || h.out_head < 0 ||
-      h.x_token > kStrideMax || h.x_head > kStrideMax || h.out_token > kStrideMax ||
-      h.out_head > kStrideMax)
+  if (!stride_ok(h.tokens, h.x_token) || !stride_ok(h.heads, h.x_head) ||
+      !stride_ok(h.tokens, h.out_token) || !stride_ok(h.heads, h.out_head))
     return VA_ERR_SHAPE;
+  if (h.heads * h.width > kItemsMax) return VA_ERR_SHAPE;   // (one token is at most a launch)
   if (!rows_apart(h.tokens, h.out_token, h.heads, h.out_head, h.width)) return VA_ERR_SHAPE;
   if (!aligned_to(h.x, h.elem) || !aligned_to(h.out, h.elem)) return VA_ERR_ALIGN;
   return VA_OK;
@@ -689,8 +694,8 @@ VA_API int va_kv_append_paged(void* kv_pool, int64_t num_slots, int64_t kv_row_s
   if (heads > 0 && tokens != 0 && (!q_pe || !q_out)) return VA_ERR_NULL;
   const size_t elem = dtype == VA_F32 ? 4 : 2;
   if (tokens < 0 || tokens > 0x7fffffff || num_slots < 1 || num_slots > 0x7fffffff ||
-      kv_row_stride < VA_D_QK || kv_row_stride > kStrideMax || new_row_stride < 0 ||
-      new_row_stride > kStrideMax || dtype < VA_F32 || dtype > VA_F16 || heads < 0 ||
+      kv_row_stride < VA_D_QK || !stride_ok(num_slots, kv_row_stride) ||
+      !stride_ok(tokens, new_row_stride) || dtype < VA_F32 || dtype > VA_F16 || heads < 0 ||
       heads > 65535 || flags < 0 || flags > VA_ROPE_INTERLEAVED || !isfinite(amplitude) ||
       !(eps >= 0.f) || !isfinite(eps))
     return VA_ERR_SHAPE;

@@ -1557,7 +1557,8 @@ VA_API int va_sample(const void* logits, int64_t row_stride, int dtype, int64_t 
   using namespace va;
   if (rows != 0 && (!logits || !uniform || !tokens)) return VA_ERR_NULL;
   if (rows < 0 || rows > kRowsMax || V < 1 || V > VA_SAMPLE_V_MAX || dtype < VA_F32 ||
-      dtype > VA_F16 || row_stride < 0 || row_stride > (int64_t(1) << 40))
+      dtype > VA_F16 || row_stride < 0 || row_stride > (int64_t(1) << 40) ||
+      rows * (row_stride >> 10) > (int64_t(1) << 40))   // (a tensor of 2^50 elements)
     return VA_ERR_SHAPE;
   const size_t elem = dtype == VA_F32 ? 4 : 2;
   if (!aligned_to(logits, elem) || !aligned_to(temperature, 4) || !aligned_to(top_k, 4) ||

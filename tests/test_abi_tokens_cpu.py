@@ -39,6 +39,10 @@ def rope(lib, **over):
     (dict(amp=float("nan")), -2), (dict(freq=ctypes.addressof(BAD)), -2),
     (dict(freq=ctypes.addressof(HUGE)), -2),
     (dict(xt=-1), -2), (dict(oh=-1), -2), (dict(xt=(1 << 40) + 1), -2),
+    # one token is at most a launch; a tensor spans at most 2^50 elements
+    (dict(heads=65535, width=16385, xh=16385, oh=16385, xt=1 << 31, ot=1 << 31), -2),
+    (dict(tokens=2 ** 31 - 1, xt=1 << 20), -2), (dict(tokens=2 ** 31 - 1, ot=1 << 20), -2),
+    (dict(heads=65535, xh=1 << 35, ot=1 << 30), -2),
     (dict(oh=63), -2), (dict(ot=511), -2), (dict(oh=0), -2), (dict(ot=0), -2),
     (dict(ot=64, oh=64), -2), (dict(ot=64, oh=319), -2),
     (dict(x=A16 + 1), -3), (dict(out=A16 + 1), -3), (dict(pos=A16 + 2), -3),
@@ -52,7 +56,8 @@ def test_rope_errors(lib, over, code):
     dict(), dict(dtype=0), dict(dtype=2, flags=3), dict(x=A16 + 2), dict(xt=0, xh=0),
     dict(tokens=0, x=None, out=None, pos=None), dict(ot=64, oh=320), dict(tokens=1, ot=0),
     dict(heads=1, oh=0, ot=64), dict(width=65, off=1, xh=65, oh=65, ot=520), dict(rot=2),
-    dict(width=256, rot=256, xh=256, oh=256, xt=2048, ot=2048), dict(tokens=2 ** 31 - 1)])
+    dict(width=256, rot=256, xh=256, oh=256, xt=2048, ot=2048), dict(tokens=2 ** 31 - 1),
+    dict(heads=65535, width=16384, xh=16384, oh=16384, xt=1 << 31, ot=1 << 31)])
 def test_good_rope_calls_end_at_the_device_check(lib, over):
     assert rope(lib, **over) in (-5, -7)
 
@@ -70,6 +75,7 @@ APPEND = dict(pool=A16, num_slots=100, stride=576, kv=A16, row=576, dtype=1, w=A
     (dict(heads=-1), -2), (dict(heads=65536), -2), (dict(flags=2), -2), (dict(eps=-1.0), -2),
     (dict(eps=float("nan")), -2), (dict(amp=float("inf")), -2),
     (dict(freq=ctypes.addressof(BAD)), -2), (dict(qoh=32), -2), (dict(qt=-1), -2),
+    (dict(num_slots=2 ** 31 - 1, stride=1 << 20), -2), (dict(tokens=2 ** 31 - 1, row=1 << 20), -2),
     (dict(stride=580), -3), (dict(row=580), -3), (dict(pool=A16 + 8), -3), (dict(kv=A16 + 8), -3),
     (dict(w=A16 + 8), -3), (dict(slots=A16 + 2), -3), (dict(pos=A16 + 1), -3),
     (dict(status=A16 + 2), -3), (dict(q=A16 + 1), -3), (dict(qo=A16 + 1), -3),
@@ -131,7 +137,7 @@ SAMPLE = dict(logits=A16, stride=1000, dtype=0, rows=3, V=1000, t=A16, k=A16, p=
     (dict(logits=None), -1), (dict(u=None), -1), (dict(tok=None), -1),
     (dict(rows=-1), -2), (dict(rows=(1 << 23) + 1), -2), (dict(V=0), -2),
     (dict(V=(1 << 20) + 1), -2), (dict(dtype=3), -2), (dict(dtype=-1), -2), (dict(stride=-1), -2),
-    (dict(stride=(1 << 40) + 1), -2),
+    (dict(stride=(1 << 40) + 1), -2), (dict(rows=1 << 23, stride=1 << 30), -2),
     (dict(logits=A16 + 2), -3), (dict(dtype=1, logits=A16 + 1), -3), (dict(t=A16 + 2), -3),
     (dict(k=A16 + 2), -3), (dict(p=A16 + 2), -3), (dict(m=A16 + 2), -3), (dict(u=A16 + 2), -3),
     (dict(tok=A16 + 2), -3), (dict(lp=A16 + 2), -3), (dict(status=A16 + 2), -3),
