@@ -427,7 +427,8 @@ bool set_freq(const double* inv_freq, int pairs, Freq* f) {
     const double x = inv_freq[i];
     if (!(fabs(x) < 0x1p40)) return false;
     const double hi = x * kHi, lo = fma(x, kHi, -hi) + x * kLo;
-    f->turn[i] = uint64_t((hi - floor(hi)) * 0x1p64) + uint64_t(int64_t(lo * 0x1p64));
+    const double part = hi - floor(hi);   // (1 for a negative trifle)
+    f->turn[i] = (part < 1.0 ? uint64_t(part * 0x1p64) : 0) + uint64_t(int64_t(lo * 0x1p64));
   }
   return true;
 }

@@ -61,14 +61,13 @@ constexpr int kAhead = 3;                 // steps on their way
 constexpr int kCoarse = 128;              // bins of the lanes' maxima: 64 octaves
 constexpr int kCoarsePer = kCoarse / 32;  // of a lane
 constexpr float kCoarsePerOctave = 2.f;
-constexpr int kBins = 2048;               // bins of all values: 64 octaves
-constexpr int kPer = kBins / kThreads;    // of a thread
-constexpr float kBinsPerOctave = 32.f;
-constexpr int kOctaveBits = 5;
-constexpr int kRest = 256;                // bins whose masses are added up: 8 octaves
+constexpr int kBins = 512;                // bins of all values: one per thread
+constexpr int kColumns = 16;              // counters of a bin, by lane
+constexpr int kLevels = 3;                // ever finer bins
 constexpr int kList = 4096;               // listed values of a row
 constexpr int kPart = 1024;               // of a part of the list
 constexpr float kListAim = 3000.f;        // values that a list is expected to hold at most
+constexpr uint32_t kListFull = 3500u;     // or is counted to
 constexpr int kSteps = 16;                // steps of a piece whose maxima are kept
 constexpr int kUnit = 43;                 // masses count 2^-43
 constexpr float kNothing = -46.f;         // a height whose mass is 0
@@ -95,14 +94,19 @@ struct SampleParams {
 
 struct alignas(16) SampleSmem {
   union {
-    uint32_t hist[kBins];                // all values: counts, of the first bins masses (top-p),
-    uint4 x_lanes[kCtasMax][kCoarse / 2];   // before that the `lanes` of the cluster's CTAs
+    uint4 x_lanes[kCtasMax][kCoarse / 2];   // the `lanes` of the cluster's CTAs, after that
+    uint32_t x_finer[kLevels - 1][kBins];   // the bins' counts of later levels
   };
-  uint32_t rest[kRest];                  // low parts of the first octaves' masses
+  uint32_t x_bins[kBins];                // the bins' counts, added up by all of the cluster
   // the lanes' maxima: counts, masses in 2^-19, two bins each
   uint4 lanes[kCoarse / 2];
-  float list_value[kList];               // this CTA's listed values (the first's: all of them, at
-  uint32_t list_index[kList];            // the end), and their places in the row
+  union {
+    struct {
+      float list_value[kList];           // this CTA's listed values (the first's: all of them, at
+      uint32_t list_index[kList];        // the end), and their places in the row
+    };
+    uint32_t bins[kBins][kColumns];      // before that
+  };
   uint16_t step_max[kSteps][kThreads];   // a lane's steps' maxima, rounded up to bf16
   // the first CTA's, written by all of the cluster
   uint32_t list_count[kCtasMax];         // values that each CTA listed
@@ -111,6 +115,7 @@ struct alignas(16) SampleSmem {
   // every CTA's, written by all of the cluster
   float x_max[kCtasMax];
   uint2 x_total[kCtasMax];               // mass
+  uint2 x_over[kLevels][kCtasMax];       // what lies above a level's bins
   // within the CTA
   uint32_t nlist, last, pick;
   float pick_value;
@@ -122,7 +127,7 @@ struct alignas(16) SampleSmem {
   uint64_t s_mass[kWarps];
   uint32_t s_cnt[kWarps];
   uint32_t piece_ties[kPieces];
-  uint32_t f_bin, f_cnt, f_in;
+  uint32_t f_bin, f_cnt, f_in, f_to;
   uint64_t f_mass, f_here;
 };
 // Where the first CTA searches, over the rings: counts of parts, and their
@@ -153,19 +158,14 @@ struct SearchSmem {
 
 // ------------------------------------------------------------- small pieces
 
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void red_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v)
+               : "memory");
 }
 __device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
@@ -227,6 +227,28 @@ __device__ __forceinline__ float down_value(uint32_t key) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+__device__ __forceinline__ uint64_t pair(float2 v) {
+  return uint64_t(__float_as_uint(v.x)) | (uint64_t(__float_as_uint(v.y)) << 32);
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+  return unpair(r);
+}
+
 // What a row's weights are made of.
 struct Scale {
   float m, c_hi, c_lo;
@@ -242,14 +264,13 @@ struct Scale {
     const float x = l - from;
     return sm100::ex2_approx(fmaf(x, c_lo, x * c_hi));
   }
+  // the same, two at once
+  __device__ __forceinline__ float2 plain(float2 l, float from) const {
+    const float2 x = add2(l, make_float2(-from, -from));
+    const float2 h = fma2(x, make_float2(c_lo, c_lo), mul2(x, make_float2(c_hi, c_hi)));
+    return make_float2(sm100::ex2_approx(h.x), sm100::ex2_approx(h.y));
+  }
 };
-// A height's bin among kBins, the nearest multiple of 1/32 octave (by the rounding of a sum
-// with 2^23), and a bin's octave.
-__device__ __forceinline__ uint32_t bin_of(float h) {
-  return min(__float_as_uint(fmaf(h, -kBinsPerOctave, 8388608.f)) - 0x4b000000u,
-             uint32_t(kBins - 1));
-}
-
 // A weight, or a sum of a few, in units of 2^-43.
 __device__ __forceinline__ uint64_t mass_of(float e) {
   const uint32_t b = __float_as_uint(e);
@@ -258,13 +279,6 @@ __device__ __forceinline__ uint64_t mass_of(float e) {
   if (up >= 0) return f << up;
   return up < -32 ? 0 : (f + (uint64_t(1) << (-up - 1))) >> -up;
 }
-// A weight in units of 2^-(22 + octave): 2^22 or a little more for one of that octave.
-__device__ __forceinline__ uint32_t octave_mass(float e, int octave) {
-  const uint32_t b = __float_as_uint(e);
-  const float v = b < 0x00800000u ? 0.f : __uint_as_float(b + (uint32_t(octave) << 23));
-  return __float_as_uint(fminf(v, 1.9f) + 2.f) - 0x40000000u;
-}
-
 // The least whole number not below p * mass, 0 < p < 1.
 __device__ __forceinline__ uint64_t part_of(float p, uint64_t mass) {
   const uint64_t q = __float2ull_rz(p * 0x1p63f);
@@ -305,14 +319,20 @@ struct Part {
   const T* row;       // element 0
   int64_t V;
   int skew;           // elements between the boundary and the row
+  int w0, w1;         // vectors without elements outside the row
   int v0, v1;
+  __device__ __forceinline__ void of(const T* r, int64_t n) {
+    row = r;
+    V = n;
+    skew = int((reinterpret_cast<uintptr_t>(r) / sizeof(T)) % kE);
+    w0 = skew ? 1 : 0;
+    w1 = int((n + skew) / kE);
+  }
   __device__ static __forceinline__ uint4 nothing() {   // a vector of -inf
     const uint32_t w = sizeof(T) == 4 ? 0xff800000u : (minus_inf_bits<T>() * 0x10001u);
     return make_uint4(w, w, w, w);
   }
-  __device__ __forceinline__ bool whole(int v) const {   // no element of v outside the row
-    return v * kE >= skew && int64_t(v) * kE + kE - skew <= V;
-  }
+  __device__ __forceinline__ bool whole(int v) const { return v >= w0 && v < w1; }
   __device__ __forceinline__ const T* at(int v) const { return row + (int64_t(v) * kE - skew); }
   __device__ __forceinline__ uint4 raw(int v) const {
     if (whole(v)) return *reinterpret_cast<const uint4*>(at(v));
@@ -349,33 +369,40 @@ struct Part {
 template <typename T, typename F, typename S>
 __device__ __forceinline__ void stream(const Part<T>& part, uint32_t ring, int p0, int p1, F&& use,
                                        S&& started) {
+  constexpr uint32_t kBytes = 512u * kStep;   // of a warp's step
   const int lane = int(threadIdx.x) & 31, steps = (p1 - p0 + 32 * kStep - 1) / (32 * kStep);
-  auto copy = [&](int t, int slot) {
+  // the whole vectors of the piece (the row's first and last may not be)
+  const int c0 = max(p0, part.w0);
+  const uint32_t count = uint32_t(max(min(p1, part.w1) - c0, 0));
+  uint32_t from = uint32_t(p0 + lane - c0);
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(part.at(p0 + lane));
+  auto copy = [&](uint32_t slot) {
 #pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      const int v = p0 + lane + 32 * (kStep * t + k);
-      if (v < p1 && part.whole(v))
-        sm100::cp_async16(ring + 512u * uint32_t(kStep * slot + k), part.at(v), 16u);
-    }
+    for (int k = 0; k < kStep; ++k)
+      if (from + uint32_t(32 * k) < count) sm100::cp_async16(slot + 512u * uint32_t(k),
+                                                             src + 512 * k, 16u);
     asm volatile("cp.async.commit_group;" ::: "memory");
+    from += 32u * kStep;
+    src += kBytes;
   };
 #pragma unroll
-  for (int t = 0; t < kAhead; ++t) copy(t, t);
+  for (int t = 0; t < kAhead; ++t) copy(ring + kBytes * uint32_t(t));
   started();
+  uint32_t slot = ring, here = uint32_t(p0 + lane - c0);
 #pragma unroll 1
-  for (int t = 0, slot = 0; t < steps; ++t) {
+  for (int t = 0; t < steps; ++t, here += 32u * kStep) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
-    const int v = p0 + lane + 32 * kStep * t;
+    const int v = int(here) + c0;
     uint4 q[kStep];
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
-      q[k] = sm100::ld_shared_v4(ring + 512u * uint32_t(kStep * slot + k));
-      if (v + 32 * k >= p1) q[k] = Part<T>::nothing();
-      else if (!part.whole(v + 32 * k)) q[k] = part.raw(v + 32 * k);
+      q[k] = sm100::ld_shared_v4(slot + 512u * uint32_t(k));
+      if (here + uint32_t(32 * k) >= count)
+        q[k] = v + 32 * k < p1 ? part.raw(v + 32 * k) : Part<T>::nothing();
     }
     use(t, v, q);
-    copy(t + kAhead, slot);   // (past the end: an empty group)
-    slot = slot + 1 == kAhead ? 0 : slot + 1;
+    copy(slot);   // (past the end: an empty group)
+    slot = slot == ring + kBytes * (kAhead - 1) ? ring : slot + kBytes;
   }
 }
 
@@ -536,7 +563,7 @@ __device__ __forceinline__ void tighten(Cut& cut, const Cut& other) {
 }
 
 // The border among the n listed values: `want` of their count, or of their mass,
-// from the top.  They are cut into parts by height (scale parts an octave, from `base` on),
+// from the top.  They are cut into parts by distance (`scale` parts to 1, from `base` down),
 // the border's part again, until so few are left in it that one warp compares each with
 // each, or all are equal.  False if the list does not reach that far, or more than kPart
 // different values lie in a part.  *kept: mass down to the cut.  The cut is tightened.
@@ -550,7 +577,7 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
 #pragma unroll 1
   for (int level = 0; level < 3; ++level) {
     auto part_of_list = [&](float l) {
-      return int(fminf(fmaxf((-s.height(l) - base) * scale, 0.f), float(kParts - 1)));
+      return int(fminf(fmaxf((base - l) * scale, 0.f), float(kParts - 1)));
     };
     ss.clear();
     if (tid == 0) sm.nlist = 0;
@@ -586,7 +613,7 @@ __device__ __noinline__ bool border_in_list(SampleSmem& sm, SearchSmem& ss, cons
       break;
     }
     if (n > kPart || level == 2) return false;
-    base += float(f.bin) / scale;
+    base -= float(f.bin) / scale;
     scale *= float(kParts);
   }
   // every warp finds the same: values above this lane's, and equal to it
@@ -811,6 +838,167 @@ __device__ __noinline__ void border_of_row(SampleSmem& sm, SearchSmem& ss, const
   *kept = sum + found.ties * w;
 }
 
+// What is listed: x_lo < x <= x_hi.  Where a window was found among the bins of top-p, the
+// border lies in it, and masses above it are added up; otherwise x_hi is infinite.
+struct Window {
+  float x_hi, x_lo;
+  bool found, lost;
+};
+
+// A value of a lane's step.
+template <typename T>
+__device__ __forceinline__ float pick(const uint4 (&q)[kStep], int i) {
+  static_assert(kStep == 2, "eight words");
+  const int w = i * int(sizeof(T)) / 4;
+  const uint32_t a = w & 1 ? (w & 2 ? q[0].w : q[0].y) : (w & 2 ? q[0].z : q[0].x);
+  const uint32_t b = w & 1 ? (w & 2 ? q[1].w : q[1].y) : (w & 2 ? q[1].z : q[1].x);
+  const uint32_t word = w & 4 ? b : a;
+  float x[16 / sizeof(T)];
+  unpack<T>(make_uint4(word, 0u, 0u, 0u), x);
+  return sizeof(T) == 2 && (i & 1) ? x[1] : x[0];
+}
+
+// The cluster's search for the border in bins of all values, from `deep` octaves below the
+// maximum on at most.
+//
+// A level counts the values of x_lo < x <= x_hi in 511 equal bins (the last is for others), and adds up what lies above
+// x_hi.  Counters are kept by lane, 16 for a bin: additions of a warp then meet in few banks
+// (512 bins of one counter each take 10 values a clock, these 20; 1024 of 8 columns 11).
+// For top-p a count takes its values to weigh what the bin's middle does.  Values above 2^-12 of
+// the row's mass lie above the first bins: there are fewer than 4096 of them, so that all can be
+// listed where the border lies among them, and what is left is off by less than 2^-12 of the
+// row's mass (a bin is 1/30 octave wide or so: 0.6 % of a weight in the mean, times
+// sqrt(2^-12)).  The border's bin, and others where that may take it to, are the next
+// level's range, until they hold so few values that these fit the list.
+template <typename T>
+__device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& part, uint32_t ring,
+                                              int p0, int p1, const Scale& s, int ctas, int rank,
+                                              bool by_count, int top_k, float top_p,
+                                              uint64_t row_mass, float deep) {
+  constexpr int kE = Part<T>::kE;
+  static_assert(kBins == kThreads && kColumns == 16, "a bin and its counters for every thread");
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const float top = s.m, mass = float(row_mass) * 0x1p-43f;
+  uint64_t want = by_count ? uint64_t(top_k) : (top_p > 0.f ? part_of(top_p, row_mass) : 1u);
+  want = want > 0 ? want : 1u;
+  float x_hi = INFINITY, base = top;
+  if (!by_count) {
+    // (weights below (1 - top_p) / V of the row's mass cannot reach the border: all of them
+    // together weigh less than what top_p drops)
+    const float share = (1.f - fmaxf(top_p, 0.f)) * 0.99f / float(part.V);
+    deep = fminf(deep + 0.1f, fmaxf(-__log2f(mass * share), 0.f));
+    const float heavy = 12.f - __log2f(mass);
+    if (heavy > 0.f) base = x_hi = top - heavy / s.c_hi;
+    deep -= fmaxf(heavy, 0.f);
+  }
+  deep = fminf(fmaxf(deep, 0x1p-5f), -kNothing);
+  float unit = deep / (float(kBins - 2) * s.c_hi);   // a bin's width
+  float x_lo = -INFINITY;
+  for (int i = tid; i < kBins * (kLevels - 1); i += kThreads) (&sm.x_finer[0][0])[i] = 0;
+#pragma unroll 1
+  for (int level = 0;; ++level) {
+#pragma unroll
+    for (int i = 0; i < kColumns / 4; ++i)
+      reinterpret_cast<uint4*>(&sm.bins[0][0])[tid + kThreads * i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    // A value's bin is the nearest multiple of `unit`, by the rounding of a sum with 2^23.
+    constexpr uint32_t kZero = 0x4b000000u;
+    const float per_unit = 1.f / unit;
+    const uint32_t to = smem_u32(&sm.bins[0][lane % kColumns]);
+    float sum = 0.f;   // (counts, too: a lane has some hundred values)
+    stream(part, ring, p0, p1, [&](int, int, const uint4 (&q)[kStep]) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        float x[kE];
+        unpack<T>(q[k], x);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          // (every lane adds, to the last bin what is none: under a condition it takes twice as
+          // long)
+          const uint32_t bin = min(
+              __float_as_uint(fmaf(base - x[i], per_unit, 8388608.f)) - kZero, uint32_t(kBins - 1));
+          const bool above = x[i] > x_hi;
+          if (above) mask |= 1u << (k * kE + i);
+          asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(
+                           to + (above ? uint32_t(kBins - 1) : bin) * uint32_t(kColumns * 4))
+                       : "memory");
+        }
+      }
+      float e = 0.f;
+#pragma unroll 1
+      for (; mask; mask &= mask - 1u)   // (few, as a rule)
+        e += by_count ? 1.f : s.plain(pick<T>(q, __ffs(mask) - 1), top);
+      sum += e;
+    });
+    uint64_t over = warp_sum(by_count ? uint64_t(sum) : mass_of(sum));
+    if (lane == 0) sm.s_mass[warp] = over;
+    __syncthreads();
+    // to every CTA: what lies above, and the bins' counts
+    uint32_t* total = level == 0 ? sm.x_bins : sm.x_finer[level - 1];
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < kColumns / 4; ++i) {
+      const uint4 c = *reinterpret_cast<const uint4*>(&sm.bins[tid][(i + tid / 2) * 4 % kColumns]);
+      n += c.x + c.y + c.z + c.w;
+    }
+    if (n && tid < kBins - 1)
+      for (int c = 0; c < ctas; ++c)
+        red_cluster(sm100::mapa(smem_u32(total + tid), uint32_t(c)), n);
+    if (tid < ctas) {
+      over = 0;
+      for (int w = 0; w < kWarps; ++w) over += sm.s_mass[w];
+      st_cluster_v2(sm100::mapa(smem_u32(&sm.x_over[level][rank]), uint32_t(tid)), uint32_t(over),
+                    uint32_t(over >> 32));
+    }
+    sm100::cluster_sync();
+    over = 0;
+    for (int c = 0; c < ctas; ++c)
+      over += uint64_t(sm.x_over[level][c].x) | (uint64_t(sm.x_over[level][c].y) << 32);
+    if (over >= want) {   // among the heaviest (or, later, lost to roundings)
+      return {INFINITY, x_hi, true, level > 0};
+    }
+    n = total[tid];
+    const uint64_t one = by_count ? 1u : mass_of(s.plain(base - float(tid) * unit, top));
+    const Sums at = block_scan(sm, n, n * one);
+    if (tid == kThreads - 1) sm.total = at.mass + n * one;
+    if (tid == 0) { sm.f_bin = kBins; sm.f_to = kBins - 1; }
+    __syncthreads();
+    // what the sums may be off by
+    uint64_t slack = 0;
+    if (!by_count)
+      slack = level == 0 ? row_mass >> (deep > 20.f ? 10 : 12) : (sm.total >> 12) + (row_mass >> 23);
+    const uint64_t least = want - over > slack ? want - over - slack : 1u, most = want - over + slack;
+    const uint64_t end = at.mass + n * one;
+    if (at.mass < least && least <= end) {
+      sm.f_bin = uint32_t(tid);
+      sm.f_cnt = at.cnt;
+    }
+    if (at.mass < most && most <= end) {
+      sm.f_to = uint32_t(tid);
+      sm.f_in = at.cnt + n;
+    } else if (tid == kThreads - 1 && end < most) {
+      sm.f_in = at.cnt + n;
+    }
+    __syncthreads();
+    const int bin = int(sm.f_bin), bin_to = int(sm.f_to);
+    const uint32_t above = sm.f_cnt, down_to = sm.f_in;
+    if (bin == kBins) {   // fewer than k have a mass: all of them
+      return {INFINITY, nextafterf(top + kNothing / s.c_hi, -INFINITY), false, !by_count};
+    }
+    // (a little more than the bins: a value at an edge may round to either side)
+    x_lo = nextafterf(base - (float(bin_to) + 0.51f) * unit, -INFINITY);
+    const uint32_t in = by_count ? uint32_t(over) + down_to : down_to - above;
+    const bool last = in <= kListFull || level == kLevels - 1 ||
+                      (by_count && uint32_t(top_k) > kListFull);
+    if (bin > 0)
+      x_hi = fminf(x_hi, nextafterf(base - (float(bin) - 0.51f) * unit, INFINITY));
+    if (last) return {by_count ? INFINITY : x_hi, x_lo, !by_count, false};
+    base = fminf(x_hi, top);
+    unit = fmaxf((base - x_lo) / float(kBins - 2), 1e-37f);
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 
 enum Mode { kAll, kTopK, kTopP };
@@ -826,18 +1014,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int r = int(blockIdx.x) / ctas, g = r / p.group, at = r - g * p.group;
   sm100::cluster_arrive_relaxed();   // (every CTA of the cluster runs before any writes to it)
   if (tid < kCoarse / 2) sm.lanes[tid] = make_uint4(0, 0, 0, 0);
+  sm.x_bins[tid] = 0;
   if (tid == 0) sm.nlist = sm.last = 0;
   griddep_wait();                // the stream's previous kernel has completed
   griddep_launch_dependents();   // the next kernel may start its set-up
   if (p.clear_status && blockIdx.x == 0 && tid == 0) *p.status = 0u;
 
   Part<T> part;
-  part.row = p.group == 1 ? static_cast<const T*>(p.logits) + int64_t(r) * p.stride
-             : at == 0    ? static_cast<const T*>(p.root) + int64_t(g) * p.V
-                          : static_cast<const T*>(p.logits) +
-                                (int64_t(g) * (p.group - 1) + (at - 1)) * p.V;
-  part.V = p.V;
-  part.skew = int((reinterpret_cast<uintptr_t>(part.row) / sizeof(T)) % kE);
+  part.of(p.group == 1 ? static_cast<const T*>(p.logits) + int64_t(r) * p.stride
+          : at == 0    ? static_cast<const T*>(p.root) + int64_t(g) * p.V
+                       : static_cast<const T*>(p.logits) +
+                             (int64_t(g) * (p.group - 1) + (at - 1)) * p.V,
+          p.V);
   const int nv = int((p.V + part.skew + kE - 1) / kE), per = (nv + ctas - 1) / ctas;
   part.v0 = rank * per < nv ? rank * per : nv;
   part.v1 = part.v0 + per < nv ? part.v0 + per : nv;
@@ -864,15 +1052,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (t < kSteps) sm.step_max[t][tid] = bf16_above(here);
     const float most = fmaxf(lane_max, here);
     if (!greedy) {
-      float sum = 0.f;
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < kStep; ++k) {
-        float e = 0.f;
+      for (int k = 0; k < kStep; ++k)
 #pragma unroll
-        for (int i = 0; i < kE; ++i) e += s.plain(x[k][i], most);
-        sum += e;
-      }
-      lane_sum = fmaf(lane_sum, s.plain(lane_max, most), sum);
+        for (int i = 0; i < kE; i += 2)
+          sum = add2(sum, s.plain(make_float2(x[k][i], x[k][i + 1]), most));
+      lane_sum = fmaf(lane_sum, s.plain(lane_max, most), sum.x + sum.y);
     }
     lane_max = most;
   }, [&] {
@@ -957,13 +1143,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     min_above = sm.min_above;
   }
 
-  int border = -1, border_to = -1;   // kTopP: bins that may hold the border, from the histogram
-  float depth = 0.f;      // octaves below the maximum that are listed
+  Window win = {INFINITY, -INFINITY, false, false};
   uint64_t row_mass = 0;
   if (!slow) {
     const float lane_top = s.plain(lane_max, top);
     uint64_t kept = warp_sum(mass_of(lane_sum * lane_top)), over = 0;
-    float reach = 0.f;   // what lies that far below the maximum is listed
     if (mode != kAll) {
       // ---- a bound from the lanes' maxima
       const float h = (lane_max - top) * s.c_hi;
@@ -1050,137 +1234,70 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool few = p.V <= kList || (bound < kCoarse && -__logf(below) * lanes < kListAim);
       __syncthreads();
       if (few) {
-        depth = bound < kCoarse ? float(bound + 1) / kCoarsePerOctave : -kNothing;
+        const float depth = bound < kCoarse ? float(bound + 1) / kCoarsePerOctave : -kNothing;
+        win.x_lo = nextafterf(top - depth * 1.00001f / s.c_hi, -INFINITY);
       } else {
-        // ---- the step of the border, from all values
-        for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0;
-        if (tid < kRest) sm.rest[tid] = 0;
-        __syncthreads();
-        // (weights below (1 - top_p) / V of the row's mass cannot reach the border: all of them
-        // together weigh less than what top_p drops)
-        const float share = (1.f - fmaxf(top_p, 0.f)) * 0.99f / float(p.V);
-        const float dropped = mode == kTopK ? 0.f : float(row_mass) * 0x1p-43f * share;
-        // (nor does it lie below the bound, if there was one)
-        constexpr int kFine = int(kBinsPerOctave / kCoarsePerOctave);
-        const int bins = bound < kCoarse ? (bound + 1) * kFine + 1 : kBins;
-        const float lowest = fmaxf(mode == kTopK ? kNothing : __log2f(dropped),
-                                   fmaxf(float(bins) / -kBinsPerOctave, kNothing));
-        const uint32_t exact = mode == kTopK ? 0u : uint32_t(kRest);
-        stream(part, ring, p0, p1, [&](int, int, const uint4 (&q)[kStep]) {
-#pragma unroll
-          for (int k = 0; k < kStep; ++k) {
-            float x[kE];
-            unpack<T>(q[k], x);
-#pragma unroll
-            for (int i = 0; i < kE; ++i) {
-              const float d = x[i] - top, hh = d * s.c_hi;
-              const uint32_t bin = bin_of(hh);
-              uint32_t add = 1u;
-              if (bin < exact) {   // (few, as a rule)
-                const float e = sm100::ex2_approx(fmaf(d, s.c_lo, hh));
-                const uint32_t w = octave_mass(e, int(bin >> kOctaveBits));
-                atomicAdd(&sm.rest[bin], w & 0xfffu);
-                add = w >> 12;
-              }
-              if (hh > lowest) atomicAdd(&sm.hist[bin], add);
-            }
-          }
-        });
-        sm100::cluster_sync();
-        const int t = tid * kPer;
-        static_assert(kPer == 4, "a 16-byte read");
-        uint4 w[kCtasMax];
-#pragma unroll
-        for (int c = 0; c < kCtasMax; ++c)
-          if (c < ctas && t < bins)
-            w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.hist + t), uint32_t(c)));
-        uint64_t sums[kPer] = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < kCtasMax; ++c)
-          if (c < ctas && t < bins) {
-            sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w;
-          }
-        auto sum_of = [&](int k) {
-          return Sums{k < 2 ? (k ? sums[1] : sums[0]) : (k == 3 ? sums[3] : sums[2]), 0u};
-        };
-        if (mode == kTopK) {   // (without a border fewer than k values have a mass: all are listed)
-          const int bin = find_bin<kPer>(sm, true, uint64_t(top_k), sum_of).bin;
-          depth = bin < kBins ? (float(bin) + 0.5f) / kBinsPerOctave : -kNothing;
-        } else {
-          if (t < kRest) {
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) sums[k] <<= 12;
-#pragma unroll
-            for (int c = 0; c < kCtasMax; ++c)
-              if (c < ctas) w[c] = ld_cluster_v4(sm100::mapa(smem_u32(sm.rest + t), uint32_t(c)));
-#pragma unroll
-            for (int c = 0; c < kCtasMax; ++c)
-              if (c < ctas) {
-                sums[0] += w[c].x; sums[1] += w[c].y; sums[2] += w[c].z; sums[3] += w[c].w;
-              }
-          }
-#pragma unroll
-          for (int k = 0; k < kPer; ++k)
-            sums[k] = t < kRest ? sums[k] << (kUnit - 22 - ((t + k) >> kOctaveBits))
-                                : sums[k] * mass_of(exp2f(float(t + k) / -kBinsPerOctave));
-          // the border's bin, and others where 1/8192 of the mass, which the counts may be off
-          // by, may take it to
-          const uint64_t want = top_p > 0.f ? part_of(top_p, row_mass) : 1u;
-          const uint64_t slack = min(want >> 13, (row_mass - min(want, row_mass)) >> 1);
-          const Found f = find_bin<kPer>(sm, true, want > slack ? want - slack : 1u, sum_of);
-          border = border_to = f.bin;
-          if (f.bin < kBins && f.mass + f.here < want + slack)
-            border_to = find_bin<kPer>(sm, true, want + slack, sum_of).bin;
-        }
+        win = find_window<T>(sm, part, ring, p0, p1, s, ctas, rank, mode == kTopK, top_k, top_p,
+                             row_mass,
+                             bound < kCoarse ? float(bound + 1) / kCoarsePerOctave : -kNothing);
       }
-      reach = depth * 1.00001f / s.c_hi;
     }
 
     // ---- the list, or masses and list
-    auto list = [&](float x, uint32_t index) {
-      const uint32_t n = atomicAdd(&sm.nlist, 1u);
-      if (n < kList) {
-        sm.list_value[n] = x;
-        sm.list_index[n] = index;
+    // A lane's values of a step that `mask` names.
+    auto list = [&](uint32_t mask, int v, const uint4 (&q)[kStep]) {
+      if (mask == 0) return;
+      uint32_t n = atomicAdd(&sm.nlist, uint32_t(__popc(mask)));
+#pragma unroll 1
+      for (; mask; mask &= mask - 1u, ++n) {
+        const int i = __ffs(mask) - 1;
+        if (n < kList) {
+          sm.list_value[n] = pick<T>(q, i);
+          sm.list_index[n] = part.index(v + 32 * (i / kE), i % kE);
+        }
       }
     };
-    if (border >= 0) {
-      const float upper = (float(border) - 0.5f) / -kBinsPerOctave;
-      const float lower = fmaxf((float(border_to) + 0.5f) / -kBinsPerOctave, kNothing);
+    // (min-p drops all of the window and more: top-p's border does not matter)
+    if (win.found && min_above >= win.x_hi) mode = kAll;
+    if (mode == kTopP && win.found && !win.lost) {
       kept = 0;
+      const float x_hi = win.x_hi, x_lo = win.x_lo;
+      float2 above = make_float2(0.f, 0.f);
       stream(part, ring, p0, p1, [&](int, int v, const uint4 (&q)[kStep]) {
-        float sum = 0.f, sum_kept = 0.f;
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t mask = 0;
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
           float x[kE];
           unpack<T>(q[k], x);
 #pragma unroll
-          for (int i = 0; i < kE; ++i) {
-            const float d = x[i] - top, hh = d * s.c_hi;
-            const float e = hh > upper ? sm100::ex2_approx(fmaf(d, s.c_lo, hh)) : 0.f;
-            sum += e;
-            if (min_p > 0.f) sum_kept += x[i] > min_above ? e : 0.f;
-            if (hh <= upper && hh > lower) list(x[i], part.index(v + 32 * k, i));
+          for (int i = 0; i < kE; i += 2) {
+            const float2 e = s.plain(make_float2(x[i], x[i + 1]), top);
+            if (x[i] > x_hi) sum.x += e.x;
+            if (x[i + 1] > x_hi) sum.y += e.y;
+            if (x[i] > x_lo && x[i] <= x_hi) mask |= 1u << (k * kE + i);
+            if (x[i + 1] > x_lo && x[i + 1] <= x_hi) mask |= 2u << (k * kE + i);
           }
         }
-        over += mass_of(sum);
-        if (min_p > 0.f) kept += mass_of(sum_kept);
+        above = add2(above, sum);
+        list(mask, v, q);
       });
-      over = warp_sum(over);
-      kept = min_p > 0.f ? warp_sum(kept) : over;
-    } else if (mode != kAll) {
+      over = warp_sum(mass_of(above.x + above.y));
+      kept = over;
+    } else if (mode != kAll && !win.lost) {
+      const float x_lo = win.x_lo;
       kept = 0;
-      visit(sm, part, ring, p0, p1, [&](float most) { return most - top >= -reach; },
+      visit(sm, part, ring, p0, p1, [&](float most) { return most > x_lo; },
             [&](int, int v, const uint4 (&q)[kStep]) {
+              uint32_t mask = 0;
 #pragma unroll
               for (int k = 0; k < kStep; ++k) {
                 float x[kE];
                 unpack<T>(q[k], x);
 #pragma unroll
-                for (int i = 0; i < kE; ++i)
-                  if (x[i] - top >= -reach && x[i] > -INFINITY)
-                    list(x[i], part.index(v + 32 * k, i));
+                for (int i = 0; i < kE; ++i) mask |= x[i] > x_lo ? 1u << (k * kE + i) : 0u;
               }
+              list(mask, v, q);
             });
     } else if (min_p > 0.f) {
       kept = 0;
@@ -1219,7 +1336,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   Cut cut = {-INFINITY, 0u};
   int n = 0;
   if (!slow && mode != kAll) {
-    bool ok = true;
+    bool ok = !win.lost;
     for (int c = 0; c < ctas; ++c) {
       ok = ok && sm.list_count[c] <= kList;
       n += int(min(sm.list_count[c], uint32_t(kList)));
@@ -1238,35 +1355,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     sm100::cluster_arrive_relaxed();   // (no CTA touches another's memory from here on)
     __syncthreads();
-    if (ok && n <= 32 && border < 0) {
+    if (ok && n <= 32 && !win.found) {
       if (warp == 0)
         draw_of_few(p, sm, s, r, n, mode == kTopK ? top_k : n, top_p, min_above,
                     mode == kTopK ? 0 : row_mass, u, temp_in);
       return;
     }
     uint64_t mass = row_mass;   // of which top-p takes its part
-    const float scale = float(kParts) / fmaxf(depth, 1e-3f);
+    // the list's values: from the largest on, and how many parts to 1
+    const float from = fminf(win.x_hi, top);
+    const float scale = float(kParts) / fmaxf(fminf(from - win.x_lo, -kNothing / s.c_hi), 1e-30f);
     if (ok && mode == kTopK)   // (fewer than k are listed where no others have a mass)
-      ok = border_in_list(sm, ss, s, n, 0.f, scale, false, uint64_t(min(top_k, n)), &cut, &mass);
+      ok = border_in_list(sm, ss, s, n, from, scale, false, uint64_t(min(top_k, n)), &cut, &mass);
     if (ok && top_p < 1.f) {
       uint64_t want = top_p > 0.f ? part_of(top_p, mass) : 1u, over = 0;
       want = want > 0 ? want : 1u;
-      if (border >= 0) {
+      if (win.found) {
         if (tid < ctas * kWarps) {
           const uint4 q = sm.piece[tid];
           over = uint64_t(q.z) | (uint64_t(q.w) << 32);
         }
         over = block_sum(sm, over);
-        ok = border < kBins && want > over;
+        ok = want > over;
       }
-      float base = 0.f, parts = scale;   // of an octave
-      if (border >= 0) {
-        base = (float(border) - 0.5f) / kBinsPerOctave;
-        parts = kBinsPerOctave * kParts / float(border_to - border + 1);
-      }
-      ok = ok && border_in_list(sm, ss, s, n, base, parts, true, want - over, &cut, &mass);
+      ok = ok && border_in_list(sm, ss, s, n, from, scale, true, want - over, &cut, &mass);
     }
-    if (ok && border < 0) {
+    if (ok && !win.found) {
       if (min_p > 0.f && min_above >= cut.above) cut = {min_above, 0u};
       draw_in_list(sm, ss, p, s, r, n, cut, u, temp_in);
       return;
@@ -1339,19 +1453,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       sm.piece_ties[warp] = ties;
     }
   } else if (mode != kAll) {
+    ss.clear();
+    __syncthreads();
 #pragma unroll 1
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += kThreads) {   // (cnt: ties)
       const float l = sm.list_value[i];
       if (l >= cut.above) {
         const int v = int((sm.list_index[i] + uint32_t(part.skew)) / uint32_t(kE)), c = v / per;
         const int len = (min((c + 1) * per, nv) - c * per + kWarps - 1) / kWarps;
-        const int piece = c * kWarps + (v - c * per) / len;
-        if (l > cut.above)
-          atomicAdd(reinterpret_cast<unsigned long long*>(&sm.piece[piece]),
-                    (unsigned long long)mass_of(s.weight(l)));
-        else
-          atomicAdd(&sm.piece_ties[piece], 1u);
+        ss.add(c * kWarps + (v - c * per) / len, l == cut.above ? 1u : 0u,
+               l > cut.above ? mass_of(s.weight(l)) : 0);
       }
+    }
+    __syncthreads();
+    if (tid < pieces) {
+      const uint4 q = sm.piece[tid];
+      const uint64_t mass = (uint64_t(q.x) | (uint64_t(q.y) << 32)) + ss.sum(tid);
+      sm.piece[tid] = make_uint4(uint32_t(mass), uint32_t(mass >> 32), 0u, 0u);
+      sm.piece_ties[tid] = ss.cnt[tid];
     }
   }
   __syncthreads();
@@ -1486,12 +1605,11 @@ bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stream_t stream) {
   const size_t elem = dtype == VA_F32 ? 4 : 2;
   const int64_t vecs = (p.V * int64_t(elem) + 15) / 16 + 1;
-  // As many CTAs per row as leave two on an SM.
-  // And more for long rows: 256 rows of 129280 32-bit logits take 142 us with one CTA each,
-  // 110 with two.
+  // As many CTAs per row as leave one on an SM, and more for long rows: 256 rows of 129280
+  // 32-bit logits take 119 us with one CTA each, 90 with two.
   int ctas = 1;
   while (ctas < kCtasMax && vecs / ctas > kThreads / 2 &&
-         (rows * ctas * 2 <= 2 * num_sms || vecs / ctas > 16384))
+         (rows * ctas <= num_sms || vecs / ctas > 16384))
     ctas *= 2;
   p.ctas = ctas;
   cudaLaunchAttribute attr[2];
