@@ -68,6 +68,9 @@ constexpr int kList = 4096;               // listed values of a row
 constexpr int kPart = 1024;               // of a part of the list
 constexpr float kListAim = 3000.f;        // values that a list is expected to hold at most
 constexpr uint32_t kListFull = 3500u;     // or is counted to
+constexpr int kPlaceBits = 20;            // of a listed value's place in the row
+constexpr uint32_t kPlace = (1u << kPlaceBits) - 1u;
+static_assert(VA_SAMPLE_V_MAX <= 1 << kPlaceBits, "the piece goes above the place");
 constexpr int kSteps = 16;                // steps of a piece whose maxima are kept
 constexpr int kUnit = 43;                 // masses count 2^-43
 constexpr float kNothing = -46.f;         // a height whose mass is 0
@@ -119,7 +122,7 @@ struct alignas(16) SampleSmem {
   // within the CTA
   uint32_t nlist, last, pick;
   float pick_value;
-  uint64_t drawn, total;
+  uint64_t drawn, total, want;
   float min_above;                       // min-p keeps what is above
   double min_gap;                        // T ln(min_p)
   float w_max[kWarps];
@@ -128,7 +131,7 @@ struct alignas(16) SampleSmem {
   uint32_t s_cnt[kWarps];
   uint32_t piece_ties[kPieces];
   uint32_t f_bin, f_cnt, f_in, f_to;
-  uint64_t f_mass, f_here;
+  uint64_t f_mass;
 };
 // Where the first CTA searches, over the rings: counts of parts, and their
 // masses (44 bits) in four pieces of 11 bits, whose sums over a row of 2^20 fit 32.
@@ -449,10 +452,12 @@ __device__ __forceinline__ void visit(const SampleSmem& sm, const Part<T>& part,
 // rolled: most of this kernel runs once per row, where fetching instructions costs more than
 // executing them (everything inline and unrolled, the search took 2.5 times as long).
 
-__device__ __noinline__ uint64_t warp_sum(uint64_t v) {
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {   // (three sums of 24 bits and less)
+  constexpr uint32_t kAll = 0xffffffffu, kLow = 0xffffffu;
+  const uint32_t a = __reduce_add_sync(kAll, uint32_t(v) & kLow);
+  const uint32_t b = __reduce_add_sync(kAll, uint32_t(v >> 24) & kLow);
+  const uint32_t c = __reduce_add_sync(kAll, uint32_t(v >> 48));
+  return uint64_t(a) + (uint64_t(b) << 24) + (uint64_t(c) << 48);
 }
 
 struct Sums {
@@ -465,7 +470,7 @@ __device__ __noinline__ Sums block_scan(SampleSmem& sm, uint32_t cnt, uint64_t m
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t c = cnt;
   uint64_t m = mass;
-#pragma unroll 1
+#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t c1 = __shfl_up_sync(0xffffffffu, c, o);
     const uint64_t m1 = __shfl_up_sync(0xffffffffu, m, o);
@@ -511,51 +516,30 @@ struct Found {
   int bin;         // (past the last: none)
   uint32_t cnt;    // above it
   uint64_t mass;
-  uint32_t in;     // values in it,
-  uint64_t here;   // and their mass
+  uint32_t in;     // values in it
 };
 
-// Where the count, or the mass, from the top reaches `want` (>= 1): this thread has kN bins in a
-// row, whose counts and masses get(k) gives.
-template <int kN, typename F>
-__device__ __forceinline__ Found find_bin(SampleSmem& sm, bool by_mass, uint64_t want, F&& get) {
-  if (threadIdx.x == 0) sm.f_bin = kN * kThreads;
-  Sums mine = {0, 0};
-#pragma unroll 1
-  for (int k = 0; k < kN; ++k) {
-    const Sums b = get(k);
-    mine.cnt += b.cnt;
-    mine.mass += b.mass;
-  }
-  Sums at = block_scan(sm, mine.cnt, mine.mass);
-  const uint64_t before = by_mass ? at.mass : at.cnt, here = by_mass ? mine.mass : mine.cnt;
-  if (before < want && want <= before + here) {
-#pragma unroll 1
-    for (int k = 0; k < kN; ++k) {
-      const Sums b = get(k);
-      if ((by_mass ? at.mass + b.mass : uint64_t(at.cnt + b.cnt)) >= want) {
-        sm.f_bin = uint32_t(int(threadIdx.x) * kN + k);
-        sm.f_cnt = at.cnt;
-        sm.f_mass = at.mass;
-        sm.f_in = b.cnt;
-        sm.f_here = b.mass;
-        break;
-      }
-      at.cnt += b.cnt;
-      at.mass += b.mass;
-    }
-  }
-  __syncthreads();
-  const Found f = {int(sm.f_bin), sm.f_cnt, sm.f_mass, sm.f_in, sm.f_here};
-  __syncthreads();
-  return f;
-}
+// The part in which the count, or the mass, from the top reaches `want` (>= 1).
 __device__ __noinline__ Found find_part(SampleSmem& sm, const SearchSmem& ss, bool by_mass,
                                         uint64_t want) {
-  return find_bin<kPer2>(sm, by_mass, want, [&](int k) {
-    const int i = int(threadIdx.x) * kPer2 + k;
-    return Sums{ss.sum(i), ss.cnt[i]};
-  });
+  static_assert(kPer2 == 2, "two parts of a thread");
+  if (threadIdx.x == 0) sm.f_bin = kParts;
+  const int i = int(threadIdx.x) * 2;
+  const Sums a = {ss.sum(i), ss.cnt[i]}, b = {ss.sum(i + 1), ss.cnt[i + 1]};
+  const Sums at = block_scan(sm, a.cnt + b.cnt, a.mass + b.mass);
+  const uint64_t before = by_mass ? at.mass : at.cnt;
+  const uint64_t mid = before + (by_mass ? a.mass : a.cnt), end = mid + (by_mass ? b.mass : b.cnt);
+  if (before < want && want <= end) {
+    const bool second = mid < want;
+    sm.f_bin = uint32_t(i + (second ? 1 : 0));
+    sm.f_cnt = at.cnt + (second ? a.cnt : 0u);
+    sm.f_mass = at.mass + (second ? a.mass : 0u);
+    sm.f_in = second ? b.cnt : a.cnt;
+  }
+  __syncthreads();
+  const Found f = {int(sm.f_bin), sm.f_cnt, sm.f_mass, sm.f_in};
+  __syncthreads();
+  return f;
 }
 
 __device__ __forceinline__ void tighten(Cut& cut, const Cut& other) {
@@ -695,7 +679,7 @@ __device__ __noinline__ void draw_of_few(const SampleParams& p, const SampleSmem
     if (at < index) before += w_other;
   }
   if (keep && before <= drawn && drawn < before + kept)   // one lane's
-    write_token(p, r, index, l == s.m ? 0.f : (l - s.m) / temp, total);
+    write_token(p, r, index & kPlace, l == s.m ? 0.f : (l - s.m) / temp, total);
 }
 
 // The token among the n listed values, of which `cut` keeps some: the part of the row's
@@ -714,7 +698,7 @@ __device__ __noinline__ void draw_in_list(SampleSmem& sm, SearchSmem& ss, const 
 #pragma unroll 1
   for (int i = tid; i < n; i += kThreads) {   // (cnt: ties)
     const float l = sm.list_value[i];
-    const int part = int(sm.list_index[i] >> shift);
+    const int part = int((sm.list_index[i] & kPlace) >> shift);
     if (l >= cut.above)
       ss.add(part, l == cut.above ? 1u : 0u, l > cut.above ? mass_of(s.weight(l)) : 0);
   }
@@ -745,7 +729,7 @@ __device__ __noinline__ void draw_in_list(SampleSmem& sm, SearchSmem& ss, const 
   const int part = int(sm.f_bin);
 #pragma unroll 1
   for (int i = tid; i < n; i += kThreads)
-    if (int(sm.list_index[i] >> shift) == part && sm.list_value[i] >= cut.above) {
+    if (int((sm.list_index[i] & kPlace) >> shift) == part && sm.list_value[i] >= cut.above) {
       const uint32_t to = atomicAdd(&sm.nlist, 1u);   // (a part of 1024 indices at most)
       ss.value[0][to] = sm.list_value[i];
       ss.index[to] = sm.list_index[i];
@@ -768,7 +752,7 @@ __device__ __noinline__ void draw_in_list(SampleSmem& sm, SearchSmem& ss, const 
     const bool tie = l == cut.above;
     const uint64_t w = tie ? 0 : mass_of(s.weight(l));
     if (drawn >= before + tied(ties) && drawn < before + w + tied(ties + (tie ? 1u : 0u)))
-      write_token(p, r, index, l == s.m ? 0.f : (l - s.m) / temp, total);
+      write_token(p, r, index & kPlace, l == s.m ? 0.f : (l - s.m) / temp, total);
   }
 }
 
@@ -879,8 +863,7 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
   static_assert(kBins == kThreads && kColumns == 16, "a bin and its counters for every thread");
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const float top = s.m, mass = float(row_mass) * 0x1p-43f;
-  uint64_t want = by_count ? uint64_t(top_k) : (top_p > 0.f ? part_of(top_p, row_mass) : 1u);
-  want = want > 0 ? want : 1u;
+  const uint64_t want = by_count ? uint64_t(top_k) : sm.want;
   float x_hi = INFINITY, base = top;
   if (!by_count) {
     // (weights below (1 - top_p) / V of the row's mass cannot reach the border: all of them
@@ -1076,9 +1059,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     s.c_lo = fmaxf((fmaf(-s.c_hi, temp_in, kHi) + kLo) / temp_in, 1e-45f);
   });
   // (a row with NaN is left to the slow way, by a maximum out of range)
+  const bool cuts = !greedy && mode != kAll;
   float top = block_max(sm, lane_sum == lane_sum ? lane_max : INFINITY);
+  if (cuts) {
+    // ---- for a bound from the lanes' maxima: their histogram, from this CTA's own maximum on
+    // (one far below the row's, or without any value, has its bins dropped below)
+    const float h = (lane_max - top) * s.c_hi, w = s.plain(lane_max, top);
+    if (h > kNothing) {
+      const int b = int(fminf(h * -kCoarsePerOctave, float(kCoarse - 1)));
+      uint32_t* bin = reinterpret_cast<uint32_t*>(sm.lanes) + 2 * b;
+      atomicAdd(bin, 1u);
+      atomicAdd(bin + 1, uint32_t(w * 0x1p19f));
+    }
+    const uint64_t mine = warp_sum(mass_of(lane_sum * w));
+    if (lane == 0) sm.s_mass[warp] = mine;
+    __syncthreads();
+  }
   sm100::cluster_wait();
   if (tid < ctas) sm100::st_cluster_f32(sm100::mapa(smem_u32(&sm.x_max[rank]), uint32_t(tid)), top);
+  if (cuts) {
+    // (written to every CTA before the barrier: a read of another's memory takes 1500 cycles)
+    for (int i = tid; i < ctas * (kCoarse / 2); i += kThreads) {
+      const uint4 q = sm.lanes[i % (kCoarse / 2)];
+      sm100::st_cluster_v4(sm100::mapa(smem_u32(&sm.x_lanes[rank][i % (kCoarse / 2)]),
+                                       uint32_t(i / (kCoarse / 2))), q.x, q.y, q.z, q.w);
+    }
+    if (tid < ctas) {
+      uint64_t m = 0;
+      for (int w = 0; w < kWarps; ++w) m += sm.s_mass[w];
+      st_cluster_v2(sm100::mapa(smem_u32(&sm.x_total[rank]), uint32_t(tid)), uint32_t(m),
+                    uint32_t(m >> 32));
+    }
+  }
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   // (64 bits are slow: one thread, while the cluster meets)
   if (tid == 0 && min_p > 0.f) sm.min_gap = fmin(double(temp) * log(double(min_p)), 0.0);
@@ -1146,48 +1158,35 @@ __global__ void __launch_bounds__(kThreads, 2)
   Window win = {INFINITY, -INFINITY, false, false};
   uint64_t row_mass = 0;
   if (!slow) {
-    const float lane_top = s.plain(lane_max, top);
-    uint64_t kept = warp_sum(mass_of(lane_sum * lane_top)), over = 0;
-    if (mode != kAll) {
+    uint64_t kept = 0, over = 0;
+    if (mode == kAll) {
+      if (!(min_p > 0.f)) kept = warp_sum(mass_of(lane_sum * s.plain(lane_max, top)));
+    } else {
       // ---- a bound from the lanes' maxima
-      const float h = (lane_max - top) * s.c_hi;
-      if (h > kNothing) {
-        const int b = int(fminf(h * -kCoarsePerOctave, float(kCoarse - 1)));
-        uint32_t* bin = reinterpret_cast<uint32_t*>(sm.lanes) + 2 * b;
-        atomicAdd(bin, 1u);
-        atomicAdd(bin + 1, uint32_t(lane_top * 0x1p19f));
-      }
-      if (lane == 0) sm.s_mass[warp] = kept;
-      __syncthreads();
-      if (tid < ctas) {
-        uint64_t m = 0;
-        for (int w = 0; w < kWarps; ++w) m += sm.s_mass[w];
-        st_cluster_v2(sm100::mapa(smem_u32(&sm.x_total[rank]), uint32_t(tid)), uint32_t(m),
-                      uint32_t(m >> 32));
-      }
-      // (written to every CTA before the barrier: a read of another's memory takes 1500 cycles)
-      for (int i = tid; i < ctas * (kCoarse / 2); i += kThreads) {
-        const uint4 q = sm.lanes[i % (kCoarse / 2)];
-        sm100::st_cluster_v4(sm100::mapa(smem_u32(&sm.x_lanes[rank][i % (kCoarse / 2)]),
-                                         uint32_t(i / (kCoarse / 2))), q.x, q.y, q.z, q.w);
-      }
-      sm100::cluster_sync();
-      for (int c = 0; c < ctas; ++c)
-        row_mass += uint64_t(sm.x_total[c].x) | (uint64_t(sm.x_total[c].y) << 32);
       if (warp == 0) {   // (one warp: no barriers)
         uint32_t cnt[kCoarsePer], mass[kCoarsePer], c1 = 0, m1 = 0;
+        // lane c's: the distance of CTA c's maximum, in bins and as a factor
+        const float own = lane < ctas ? sm.x_max[lane] : kLowest;
+        const float factor = s.plain(own, top);
+        const int bins = int(fminf(ceilf((top - own) * s.c_hi * kCoarsePerOctave), float(kCoarse)));
+        uint64_t total = 0;
+        if (lane < ctas)
+          total = uint64_t(sm.x_total[lane].x) | (uint64_t(sm.x_total[lane].y) << 32);
+        if (factor < 1.f) total = __umul64hi(total, __float2ull_rz(factor * 0x1p64f));
+        total = warp_sum(total);
 #pragma unroll
         for (int k = 0; k < kCoarsePer; ++k) cnt[k] = mass[k] = 0;
 #pragma unroll 1
         for (int c = 0; c < ctas; ++c) {
+          const int at = lane * kCoarsePer - __shfl_sync(0xffffffffu, bins, c);
+          const float f = __shfl_sync(0xffffffffu, factor, c);
 #pragma unroll
-          for (int k = 0; k < kCoarsePer; k += 2) {
-            const uint4 q = sm.x_lanes[c][(lane * kCoarsePer + k) / 2];
-            cnt[k] += q.x;
-            mass[k] += q.y;
-            cnt[k + 1] += q.z;
-            mass[k + 1] += q.w;
-          }
+          for (int k = 0; k < kCoarsePer; ++k)
+            if (at + k >= 0) {
+              const uint2 q = reinterpret_cast<const uint2*>(sm.x_lanes[c])[at + k];
+              cnt[k] += q.x;
+              mass[k] += uint32_t(float(q.y) * f);
+            }
         }
 #pragma unroll
         for (int k = 0; k < kCoarsePer; ++k) { c1 += cnt[k]; m1 += mass[k]; }
@@ -1203,9 +1202,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         // (weights round down here, and sums elsewhere by 2^-23: a little more is asked for)
         uint32_t want = uint32_t(top_k);
         if (mode == kTopP) {
-          const uint64_t part_p = top_p > 0.f ? part_of(top_p, row_mass) : 0;
+          const uint64_t part_p = top_p > 0.f ? part_of(top_p, total) : 1u;
           want = uint32_t(min((part_p >> (kUnit - 19)) * 65537 / 65536 + 2, uint64_t(~0u)));
+          if (lane == 0) sm.want = part_p > 0 ? part_p : 1u;
         }
+        if (lane == 0) sm.total = total;
         if (lane == 0) sm.f_bin = kCoarse;
         __syncwarp();
         const uint32_t before = mode == kTopK ? c_at : m_at, mine = mode == kTopK ? c1 : m1;
@@ -1226,6 +1227,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       __syncthreads();
       const int bound = int(sm.f_bin);
+      row_mass = sm.total;
       // (no bound: fewer than k values have a mass, of all lanes' maxima at least.)
       // With a share f of the lanes' maxima above it, the bound has some -ln(1 - f) values
       // above it for every lane.
@@ -1244,7 +1246,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ---- the list, or masses and list
-    // A lane's values of a step that `mask` names.
+    // A lane's values of a step that `mask` names; their places, and above these the piece.
+    const uint32_t place = uint32_t(rank * kWarps + warp) << kPlaceBits;
     auto list = [&](uint32_t mask, int v, const uint4 (&q)[kStep]) {
       if (mask == 0) return;
       uint32_t n = atomicAdd(&sm.nlist, uint32_t(__popc(mask)));
@@ -1253,7 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int i = __ffs(mask) - 1;
         if (n < kList) {
           sm.list_value[n] = pick<T>(q, i);
-          sm.list_index[n] = part.index(v + 32 * (i / kE), i % kE);
+          sm.list_index[n] = place | part.index(v + 32 * (i / kE), i % kE);
         }
       }
     };
@@ -1368,14 +1371,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (ok && mode == kTopK)   // (fewer than k are listed where no others have a mass)
       ok = border_in_list(sm, ss, s, n, from, scale, false, uint64_t(min(top_k, n)), &cut, &mass);
     if (ok && top_p < 1.f) {
-      uint64_t want = top_p > 0.f ? part_of(top_p, mass) : 1u, over = 0;
-      want = want > 0 ? want : 1u;
-      if (win.found) {
-        if (tid < ctas * kWarps) {
-          const uint4 q = sm.piece[tid];
-          over = uint64_t(q.z) | (uint64_t(q.w) << 32);
+      uint64_t want = sm.want, over = 0;
+      if (mode == kTopK) {
+        want = top_p > 0.f ? part_of(top_p, mass) : 1u;
+        want = want > 0 ? want : 1u;
+      }
+      if (win.found) {   // (every warp: no barriers)
+#pragma unroll 1
+        for (int i = lane; i < ctas * kWarps; i += 32) {
+          const uint4 q = sm.piece[i];
+          over += uint64_t(q.z) | (uint64_t(q.w) << 32);
         }
-        over = block_sum(sm, over);
+        over = warp_sum(over);
         ok = want > over;
       }
       ok = ok && border_in_list(sm, ss, s, n, from, scale, true, want - over, &cut, &mass);
@@ -1459,9 +1466,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = tid; i < n; i += kThreads) {   // (cnt: ties)
       const float l = sm.list_value[i];
       if (l >= cut.above) {
-        const int v = int((sm.list_index[i] + uint32_t(part.skew)) / uint32_t(kE)), c = v / per;
-        const int len = (min((c + 1) * per, nv) - c * per + kWarps - 1) / kWarps;
-        ss.add(c * kWarps + (v - c * per) / len, l == cut.above ? 1u : 0u,
+        ss.add(int(sm.list_index[i] >> kPlaceBits), l == cut.above ? 1u : 0u,
                l > cut.above ? mass_of(s.weight(l)) : 0);
       }
     }
