@@ -266,6 +266,7 @@ __device__ __forceinline__ bool va_trace_first_of_role() {
 struct DeviceInfo {
   int num_sms;
   int pairs, quads;   // resident clusters of the tensor-core kernel (2, 4 CTAs)
+  int octets;         // resident clusters of the sampling kernel (8 CTAs)
 };
 int device_info(DeviceInfo* out);
 

@@ -17,7 +17,7 @@ cudaError_t init_partial_fma();
 cudaError_t init_partial_tc(int* max_pairs, int* max_quads);
 cudaError_t init_weights_tc();
 cudaError_t init_evict();
-cudaError_t init_sample();
+cudaError_t init_sample(int* max_octets);
 cudaError_t init_decode_tc();
 cudaError_t init_prefill_tc();
 bool tc_supported(int B, int T, int H);
@@ -35,6 +35,7 @@ struct DeviceState {
   int num_sms;
   int tc_pairs;   // two-CTA clusters of the tensor-core kernel resident at once
   int tc_quads;   // four-CTA clusters (two-SM products) resident at once
+  int octets;     // eight-CTA clusters of the sampling kernel resident at once
 };
 DeviceState g_dev[kMaxDevices];   // written by va_init only
 cudaEvent_t g_ev_before = nullptr; // benchmark timing hook (va_set_partial_events)
@@ -214,6 +215,7 @@ int va::device_info(DeviceInfo* out) {
   out->num_sms = ds.num_sms;
   out->pairs = ds.tc_pairs;
   out->quads = ds.tc_quads;
+  out->octets = ds.octets;
   return VA_OK;
 }
 
@@ -228,11 +230,11 @@ VA_API int va_init(int device) {
   if (cudaGetDevice(&prev) != cudaSuccess) return VA_ERR_CUDA;
   if (cudaSetDevice(device) != cudaSuccess) return VA_ERR_CUDA;
   cudaError_t e1 = va::init_partial_fma();
-  int pairs = 0, quads = 0;
+  int pairs = 0, quads = 0, octets = 0;
   cudaError_t e2 = va::init_partial_tc(&pairs, &quads);
   cudaError_t e3 = va::init_weights_tc();
   if (e3 == cudaSuccess) e3 = va::init_evict();
-  if (e3 == cudaSuccess) e3 = va::init_sample();
+  if (e3 == cudaSuccess) e3 = va::init_sample(&octets);
   if (e3 == cudaSuccess) e3 = va::init_decode_tc();
   if (e3 == cudaSuccess) e3 = va::init_prefill_tc();
   // the no-allocation scratch array: placed now, with the device current; a
@@ -244,6 +246,7 @@ VA_API int va_init(int device) {
   g_dev[device].num_sms = prop.multiProcessorCount;
   g_dev[device].tc_pairs = pairs > 0 ? pairs : prop.multiProcessorCount / 2;
   g_dev[device].tc_quads = quads > 0 ? quads : prop.multiProcessorCount / 4;
+  g_dev[device].octets = octets > 0 ? octets : prop.multiProcessorCount / 10;
   g_dev[device].ready = 1;
   return VA_OK;
 }

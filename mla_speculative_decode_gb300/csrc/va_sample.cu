@@ -887,7 +887,7 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
     // A value's bin is the nearest multiple of `unit`, by the rounding of a sum with 2^23.
     constexpr uint32_t kZero = 0x4b000000u;
     const float per_unit = 1.f / unit;
-    const uint32_t to = smem_u32(&sm.bins[0][lane % kColumns]);
+    const uint32_t to = smem_u32(&sm.bins[0][lane % kColumns]) - kZero * uint32_t(kColumns * 4);
     float sum = 0.f;   // (counts, too: a lane has some hundred values)
     stream(part, ring, p0, p1, [&](int, int, const uint4 (&q)[kStep]) {
       uint32_t mask = 0;
@@ -898,20 +898,20 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
           // (every lane adds, to the last bin what is none: under a condition it takes twice as
-          // long)
-          const uint32_t bin = min(
-              __float_as_uint(fmaf(base - x[i], per_unit, 8388608.f)) - kZero, uint32_t(kBins - 1));
-          const bool above = x[i] > x_hi;
-          if (above) mask |= 1u << (k * kE + i);
-          asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(
-                           to + (above ? uint32_t(kBins - 1) : bin) * uint32_t(kColumns * 4))
+          // long; marks by signs, for the same reason)
+          const float d = base - x[i];   // < 0: above
+          const uint32_t sign = __float_as_uint(d) & 0x80000000u;
+          const uint32_t bin = min(__float_as_uint(fmaf(d, per_unit, 8388608.f)) | sign,
+                                   kZero + uint32_t(kBins - 1));
+          mask = __funnelshift_l(sign, mask, 1);
+          asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(to + bin * uint32_t(kColumns * 4))
                        : "memory");
         }
       }
       float e = 0.f;
 #pragma unroll 1
       for (; mask; mask &= mask - 1u)   // (few, as a rule)
-        e += by_count ? 1.f : s.plain(pick<T>(q, __ffs(mask) - 1), top);
+        e += by_count ? 1.f : s.plain(pick<T>(q, kStep * kE - __ffs(mask)), top);
       sum += e;
     });
     uint64_t over = warp_sum(by_count ? uint64_t(sum) : mass_of(sum));
@@ -1086,6 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (tid < ctas) {
       uint64_t m = 0;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) m += sm.s_mass[w];
       st_cluster_v2(sm100::mapa(smem_u32(&sm.x_total[rank]), uint32_t(tid)), uint32_t(m),
                     uint32_t(m >> 32));
@@ -1163,31 +1164,44 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!(min_p > 0.f)) kept = warp_sum(mass_of(lane_sum * s.plain(lane_max, top)));
     } else {
       // ---- a bound from the lanes' maxima
+      if (warp < ctas) {   // a CTA's bins, as seen from the row's maximum
+        const float own = sm.x_max[warp], factor = s.plain(own, top);
+        const int down = int(fminf(ceilf((top - own) * s.c_hi * kCoarsePerOctave), float(kCoarse)));
+        uint2 q[kCoarsePer];
+#pragma unroll
+        for (int k = 0; k < kCoarsePer; ++k) {
+          const int from = lane * kCoarsePer + k - down;
+          q[k] = from >= 0 ? reinterpret_cast<const uint2*>(sm.x_lanes[warp])[from]
+                           : make_uint2(0u, 0u);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kCoarsePer; k += 2)
+          sm.x_lanes[warp][(lane * kCoarsePer + k) / 2] =
+              make_uint4(q[k].x, uint32_t(float(q[k].y) * factor), q[k + 1].x,
+                         uint32_t(float(q[k + 1].y) * factor));
+        if (lane == 0) {
+          uint64_t total = uint64_t(sm.x_total[warp].x) | (uint64_t(sm.x_total[warp].y) << 32);
+          if (factor < 1.f) total = __umul64hi(total, __float2ull_rz(factor * 0x1p64f));
+          sm.s_mass[warp] = total;
+        }
+      }
+      __syncthreads();
       if (warp == 0) {   // (one warp: no barriers)
         uint32_t cnt[kCoarsePer], mass[kCoarsePer], c1 = 0, m1 = 0;
-        // lane c's: the distance of CTA c's maximum, in bins and as a factor
-        const float own = lane < ctas ? sm.x_max[lane] : kLowest;
-        const float factor = s.plain(own, top);
-        const int bins = int(fminf(ceilf((top - own) * s.c_hi * kCoarsePerOctave), float(kCoarse)));
-        uint64_t total = 0;
-        if (lane < ctas)
-          total = uint64_t(sm.x_total[lane].x) | (uint64_t(sm.x_total[lane].y) << 32);
-        if (factor < 1.f) total = __umul64hi(total, __float2ull_rz(factor * 0x1p64f));
-        total = warp_sum(total);
 #pragma unroll
         for (int k = 0; k < kCoarsePer; ++k) cnt[k] = mass[k] = 0;
-#pragma unroll 1
-        for (int c = 0; c < ctas; ++c) {
-          const int at = lane * kCoarsePer - __shfl_sync(0xffffffffu, bins, c);
-          const float f = __shfl_sync(0xffffffffu, factor, c);
+#pragma unroll 2
+        for (int c = 0; c < ctas; ++c)
 #pragma unroll
-          for (int k = 0; k < kCoarsePer; ++k)
-            if (at + k >= 0) {
-              const uint2 q = reinterpret_cast<const uint2*>(sm.x_lanes[c])[at + k];
-              cnt[k] += q.x;
-              mass[k] += uint32_t(float(q.y) * f);
-            }
-        }
+          for (int k = 0; k < kCoarsePer; k += 2) {
+            const uint4 q = sm.x_lanes[c][(lane * kCoarsePer + k) / 2];
+            cnt[k] += q.x;
+            mass[k] += q.y;
+            cnt[k + 1] += q.z;
+            mass[k + 1] += q.w;
+          }
+        const uint64_t total = warp_sum(lane < ctas ? sm.s_mass[lane] : 0);
 #pragma unroll
         for (int k = 0; k < kCoarsePer; ++k) { c1 += cnt[k]; m1 += mass[k]; }
         uint32_t c_at = c1, m_at = m1;
@@ -1607,15 +1621,29 @@ constexpr int64_t kRowsMax = int64_t(1) << 23;
 
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stream_t stream) {
-  const size_t elem = dtype == VA_F32 ? 4 : 2;
-  const int64_t vecs = (p.V * int64_t(elem) + 15) / 16 + 1;
-  // As many CTAs per row as leave one on an SM, and more for long rows: 256 rows of 129280
-  // 32-bit logits take 119 us with one CTA each, 90 with two.
+// The CTAs of a row: as many as leave one or two on an SM, and more for long rows.  Clusters of
+// eight only where each has eight SMs at once (15 do, of 152 SMs: some
+// are left over in each of the groups that clusters are placed in).  In us, 32-bit logits,
+// rows of 129280:                  1 CTA   2    4    8
+//   8 rows, top-p                   51    33   24   22
+//   17 rows, no filters             18    12   9.6  13.1
+//   64 rows, top-p                  55    39   36   40
+//   256 rows, mixed                 80    63   68  102
+// 17 rows of 500000, top-p         224   122   73   50
+int ctas_of(int64_t rows, int64_t vecs, const DeviceInfo& di) {
   int ctas = 1;
   while (ctas < kCtasMax && vecs / ctas > kThreads / 2 &&
-         (rows * ctas <= num_sms || vecs / ctas > 16384))
+         (vecs / ctas > 16384 ||
+          (2 * ctas < kCtasMax ? rows * ctas <= di.num_sms : rows <= di.octets)))
     ctas *= 2;
+  return ctas;
+}
+
+int launch_sample(SampleParams& p, int dtype, int64_t rows, const DeviceInfo& di,
+                  va_stream_t stream) {
+  const size_t elem = dtype == VA_F32 ? 4 : 2;
+  const int64_t vecs = (p.V * int64_t(elem) + 15) / 16 + 1;
+  const int ctas = ctas_of(rows, vecs, di);
   p.ctas = ctas;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1628,8 +1656,8 @@ int launch_sample(SampleParams& p, int dtype, int64_t rows, int num_sms, va_stre
   memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(unsigned(rows * ctas), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  // (one CTA on an SM where there are enough of them: 17 rows in trees 35 us, two 38)
-  cfg.dynamicSmemBytes = rows * ctas <= num_sms ? kSmemAlone : kSmem;
+  // (one CTA on an SM where there are enough of them)
+  cfg.dynamicSmemBytes = rows * ctas <= di.num_sms ? kSmemAlone : kSmem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -1657,7 +1685,7 @@ TreeLayout tree_layout(int B, int T) {
 
 }  // namespace
 
-cudaError_t init_sample() {
+cudaError_t init_sample(int* max_octets) {
   static_assert(kSmem <= 113 * 1024 && kSmemAlone >= kSmem, "two CTAs on an SM");
   const int smem = int(kSmemAlone);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<float>,
@@ -1668,6 +1696,22 @@ cudaError_t init_sample() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(sample_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kCtasMax;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(kCtasMax, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemAlone;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(max_octets, sample_kernel<float>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    *max_octets = 0;
+  }
   return e;
 }
 
@@ -1705,7 +1749,7 @@ VA_API int va_sample(const void* logits, int64_t row_stride, int dtype, int64_t 
   p.tokens = tokens;
   p.logprob = logprob;
   p.status = status;
-  return launch_sample(p, dtype, rows, di.num_sms, stream);
+  return launch_sample(p, dtype, rows, di, stream);
 }
 
 VA_API size_t va_tree_accept_sampled_workspace_bytes(int B, int T) {
@@ -1758,7 +1802,7 @@ VA_API int va_tree_accept_sampled(const void* root_logits, const void* logits, i
   p.logprob = logprob ? logprob : reinterpret_cast<float*>(w + L.logprob);
   p.status = reinterpret_cast<uint32_t*>(w);
   p.clear_status = true;
-  rc = launch_sample(p, dtype, int64_t(B) * (T + 1), di.num_sms, stream);
+  rc = launch_sample(p, dtype, int64_t(B) * (T + 1), di, stream);
   if (rc != VA_OK) return rc;
   // the walk reads each row's token as the one chunk of an argmax, and its logprob as the value
   AcceptParams a;
