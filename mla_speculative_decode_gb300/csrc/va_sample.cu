@@ -61,6 +61,7 @@ constexpr int kAhead = 3;                 // steps on their way
 constexpr int kCoarse = 128;              // bins of the lanes' maxima: 64 octaves
 constexpr int kCoarsePer = kCoarse / 32;  // of a lane
 constexpr float kCoarsePerOctave = 2.f;
+constexpr float kDeep = float(kCoarse) / kCoarsePerOctave + 1.f;   // octaves a list reaches at most
 constexpr int kBins = 512;                // bins of all values: one per thread
 constexpr int kColumns = 16;              // counters of a bin, by lane
 constexpr int kLevels = 3;                // ever finer bins
@@ -850,10 +851,10 @@ __device__ __forceinline__ float pick(const uint4 (&q)[kStep], int i) {
 // (512 bins of one counter each take 10 values a clock, these 20; 1024 of 8 columns 11).
 // For top-p a count takes its values to weigh what the bin's middle does.  Values above 2^-12 of
 // the row's mass lie above the first bins: there are fewer than 4096 of them, so that all can be
-// listed where the border lies among them, and what is left is off by less than 2^-12 of the
-// row's mass (a bin is 1/30 octave wide or so: 0.6 % of a weight in the mean, times
-// sqrt(2^-12)).  The border's bin, and others where that may take it to, are the next
-// level's range, until they hold so few values that these fit the list.
+// listed where the border lies among them, and what is left is off by some 2^-12 of the row's
+// mass (a bin is 1/50 octave wide or so: 0.4 % of a weight in the mean, times sqrt(2^-12)).  The
+// border's bin, and others where that may take it to, are the next level's range, until they
+// hold so few values that these fit the list.
 template <typename T>
 __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& part, uint32_t ring,
                                               int p0, int p1, const Scale& s, int ctas, int rank,
@@ -947,10 +948,15 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
     if (tid == kThreads - 1) sm.total = at.mass + n * one;
     if (tid == 0) { sm.f_bin = kBins; sm.f_to = kBins - 1; }
     __syncthreads();
-    // what the sums may be off by
+    // What the sums may be off by: a value by its distance from its bin's middle, sqrt(1/12) of
+    // a bin in the mean; n of them by sqrt(n) as much (four times that is allowed for); by the
+    // curvature of exp; and by the roundings of `over` and of the row's mass.
     uint64_t slack = 0;
-    if (!by_count)
-      slack = level == 0 ? row_mass >> (deep > 20.f ? 10 : 12) : (sm.total >> 12) + (row_mass >> 23);
+    if (!by_count) {
+      const float total = float(sm.total) * 0x1p-43f, u = unit * s.c_hi * 0.6931472f;
+      const float off = 1.2f * u * sqrtf(s.plain(base, top) * total) + 0.25f * u * u * total;
+      slack = __float2ull_rz(off * 0x1p43f) + (row_mass >> 21);
+    }
     const uint64_t least = want - over > slack ? want - over - slack : 1u, most = want - over + slack;
     const uint64_t end = at.mass + n * one;
     if (at.mass < least && least <= end) {
@@ -1226,17 +1232,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t before = mode == kTopK ? c_at : m_at, mine = mode == kTopK ? c1 : m1;
         if (before < want && want - before <= mine) {
           uint32_t run = before;
-          bool found = false;
+          int k = 0;
 #pragma unroll
-          for (int k = 0; k < kCoarsePer; ++k) {
-            run += mode == kTopK ? cnt[k] : mass[k];
-            if (!found) c_at += cnt[k];
-            if (!found && run >= want) {
-              found = true;
-              sm.f_bin = uint32_t(lane * kCoarsePer + k);
-            }
+          for (int i = 0; i < kCoarsePer - 1; ++i) {
+            run += mode == kTopK ? cnt[i] : mass[i];
+            if (run < want) k = i + 1;
           }
-          sm.f_cnt = c_at;   // down to the bound
+          sm.f_bin = uint32_t(lane * kCoarsePer + k);
+        }
+        __syncwarp();
+        // lanes' maxima down to the bound, and a bin more: what is another CTA's lies in its bin or
+        // in the one before
+        const int next = min(int(sm.f_bin) + 1, kCoarse - 1);
+        if (next / kCoarsePer == lane) {
+#pragma unroll
+          for (int i = 0; i < kCoarsePer; ++i) c_at += i <= next % kCoarsePer ? cnt[i] : 0u;
+          sm.f_cnt = c_at;
         }
       }
       __syncthreads();
@@ -1381,7 +1392,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t mass = row_mass;   // of which top-p takes its part
     // the list's values: from the largest on, and how many parts to 1
     const float from = fminf(win.x_hi, top);
-    const float scale = float(kParts) / fmaxf(fminf(from - win.x_lo, -kNothing / s.c_hi), 1e-30f);
+    const float scale = float(kParts) / fmaxf(fminf(from - win.x_lo, kDeep / s.c_hi), 1e-30f);
     if (ok && mode == kTopK)   // (fewer than k are listed where no others have a mass)
       ok = border_in_list(sm, ss, s, n, from, scale, false, uint64_t(min(top_k, n)), &cut, &mass);
     if (ok && top_p < 1.f) {
