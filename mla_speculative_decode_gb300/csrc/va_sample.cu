@@ -94,6 +94,7 @@ struct SampleParams {
   uint32_t* status;      // or NULL
   bool clear_status;
   int ctas;              // of a row
+  int ordered;           // groups, where their order is that of `longest_first`, or 0
 };
 
 struct alignas(16) SampleSmem {
@@ -988,6 +989,26 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
   }
 }
 
+// The group of rows that a cluster takes: those with top-p alone first, which take up to three
+// times as long as others (256 rows of mixed settings, in two waves of clusters: 61 us in the
+// order of the rows, 57 so).  kThreads groups at most.
+__device__ __forceinline__ int longest_first(SampleSmem& sm, const SampleParams& p, int which) {
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const bool is = tid < p.ordered && p.top_p[tid] < 1.f &&
+                  (!p.temperature || p.temperature[tid] > 0.f) && (!p.top_k || p.top_k[tid] <= 0);
+  const uint32_t mine = __ballot_sync(0xffffffffu, is);
+  if (lane == 0) sm.s_cnt[warp] = uint32_t(__popc(mine));
+  __syncthreads();
+  const uint32_t n = lane < kWarps ? sm.s_cnt[lane] : 0u;
+  const uint32_t all = __reduce_add_sync(0xffffffffu, n);
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0u) +
+                          uint32_t(__popc(mine & ((1u << lane) - 1u)));
+  if (tid < p.ordered && uint32_t(which) == (is ? before : all + uint32_t(tid) - before))
+    sm.pick = uint32_t(tid);
+  __syncthreads();
+  return int(sm.pick);
+}
+
 // ------------------------------------------------------------------ kernel
 
 enum Mode { kAll, kTopK, kTopP };
@@ -1000,7 +1021,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kE = Part<T>::kE;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const int ctas = p.ctas, rank = int(sm100::cluster_ctarank());
-  const int r = int(blockIdx.x) / ctas, g = r / p.group, at = r - g * p.group;
+  int r = int(blockIdx.x) / ctas, g = r / p.group;
+  const int at = r - g * p.group;
   sm100::cluster_arrive_relaxed();   // (every CTA of the cluster runs before any writes to it)
   if (tid < kCoarse / 2) sm.lanes[tid] = make_uint4(0, 0, 0, 0);
   sm.x_bins[tid] = 0;
@@ -1008,6 +1030,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_wait();                // the stream's previous kernel has completed
   griddep_launch_dependents();   // the next kernel may start its set-up
   if (p.clear_status && blockIdx.x == 0 && tid == 0) *p.status = 0u;
+  if (p.ordered) {
+    g = longest_first(sm, p, g);
+    r = g * p.group + at;
+  }
 
   Part<T> part;
   part.of(p.group == 1 ? static_cast<const T*>(p.logits) + int64_t(r) * p.stride
@@ -1656,6 +1682,9 @@ int launch_sample(SampleParams& p, int dtype, int64_t rows, const DeviceInfo& di
   const int64_t vecs = (p.V * int64_t(elem) + 15) / 16 + 1;
   const int ctas = ctas_of(rows, vecs, di);
   p.ctas = ctas;
+  // (one wave of two CTAs on an SM has no order)
+  const int64_t groups = rows / p.group;
+  p.ordered = p.top_p && groups <= kThreads && rows * ctas > 2 * di.num_sms ? int(groups) : 0;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

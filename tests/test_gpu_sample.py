@@ -1,11 +1,12 @@
 """Tokens drawn from rows of logits, and tree acceptance by sampling (va_sample,
 va_tree_accept_sampled), against the oracle in 64 bits (needs an sm_103 GPU).
 
-How far a mass may be off: the exponent (l - m) / T loses three roundings of 2^-24 of
-itself, at most 20 for a token whose mass matters here (e^-20 of the largest's, a hundred
-thousand times, is 2e-4 of a row), so 60 * 2^-24; the power of two and the sum of up to eight
-weights lose less than 2^-21, the whole number 2^-24.  In all less than 2^-17.8 of every weight,
-hence of every sum of them: BOUND.  Where the oracle finds every comparison decided by
+How far a mass may be off, in units of 2^-24 of itself: the exponent (l - m) / T loses three
+roundings of itself, at most 20 for a token whose mass matters here (e^-20 of the largest's, a
+hundred thousand times, is 2e-4 of a row), so 60, also where it is taken in two parts, to the
+maximum of a part of the row and from there; the powers of two 4 each; the sum of a step's
+weights 5, of a lane's steps (32 at most) 32, the whole numbers 2.  In all 107, less than 2^-17.2 of
+every weight, hence of every sum of them: BOUND.  Where the oracle finds every comparison decided by
 more than BOUND of the kept mass, the token has to be the oracle's; elsewhere it has to be
 a token whose stretch lies as near.  ln of a share is then off by 2 BOUND, and rounds
 to 2^-24 of itself and of the two logarithms it is made of (at most 40 together)."""
@@ -17,7 +18,7 @@ import oracle
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
-BOUND = 2.0 ** -17.8
+BOUND = 2.0 ** -17.2
 INF, NAN = float("inf"), float("nan")
 
 
@@ -257,6 +258,40 @@ def test_borders_among_thousands_of_tokens(va, V, sigma, dtype):
             assert w[between].sum() <= 4 * BOUND * w.sum() + w[between].max(), kw
 
 
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("V,sigma", [(9001, 0.1), (70001, 0.5), (70001, 0.02), (300000, 0.1)])
+def test_flat_rows_with_any_filters(va, V, sigma, dtype):
+    """No token is likely: borders of top-k and top-p lie among values that are close together."""
+    g = torch.Generator().manual_seed(V + int(100 * sigma))
+    n = 10
+    row = (sigma * torch.randn(n, V, generator=g)).to(dtype)
+    s = dict(temperature=[0.6, 1.0, 1.3, 1.0, 0.8, 1.0, 30.0, 1.0, 0.7, 1.0],
+             top_k=[0, 20, 0, 200, 1000, 3000, 50, 0, 4000, 0],
+             top_p=[0.5, 1.0, 0.9, 0.95, 0.8, 1.0, 0.9, 0.999, 0.9, 0.9999],
+             min_p=[0.0, 0.0, 0.02, 0.1, 0.0, 0.0, 0.0, 0.0, 0.5, 0.0])
+    u = np.random.default_rng(V).random(n).astype(np.float32)
+    tok, _ = va.sample(row.cuda(), dev(u.tolist()), temperature=dev(s["temperature"]),
+                       top_k=dev(s["top_k"], torch.int32), top_p=dev(s["top_p"]),
+                       min_p=dev(s["min_p"]))
+    for i, t in enumerate(tok.tolist()):
+        T, k, p, m = (float(np.float32(s[x][i])) for x in ("temperature", "top_k", "top_p", "min_p"))
+        l = row[i].double().numpy() / T
+        w = np.exp(l - l.max())
+        order = np.argsort(-l, kind="stable")[:int(k) or V]
+        before = np.concatenate([[0.0], np.cumsum(w[order])])
+        mass, before = before[-1], before[:-1]
+        keep = np.zeros(V, bool)
+        keep[order[before < p * mass] if p < 1 else order] = True
+        keep &= w >= m * (1 - BOUND)
+        rank = int(np.flatnonzero(order == t)[0])       # (among the k largest, exactly)
+        assert before[rank] < (p + 2 * BOUND) * mass and w[t] >= m * (1 - BOUND)
+        # the token's stretch holds u, but for BOUND of both sides' masses, and of the border's
+        # (kept or dropped on either side of the drawn one, and in the whole)
+        c = np.cumsum(np.where(keep, w, 0.0))
+        tol = 8 * BOUND * mass / c[-1] + w[t] / c[-1]
+        assert c[t] / c[-1] - w[t] / c[-1] - tol <= u[i] <= c[t] / c[-1] + tol, (i, t)
+
+
 @pytest.mark.parametrize("V", [3000, 6000, 20000])
 @pytest.mark.parametrize("levels", [2, 5])
 def test_few_different_logits(va, V, levels):
@@ -382,7 +417,8 @@ def tree(B, T, V, seed, dtype=F32):
 
 
 @pytest.mark.parametrize("B,T,V,dtype", [(1, 1, 37, F32), (3, 16, 5003, F32), (8, 16, 32000, BF16),
-                                         (2, 64, 9000, F16), (1, 16, 129280, F32), (20, 5, 300, F32)])
+                                         (2, 64, 9000, F16), (1, 16, 129280, F32), (20, 5, 300, F32),
+                                         (24, 16, 900, F32)])
 def test_tree_acceptance(va, B, T, V, dtype):
     lg, par, tok, slots, u = tree(B, T, V, 21 + B, dtype)
     s = settings(B, 22)
