@@ -14,29 +14,29 @@
 // One cluster of CTAs per row, a warp per piece of it.
 //   1. Each warp reads its piece (copies into a ring in shared memory, three steps ahead), with
 //      a running maximum and sum per lane, and keeps the maximum of each lane's step of 32
-//      bytes.  The cluster exchanges the maximum; the pieces' masses are then known, and a
-//      row without top-k and top-p is done but for 4.
+//      bytes.  The cluster exchanges the CTAs' maxima and sums, and where there is top-k or
+//      top-p a histogram of the lanes' maxima; a row without these is done but for 4.
 //   2. The lanes' maxima are values of the row: where k of them lie above a value, so do the k
-//      largest, and where they hold top_p of the mass, so does what lies above.  A histogram
-//      of them, over the cluster, gives that bound.
-//      Where the bound would leave too much (rows whose mass lies in thousands of tokens, or a
-//      k of thousands) a histogram of all values over -log2 w in steps of 1/32 octave finds
-//      the step of the border.  It counts values, which gives the mass of the many small ones
-//      to some 1e-4 of the row's, and adds up the masses of the first 8 octaves.
+//      largest, and where they hold top_p of the mass, so does what lies above.  That is a bound.
+//      Where it would leave too much (rows whose mass lies in thousands of tokens, or a k of
+//      thousands) `find_window` finds the border among 511 bins of all values, and if need be
+//      in the finer bins of one of these: for top-p a window of some hundred values around it.
 //   3. The values above the bound, from the steps whose maximum lies above it, go to lists, which
-//      the first CTA gathers.  (Around a border from the histogram: those of its step or
-//      two, with the exact mass of what lies above, in another pass over the row.)
+//      the first CTA gathers.  (Of a window: those in it, with the exact mass of what lies above,
+//      in another pass over the row.)
 //   4. The first CTA, alone: the border among the listed values, and the token, among what is
 //      kept of them, or in the piece in which the drawn mass falls.
-// Where the list does not hold what it should (thousands of values that lie as close as
-// 1/32 octave), and for rows with NaN or a maximum beyond 1e30, the first CTA goes through the
-// whole row again, digit by digit of the ordered values.
+// Where the list does not hold what it should (thousands of values that are equal, or cannot
+// be told apart by three levels of bins), and for rows with NaN or a maximum beyond 1e30, the
+// first CTA goes through the whole row again, digit by digit of the ordered values (0.4 ms).
 //
-// What bounds it: 256 rows of 129280 32-bit logits are read at the memory's rate in step 1 (20 us
-// of 39 without filters, one CTA per row); the rest, and all of a small batch, is latency, a
-// dozen exchanges over the block and three over the cluster.  Measured, with the clusters
-// that launch_sample chooses: 1 row of 32000 9.5 us; 64 rows of 129280 without filters 16,
-// with top-k 26, with top-p 49; 256 rows 44, 56 and 98, mixed 89.
+// What bounds it: 256 rows of 129280 32-bit logits are read at the memory's rate in step 1 (21 us
+// of 36 without filters, one CTA per row); the rest, and all of a small batch, is latency: a
+// dozen exchanges over the block, two or three over the cluster, and instructions that are
+// fetched to be executed once.  A window costs two more passes, bound by the instructions per
+// value (a dozen each).  Measured, with the clusters that ctas_of chooses: 1 row of 32000 8.5
+// us; 64 rows of 129280 without filters 13.5, with top-k 22, with top-p 35; 256 rows 39, 49 and
+// 71, mixed 57.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <string.h>
@@ -61,7 +61,7 @@ constexpr int kAhead = 3;                 // steps on their way
 constexpr int kCoarse = 128;              // bins of the lanes' maxima: 64 octaves
 constexpr int kCoarsePer = kCoarse / 32;  // of a lane
 constexpr float kCoarsePerOctave = 2.f;
-constexpr float kDeep = float(kCoarse) / kCoarsePerOctave + 1.f;   // octaves a list reaches at most
+constexpr float kDeep = float(kCoarse) / kCoarsePerOctave + 1.f;   // octaves that a list reaches
 constexpr int kBins = 512;                // bins of all values: one per thread
 constexpr int kColumns = 16;              // counters of a bin, by lane
 constexpr int kLevels = 3;                // ever finer bins
@@ -115,7 +115,7 @@ struct alignas(16) SampleSmem {
   uint16_t step_max[kSteps][kThreads];   // a lane's steps' maxima, rounded up to bf16
   // the first CTA's, written by all of the cluster
   uint32_t list_count[kCtasMax];         // values that each CTA listed
-  uint4 piece[kPieces];                  // kept mass, mass above the border's step
+  uint4 piece[kPieces];                  // kept mass, mass above the window
   uint32_t first[kCtasMax];              // lowest index of the maximum
   // every CTA's, written by all of the cluster
   float x_max[kCtasMax];
@@ -450,9 +450,9 @@ __device__ __forceinline__ void visit(const SampleSmem& sm, const Part<T>& part,
   }
 }
 
-// The functions below are called from several places and kept out of line, and their loops
-// rolled: most of this kernel runs once per row, where fetching instructions costs more than
-// executing them (everything inline and unrolled, the search took 2.5 times as long).
+// Most of what follows runs once per row, where fetching instructions costs more than executing
+// them: what is called from several places is out of line, and loops are rolled (inline and
+// unrolled, the search of 4 took 9500 cycles instead of 6000).
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {   // (three sums of 24 bits and less)
   constexpr uint32_t kAll = 0xffffffffu, kLow = 0xffffffu;
@@ -847,9 +847,10 @@ __device__ __forceinline__ float pick(const uint4 (&q)[kStep], int i) {
 // The cluster's search for the border in bins of all values, from `deep` octaves below the
 // maximum on at most.
 //
-// A level counts the values of x_lo < x <= x_hi in 511 equal bins (the last is for others), and adds up what lies above
-// x_hi.  Counters are kept by lane, 16 for a bin: additions of a warp then meet in few banks
-// (512 bins of one counter each take 10 values a clock, these 20; 1024 of 8 columns 11).
+// A level counts the values of x_lo < x <= x_hi in 511 equal bins (one more is for others), and
+// adds up what lies above x_hi.  Counters are kept by lane, 16 for a bin: a warp's additions then
+// meet in few banks (one counter for a bin takes 10 values a clock, 8 in 1024 bins 11, 32 in 256
+// bins 26).
 // For top-p a count takes its values to weigh what the bin's middle does.  Values above 2^-12 of
 // the row's mass lie above the first bins: there are fewer than 4096 of them, so that all can be
 // listed where the border lies among them, and what is left is off by some 2^-12 of the row's
@@ -958,7 +959,8 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
       const float off = 1.2f * u * sqrtf(s.plain(base, top) * total) + 0.25f * u * u * total;
       slack = __float2ull_rz(off * 0x1p43f) + (row_mass >> 21);
     }
-    const uint64_t least = want - over > slack ? want - over - slack : 1u, most = want - over + slack;
+    const uint64_t least = want - over > slack ? want - over - slack : 1u;
+    const uint64_t most = want - over + slack;
     const uint64_t end = at.mass + n * one;
     if (at.mass < least && least <= end) {
       sm.f_bin = uint32_t(tid);
@@ -1664,8 +1666,8 @@ bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 // rows of 129280:                  1 CTA   2    4    8
 //   8 rows, top-p                   51    33   24   22
 //   17 rows, no filters             18    12   9.6  13.1
-//   64 rows, top-p                  55    39   36   40
-//   256 rows, mixed                 80    63   68  102
+//   64 rows, top-p                  54    38   34   40
+//   256 rows, mixed                 82    56   68  108
 // 17 rows of 500000, top-p         224   122   73   50
 int ctas_of(int64_t rows, int64_t vecs, const DeviceInfo& di) {
   int ctas = 1;
