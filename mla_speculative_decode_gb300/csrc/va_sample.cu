@@ -903,10 +903,10 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
           // (every lane adds, to the last bin what is none: under a condition it takes twice as
           // long; marks by signs, for the same reason)
           const float d = base - x[i];   // < 0: above
-          const uint32_t sign = __float_as_uint(d) & 0x80000000u;
-          const uint32_t bin = min(__float_as_uint(fmaf(d, per_unit, 8388608.f)) | sign,
+          const uint32_t bin = min(__float_as_uint(fmaf(d, per_unit, 8388608.f)) |
+                                       (__float_as_uint(d) & 0x80000000u),
                                    kZero + uint32_t(kBins - 1));
-          mask = __funnelshift_l(sign, mask, 1);
+          mask = __funnelshift_l(__float_as_uint(d), mask, 1);
           asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(to + bin * uint32_t(kColumns * 4))
                        : "memory");
         }
