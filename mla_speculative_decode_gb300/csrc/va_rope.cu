@@ -426,11 +426,11 @@ bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 bool set_freq(const double* inv_freq, int pairs, Freq* f) {
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
   for (int i = 0; i < pairs; ++i) {
-    const double x = inv_freq[i];
-    if (!(fabs(x) < 0x1p40)) return false;
+    const double x = fabs(inv_freq[i]);
+    if (!(x < 0x1p40)) return false;
     const double hi = x * kHi, lo = fma(x, kHi, -hi) + x * kLo;
-    const double part = hi - floor(hi);   // (1 for a negative trifle)
-    f->turn[i] = (part < 1.0 ? uint64_t(part * 0x1p64) : 0) + uint64_t(int64_t(lo * 0x1p64));
+    const uint64_t turn = uint64_t((hi - floor(hi)) * 0x1p64) + uint64_t(int64_t(lo * 0x1p64));
+    f->turn[i] = inv_freq[i] < 0.0 ? 0 - turn : turn;   // (1 - a trifle would lose its last bits)
   }
   return true;
 }

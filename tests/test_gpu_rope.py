@@ -123,6 +123,20 @@ def test_far_and_negative_positions(va):
     assert torch.equal(va.rope(x, pos, freq)[0], x[0])          # position 0
 
 
+def test_negative_frequencies_turn_the_other_way(va):
+    """Small ones too, at far positions: they keep all their bits.  (Angles of a few radians,
+    of which the reference's product loses 2^-53.)"""
+    freq = [-1e-9, -3.3e-10, -1e-20, -7.7e-10, -2.9e-9, 1.1e-12, -5.5e-10, 0.0]
+    _, x = heads(6, 2, 16, F32, 13)
+    pos = torch.tensor([0, 1, 2 ** 31 - 1, -2 ** 31, 1000003, 2 ** 30 + 12345], dtype=torch.int32,
+                       device="cuda")
+    check(va.rope(x, pos, freq), x, pos, freq)
+    other = _tokens.f64(va.rope(x, pos, [-f for f in freq], inverse=True))
+    # the same angle but for its last place, 2^-34 of a turn, and 2^-24 of it
+    bound = (2 * np.pi * 2.0 ** -34 + 8 * 2.0 ** -24) * _tokens.pair_sums(_tokens.f64(x), 0, 8, False)
+    assert np.all(np.abs(_tokens.f64(va.rope(x, pos, freq)) - other) <= bound)
+
+
 def test_frequencies_of_whole_turns(va):
     """Frequencies of 2 pi times a whole number and one over a power of two turn by exact
     fractions: eighths and quarters of a turn at every position."""

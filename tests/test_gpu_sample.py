@@ -115,7 +115,8 @@ def test_one_setting_at_a_time(va, V, which):
     check(va, model_logits(n, V, 7, F32), u, **({which: s[which]} if which != "none" else {}))
 
 
-@pytest.mark.parametrize("rows,V", [(1, 129280), (3, 129281), (70, 9001), (160, 2000), (330, 700)])
+@pytest.mark.parametrize("rows,V", [(1, 129280), (3, 129281), (70, 9001), (160, 2000), (330, 700),
+                                    (700, 90)])
 def test_batches_of_all_sizes(va, rows, V):
     """Eight CTAs a row down to one."""
     u = np.random.default_rng(8).random(rows).tolist()
