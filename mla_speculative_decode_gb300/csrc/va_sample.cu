@@ -120,6 +120,7 @@ struct alignas(16) SampleSmem {
   // every CTA's, written by all of the cluster
   float x_max[kCtasMax];
   uint2 x_total[kCtasMax];               // mass
+  uint4 x_set[2];                        // the first CTA's settings
   uint2 x_over[kLevels][kCtasMax];       // what lies above a level's bins
   // within the CTA
   uint32_t nlist, last, pick;
@@ -1093,7 +1094,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     s.c_lo = fmaxf((fmaf(-s.c_hi, temp_in, kHi) + kLo) / temp_in, 1e-45f);
   });
   // (a row with NaN is left to the slow way, by a maximum out of range)
-  const bool cuts = !greedy && mode != kAll;
+  // (a matter of the call: what the CTAs exchange, and how often, must not depend on what each of
+  // them read)
+  const bool cuts = p.top_k || p.top_p;
   float top = block_max(sm, lane_sum == lane_sum ? lane_max : INFINITY);
   if (cuts) {
     // ---- for a bound from the lanes' maxima: their histogram, from this CTA's own maximum on
@@ -1110,7 +1113,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   }
   sm100::cluster_wait();
-  if (tid < ctas) sm100::st_cluster_f32(sm100::mapa(smem_u32(&sm.x_max[rank]), uint32_t(tid)), top);
+  if (tid < ctas) {
+    sm100::st_cluster_f32(sm100::mapa(smem_u32(&sm.x_max[rank]), uint32_t(tid)), top);
+    if (rank == 0) {
+      const uint32_t to = sm100::mapa(smem_u32(sm.x_set), uint32_t(tid));
+      sm100::st_cluster_v4(to, __float_as_uint(s.c_hi), __float_as_uint(s.c_lo),
+                           __float_as_uint(temp_in), __float_as_uint(u));
+      sm100::st_cluster_v4(to + 16u, __float_as_uint(top_p), __float_as_uint(min_p),
+                           uint32_t(top_k), greedy ? 1u : 0u);
+    }
+  }
   if (cuts) {
     // (written to every CTA before the barrier: a read of another's memory takes 1500 cycles)
     for (int i = tid; i < ctas * (kCoarse / 2); i += kThreads) {
@@ -1130,6 +1142,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   // (64 bits are slow: one thread, while the cluster meets)
   if (tid == 0 && min_p > 0.f) sm.min_gap = fmin(double(temp) * log(double(min_p)), 0.0);
   sm100::cluster_wait();
+  // From here on the first CTA's settings: if they change during the call, against the rules, the
+  // CTAs still agree on the barriers to come.
+  {
+    const uint4 a = sm.x_set[0], b = sm.x_set[1];
+    s.c_hi = __uint_as_float(a.x);
+    s.c_lo = __uint_as_float(a.y);
+    temp_in = __uint_as_float(a.z);
+    u = __uint_as_float(a.w);
+    top_p = __uint_as_float(b.x);
+    min_p = __uint_as_float(b.y);
+    top_k = int(b.z);
+    greedy = b.w != 0u;
+    mode = top_k > 0 && top_k < p.V ? kTopK : (top_p < 1.f ? kTopP : kAll);
+  }
+  const bool lists = mode != kAll;
   top = sm.x_max[0];
   for (int c = 1; c < ctas; ++c) top = fmaxf(top, sm.x_max[c]);
   s.m = top;
@@ -1379,12 +1406,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0) sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.list_count[rank]), 0u), sm.nlist);
     sm100::cluster_sync();
     if (rank != 0) {   // (the first CTA may read this one's list)
-      if (mode != kAll) {
+      if (lists) {
         sm100::cluster_arrive_relaxed();
         sm100::cluster_wait();
       }
       return;
     }
+    if (lists && mode == kAll) sm100::cluster_arrive_relaxed();
   }
 
   // ---- the first CTA: what is kept of the list
