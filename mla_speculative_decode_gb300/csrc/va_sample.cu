@@ -116,12 +116,13 @@ struct alignas(16) SampleSmem {
   uint16_t step_max[kSteps][kThreads];   // a lane's steps' maxima, rounded up to bf16
   // the first CTA's, written by all of the cluster
   uint32_t list_count[kCtasMax];         // values that each CTA listed
-  uint4 piece[kPieces];                  // kept mass, mass above the window
+  uint4 piece[kPieces];                  // kept mass, or what lies above the window; its ties
   uint32_t first[kCtasMax];              // lowest index of the maximum
   // every CTA's, written by all of the cluster
   float x_max[kCtasMax];
   uint2 x_total[kCtasMax];               // mass
   uint4 x_set[2];                        // the first CTA's settings
+  uint4 x_count[kCtasMax];               // of a window: values above, its largest, minus its least
   uint2 x_over[kLevels][kCtasMax];       // what lies above a level's bins
   // within the CTA
   uint32_t nlist, last, pick;
@@ -826,12 +827,51 @@ __device__ __noinline__ void border_of_row(SampleSmem& sm, SearchSmem& ss, const
   *kept = sum + found.ties * w;
 }
 
-// What is listed: x_lo < x <= x_hi.  Where a window was found among the bins of top-p, the
-// border lies in it, and masses above it are added up; otherwise x_hi is infinite.
+// What is listed, x_lo < x <= x_hi: all that may be kept (x_hi is infinite then), or a window that
+// the border lies in, with the mass of what lies above it added up.  kTies: the window holds too
+// many values for a list, one many times, as a rule.
+enum Listed { kAbove, kWindow, kTies, kLost };
 struct Window {
   float x_hi, x_lo;
-  bool found, lost;
+  Listed what;
 };
+
+// What lies above a window and in it, of a warp's piece (the counts and the mass), or of the
+// lane's part of it (the values).
+struct Counted {
+  uint64_t over;
+  uint32_t above, in;
+  float most, least;
+};
+template <typename T>
+__device__ __noinline__ Counted count_window(const Part<T> part, uint32_t ring, int p0, int p1,
+                                             const Scale s, float x_hi, float x_lo) {
+  constexpr int kE = Part<T>::kE;
+  Counted c = {0, 0u, 0u, -INFINITY, INFINITY};
+  float over = 0.f;
+  stream(part, ring, p0, p1, [&](int, int, const uint4 (&q)[kStep]) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      float x[kE];
+      unpack<T>(q[k], x);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const bool above = x[i] > x_hi, in = !above && x[i] > x_lo;
+        sum += above ? s.plain(x[i], s.m) : 0.f;
+        c.above += above ? 1u : 0u;
+        c.in += in ? 1u : 0u;
+        c.most = fmaxf(c.most, in ? x[i] : -INFINITY);
+        c.least = fminf(c.least, in ? x[i] : INFINITY);
+      }
+    }
+    over += sum;
+  });
+  c.over = warp_sum(mass_of(over));
+  c.above = __reduce_add_sync(0xffffffffu, c.above);
+  c.in = __reduce_add_sync(0xffffffffu, c.in);
+  return c;
+}
 
 // A value of a lane's step.
 template <typename T>
@@ -944,7 +984,7 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
     for (int c = 0; c < ctas; ++c)
       over += uint64_t(sm.x_over[level][c].x) | (uint64_t(sm.x_over[level][c].y) << 32);
     if (over >= want) {   // among the heaviest (or, later, lost to roundings)
-      return {INFINITY, x_hi, true, level > 0};
+      return {INFINITY, x_hi, level > 0 ? kLost : kWindow};
     }
     n = total[tid];
     const uint64_t one = by_count ? 1u : mass_of(s.plain(base - float(tid) * unit, top));
@@ -978,16 +1018,18 @@ __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& par
     const int bin = int(sm.f_bin), bin_to = int(sm.f_to);
     const uint32_t above = sm.f_cnt, down_to = sm.f_in;
     if (bin == kBins) {   // fewer than k have a mass: all of them
-      return {INFINITY, nextafterf(top + kNothing / s.c_hi, -INFINITY), false, !by_count};
+      return {INFINITY, nextafterf(top + kNothing / s.c_hi, -INFINITY), by_count ? kAbove : kLost};
     }
     // (a little more than the bins: a value at an edge may round to either side)
     x_lo = nextafterf(base - (float(bin_to) + 0.51f) * unit, -INFINITY);
-    const uint32_t in = by_count ? uint32_t(over) + down_to : down_to - above;
-    const bool last = in <= kListFull || level == kLevels - 1 ||
-                      (by_count && uint32_t(top_k) > kListFull);
     if (bin > 0)
       x_hi = fminf(x_hi, nextafterf(base - (float(bin) - 0.51f) * unit, INFINITY));
-    if (last) return {by_count ? INFINITY : x_hi, x_lo, !by_count, false};
+    // (a list of all that top-k keeps serves top-p, too)
+    if (by_count && uint32_t(over) + down_to <= kListFull) return {INFINITY, x_lo, kAbove};
+    const bool last = level == kLevels - 1;
+    const bool apart = last || !by_count || uint32_t(top_k) > kListFull || !(top_p < 1.f);
+    if (apart && down_to - above <= kListFull) return {x_hi, x_lo, kWindow};
+    if (last) return {x_hi, x_lo, kTies};
     base = fminf(x_hi, top);
     unit = fmaxf((base - x_lo) / float(kBins - 2), 1e-37f);
   }
@@ -1218,10 +1260,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     min_above = sm.min_above;
   }
 
-  Window win = {INFINITY, -INFINITY, false, false};
+  Window win = {INFINITY, -INFINITY, kAbove};
   uint64_t row_mass = 0;
   if (!slow) {
-    uint64_t kept = 0, over = 0;
+    uint64_t kept = 0;
     if (mode == kAll) {
       if (!(min_p > 0.f)) kept = warp_sum(mass_of(lane_sum * s.plain(lane_max, top)));
     } else {
@@ -1341,9 +1383,28 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     };
-    // (min-p drops all of the window and more: top-p's border does not matter)
-    if (win.found && min_above >= win.x_hi) mode = kAll;
-    if (mode == kTopP && win.found && !win.lost) {
+    // (min-p drops all of the window and more: the border in it does not matter, unless the mass
+    // that top-k keeps does)
+    if ((win.what == kWindow || win.what == kTies) && min_above >= win.x_hi) {
+      if (mode == kTopK && top_p < 1.f) win.what = kLost;
+      else mode = kAll;
+    }
+    uint32_t ties = 0;   // of a piece: values in a kTies window
+    if (mode != kAll && (win.what == kTies || (win.what == kWindow && mode == kTopK))) {
+      const Counted c = count_window<T>(part, ring, p0, p1, s, win.x_hi, win.x_lo);
+      kept = c.over;
+      ties = win.what == kTies ? c.in : 0u;
+      const float most = block_max(sm, c.most), least = block_max(sm, -c.least);
+      if (lane == 0) sm.s_cnt[warp] = c.above;
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t above = 0;
+        for (int w = 0; w < kWarps; ++w) above += sm.s_cnt[w];
+        sm100::st_cluster_v4(sm100::mapa(smem_u32(&sm.x_count[rank]), 0u), above,
+                             __float_as_uint(most), __float_as_uint(least), 0u);
+      }
+    }
+    if (mode == kTopP && win.what == kWindow) {
       kept = 0;
       const float x_hi = win.x_hi, x_lo = win.x_lo;
       float2 above = make_float2(0.f, 0.f);
@@ -1366,11 +1427,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         above = add2(above, sum);
         list(mask, v, q);
       });
-      over = warp_sum(mass_of(above.x + above.y));
-      kept = over;
-    } else if (mode != kAll && !win.lost) {
-      const float x_lo = win.x_lo;
-      kept = 0;
+      kept = warp_sum(mass_of(above.x + above.y));
+    } else if (mode != kAll && (win.what == kAbove || win.what == kWindow)) {
+      const float x_hi = win.x_hi, x_lo = win.x_lo;
       visit(sm, part, ring, p0, p1, [&](float most) { return most > x_lo; },
             [&](int, int v, const uint4 (&q)[kStep]) {
               uint32_t mask = 0;
@@ -1379,11 +1438,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                 float x[kE];
                 unpack<T>(q[k], x);
 #pragma unroll
-                for (int i = 0; i < kE; ++i) mask |= x[i] > x_lo ? 1u << (k * kE + i) : 0u;
+                for (int i = 0; i < kE; ++i)
+                  mask |= x[i] > x_lo && x[i] <= x_hi ? 1u << (k * kE + i) : 0u;
               }
               list(mask, v, q);
             });
-    } else if (min_p > 0.f) {
+    } else if (mode == kAll && min_p > 0.f) {
       kept = 0;
       visit(sm, part, ring, p0, p1, [&](float most) { return most > min_above; },
             [&](int, int, const uint4 (&q)[kStep]) {
@@ -1400,8 +1460,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (lane == 0) {
       const uint32_t to = sm100::mapa(smem_u32(&sm.piece[rank * kWarps + warp]), 0u);
-      sm100::st_cluster_v4(to, uint32_t(kept), uint32_t(kept >> 32), uint32_t(over),
-                           uint32_t(over >> 32));
+      sm100::st_cluster_v4(to, uint32_t(kept), uint32_t(kept >> 32), ties, 0u);
     }
     __syncthreads();
     if (tid == 0) sm100::st_cluster_u32(sm100::mapa(smem_u32(&sm.list_count[rank]), 0u), sm.nlist);
@@ -1421,7 +1480,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   Cut cut = {-INFINITY, 0u};
   int n = 0;
   if (!slow && mode != kAll) {
-    bool ok = !win.lost;
+    bool ok = win.what != kLost;
     for (int c = 0; c < ctas; ++c) {
       ok = ok && sm.list_count[c] <= kList;
       n += int(min(sm.list_count[c], uint32_t(kList)));
@@ -1440,7 +1499,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     sm100::cluster_arrive_relaxed();   // (no CTA touches another's memory from here on)
     __syncthreads();
-    if (ok && n <= 32 && !win.found) {
+    if (ok && n <= 32 && win.what == kAbove) {
       if (warp == 0)
         draw_of_few(p, sm, s, r, n, mode == kTopK ? top_k : n, top_p, min_above,
                     mode == kTopK ? 0 : row_mass, u, temp_in);
@@ -1450,26 +1509,57 @@ __global__ void __launch_bounds__(kThreads, 2)
     // the list's values: from the largest on, and how many parts to 1
     const float from = fminf(win.x_hi, top);
     const float scale = float(kParts) / fmaxf(fminf(from - win.x_lo, kDeep / s.c_hi), 1e-30f);
-    if (ok && mode == kTopK)   // (fewer than k are listed where no others have a mass)
-      ok = border_in_list(sm, ss, s, n, from, scale, false, uint64_t(min(top_k, n)), &cut, &mass);
-    if (ok && top_p < 1.f) {
-      uint64_t want = sm.want, over = 0;
-      if (mode == kTopK) {
-        want = top_p > 0.f ? part_of(top_p, mass) : 1u;
-        want = want > 0 ? want : 1u;
-      }
-      if (win.found) {   // (every warp: no barriers)
+    uint64_t over = 0;   // above the window
+    uint32_t above = 0, in = 0;
+    if (win.what != kAbove) {   // (every warp: no barriers)
 #pragma unroll 1
-        for (int i = lane; i < ctas * kWarps; i += 32) {
-          const uint4 q = sm.piece[i];
-          over += uint64_t(q.z) | (uint64_t(q.w) << 32);
-        }
-        over = warp_sum(over);
-        ok = want > over;
+      for (int i = lane; i < ctas * kWarps; i += 32) {
+        const uint4 q = sm.piece[i];
+        over += uint64_t(q.x) | (uint64_t(q.y) << 32);
+        in += q.z;
       }
-      ok = ok && border_in_list(sm, ss, s, n, from, scale, true, want - over, &cut, &mass);
+      over = warp_sum(over);
+      in = __reduce_add_sync(0xffffffffu, in);
+      if (mode == kTopK)
+        for (int c = 0; c < ctas; ++c) above += sm.x_count[c].x;
     }
-    if (ok && !win.found) {
+    if (win.what == kTies) {
+      float most = -INFINITY, least = -INFINITY;
+      for (int c = 0; c < ctas; ++c) {
+        most = fmaxf(most, __uint_as_float(sm.x_count[c].y));
+        least = fmaxf(least, __uint_as_float(sm.x_count[c].z));
+      }
+      ok = ok && most == -least;   // one value
+      const uint64_t w = mass_of(s.weight(most));
+      if (ok && mode == kTopK) {
+        ok = above < uint32_t(top_k) && uint32_t(top_k) - above <= in;
+        in = uint32_t(top_k) - above;
+        mass = over + in * w;
+      }
+      if (ok && top_p < 1.f) {
+        uint64_t want = sm.want;
+        if (mode == kTopK) want = top_p > 0.f ? part_of(top_p, mass) : 1u;
+        ok = want > over && want - over <= in * w;
+        if (ok) in = ties_of(want - over, w, in);
+      }
+      cut = {most, in};
+    } else {
+      if (ok && mode == kTopK) {   // (fewer than k are listed where no others have a mass)
+        ok = above < uint32_t(top_k) &&
+             (win.what == kAbove || uint32_t(top_k) - above <= uint32_t(n));
+        ok = ok && border_in_list(sm, ss, s, n, from, scale, false,
+                                  uint64_t(min(top_k - int(above), n)), &cut, &mass);
+        mass += over;
+      }
+      if (ok && top_p < 1.f) {
+        uint64_t want = sm.want;
+        if (mode == kTopK) want = top_p > 0.f ? part_of(top_p, mass) : 1u;
+        want = want > 0 ? want : 1u;
+        ok = want > over;
+        ok = ok && border_in_list(sm, ss, s, n, from, scale, true, want - over, &cut, &mass);
+      }
+    }
+    if (ok && win.what == kAbove) {
       if (min_p > 0.f && min_above >= cut.above) cut = {min_above, 0u};
       draw_in_list(sm, ss, p, s, r, n, cut, u, temp_in);
       return;
@@ -1557,7 +1647,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint4 q = sm.piece[tid];
       const uint64_t mass = (uint64_t(q.x) | (uint64_t(q.y) << 32)) + ss.sum(tid);
       sm.piece[tid] = make_uint4(uint32_t(mass), uint32_t(mass >> 32), 0u, 0u);
-      sm.piece_ties[tid] = ss.cnt[tid];
+      sm.piece_ties[tid] = ss.cnt[tid] + q.z;
     }
   }
   __syncthreads();

@@ -259,18 +259,11 @@ def test_borders_among_thousands_of_tokens(va, V, sigma, dtype):
             assert w[between].sum() <= 4 * BOUND * w.sum() + w[between].max(), kw
 
 
-@pytest.mark.parametrize("dtype", [F32, F16])
-@pytest.mark.parametrize("V,sigma", [(9001, 0.1), (70001, 0.5), (70001, 0.02), (300000, 0.1)])
-def test_flat_rows_with_any_filters(va, V, sigma, dtype):
-    """No token is likely: borders of top-k and top-p lie among values that are close together."""
-    g = torch.Generator().manual_seed(V + int(100 * sigma))
-    n = 10
-    row = (sigma * torch.randn(n, V, generator=g)).to(dtype)
-    s = dict(temperature=[0.6, 1.0, 1.3, 1.0, 0.8, 1.0, 30.0, 1.0, 0.7, 1.0],
-             top_k=[0, 20, 0, 200, 1000, 3000, 50, 0, 4000, 0],
-             top_p=[0.5, 1.0, 0.9, 0.95, 0.8, 1.0, 0.9, 0.999, 0.9, 0.9999],
-             min_p=[0.0, 0.0, 0.02, 0.1, 0.0, 0.0, 0.0, 0.0, 0.5, 0.0])
-    u = np.random.default_rng(V).random(n).astype(np.float32)
+def check_stretches(va, row, s, seed):
+    """Each row's token is kept and its stretch holds the uniform, both to BOUND; s: settings of
+    every row."""
+    n, V = row.shape
+    u = np.random.default_rng(seed).random(n).astype(np.float32)
     tok, _ = va.sample(row.cuda(), dev(u.tolist()), temperature=dev(s["temperature"]),
                        top_k=dev(s["top_k"], torch.int32), top_p=dev(s["top_p"]),
                        min_p=dev(s["min_p"]))
@@ -291,6 +284,35 @@ def test_flat_rows_with_any_filters(va, V, sigma, dtype):
         c = np.cumsum(np.where(keep, w, 0.0))
         tol = 8 * BOUND * mass / c[-1] + w[t] / c[-1]
         assert c[t] / c[-1] - w[t] / c[-1] - tol <= u[i] <= c[t] / c[-1] + tol, (i, t)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("V,sigma", [(9001, 0.1), (70001, 0.5), (70001, 0.02), (300000, 0.1)])
+def test_flat_rows_with_any_filters(va, V, sigma, dtype):
+    """No token is likely: borders of top-k and top-p lie among values that are close together."""
+    g = torch.Generator().manual_seed(V + int(100 * sigma))
+    n = 10
+    row = (sigma * torch.randn(n, V, generator=g)).to(dtype)
+    s = dict(temperature=[0.6, 1.0, 1.3, 1.0, 0.8, 1.0, 30.0, 1.0, 0.7, 1.0],
+             top_k=[0, 20, 0, 200, 1000, 3000, 50, 0, 4000, 0],
+             top_p=[0.5, 1.0, 0.9, 0.95, 0.8, 1.0, 0.9, 0.999, 0.9, 0.9999],
+             min_p=[0.0, 0.0, 0.02, 0.1, 0.0, 0.0, 0.0, 0.0, 0.5, 0.0])
+    check_stretches(va, row, s, V)
+
+
+@pytest.mark.parametrize("V,step", [(50000, 0.125), (262144, 0.125), (262144, 2.0), (1 << 20, 0.5)])
+def test_thousands_of_ties_at_the_border(va, V, step):
+    """Large logits of a 16-bit type: few different values, each thousands of times, and a
+    top-k of thousands."""
+    g = torch.Generator().manual_seed(V)
+    n = 9
+    row = ((torch.randn(n, V, generator=g) * 2 + 20) / step).round().mul(step).to(BF16)
+    row[8] = 20.0
+    s = dict(temperature=[1.0, 1.0, 2.0, 1.0, 1.0, 0.7, 1.0, 1.0, 1.0],
+             top_k=[0, 0, 0, 10000, 5000, 0, 20000, V // 2, 0],
+             top_p=[0.9, 0.99, 0.5, 1.0, 0.8, 0.95, 0.9999, 0.999, 0.9],
+             min_p=[0.0, 0.0, 0.0, 0.0, 0.0, 0.05, 0.3, 0.0, 0.0])
+    check_stretches(va, row, s, V)
 
 
 @pytest.mark.parametrize("V", [3000, 6000, 20000])
