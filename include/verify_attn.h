@@ -691,8 +691,8 @@ int va_kv_append_paged(void *kv_pool, int64_t num_slots, int64_t kv_row_stride,
  * the result does not depend on the order of sums: the same call gives the same token.
  * One launch; each logit is read from memory once, and again, from L2 as a rule, where a
  * border of top-k or top-p asks for it.  Settings and logits must not change during the call.
- * Rows with NaN, with a top-k of more than 3500 or so, or whose border lies among more than 4096
- * equal logits take longer than others, one CTA each (0.4 ms for 129280 logits).
+ * Rows with NaN, and rare others (a top-p within a top-k of thousands), take longer, one CTA each
+ * (0.35 ms for 129280 logits).
  */
 #define VA_SAMPLE_V_MAX (1 << 20)
 int va_sample(const void *logits, int64_t row_stride, int dtype, int64_t rows, int64_t V,

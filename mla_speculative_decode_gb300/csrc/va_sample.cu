@@ -20,16 +20,17 @@
 //      largest, and where they hold top_p of the mass, so does what lies above.  That is a bound.
 //      Where it would leave too much (rows whose mass lies in thousands of tokens, or a k of
 //      thousands) `find_window` finds the border among 511 bins of all values, and if need be
-//      in the finer bins of one of these: for top-p a window of some hundred values around it.
+//      in the finer bins of one of these: a window of some hundred values around it, or of one
+//      value that the row has thousands of times.
 //   3. The values above the bound, from the steps whose maximum lies above it, go to lists, which
 //      the first CTA gathers.  (Of a window: those in it, with the exact mass of what lies above,
-//      in another pass over the row.)
+//      in another pass over the row; of a single value its count.)
 //   4. The first CTA, alone: the border among the listed values, and the token, among what is
 //      kept of them, or in the piece in which the drawn mass falls.
-// Where the list does not hold what it should (a top-k of more than 3500 or so, thousands of
-// values that are equal, or cannot be told apart by three levels of bins), and for rows with NaN
-// or a maximum beyond 1e30, the first CTA goes through the whole row again, digit by digit of the
-// ordered values (0.4 ms for 129280 of them).
+// Where the list does not hold what it should (thousands of values that three levels of bins do
+// not tell apart, a top-p within a top-k of thousands whose border lies above that of top-k), and
+// for rows with NaN or a maximum beyond 1e30, the first CTA goes through the whole row again, digit
+// by digit of the ordered values (0.35 ms for 129280 of them).
 //
 // What bounds it: 256 rows of 129280 32-bit logits are read at the memory's rate in step 1 (21 us
 // of 36 without filters, one CTA per row); the rest, and all of a small batch, is latency: a
@@ -898,7 +899,8 @@ __device__ __forceinline__ float pick(const uint4 (&q)[kStep], int i) {
 // listed where the border lies among them, and what is left is off by some 2^-12 of the row's
 // mass (a bin is 1/50 octave wide or so: 0.4 % of a weight in the mean, times sqrt(2^-12)).  The
 // border's bin, and others where that may take it to, are the next level's range, until they
-// hold so few values that these fit the list.
+// hold so few values that these fit the list.  After the last level a bin is so narrow that more of
+// them are equal, as a rule: kTies.
 template <typename T>
 __device__ __forceinline__ Window find_window(SampleSmem& sm, const Part<T>& part, uint32_t ring,
                                               int p0, int p1, const Scale& s, int ctas, int rank,
