@@ -586,6 +586,40 @@ def test_memory_of_a_given_stream(va):
         side.synchronize()
 
 
+def test_calls_on_two_streams_at_once(va):
+    """Long and short rows, one CTA each and clusters, prepared and captured: what each gives by
+    itself."""
+    V = 60000
+    calls, alone = [], []
+    for i, n in enumerate((3, 40, 200, 7)):
+        x = model_logits(n, V, 60 + i, (F32, BF16)[i % 2]).cuda()
+        s = settings(n, 61 + i)
+        u = dev(np.random.default_rng(62 + i).random(n).tolist())
+        calls.append(dict(logits=x, uniform=u, temperature=dev(s["temperature"]),
+                          top_k=dev(s["top_k"], torch.int32), top_p=dev(s["top_p"]),
+                          min_p=dev(s["min_p"])))
+        alone.append([t.clone() for t in va.sample(**calls[-1])])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    graphs = []
+    for c, s in zip(calls, streams):
+        call = va.prepare_sample(**c)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call()
+        graphs.append((g, call))
+    for _ in range(5):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(va.sample(**c))
+                graphs[i][0].replay()
+    torch.cuda.synchronize()
+    for i, want in enumerate(alone):
+        for tok, lp in got[i] + [graphs[i][1].result]:
+            assert torch.equal(tok, want[0]) and torch.equal(lp, want[1])
+
+
 def test_refusals(va):
     x, u = torch.zeros(3, 10, device="cuda"), torch.zeros(3, device="cuda")
     k = torch.zeros(3, dtype=torch.int32, device="cuda")
